@@ -6,7 +6,8 @@ kernels of libmoe.so.  There is no fallback: if the library is missing or cannot
 import-time use fails loudly.
 
 MoeLayer is a small convenience wrapper that takes torch CUDA tensors (PyTorch is used only
-for device memory and streams) and raises MoeError on a non-zero status.
+for device memory and streams) and raises MoeError on a non-zero status.  PagedAttention is the
+same for the attention step over a paged 4-bit cache (include/attn.h).
 
 With MOE_DEBUG_LIBRARY=1 in the environment the binding loads libmoe_debug.so instead: the same
 library built with MOE_DEBUG, which checks every routing it produces (moe_check_routing) and
@@ -37,6 +38,9 @@ EXPORTS = ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_ge
            "moe_profile_end", "moe_route_one_noalloc", "moe_create_q4", "moe_read_probe",
            "moe_test_expire_waits", "gdn_scan", "moe_check_routing")
 
+ATTN_EXPORTS = ("attn_create", "attn_destroy", "attn_get_device_error", "attn_plan",
+                "attn_qk_norm_rope", "attn_kv4_append", "attn_kv4_read", "attn_kv4_forward")
+
 # kernel order reported by moe_profile_end
 KERNELS_GEMM = ("router_topk", "route_plan_scatter", "experts", "combine")
 KERNELS_GEMV = ("decode_router_shared", "decode_gateup", "decode_down_combine")
@@ -65,6 +69,17 @@ class moe_weights_q4(ctypes.Structure):
                 ("w_gate", moe_q4_matrix), ("w_up", moe_q4_matrix), ("w_down", moe_q4_matrix),
                 ("ws_gate", moe_q4_matrix), ("ws_up", moe_q4_matrix),
                 ("ws_down", moe_q4_matrix)]
+
+
+class attn_config(ctypes.Structure):
+    _fields_ = [("n_q_heads", _c_int), ("n_kv_heads", _c_int), ("head_dim", _c_int),
+                ("page_size", _c_int), ("n_pages", _c_int), ("max_requests", _c_int),
+                ("scale", ctypes.c_float)]
+
+
+class attn_kv4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", _c_void_p), ("k_params", _c_void_p), ("v_codes", _c_void_p),
+                ("v_params", _c_void_p)]
 
 
 _lib = None
@@ -103,6 +118,26 @@ def lib():
         L.gdn_scan.argtypes = [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                _c_void_p, _c_void_p, ctypes.c_int64, _c_int, _c_int, _c_int,
                                _c_void_p]
+        i64, cache = ctypes.c_int64, ctypes.POINTER(attn_kv4_cache)
+        L.attn_create.argtypes = [ctypes.POINTER(attn_config), ctypes.POINTER(_c_void_p)]
+        L.attn_destroy.argtypes = [_c_void_p]
+        L.attn_get_device_error.argtypes = [_c_void_p, _c_void_p]
+        L.attn_plan.argtypes = [_c_void_p, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_int,
+                                _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_void_p,
+                                _c_void_p, _c_void_p, _c_void_p, _c_void_p]
+        L.attn_qk_norm_rope.argtypes = [_c_void_p, _c_void_p, i64, _c_void_p, i64, _c_void_p,
+                                        _c_void_p, _c_void_p, ctypes.c_float, _c_void_p, _c_int,
+                                        _c_int, _c_int, _c_int, _c_void_p, i64, _c_void_p, i64,
+                                        _c_void_p]
+        L.attn_kv4_append.argtypes = [_c_void_p, _c_void_p, i64, _c_void_p, i64, _c_void_p,
+                                      _c_int, cache, _c_void_p]
+        L.attn_kv4_read.argtypes = [_c_void_p, cache, _c_void_p, _c_int, _c_void_p, i64,
+                                    _c_void_p, i64, _c_void_p]
+        L.attn_kv4_forward.argtypes = [_c_void_p, _c_void_p, i64, cache, _c_void_p, _c_int,
+                                       _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                                       _c_void_p, i64, _c_void_p]
+        for fn in ATTN_EXPORTS:
+            getattr(L, fn).restype = _c_int
         for fn in ("moe_create", "moe_create_q4", "moe_read_probe", "moe_route", "moe_forward", "moe_forward_host",
                    "moe_get_device_error", "moe_destroy", "moe_last_cuda_error",
                    "moe_profile_begin", "moe_profile_end", "moe_route_one_noalloc",
@@ -173,6 +208,50 @@ def gdn_scan(q, k, v, alpha, beta, state_in, state_out, o, T, H, dk, dv, stream)
     """Gated DeltaNet recurrent scan over T tokens of H heads (see include/gdn.h); device
     pointers, state_in may be None (zero state)."""
     return lib().gdn_scan(q, k, v, alpha, beta, state_in, state_out, o, T, H, dk, dv, stream)
+
+
+def attn_create(cfg):
+    """Returns (status, handle)."""
+    h = _c_void_p()
+    st = lib().attn_create(ctypes.byref(cfg), ctypes.byref(h))
+    return st, h
+
+
+def attn_destroy(h):
+    return lib().attn_destroy(h)
+
+
+def attn_get_device_error(h, stream):
+    return lib().attn_get_device_error(h, stream)
+
+
+def attn_plan(h, block_table, table_width, ctx_lens, new_lens, B, free_pages, n_free, cursor, T,
+              q_offsets, kv_lens, positions, slots, cursor_out, stream):
+    return lib().attn_plan(h, block_table, table_width, ctx_lens, new_lens, B, free_pages, n_free,
+                           cursor, T, q_offsets, kv_lens, positions, slots, cursor_out, stream)
+
+
+def attn_qk_norm_rope(h, q, q_stride, k, k_stride, positions, q_weight, k_weight, eps, cos_sin,
+                      n_positions, rotary_dim, interleaved, T, q_out, q_out_stride, k_out,
+                      k_out_stride, stream):
+    return lib().attn_qk_norm_rope(h, q, q_stride, k, k_stride, positions, q_weight, k_weight,
+                                   eps, cos_sin, n_positions, rotary_dim, interleaved, T, q_out,
+                                   q_out_stride, k_out, k_out_stride, stream)
+
+
+def attn_kv4_append(h, k, k_stride, v, v_stride, slots, T, cache, stream):
+    """cache: an attn_kv4_cache (or None)."""
+    return lib().attn_kv4_append(h, k, k_stride, v, v_stride, slots, T, cache, stream)
+
+
+def attn_kv4_read(h, cache, slots, T, k, k_stride, v, v_stride, stream):
+    return lib().attn_kv4_read(h, cache, slots, T, k, k_stride, v, v_stride, stream)
+
+
+def attn_kv4_forward(h, q, q_stride, cache, block_table, table_width, q_offsets, kv_lens, B, T,
+                     max_q_len, max_kv_len, out, out_stride, stream):
+    return lib().attn_kv4_forward(h, q, q_stride, cache, block_table, table_width, q_offsets,
+                                  kv_lens, B, T, max_q_len, max_kv_len, out, out_stride, stream)
 
 
 def moe_test_expire_waits(h, n_calls):
@@ -295,6 +374,185 @@ class MoeLayer:
     def close(self):
         if self.handle:
             _check(moe_destroy(self.handle), "moe_destroy")
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _stream_of(stream):
+    import torch
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _want(t, what, dtype, shape):
+    """Checks a tensor argument: on the GPU, of this type and shape (None: any size)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)) or not t.is_cuda:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: expected a CUDA {dtype} tensor of shape "
+                       f"{tuple('any' if n is None else n for n in shape)}, got {t.device.type} "
+                       f"{t.dtype} {tuple(t.shape)}")
+    return t
+
+
+class Kv4Cache:
+    """One layer's 4-bit cache as torch tensors (layout in include/attn.h).  `struct` is the
+    attn_kv4_cache that the C entry points take."""
+
+    def __init__(self, n_pages, n_kv_heads, page_size, head_dim, device="cuda"):
+        import torch
+        rows = (n_pages, n_kv_heads, page_size)
+        self.k_codes = torch.zeros(rows + (head_dim // 2,), dtype=torch.uint8, device=device)
+        self.v_codes = torch.zeros_like(self.k_codes)
+        self.k_params = torch.zeros(rows + (head_dim // 64,), dtype=torch.int32, device=device)
+        self.v_params = torch.zeros_like(self.k_params)
+        self.struct = attn_kv4_cache(_ptr(self.k_codes), _ptr(self.k_params), _ptr(self.v_codes),
+                                     _ptr(self.v_params))
+
+
+class PagedAttention:
+    """The attention step over a paged 4-bit cache (include/attn.h) on torch CUDA tensors.
+
+    One object serves every layer of the same shape; each layer has a cache of its own
+    (new_cache).  Queries, keys, values and outputs are bf16 [T][heads][head_dim], rows may be
+    strided (views of a fused projection's output).  Outputs not given are allocated.  Calls are
+    enqueued on the current stream, or on `stream`.
+    """
+
+    def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
+                 scale=0.0):
+        self.handle = None
+        self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self.page_size, self.n_pages, self.max_requests = page_size, n_pages, max_requests
+        cfg = attn_config(n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
+                          scale)
+        st, self.handle = attn_create(cfg)
+        _check(st, "attn_create")
+
+    def new_cache(self):
+        return Kv4Cache(self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
+
+    def _rows(self, t, what, heads, tokens=None):
+        import torch
+        _want(t, what, torch.bfloat16, (tokens, heads, self.head_dim))
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim):
+            raise MoeError(MOE_ERR_UNSUPPORTED, f"{what}: a token's heads must be contiguous")
+        # with one token the stride says nothing
+        return t.stride(0) if t.shape[0] > 1 else heads * self.head_dim
+
+    @staticmethod
+    def _ints(t, what, *shape):
+        import torch
+        _want(t, what, torch.int32, shape)
+        if not t.is_contiguous():
+            raise MoeError(MOE_ERR_UNSUPPORTED, f"{what}: must be contiguous")
+        return t.data_ptr()
+
+    def plan(self, block_table, ctx_lens, new_lens, free_pages, cursor, q_offsets=None,
+             kv_lens=None, positions=None, slots=None, cursor_out=None, T=None, stream=None):
+        """Extends block_table for new_lens tokens after ctx_lens cached ones, taking pages from
+        free_pages[cursor:]; returns (q_offsets, kv_lens, positions, slots, cursor_out).  Without
+        positions and slots, T gives their size."""
+        import torch
+        B, width = block_table.shape
+        like = dict(dtype=torch.int32, device=block_table.device)
+        if positions is not None:
+            T = positions.shape[0]
+        elif T is None:
+            raise MoeError(MOE_ERR_INVALID_ARG, "plan: positions or T")
+        else:
+            positions = torch.empty(T, **like)
+        slots = torch.empty(T, **like) if slots is None else slots
+        q_offsets = torch.empty(B + 1, **like) if q_offsets is None else q_offsets
+        kv_lens = torch.empty(B, **like) if kv_lens is None else kv_lens
+        cursor_out = torch.empty(1, **like) if cursor_out is None else cursor_out
+        ints = self._ints
+        _check(lib().attn_plan(
+            self.handle, ints(block_table, "block_table", B, width), width,
+            ints(ctx_lens, "ctx_lens", B), ints(new_lens, "new_lens", B), B,
+            ints(free_pages, "free_pages", None), free_pages.shape[0],
+            ints(cursor, "cursor", 1), T, ints(q_offsets, "q_offsets", B + 1),
+            ints(kv_lens, "kv_lens", B), ints(positions, "positions", T),
+            ints(slots, "slots", T), ints(cursor_out, "cursor_out", 1), _stream_of(stream)),
+            "attn_plan")
+        return q_offsets, kv_lens, positions, slots, cursor_out
+
+    def qk_norm_rope(self, q, k, positions, q_weight, k_weight, cos_sin, eps=1e-6,
+                     interleaved=False, q_out=None, k_out=None, stream=None):
+        """Norm of each query and key head and rotation by cos_sin [positions][rotary_dim] (None:
+        no rotation); returns (q_out, k_out)."""
+        import torch
+        T = q.shape[0]
+        D = self.head_dim
+        qs, ks = self._rows(q, "q", self.n_q_heads), self._rows(k, "k", self.n_kv_heads, T)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        qos = self._rows(q_out, "q_out", self.n_q_heads, T)
+        kos = self._rows(k_out, "k_out", self.n_kv_heads, T)
+        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            _want(w, what, torch.bfloat16, (D,))
+        n_pos = rot = 0
+        if cos_sin is not None:
+            n_pos, rot = _want(cos_sin, "cos_sin", torch.float32, (None, None)).shape
+            if not cos_sin.is_contiguous():
+                raise MoeError(MOE_ERR_UNSUPPORTED, "cos_sin: must be contiguous")
+        _check(lib().attn_qk_norm_rope(
+            self.handle, q.data_ptr(), qs, k.data_ptr(), ks,
+            None if rot == 0 else self._ints(positions, "positions", T), q_weight.data_ptr(),
+            k_weight.data_ptr(), eps, _ptr(cos_sin), n_pos, rot, int(interleaved), T,
+            q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream_of(stream)),
+            "attn_qk_norm_rope")
+        return q_out, k_out
+
+    def append(self, k, v, slots, cache, stream=None):
+        """Quantises keys and values [T][Hkv][D] into the cached rows of slots [T]."""
+        T = k.shape[0]
+        ks, vs = self._rows(k, "k", self.n_kv_heads), self._rows(v, "v", self.n_kv_heads, T)
+        _check(lib().attn_kv4_append(self.handle, k.data_ptr(), ks, v.data_ptr(), vs,
+                                     self._ints(slots, "slots", T), T, cache.struct,
+                                     _stream_of(stream)), "attn_kv4_append")
+
+    def read(self, slots, cache, k_out=None, v_out=None, stream=None):
+        """Cached rows of slots [T] as bf16; returns (k_out, v_out)."""
+        import torch
+        T = slots.shape[0]
+        shape = (T, self.n_kv_heads, self.head_dim)
+        like = dict(dtype=torch.bfloat16, device=slots.device)
+        k_out = torch.empty(shape, **like) if k_out is None else k_out
+        v_out = torch.empty(shape, **like) if v_out is None else v_out
+        ks = self._rows(k_out, "k_out", self.n_kv_heads, T)
+        vs = self._rows(v_out, "v_out", self.n_kv_heads, T)
+        _check(lib().attn_kv4_read(self.handle, cache.struct, self._ints(slots, "slots", T), T,
+                                   k_out.data_ptr(), ks, v_out.data_ptr(), vs,
+                                   _stream_of(stream)), "attn_kv4_read")
+        return k_out, v_out
+
+    def forward(self, q, cache, block_table, q_offsets, kv_lens, max_q_len, max_kv_len, out=None,
+                stream=None):
+        """Causal attention of the requests' new tokens over their cached rows; returns out."""
+        import torch
+        T = q.shape[0]
+        B, width = block_table.shape
+        qs = self._rows(q, "q", self.n_q_heads)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        os_ = self._rows(out, "out", self.n_q_heads, T)
+        ints = self._ints
+        _check(lib().attn_kv4_forward(
+            self.handle, q.data_ptr(), qs, cache.struct,
+            ints(block_table, "block_table", B, width), width,
+            ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B), B, T, max_q_len,
+            max_kv_len, out.data_ptr(), os_, _stream_of(stream)), "attn_kv4_forward")
+        return out
+
+    def device_error(self, stream=None):
+        return attn_get_device_error(self.handle, _stream_of(stream))
+
+    def close(self):
+        if self.handle:
+            _check(attn_destroy(self.handle), "attn_destroy")
             self.handle = None
 
     def __del__(self):

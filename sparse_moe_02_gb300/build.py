@@ -13,8 +13,9 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_debug.so")
 SOURCES = ["api.cu", "route.cu", "experts.cu", "decode.cu", "decode_q4.cu", "noalloc.cu", "probe.cu",
-           "hostio.cu", "gdn.cu", "check.cu"]
-HEADERS = ["layer.cuh", "plan.cuh", "ptx.cuh", "select.cuh", "q4.cuh"]
+           "hostio.cu", "gdn.cu", "check.cu", "attn_api.cu", "attn_plan.cu", "attn_rows.cu",
+           "attn_decode.cu"]
+HEADERS = ["layer.cuh", "plan.cuh", "ptx.cuh", "select.cuh", "q4.cuh", "attn.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + CSRC,
          "-I" + os.path.join(ROOT, "include")]
@@ -25,7 +26,7 @@ def _stale():
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(LIB_DEBUG))
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps += [os.path.join(ROOT, "include", h) for h in ("moe.h", "gdn.h")]
+    deps += [os.path.join(ROOT, "include", h) for h in ("moe.h", "gdn.h", "attn.h")]
     deps += [os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 

@@ -8,6 +8,7 @@
 #include <new>
 #include <vector>
 
+#include "attn.cuh"
 #include "layer.cuh"
 #include "moe.h"
 
@@ -86,6 +87,10 @@ void* device_view(const void* p) {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
+
+namespace moe {
+int record_cuda_status(cudaError_t e) { return cuda_status(e); }
+}  // namespace moe
 
 struct moe_handle_s {
   moe_config cfg;

@@ -1,0 +1,138 @@
+// Internal interface of the attention step (include/attn.h): argument blocks, launchers, and the
+// arithmetic of a cached row that the kernels share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "layer.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kGroup = 64;        // channels per scale and bias
+constexpr int kDevErrNoMemory = 7;
+constexpr int kDevErrArg = 1;
+
+struct AttnDims {
+  int Hq, Hkv, G, D;
+  int page_shift;  // log2 of the page size
+  int n_pages;
+  float scale_log2;  // softmax scale * log2(e)
+};
+
+struct Kv4 {
+  uint8_t* kc;
+  uint32_t* kp;
+  uint8_t* vc;
+  uint32_t* vp;
+};
+
+// Position (in units of D/64 words) of word j of every group in the row of slot s.
+__host__ __device__ __forceinline__ int row_swz(int s) { return ((s & 3) << 1) ^ (s & 4); }
+
+// A device-side error: of several the largest value stays.
+__device__ __forceinline__ void record_error(int* err, int code) { atomicMax(err, code); }
+
+// One request of a step as the kernels see it: its rows, and its lengths moved into range.
+struct Req {
+  int q0, qn, kv;
+};
+
+struct FwdArgs {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  __nv_bfloat16* out;
+  int64_t out_stride;
+  Kv4 c;
+  const int32_t* table;
+  int table_width;
+  const int32_t* q_off;
+  const int32_t* kv_lens;
+  int B, T, max_q;
+  AttnDims d;
+  float* part_o;     // partial outputs: [2 * blocks][columns][D] fp32
+  float2* part_ml;   // their softmax reference and sum: [2 * blocks][columns]
+  int4* desc;        // [blocks]: (parts, request, head, row tile) of a shared context
+  int* err;
+};
+
+__device__ __forceinline__ Req load_req(const FwdArgs& a, int b) {
+  const int lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_lens[b];
+  Req r;
+  r.q0 = min(max(lo, 0), a.T);
+  r.qn = min(max(hi, r.q0), a.T) - r.q0;
+  if (r.qn > a.max_q) r.qn = a.max_q;
+  const int64_t cap = (int64_t)a.table_width << a.d.page_shift;
+  r.kv = (int)min((int64_t)max(kv, 0), cap);
+  return r;
+}
+
+// Whether load_req had to move something into range.
+__device__ __forceinline__ bool req_out_of_range(const FwdArgs& a, int b) {
+  const int lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_lens[b];
+  return lo < 0 || hi < lo || hi > a.T || hi - lo > a.max_q || kv < 0 ||
+         kv > ((int64_t)a.table_width << a.d.page_shift);
+}
+
+// Records the cudaError_t for moe_last_cuda_error and returns the status.
+int record_cuda_status(cudaError_t e);
+
+struct PlanArgs {
+  int32_t* table;
+  int table_width;
+  const int32_t* ctx;
+  const int32_t* news;
+  int B;
+  const int32_t* free_pages;
+  int n_free;
+  const int32_t* cursor;
+  int T;
+  int32_t *q_offsets, *kv_lens, *positions, *slots, *cursor_out;
+  int page_shift;
+  int* ticket;  // blocks that are done; back to 0 when the launch ends
+  int* err;
+};
+
+cudaError_t prepare_attn_plan_kernel(int max_requests);
+cudaError_t launch_attn_plan(const PlanArgs& a, int sms, cudaStream_t s);
+
+struct RopeArgs {
+  const __nv_bfloat16 *q, *k;
+  __nv_bfloat16 *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const int32_t* positions;
+  const __nv_bfloat16 *qw, *kw;
+  float eps;
+  const float* cos_sin;
+  int n_positions, rot, T, Hq, Hkv;
+  int* err;
+};
+
+cudaError_t launch_attn_qk_norm_rope(const RopeArgs& a, int D, bool interleaved, int sms,
+                                     cudaStream_t s);
+
+struct RowsArgs {
+  const __nv_bfloat16 *k, *v;  // append: inputs
+  __nv_bfloat16 *ko, *vo;      // read: outputs
+  int64_t k_stride, v_stride;
+  const int32_t* slots;
+  int T, Hkv, page_shift;
+  int64_t n_slots;
+  Kv4 c;
+  int* err;
+};
+
+cudaError_t launch_attn_append(const RowsArgs& a, int D, int sms, cudaStream_t s);
+cudaError_t launch_attn_read(const RowsArgs& a, int D, int sms, cudaStream_t s);
+
+// Attention of few query rows per key/value head and request (n_b G <= 16): attn_decode.cu.
+constexpr int kDecodeRows = 16;
+cudaError_t prepare_attn_decode_kernels();
+int attn_decode_blocks(int sms);          // blocks of a split launch
+size_t attn_decode_part_floats(int D);    // fp32 of one partial result
+cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,318 @@
+// The row kernels of the attention step (include/attn.h): norm and rotation of query and key
+// heads, quantisation of keys and values into the paged 4-bit cache, and the way back.  Each is
+// one pass over its rows, bound by HBM for prompts and by launch latency for single tokens: a
+// lane holds 8 channels (one 16-byte load), the D / 8 lanes of a row reduce by shuffles.
+#include "attn.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Row8 {
+  float x[8];
+};
+
+__device__ __forceinline__ Row8 widen(uint4 w) {
+  Row8 r;
+  r.x[0] = bf16_lo(w.x); r.x[1] = bf16_hi(w.x); r.x[2] = bf16_lo(w.y); r.x[3] = bf16_hi(w.y);
+  r.x[4] = bf16_lo(w.z); r.x[5] = bf16_hi(w.z); r.x[6] = bf16_lo(w.w); r.x[7] = bf16_hi(w.w);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 narrow(const Row8& r) {
+  return make_uint4(pack_bf16(r.x[0], r.x[1]), pack_bf16(r.x[2], r.x[3]),
+                    pack_bf16(r.x[4], r.x[5]), pack_bf16(r.x[6], r.x[7]));
+}
+
+// ------------------------------------------------------------------- norm and rotation
+
+// A group of L = D / 8 lanes takes one token's heads first, first + step, ...: the token's cosines and
+// sines and the norm weights stay in registers for all of them.  Single tokens spread their
+// heads over as many groups as there are (heads_per = 1); prompts keep a token's heads together.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads) attn_rope_kernel(RopeArgs a, int heads_per) {
+  constexpr int L = D / 8;
+  constexpr int kPerBlock = kThreads / L;
+  const int li = threadIdx.x % L;
+  const int ch = 8 * li;
+  const int heads = a.Hq + a.Hkv;
+  const int splits = (heads + heads_per - 1) / heads_per;
+  const int64_t items = (int64_t)a.T * splits;
+  const int half = a.rot / 2;
+  const bool turn = ch < a.rot;
+  pdl_wait();
+  pdl_trigger();
+  const Row8 wq = widen(*reinterpret_cast<const uint4*>(a.qw + ch));
+  const Row8 wk = widen(*reinterpret_cast<const uint4*>(a.kw + ch));
+  // groups of one warp run the same number of rounds, so that their shuffles meet
+  const int64_t rounds = (items + (int64_t)gridDim.x * kPerBlock - 1) / ((int64_t)gridDim.x * kPerBlock);
+  for (int64_t it = 0; it < rounds; ++it) {
+    const int64_t item = (it * gridDim.x + blockIdx.x) * kPerBlock + threadIdx.x / L;
+    const bool live = item < items;
+    const int t = live ? (int)(item / splits) : 0;
+    const int h0 = live ? (int)(item % splits) * heads_per : heads;
+    float cs[8], sn[8];
+    if (turn && live) {
+      int pos = a.positions[t];
+      if (pos < 0 || pos >= a.n_positions) {
+        if (li == 0) record_error(a.err, kDevErrState);
+        pos = 0;
+      }
+      const float* row = a.cos_sin + (int64_t)pos * a.rot;
+      if (INTER) {  // pairs ch / 2 .. ch / 2 + 3
+        const float4 c = *reinterpret_cast<const float4*>(row + ch / 2);
+        const float4 s = *reinterpret_cast<const float4*>(row + half + ch / 2);
+        cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+        sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
+      } else {
+        const int i = ch < half ? ch : ch - half;
+        // the upper half of a pair turns to b cos + a sin: its sine enters with the other sign
+        const float sg = ch < half ? -1.f : 1.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * e);
+          const float4 s = *reinterpret_cast<const float4*>(row + half + i + 4 * e);
+          cs[4 * e] = c.x; cs[4 * e + 1] = c.y; cs[4 * e + 2] = c.z; cs[4 * e + 3] = c.w;
+          sn[4 * e] = sg * s.x; sn[4 * e + 1] = sg * s.y;
+          sn[4 * e + 2] = sg * s.z; sn[4 * e + 3] = sg * s.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
+    }
+#pragma unroll 4
+    for (int i = 0; i < heads_per; ++i) {
+      const int h = h0 + i;
+      const bool on = h < heads;
+      const bool isq = h < a.Hq;
+      Row8 r;
+      if (on) {
+        const __nv_bfloat16* src = isq ? a.q + t * a.q_stride + (int64_t)h * D
+                                       : a.k + t * a.k_stride + (int64_t)(h - a.Hq) * D;
+        r = widen(*reinterpret_cast<const uint4*>(src + ch));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.x[e] = 0.f;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(r.x[e], r.x[e], sum);
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      const float inv = rsqrtf(sum * (1.f / D) + a.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.x[e] = r.x[e] * inv * (isq ? wq.x[e] : wk.x[e]);
+      if (a.rot) {
+        if (INTER) {
+          if (turn) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = r.x[2 * e], y = r.x[2 * e + 1];
+              r.x[2 * e] = x * cs[e] - y * sn[e];
+              r.x[2 * e + 1] = y * cs[e] + x * sn[e];
+            }
+          }
+        } else {
+          // the pair's other half sits half / 8 lanes away
+          const int base = (threadIdx.x & 31) - li;
+          const int mate = turn ? base + (ch < half ? li + half / 8 : li - half / 8)
+                                : (threadIdx.x & 31);
+          Row8 m;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m.x[e] = __shfl_sync(~0u, r.x[e], mate);
+          if (turn) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.x[e] = r.x[e] * cs[e] + m.x[e] * sn[e];
+          }
+        }
+      }
+      if (on) {
+        __nv_bfloat16* dst = isq ? a.q_out + t * a.q_out_stride + (int64_t)h * D
+                                 : a.k_out + t * a.k_out_stride + (int64_t)(h - a.Hq) * D;
+        *reinterpret_cast<uint4*>(dst + ch) = narrow(r);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- cached rows
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+struct Coded {
+  uint32_t word;    // the lane's 8 codes
+  uint32_t params;  // the group's scale and bias
+  bool finite;
+};
+
+// Codes of the lane's 8 channels; the 8 lanes of a group share lo, step.  The division and the
+// rounding are the plain fp32 operations, so every code equals the definition's.
+__device__ __forceinline__ Coded code_row(const Row8& r) {
+  float lo = r.x[0], hi = r.x[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) lo = min_nan(lo, r.x[e]), hi = max_nan(hi, r.x[e]);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(~0u, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(~0u, hi, o));
+  }
+  const float raw = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
+  const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
+  const float step = __bfloat162float(sb);
+  Coded c;
+  c.finite = fabsf(raw) < __int_as_float(0x7f800000) && fabsf(step) < __int_as_float(0x7f800000);
+  c.word = 0;
+  if (step > 0.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = rintf(__fdiv_rn(__fsub_rn(r.x[e], lo), step));
+      c.word |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (4 * e);
+    }
+  }
+  const __nv_bfloat16 lb = __float2bfloat16_rn(lo);
+  c.params = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(lb) << 16);
+  return c;
+}
+
+// A group of L = D / 8 lanes per (token, head): key row and value row together, since a
+// non-finite channel of either marks both.  Prompts keep two rows in flight per group.
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
+  constexpr int L = D / 8, NG = D / kGroup;
+  constexpr int kPerBlock = kThreads / L;
+  const int li = threadIdx.x % L;
+  const unsigned group_mask = L == 32 ? ~0u : ((1u << L) - 1) << ((threadIdx.x & 31) - li);
+  const int64_t rows = (int64_t)a.T * a.Hkv;
+  const int page = 1 << a.page_shift;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t per_round = (int64_t)gridDim.x * kPerBlock;
+  const int64_t rounds = (rows + per_round - 1) / per_round;
+#pragma unroll 2
+  for (int64_t it = 0; it < rounds; ++it) {
+    const int64_t row = (it * gridDim.x + blockIdx.x) * kPerBlock + threadIdx.x / L;
+    const bool live = row < rows;
+    const int t = live ? (int)(row / a.Hkv) : 0, h = live ? (int)(row % a.Hkv) : 0;
+    const int slot = live ? a.slots[t] : -1;
+    const uint4 kw = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + 8 * li);
+    const uint4 vw = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + 8 * li);
+    Coded k = code_row(widen(kw)), v = code_row(widen(vw));
+    const bool good = (__ballot_sync(~0u, !(k.finite && v.finite)) & group_mask) == 0;
+    if (!good) {  // queries that see the token read NaN, through its scores
+      k.word = v.word = 0;
+      k.params = 0x7fc00000u;
+      v.params = 0;
+    }
+    if (slot >= a.n_slots) {
+      if (li == 0) record_error(a.err, kDevErrState);
+    } else if (slot >= 0) {
+      const int64_t at = ((int64_t)(slot >> a.page_shift) * a.Hkv + h) * page + (slot & (page - 1));
+      const int word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
+      reinterpret_cast<uint32_t*>(a.c.kc)[at * (D / 8) + word] = k.word;
+      reinterpret_cast<uint32_t*>(a.c.vc)[at * (D / 8) + word] = v.word;
+      if ((li & 7) == 0) {
+        a.c.kp[at * NG + (li >> 3)] = k.params;
+        a.c.vp[at * NG + (li >> 3)] = v.params;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t params) {
+  const float step = bf16_lo(params), lo = bf16_hi(params);
+  Row8 r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    r.x[e] = __fadd_rn(__fmul_rn(step, (float)((w >> (4 * e)) & 15u)), lo);
+  return narrow(r);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_read_kernel(RowsArgs a) {
+  constexpr int L = D / 8, NG = D / kGroup;
+  constexpr int kPerBlock = kThreads / L;
+  const int li = threadIdx.x % L;
+  const int64_t rows = (int64_t)a.T * a.Hkv;
+  const int page = 1 << a.page_shift;
+  pdl_wait();
+  pdl_trigger();
+#pragma unroll 2
+  for (int64_t row = (int64_t)blockIdx.x * kPerBlock + threadIdx.x / L; row < rows;
+       row += (int64_t)gridDim.x * kPerBlock) {
+    const int t = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
+    const int slot = a.slots[t];
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (slot >= 0 && slot < a.n_slots) {
+      const int64_t at = ((int64_t)(slot >> a.page_shift) * a.Hkv + h) * page + (slot & (page - 1));
+      const int word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
+      k = decode_word(reinterpret_cast<const uint32_t*>(a.c.kc)[at * (D / 8) + word],
+                      a.c.kp[at * NG + (li >> 3)]);
+      v = decode_word(reinterpret_cast<const uint32_t*>(a.c.vc)[at * (D / 8) + word],
+                      a.c.vp[at * NG + (li >> 3)]);
+    } else if (slot >= a.n_slots && li == 0) {
+      record_error(a.err, kDevErrState);
+    }
+    *reinterpret_cast<uint4*>(a.ko + t * a.k_stride + h * D + 8 * li) = k;
+    *reinterpret_cast<uint4*>(a.vo + t * a.v_stride + h * D + 8 * li) = v;
+  }
+}
+
+int row_grid(int64_t items, int per_block, int sms) {
+  const int64_t blocks = (items + per_block - 1) / per_block;
+  const int64_t most = (int64_t)sms * (2048 / kThreads);
+  return (int)(blocks < most ? blocks : most);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_qk_norm_rope(const RopeArgs& a, int D, bool inter, int sms,
+                                     cudaStream_t s) {
+  const int per_block = kThreads / (D / 8);
+  const int heads = a.Hq + a.Hkv;
+  // as few heads per group as still leave one item for every group that fits the GPU
+  const int64_t groups = (int64_t)sms * (2048 / kThreads) * per_block;
+  int heads_per = (int)((a.T * (int64_t)heads + groups - 1) / groups);
+  if (heads_per > heads) heads_per = heads;
+  const int splits = (heads + heads_per - 1) / heads_per;
+  const dim3 grid(row_grid((int64_t)a.T * splits, per_block, sms)), block(kThreads);
+  if (D == 64)
+    return inter ? launch_pdl(attn_rope_kernel<64, true>, grid, block, 0, s, a, heads_per)
+                 : launch_pdl(attn_rope_kernel<64, false>, grid, block, 0, s, a, heads_per);
+  if (D == 128)
+    return inter ? launch_pdl(attn_rope_kernel<128, true>, grid, block, 0, s, a, heads_per)
+                 : launch_pdl(attn_rope_kernel<128, false>, grid, block, 0, s, a, heads_per);
+  return inter ? launch_pdl(attn_rope_kernel<256, true>, grid, block, 0, s, a, heads_per)
+               : launch_pdl(attn_rope_kernel<256, false>, grid, block, 0, s, a, heads_per);
+}
+
+cudaError_t launch_attn_append(const RowsArgs& a, int D, int sms, cudaStream_t s) {
+  const dim3 grid(row_grid((int64_t)a.T * a.Hkv, kThreads / (D / 8), sms)), block(kThreads);
+  if (D == 64) return launch_pdl(attn_append_kernel<64>, grid, block, 0, s, a);
+  if (D == 128) return launch_pdl(attn_append_kernel<128>, grid, block, 0, s, a);
+  return launch_pdl(attn_append_kernel<256>, grid, block, 0, s, a);
+}
+
+cudaError_t launch_attn_read(const RowsArgs& a, int D, int sms, cudaStream_t s) {
+  const dim3 grid(row_grid((int64_t)a.T * a.Hkv, kThreads / (D / 8), sms)), block(kThreads);
+  if (D == 64) return launch_pdl(attn_read_kernel<64>, grid, block, 0, s, a);
+  if (D == 128) return launch_pdl(attn_read_kernel<128>, grid, block, 0, s, a);
+  return launch_pdl(attn_read_kernel<256>, grid, block, 0, s, a);
+}
+
+}  // namespace moe
