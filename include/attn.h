@@ -36,14 +36,17 @@
  *     i of request b (kv_b = its cached tokens with the new ones); a query that sees no token
  *     gives 0.  Scores, softmax sums and outputs are held in fp32 and rounded once to bf16.
  *
- * Cache of one layer (caller-owned device memory, each array 16-byte aligned, written by
- * attn_kv4_append only; slot s = page * P + offset):
- *   codes   uint8 [n_pages][Hkv][P][D/2]
- *   params  uint32 [n_pages][Hkv][P][D/64]: group g's scale (bf16, lower half) and bias (upper)
- * Inside a row of codes, 32-bit word j (0..7) of group g holds the codes of channels 64g + 8j ..
- * 64g + 8j + 7, the lowest nibble first, and lies at word (j ^ f(s)) * (D/64) + g, f(s) = 2 (s &
- * 3) ^ (s & 4): the order in which the attention kernels read rows without shared-memory bank
- * conflicts.  A row takes D/2 + D/16 bytes: 0.5625 bytes a channel.
+ * Cache of one layer: one caller-owned device array of n_pages * Hkv * P * (D + D / 8) bytes (0.5625
+ * bytes a channel), 128-byte aligned, written by attn_kv4_append only: records [n_pages][Hkv][P / 16]
+ * of 16 tokens of one head each, so that an attention kernel takes 16 tokens in one copy.  A record:
+ *   key codes     uint8 [16][D/2]
+ *   key params    uint32 [16][D/64]: group g's scale (bf16, lower half) and bias (upper half)
+ *   value codes   uint8 [16][D/2]
+ *   value params  uint32 [16][D/64]
+ * Slot s = page * P + offset is row offset % 16 of record offset / 16 of its page.  Inside a row of
+ * codes, 32-bit word j (0..7) of group g holds the codes of channels 64g + 8j .. 64g + 8j + 7, the
+ * lowest nibble first, and lies at word (j ^ f(s)) * (D/64) + g, f(s) = 2 (s & 3) ^ (s & 4): the
+ * order in which the attention kernels read rows without shared-memory bank conflicts.
  *
  * Ownership and threading: every tensor is a caller-owned device pointer; calls only enqueue
  * work on `stream` (a cudaStream_t as void*, NULL = the legacy default stream) and never
@@ -81,16 +84,9 @@ typedef struct {
   int head_dim;     /* D: 64, 128 or 256 */
   int page_size;    /* P: 16, 32, 64, 128 or 256 */
   int n_pages;      /* pages of a layer's cache; n_pages * page_size < 2^31 */
-  int max_requests; /* largest B accepted later: 1..4096 */
+  int max_requests; /* largest B accepted later: 1..1024 */
   float scale;      /* softmax scale, > 0; 0 means D^-1/2 */
 } attn_config;
-
-typedef struct { /* one layer's cache, device pointers (see above) */
-  void* k_codes;
-  void* k_params;
-  void* v_codes;
-  void* v_params;
-} attn_kv4_cache;
 
 /* Validates cfg, allocates the workspace on the current CUDA device and returns a handle in *out.
  * May synchronise the device.  On failure *out is NULL and nothing stays allocated.  One handle
@@ -140,13 +136,12 @@ int attn_qk_norm_rope(attn_handle h, const void* q, int64_t q_stride, const void
  * [T] (int32); one launch.  A negative slot is skipped; one beyond the cache is skipped and
  * recorded (MOE_ERR_DEVICE).  The slots of a call are distinct. */
 int attn_kv4_append(attn_handle h, const void* k, int64_t k_stride, const void* v,
-                    int64_t v_stride, const int32_t* slots, int T, const attn_kv4_cache* cache,
-                    void* stream);
+                    int64_t v_stride, const int32_t* slots, int T, void* cache, void* stream);
 
 /* Cached rows of T slots as bf16 [T][Hkv][D], step * code + lo in fp32 rounded once; a slot
  * outside the cache gives zeros (recorded unless negative). */
-int attn_kv4_read(attn_handle h, const attn_kv4_cache* cache, const int32_t* slots, int T,
-                  void* k, int64_t k_stride, void* v, int64_t v_stride, void* stream);
+int attn_kv4_read(attn_handle h, const void* cache, const int32_t* slots, int T, void* k,
+                  int64_t k_stride, void* v, int64_t v_stride, void* stream);
 
 /* Causal attention of B requests' new tokens over the cache (their own rows are appended
  * already).  q, out [T][Hq][D] bf16: request b's tokens are rows q_offsets[b] .. q_offsets[b+1] - 1;
@@ -154,7 +149,7 @@ int attn_kv4_read(attn_handle h, const attn_kv4_cache* cache, const int32_t* slo
  * max_q_len >= 1 and max_kv_len >= 0 bound n_b and kv_b (from above; they choose kernels and
  * grids, a capacity will do): a request beyond max_q_len is cut to it (MOE_ERR_DEVICE).  Rows of
  * out that belong to no request are left as they are.  The same inputs give the same bits. */
-int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const attn_kv4_cache* cache,
+int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void* cache,
                      const int32_t* block_table, int table_width, const int32_t* q_offsets,
                      const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
                      void* out, int64_t out_stride, void* stream);

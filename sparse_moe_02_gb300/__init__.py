@@ -77,11 +77,6 @@ class attn_config(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
-class attn_kv4_cache(ctypes.Structure):
-    _fields_ = [("k_codes", _c_void_p), ("k_params", _c_void_p), ("v_codes", _c_void_p),
-                ("v_params", _c_void_p)]
-
-
 _lib = None
 
 
@@ -118,7 +113,7 @@ def lib():
         L.gdn_scan.argtypes = [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                _c_void_p, _c_void_p, ctypes.c_int64, _c_int, _c_int, _c_int,
                                _c_void_p]
-        i64, cache = ctypes.c_int64, ctypes.POINTER(attn_kv4_cache)
+        i64 = ctypes.c_int64
         L.attn_create.argtypes = [ctypes.POINTER(attn_config), ctypes.POINTER(_c_void_p)]
         L.attn_destroy.argtypes = [_c_void_p]
         L.attn_get_device_error.argtypes = [_c_void_p, _c_void_p]
@@ -130,10 +125,10 @@ def lib():
                                         _c_int, _c_int, _c_int, _c_void_p, i64, _c_void_p, i64,
                                         _c_void_p]
         L.attn_kv4_append.argtypes = [_c_void_p, _c_void_p, i64, _c_void_p, i64, _c_void_p,
-                                      _c_int, cache, _c_void_p]
-        L.attn_kv4_read.argtypes = [_c_void_p, cache, _c_void_p, _c_int, _c_void_p, i64,
+                                      _c_int, _c_void_p, _c_void_p]
+        L.attn_kv4_read.argtypes = [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p, i64,
                                     _c_void_p, i64, _c_void_p]
-        L.attn_kv4_forward.argtypes = [_c_void_p, _c_void_p, i64, cache, _c_void_p, _c_int,
+        L.attn_kv4_forward.argtypes = [_c_void_p, _c_void_p, i64, _c_void_p, _c_void_p, _c_int,
                                        _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
                                        _c_void_p, i64, _c_void_p]
         for fn in ATTN_EXPORTS:
@@ -240,7 +235,6 @@ def attn_qk_norm_rope(h, q, q_stride, k, k_stride, positions, q_weight, k_weight
 
 
 def attn_kv4_append(h, k, k_stride, v, v_stride, slots, T, cache, stream):
-    """cache: an attn_kv4_cache (or None)."""
     return lib().attn_kv4_append(h, k, k_stride, v, v_stride, slots, T, cache, stream)
 
 
@@ -399,18 +393,14 @@ def _want(t, what, dtype, shape):
 
 
 class Kv4Cache:
-    """One layer's 4-bit cache as torch tensors (layout in include/attn.h).  `struct` is the
-    attn_kv4_cache that the C entry points take."""
+    """One layer's 4-bit cache as a torch tensor of records [n_pages][Hkv][page_size / 16][bytes]
+    (layout in include/attn.h)."""
 
     def __init__(self, n_pages, n_kv_heads, page_size, head_dim, device="cuda"):
         import torch
-        rows = (n_pages, n_kv_heads, page_size)
-        self.k_codes = torch.zeros(rows + (head_dim // 2,), dtype=torch.uint8, device=device)
-        self.v_codes = torch.zeros_like(self.k_codes)
-        self.k_params = torch.zeros(rows + (head_dim // 64,), dtype=torch.int32, device=device)
-        self.v_params = torch.zeros_like(self.k_params)
-        self.struct = attn_kv4_cache(_ptr(self.k_codes), _ptr(self.k_params), _ptr(self.v_codes),
-                                     _ptr(self.v_params))
+        self.data = torch.zeros((n_pages, n_kv_heads, page_size // 16, 18 * head_dim),
+                                dtype=torch.uint8, device=device)
+        self.ptr = self.data.data_ptr()
 
 
 class PagedAttention:
@@ -512,7 +502,7 @@ class PagedAttention:
         T = k.shape[0]
         ks, vs = self._rows(k, "k", self.n_kv_heads), self._rows(v, "v", self.n_kv_heads, T)
         _check(lib().attn_kv4_append(self.handle, k.data_ptr(), ks, v.data_ptr(), vs,
-                                     self._ints(slots, "slots", T), T, cache.struct,
+                                     self._ints(slots, "slots", T), T, cache.ptr,
                                      _stream_of(stream)), "attn_kv4_append")
 
     def read(self, slots, cache, k_out=None, v_out=None, stream=None):
@@ -525,7 +515,7 @@ class PagedAttention:
         v_out = torch.empty(shape, **like) if v_out is None else v_out
         ks = self._rows(k_out, "k_out", self.n_kv_heads, T)
         vs = self._rows(v_out, "v_out", self.n_kv_heads, T)
-        _check(lib().attn_kv4_read(self.handle, cache.struct, self._ints(slots, "slots", T), T,
+        _check(lib().attn_kv4_read(self.handle, cache.ptr, self._ints(slots, "slots", T), T,
                                    k_out.data_ptr(), ks, v_out.data_ptr(), vs,
                                    _stream_of(stream)), "attn_kv4_read")
         return k_out, v_out
@@ -541,7 +531,7 @@ class PagedAttention:
         os_ = self._rows(out, "out", self.n_q_heads, T)
         ints = self._ints
         _check(lib().attn_kv4_forward(
-            self.handle, q.data_ptr(), qs, cache.struct,
+            self.handle, q.data_ptr(), qs, cache.ptr,
             ints(block_table, "block_table", B, width), width,
             ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B), B, T, max_q_len,
             max_kv_len, out.data_ptr(), os_, _stream_of(stream)), "attn_kv4_forward")

@@ -23,11 +23,15 @@ struct AttnDims {
   float scale_log2;  // softmax scale * log2(e)
 };
 
-struct Kv4 {
-  uint8_t* kc;
-  uint32_t* kp;
-  uint8_t* vc;
-  uint32_t* vp;
+// A cache record: 16 tokens of one head.
+template <int D>
+struct Record {
+  static constexpr int kRow = D / 2;            // code bytes of a row
+  static constexpr int kPar = 4 * (D / kGroup);  // parameter bytes of a row
+  static constexpr int kKp = 16 * kRow;
+  static constexpr int kV = kKp + 16 * kPar;
+  static constexpr int kVp = kV + 16 * kRow;
+  static constexpr int kBytes = kVp + 16 * kPar;
 };
 
 // Position (in units of D/64 words) of word j of every group in the row of slot s.
@@ -46,16 +50,16 @@ struct FwdArgs {
   int64_t q_stride;
   __nv_bfloat16* out;
   int64_t out_stride;
-  Kv4 c;
+  const uint8_t* cache;
   const int32_t* table;
   int table_width;
   const int32_t* q_off;
   const int32_t* kv_lens;
   int B, T, max_q;
   AttnDims d;
-  float* part_o;     // partial outputs: [2 * blocks][columns][D] fp32
-  float2* part_ml;   // their softmax reference and sum: [2 * blocks][columns]
-  int4* desc;        // [blocks]: (parts, request, head, row tile) of a shared context
+  float* part_o;     // partial outputs: [slots][columns][D] fp32
+  float2* part_ml;   // their softmax reference and sum: [slots][columns]
+  int4* desc;        // [2 * blocks]: (parts, head, row tile, first row), (rows) of shared contexts
   int* err;
 };
 
@@ -121,7 +125,7 @@ struct RowsArgs {
   const int32_t* slots;
   int T, Hkv, page_shift;
   int64_t n_slots;
-  Kv4 c;
+  uint8_t* cache;
   int* err;
 };
 
@@ -130,9 +134,9 @@ cudaError_t launch_attn_read(const RowsArgs& a, int D, int sms, cudaStream_t s);
 
 // Attention of few query rows per key/value head and request (n_b G <= 16): attn_decode.cu.
 constexpr int kDecodeRows = 16;
-cudaError_t prepare_attn_decode_kernels();
-int attn_decode_blocks(int sms);          // blocks of a split launch
-size_t attn_decode_part_floats(int D);    // fp32 of one partial result
+cudaError_t prepare_attn_decode_kernels(int max_requests);
+int attn_decode_slots(int sms);         // partial results of a launch
+size_t attn_decode_part_floats(int D);  // fp32 of one partial result
 cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s);
 
 }  // namespace moe

@@ -41,7 +41,7 @@ int check_config(const attn_config* c) {
       c->page_size != 256)
     return MOE_ERR_UNSUPPORTED;
   if ((int64_t)c->n_pages * c->page_size > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  if (c->max_requests > 4096) return MOE_ERR_UNSUPPORTED;
+  if (c->max_requests > 1024) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -56,27 +56,19 @@ int check_tokens(int T) {
   return T < 0 ? MOE_ERR_INVALID_ARG : T > kMaxTokens ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-int check_cache(const attn_kv4_cache* c) {
-  if (!c || !c->k_codes || !c->k_params || !c->v_codes || !c->v_params)
-    return MOE_ERR_INVALID_ARG;
-  if (off16(c->k_codes) || off16(c->k_params) || off16(c->v_codes) || off16(c->v_params))
-    return MOE_ERR_ALIGNMENT;
-  return MOE_OK;
+int check_cache(const void* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  return (reinterpret_cast<uintptr_t>(c) & 127u) ? MOE_ERR_ALIGNMENT : MOE_OK;
 }
 
-moe::Kv4 device_cache(const attn_kv4_cache* c) {
-  return moe::Kv4{static_cast<uint8_t*>(c->k_codes), static_cast<uint32_t*>(c->k_params),
-                  static_cast<uint8_t*>(c->v_codes), static_cast<uint32_t*>(c->v_params)};
-}
-
-moe::RowsArgs rows_args(attn_handle h, const attn_kv4_cache* cache, const int32_t* slots, int T) {
+moe::RowsArgs rows_args(attn_handle h, const void* cache, const int32_t* slots, int T) {
   moe::RowsArgs a{};
   a.slots = slots;
   a.T = T;
   a.Hkv = h->d.Hkv;
   a.page_shift = h->d.page_shift;
   a.n_slots = (int64_t)h->d.n_pages << h->d.page_shift;
-  a.c = device_cache(cache);
+  a.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
   a.err = h->err;
   return a;
 }
@@ -98,7 +90,7 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))))
     return st;
   if ((st = record_cuda_status(moe::prepare_attn_plan_kernel(cfg->max_requests)))) return st;
-  if ((st = record_cuda_status(moe::prepare_attn_decode_kernels()))) return st;
+  if ((st = record_cuda_status(moe::prepare_attn_decode_kernels(cfg->max_requests)))) return st;
 
   attn_handle h = new (std::nothrow) attn_handle_s;
   if (!h) return MOE_ERR_NO_MEMORY;
@@ -114,12 +106,13 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
   const double scale = cfg->scale > 0.f ? cfg->scale : 1.0 / std::sqrt((double)cfg->head_dim);
   h->d.scale_log2 = (float)(scale * 1.4426950408889634);
 
-  const int blocks = moe::attn_decode_blocks(sms);
+  const size_t slots = moe::attn_decode_slots(sms);
   const size_t o_bytes =
-      round256(2 * (size_t)blocks * moe::attn_decode_part_floats(cfg->head_dim) * sizeof(float));
-  const size_t ml_bytes = round256(2 * (size_t)blocks * moe::kDecodeRows * sizeof(float2));
-  const size_t desc_bytes = round256((size_t)blocks * sizeof(int4));
-  const size_t bytes = o_bytes + ml_bytes + desc_bytes + 256;
+      round256(slots * moe::attn_decode_part_floats(cfg->head_dim) * sizeof(float));
+  const size_t ml_bytes = round256(slots * moe::kDecodeRows * sizeof(float2));
+  const size_t desc_bytes = round256(slots * sizeof(int4));
+  const size_t zeroed = 2 * sizeof(int);  // the plan's ticket, the error word
+  const size_t bytes = o_bytes + ml_bytes + desc_bytes + zeroed;
   cudaError_t e = cudaMalloc(&h->ws, bytes);
   if (e == cudaErrorMemoryAllocation) {
     cudaGetLastError();
@@ -133,7 +126,7 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
     h->desc = reinterpret_cast<int4*>(p + o_bytes + ml_bytes);
     h->ticket = reinterpret_cast<int*>(p + o_bytes + ml_bytes + desc_bytes);
     h->err = h->ticket + 1;
-    e = cudaMemset(h->ticket, 0, 256);
+    e = cudaMemset(h->ticket, 0, zeroed);
     // the handle may be used on a stream that does not order itself behind the default one
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
   }
@@ -237,8 +230,7 @@ int attn_qk_norm_rope(attn_handle h, const void* q, int64_t q_stride, const void
 }
 
 int attn_kv4_append(attn_handle h, const void* k, int64_t k_stride, const void* v,
-                    int64_t v_stride, const int32_t* slots, int T, const attn_kv4_cache* cache,
-                    void* stream) {
+                    int64_t v_stride, const int32_t* slots, int T, void* cache, void* stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
   int st = check_tokens(T);
   if (st) return st;
@@ -258,8 +250,8 @@ int attn_kv4_append(attn_handle h, const void* k, int64_t k_stride, const void* 
       moe::launch_attn_append(a, h->d.D, h->sms, static_cast<cudaStream_t>(stream)));
 }
 
-int attn_kv4_read(attn_handle h, const attn_kv4_cache* cache, const int32_t* slots, int T,
-                  void* k, int64_t k_stride, void* v, int64_t v_stride, void* stream) {
+int attn_kv4_read(attn_handle h, const void* cache, const int32_t* slots, int T, void* k,
+                  int64_t k_stride, void* v, int64_t v_stride, void* stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
   int st = check_tokens(T);
   if (st) return st;
@@ -279,7 +271,7 @@ int attn_kv4_read(attn_handle h, const attn_kv4_cache* cache, const int32_t* slo
       moe::launch_attn_read(a, h->d.D, h->sms, static_cast<cudaStream_t>(stream)));
 }
 
-int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const attn_kv4_cache* cache,
+int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void* cache,
                      const int32_t* block_table, int table_width, const int32_t* q_offsets,
                      const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
                      void* out, int64_t out_stride, void* stream) {
@@ -300,7 +292,7 @@ int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const attn_
   a.q_stride = q_stride;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.out_stride = out_stride;
-  a.c = device_cache(cache);
+  a.cache = static_cast<const uint8_t*>(cache);
   a.table = block_table;
   a.table_width = table_width;
   a.q_off = q_offsets;

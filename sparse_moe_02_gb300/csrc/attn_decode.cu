@@ -18,50 +18,75 @@
 //
 // Layout of the work.  The rows of a key/value head (G query heads x new tokens) are the MMA's N
 // side in tiles of 8, its 16 tokens the M side of the scores; a cached row is read once for all
-// of them.  A block of four warps, two blocks per SM; each warp takes every fourth tile of 32
-// tokens of a context through a ring of its own (bulk copies: a tile of one head lies contiguous
-// in its page) and keeps its own softmax state and outputs; the block joins its warps through
-// shared memory.  Contexts are cut evenly over the blocks: with W tiles in all, block i takes
-// tiles [i W / n, (i + 1) W / n) whatever requests they belong to, so ragged batches balance; a
-// context that several blocks share leaves partial results that a second small launch joins in
-// block order (the same inputs give the same bits).  Short contexts (max_kv small) take one block
-// per context and no second launch.
+// of them.  One block of twelve warps per SM; each warp takes every twelfth tile of
+// 16 tokens of a context through a ring of its own (one bulk copy a tile, its cache record) and keeps its own softmax state and outputs; the block joins its warps through
+// shared memory.  Contexts are cut evenly over the blocks: with W units of work in all (a tile is
+// one, a context's fixed cost kPartCost more), block i takes [i W / n, (i + 1) W / n) whatever
+// requests they belong to, so ragged batches balance; a second launch joins the partial results of
+// contexts that several blocks share, in block order (the same inputs give the same bits).  Short
+// contexts (max_kv small) take one block each and no second launch.
+#include <climits>
+
 #include "attn.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 32;  // tokens per ring stage
-// One block per context, no second launch, up to this many tokens.
+constexpr int kTile = 16;  // tokens per ring stage: the MMA's M side, and a whole number per page
+// One block per context, no partial results, up to this many tokens.
 constexpr int kWholeKv = 512;
-constexpr float kSlack = 6.f;     // growth of the reference a tile may bring before a rescale
-constexpr float kLift = 9.f;      // w <= 2^(kLift + kSlack) at the reference
+constexpr float kSlack = 6.f;  // growth of the reference a tile may bring before a rescale
+constexpr float kLift = 9.f;   // w <= 2^(kLift + kSlack) at the reference
+constexpr int kJoinWarps = 4;  // warps whose outputs the join buffer holds at once
+static_assert(kWarps % kJoinWarps == 0, "whole rounds of the join");
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int NG = D / kGroup;
-  static constexpr int kRow = D / 2;     // code bytes per row
-  static constexpr int kPar = 4 * NG;    // parameter bytes per row
-  static constexpr int kOffV = kTile * kRow;
-  static constexpr int kOffKp = 2 * kTile * kRow;
-  static constexpr int kOffVp = kOffKp + kTile * kPar;
-  static constexpr int kStage = kOffVp + kTile * kPar;
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 6 : 8;
+  static constexpr int kStage = Record<D>::kBytes;
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 5 : 8;
   static constexpr int kCols = 8 * NT;
-  static constexpr int kPitch = D + 8;   // floats per column of the join buffer
-  static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kJoin = kWarps * kCols * kPitch * 4;
-  static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + 128;
+  static constexpr int kPitch = D + 4;        // floats per column of the join buffer
+  static constexpr int kQPitch = 2 * D + 64;  // bytes per staged query row
+  // shared memory: ring, join buffer, staged queries (two parts), work before each request
+  static constexpr int kJoin = kWarps * kStages * kStage;
+  static constexpr int kQuery = kJoin + kJoinWarps * kCols * kPitch * 4;
+  static constexpr int kFirst = kQuery + 2 * kCols * kQPitch;
+  static constexpr int kSmem = kFirst;
+  // threads that own outputs in the joins, and float4s of each
+  static constexpr int kOwners = kCols * D / 4 < 256 ? kCols * D / 4 : 256;
+  static constexpr int kVec = kCols * D / 4 / kOwners;
+  static constexpr int kLanes = kOwners / kCols;  // owners of a column
 };
 
+// c += A B; mma_f16_first: c = A B.
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                              uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// c = A B with tf32 operands (16 x 8 by 8 x 8).
+__device__ __forceinline__ void mma_tf32_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -117,164 +142,195 @@ constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 // tokens c and c + 4, whose cached words lie in different shared-memory banks (row_swz).
 __device__ __forceinline__ int row_token(int r) { return (r >> 1) | ((r & 1) << 2); }
 
-// One block's range of work: tiles [w0, w1) of all contexts in order.
-struct Range {
-  int64_t total, w0, w1;
-  int blocks;  // that take part
-  int b;       // request of w0
-  int64_t before;  // tiles of the requests before it
-};
-
 __device__ __forceinline__ int row_tiles(const FwdArgs& a, int qn, int cols) {
   return (qn * a.d.G + cols - 1) / cols;
 }
 
 __device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1) / kTile); }
 
-__device__ __forceinline__ int64_t request_tiles(const FwdArgs& a, const Req& r, int cols) {
-  return r.qn > 0 ? (int64_t)a.d.Hkv * row_tiles(a, r.qn, cols) * kv_tiles(r.kv) : 0;
+// Work of a context: its tiles, and kPartCost tiles' worth for what a part costs besides (queries,
+// page ids, first copies, joins), so that blocks of many short contexts get fewer tiles.
+constexpr int kPartCost = 40;
+constexpr int kLeastWork = 32;  // of a block
+
+// a / b of nonnegative numbers, in 32 bits where they fit (a 64-bit division is a long routine)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-__device__ __forceinline__ int64_t bound(int64_t total, int blocks, int i) {
-  return total * i / blocks;
-}
-
-__device__ __forceinline__ int64_t scan64(int64_t v, int64_t* sums, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(~0u, v, o);
-    if (lane >= o) v += u;
+struct Cut {
+  int64_t share;  // work of a block, one more in the first `rest` blocks
+  int rest;
+  int blocks;
+  __device__ __forceinline__ int64_t bound(int i) const { return share * i + min(i, rest); }
+  // the block that does unit x
+  __device__ __forceinline__ int block_of(int64_t x) const {
+    const int64_t wide = (share + 1) * rest;
+    return x < wide ? (int)divide(x, share + 1) : rest + (int)divide(x - wide, share);
   }
-  if (lane == 31) sums[warp] = v;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
-  }
-  __syncthreads();
-  *total = all;
-  return v + before;
-}
-
-// The block's range (every thread gets the same answer).
-__device__ Range find_range(const FwdArgs& a, int cols, int64_t* sums, int64_t* found) {
-  Range R;
-  int64_t total = 0, sum, incl = 0, cnt = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    cnt = b < a.B ? request_tiles(a, load_req(a, b), cols) : 0;
-    if (blockIdx.x == 0 && b < a.B && req_out_of_range(a, b)) record_error(a.err, kDevErrState);
-    incl = total + scan64(cnt, sums, &sum);
-    total += sum;
-  }
-  R.total = total;
-  const int64_t most = (total + kWarps - 1) / kWarps;  // a tile for each warp at least
-  R.blocks = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
-  R.w0 = R.w1 = 0;
-  R.b = 0;
-  R.before = 0;
-  if ((int)blockIdx.x >= R.blocks) return R;
-  R.w0 = bound(total, R.blocks, blockIdx.x);
-  R.w1 = bound(total, R.blocks, blockIdx.x + 1);
-  int64_t run = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    if (a.B > kThreads) {
-      cnt = b < a.B ? request_tiles(a, load_req(a, b), cols) : 0;
-      incl = run + scan64(cnt, sums, &sum);
-      run += sum;
-    }
-    if (incl - cnt <= R.w0 && R.w0 < incl) {
-      found[0] = b;
-      found[1] = incl - cnt;
-    }
-  }
-  __syncthreads();
-  R.b = (int)found[0];
-  R.before = found[1];
-  return R;
-}
-
-// Query rows of one context and tile of columns, as MMA B fragments, for the warp's lanes.
-template <int D, int NT>
-struct Query {
-  static constexpr int NG = D / kGroup;
-  uint32_t f[NT][NG][2][4];  // [column tile][group][word][registers of two MMAs]
-  float sum[NT][2][NG];      // sum of the scaled row over a group, times 2^-24, columns 2c, 2c + 1
-  float scale[NT][2];        // turns the MMA's units into log2 units
-  int lim[NT][2];            // tokens the column sees
 };
 
+// Fills first[b], b = 0 .. B: the work before request b.  One warp.
+__device__ __forceinline__ Cut cut_contexts(const FwdArgs& a, int cols, int64_t* first) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t n = 0;
+    if (b < a.B) {
+      const Req r = load_req(a, b);
+      if (blockIdx.x == 0 && req_out_of_range(a, b)) record_error(a.err, kDevErrState);
+      if (r.qn > 0)
+        n = (int64_t)(a.d.Hkv * row_tiles(a, r.qn, cols)) * (kv_tiles(r.kv) + kPartCost);
+    }
+    int64_t end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(~0u, end, o);
+      if (lane >= o) end += u;
+    }
+    if (b < a.B) first[b] = total + end - n;
+    total += __shfl_sync(~0u, end, 31);
+  }
+  if (lane == 0) first[a.B] = total;
+  __syncwarp();
+  const int64_t most = (total + kLeastWork - 1) / kLeastWork;
+  Cut c;
+  c.blocks = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
+  c.share = c.blocks ? divide(total, c.blocks) : 0;
+  c.rest = (int)(total - c.share * c.blocks);
+  return c;
+}
+
+// What a lane keeps of the query rows (columns) of one context; their MMA B fragments lie in
+// shared memory, [column tile][group][word][lane] registers of two MMAs, for all warps.
+template <int NT>
+struct Query {
+  uint32_t sum[NT][2];  // of column lane / 4: its scaled sum over group lane % 4 as two tf32 parts
+  float scale[NT][2];   // of columns 2c, 2c + 1: turns the MMA's units into log2 units
+  int lim[NT][2];       // tokens the column sees
+  int least;            // smallest lim of the columns in use
+};
+
+// The same for the block.
 template <int D, int NT>
-__device__ __forceinline__ void load_query(const FwdArgs& a, const Req& r, int h, int rt,
-                                           Query<D, NT>& Q) {
+struct QueryShared {
+  uint4 frags[NT * (D / kGroup) * 2 * 32];
+  float sum[8 * NT][D / kGroup];
+  float scale[8 * NT];
+  int lim[8 * NT];
+};
+
+// The part of a context that a block works on.
+struct Part {
+  int b, h, rt;
+  int t0, t1, tiles;  // its tiles, and the context's
+  Req r;
+  int64_t start;  // work before the context's first tile
+  int64_t next;   // the block's work after this part
+  bool some;
+};
+
+// Starts copying the part's query rows [column][D] into shared memory.
+template <int D, int NT>
+__device__ __forceinline__ void fetch_query(const FwdArgs& a, const Part& p, uint8_t* raw) {
+  constexpr int kPieces = D / 8;
+  static_assert(8 * NT * kPieces <= kThreads, "one piece a thread");
+  const int col = threadIdx.x / kPieces, piece = threadIdx.x % kPieces;
+  if (col < 8 * NT) {
+    const int row = p.rt * 8 * NT + col;
+    uint8_t* dst = raw + col * Cfg<D, NT>::kQPitch + 16 * piece;
+    if (row < p.r.qn * a.d.G) {
+      const __nv_bfloat16* src = a.q + (int64_t)(p.r.q0 + row / a.d.G) * a.q_stride +
+                                 (int64_t)(p.h * a.d.G + row % a.d.G) * D + 8 * piece;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                   : "memory");
+    } else {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// One warp prepares group g of column tile nt.
+template <int D, int NT>
+__device__ __forceinline__ void prepare_query(const FwdArgs& a, const Part& p, const uint8_t* raw,
+                                              int nt, int g, QueryShared<D, NT>& S) {
   constexpr int NG = D / kGroup;
   const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+  const uint8_t* src = raw + (8 * nt + n) * Cfg<D, NT>::kQPitch + 16 * c;
+  uint32_t top = 0;  // largest magnitude, as the order of bf16 bit patterns
+#pragma unroll
+  for (int k = 0; k < 2 * NG; ++k) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src + 64 * k);
+    const uint32_t x = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+    top = __vmaxu2(top, __vmaxu2(x, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+  }
+  top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 1));
+  top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 2));
+  top = max(top & 0xffffu, top >> 16);
+  // 2^-e with the row's largest entry in [2^e, 2^(e+1)), kept a normal number
+  const int e = min(max((int)(top >> 7) - 127, -100), 126);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src + 128 * g + 64 * i);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    float v[8];
+    uint32_t f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16_lo(x[k]) * down;
+      v[2 * k + 1] = bf16_hi(x[k]) * down;
+    }
+    // the row in [2^13, 2^14) at its top; odd nibbles of a byte arrive 16 times as large
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float m = (k & 1) ? 512.f : 8192.f;
+      f[k] = pack_f16(v[k] * m, v[k + 4] * m);
+      sum += v[k] + v[k + 4];
+    }
+    S.frags[((nt * NG + g) * 2 + i) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+  }
+  sum += __shfl_xor_sync(~0u, sum, 1);
+  sum += __shfl_xor_sync(~0u, sum, 2);
+  if (c == 0) {
+    const int col = 8 * nt + n, row = p.rt * 8 * NT + col;
+    S.sum[col][g] = sum * (8192.f / 16777216.f);
+    if (g == 0) {
+      // code * 2^-24 * q * 2^13-e  ->  log2 units
+      S.scale[col] = up * (16777216.f / 8192.f) * a.d.scale_log2;
+      // columns beyond the rows see everything: nothing of them is written
+      const int seen = p.r.kv - p.r.qn + row / a.d.G + 1;
+      S.lim[col] = row < p.r.qn * a.d.G ? min(max(seen, 0), p.r.kv) : p.r.kv;
+    }
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void load_query(const QueryShared<D, NT>& S, Query<NT>& Q) {
+  constexpr int NG = D / kGroup;
+  const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+  Q.least = INT_MAX;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int row = (rt * NT + nt) * 8 + n;
-    const bool on = row < r.qn * a.d.G;
-    const int tok = row / a.d.G;
-    const __nv_bfloat16* p =
-        a.q + (int64_t)(r.q0 + tok) * a.q_stride + (int64_t)(h * a.d.G + row % a.d.G) * D;
-    uint4 raw[NG][2];
-    float top = 0.f;
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        raw[g][i] = on ? *reinterpret_cast<const uint4*>(p + 64 * g + 8 * (c + 4 * i))
-                       : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {raw[g][i].x, raw[g][i].y, raw[g][i].z, raw[g][i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
-      }
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-    // 2^-e with the row's largest entry in [2^e, 2^(e+1)), kept a normal number
-    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 126);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-    float sums[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      sums[g] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x[4] = {raw[g][i].x, raw[g][i].y, raw[g][i].z, raw[g][i].w};
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[2 * k] = bf16_lo(x[k]) * down;
-          v[2 * k + 1] = bf16_hi(x[k]) * down;
-        }
-        // the row in [2^13, 2^14) at its top; odd nibbles of a byte arrive 16 times as large
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float m = (k & 1) ? 512.f : 8192.f;
-          Q.f[nt][g][i][k] = pack_f16(v[k] * m, v[k + 4] * m);
-          sums[g] += v[k] + v[k + 4];
-        }
-      }
-      sums[g] += __shfl_xor_sync(~0u, sums[g], 1);
-      sums[g] += __shfl_xor_sync(~0u, sums[g], 2);
-      sums[g] *= 8192.f / 16777216.f;
-    }
-    // code * 2^-24 * q * 2^13-e  ->  log2 units
-    const float unit = up * (16777216.f / 8192.f) * a.d.scale_log2;
-    const int seen = on ? min(max(r.kv - r.qn + tok + 1, 0), r.kv) : 0;
+    // two tf32 parts of the sum: 22 bits of it
+    const float sum = c < NG ? S.sum[8 * nt + n][c % NG] : 0.f;
+    Q.sum[nt][0] = __float_as_uint(sum) & 0xffffe000u;
+    Q.sum[nt][1] = __float_as_uint(sum - __uint_as_float(Q.sum[nt][0])) & 0xffffe000u;
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc) {
-      const int from = (2 * c + cc) * 4;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) Q.sum[nt][cc][g] = __shfl_sync(~0u, sums[g], from);
-      Q.scale[nt][cc] = __shfl_sync(~0u, unit, from);
-      Q.lim[nt][cc] = __shfl_sync(~0u, seen, from);
+      Q.scale[nt][cc] = S.scale[8 * nt + 2 * c + cc];
+      Q.lim[nt][cc] = S.lim[8 * nt + 2 * c + cc];
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) Q.least = min(Q.least, S.lim[8 * nt + k]);
   }
 }
 
@@ -304,112 +360,90 @@ __device__ __forceinline__ void clear(State<D, NT>& s) {
   }
 }
 
-// One tile of 32 tokens (n of them valid from the first on, in `halves` halves of 16) at shared
-// address `st`; tok0 is the first token's index in its context.
+// One tile of 16 tokens at shared address `st`; tok0 is the first token's index in its context.
 template <int D, int NT>
-__device__ __forceinline__ void tile_step(uint32_t st, int tok0, int kv, const Query<D, NT>& Q,
-                                          State<D, NT>& s) {
-  using C = Cfg<D, NT>;
-  constexpr int NG = C::NG;
+__device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0, int kv,
+                                          const Query<NT>& Q, State<D, NT>& s) {
+  using R = Record<D>;
+  constexpr int NG = D / kGroup;
   const int lane = threadIdx.x & 31, j = lane >> 2, c = lane & 3;
-  const int tr = row_token(j);
-  const int halves = kv - tok0 > 16 ? 2 : 1;
-  float x[2][NT][4];    // scores, then weights
-  Words<NG> vp[2][2];   // value parameters of the lane's rows
+  const int tr = row_token(j);  // the lane's score rows are tokens tr and tr + 8
+  float x[NT][4];               // scores in MMA units, then weights
+  {
+    Words<NG> kw[2][2];  // [word][row]
+    Words<NG> kp[2];
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    if (hf >= halves) {
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t at = st + tr * R::kRow + (((c + 4 * i) ^ row_swz(tr)) * NG) * 4;
+      kw[i][0] = lds_words<NG>(at);
+      kw[i][1] = lds_words<NG>(at + 8 * R::kRow);
+    }
+    // the bias part: biases of group c (their upper halves are tf32 numbers) by the sums
+    const uint32_t par = st + R::kKp + tr * R::kPar;
+    const uint32_t ba = lds_words<1>(par + 4 * (c % NG)).w[0] & 0xffff0000u;
+    const uint32_t bb = lds_words<1>(par + 8 * R::kPar + 4 * (c % NG)).w[0] & 0xffff0000u;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      mma_tf32_first(x[nt], ba, bb, ba, bb, Q.sum[nt][0], Q.sum[nt][1]);
+    kp[0] = lds_words<NG>(par);
+    kp[1] = lds_words<NG>(par + 8 * R::kPar);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float acc[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Words<4> f = lds_words<4>(frags + (((nt * NG + g) * 2 + i) * 32 + lane) * 16);
+          const uint32_t a0 = kw[i][0].w[g], b0 = kw[i][1].w[g];
+          const uint32_t a8 = a0 >> 8, b8 = b0 >> 8;
+          if (i == 0)
+            mma_f16_first(acc, a0 & kNib0, b0 & kNib0, a0 & kNib1, b0 & kNib1, f.w[0], f.w[1]);
+          else
+            mma_f16(acc, a0 & kNib0, b0 & kNib0, a0 & kNib1, b0 & kNib1, f.w[0], f.w[1]);
+          mma_f16(acc, a8 & kNib0, b8 & kNib0, a8 & kNib1, b8 & kNib1, f.w[2], f.w[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[nt][e] = fmaf(bf16_lo(kp[e >> 1].w[g]), acc[e], x[nt][e]);
+      }
+  }
+  Words<NG> vp[2];  // value parameters of the lane's rows
+#pragma unroll
+  for (int r = 0; r < 2; ++r) vp[r] = lds_words<NG>(st + R::kVp + (8 * r + tr) * R::kPar);
+  // what a row may not see, and what lies behind the context (never written: anything)
+  if (tok0 + kTile > Q.least) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int t = tok0 + 8 * r + tr;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[hf][nt][e] = -INFINITY;
+        for (int cc = 0; cc < 2; ++cc)
+          if (t >= Q.lim[nt][cc]) x[nt][2 * r + cc] = -INFINITY;
+      if (t >= kv) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) vp[hf][0].w[g] = vp[hf][1].w[g] = 0;
-      continue;
-    }
-    const int row = 16 * hf + tr;
-    float acc[NT][NG][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][g][e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t at = st + row * C::kRow + (((c + 4 * i) ^ row_swz(tr)) * NG) * 4;
-      const Words<NG> wa = lds_words<NG>(at), wb = lds_words<NG>(at + 8 * C::kRow);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t a8 = wa.w[g] >> 8, b8 = wb.w[g] >> 8;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(acc[nt][g], wa.w[g] & kNib0, wb.w[g] & kNib0, wa.w[g] & kNib1, wb.w[g] & kNib1,
-                  Q.f[nt][g][i][0], Q.f[nt][g][i][1]);
-          mma_f16(acc[nt][g], a8 & kNib0, b8 & kNib0, a8 & kNib1, b8 & kNib1, Q.f[nt][g][i][2],
-                  Q.f[nt][g][i][3]);
-        }
+        for (int g = 0; g < NG; ++g) vp[r].w[g] = 0;
       }
     }
-    const Words<NG> ka = lds_words<NG>(st + C::kOffKp + row * C::kPar);
-    const Words<NG> kb = lds_words<NG>(st + C::kOffKp + (row + 8) * C::kPar);
-    vp[hf][0] = lds_words<NG>(st + C::kOffVp + row * C::kPar);
-    vp[hf][1] = lds_words<NG>(st + C::kOffVp + (row + 8) * C::kPar);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const Words<NG>& k = e < 2 ? ka : kb;
-        float v = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          v = fmaf(bf16_lo(k.w[g]), acc[nt][g][e], v);
-          v = fmaf(bf16_hi(k.w[g]), Q.sum[nt][e & 1][g], v);
-        }
-        x[hf][nt][e] = v * Q.scale[nt][e & 1];
-      }
   }
-  // what a row may not see, and what lies behind the context (never written: anything)
-  int least = Q.lim[0][0];
+  // 2^ev bounds the tile's scales (nonnegative bf16, the lower halves)
+  uint32_t big = 0;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) least = min(least, min(Q.lim[nt][0], Q.lim[nt][1]));
-  if (__any_sync(~0u, tok0 + kTile > least)) {
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int t = tok0 + 16 * hf + 8 * r + tr;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-            if (t >= Q.lim[nt][cc]) x[hf][nt][2 * r + cc] = -INFINITY;
-        if (t >= kv) {
-#pragma unroll
-          for (int g = 0; g < NG; ++g) vp[hf][r].w[g] = 0;
-        }
-      }
-  }
-  // exponent of the largest scale of each of the lane's four tokens
-  float ev[2][2];
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) top = max(top, (vp[hf][r].w[g] << 16) & 0x7fffffffu);
-      ev[hf][r] = (float)max((int)(top >> 23) - 126, -60);
-    }
+    for (int g = 0; g < NG; ++g) big = __vmaxu2(big, vp[r].w[g]);
+  big = __reduce_max_sync(~0u, big & 0x7fffu);
+  const float ev = (float)max((int)(big >> 7) - 126, -60);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float top[2];
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc) {
-      top[cc] = fmaxf(fmaxf(x[0][nt][cc] + ev[0][0], x[0][nt][2 + cc] + ev[0][1]),
-                      fmaxf(x[1][nt][cc] + ev[1][0], x[1][nt][2 + cc] + ev[1][1]));
+      top[cc] = fmaxf(x[nt][cc], x[nt][2 + cc]);
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) top[cc] = fmaxf(top[cc], __shfl_xor_sync(~0u, top[cc], o));
+      top[cc] = fmaf(top[cc], Q.scale[nt][cc], ev);
     }
     if (__any_sync(~0u, top[0] > s.m[nt][0] + kSlack || top[1] > s.m[nt][1] + kSlack)) {
 #pragma unroll
@@ -431,394 +465,569 @@ __device__ __forceinline__ void tile_step(uint32_t st, int tok0, int kv, const Q
     }
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc) {
-      const float m = s.m[nt][cc] == -INFINITY ? 0.f : s.m[nt][cc] - kLift;
+      const float m = s.m[nt][cc] == -INFINITY ? 0.f : kLift - s.m[nt][cc];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int r = 0; r < 2; ++r) {
+        const float p = exp2_fast(fmaf(x[nt][2 * r + cc], Q.scale[nt][cc], m));
+        x[nt][2 * r + cc] = p;
+        s.l[nt][cc] += p;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float p = exp2_fast(x[hf][nt][2 * r + cc] - m);
-          x[hf][nt][2 * r + cc] = p;
-          s.l[nt][cc] += p;
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-            s.ob[nt][cc][g] = fmaf(p, bf16_hi(vp[hf][r].w[g]), s.ob[nt][cc][g]);
-        }
+        for (int g = 0; g < NG; ++g)
+          s.ob[nt][cc][g] = fmaf(p, bf16_hi(vp[r].w[g]), s.ob[nt][cc][g]);
+      }
     }
   }
-  uint32_t wt[2][NT][NG][2];
-  Words<NG> v[2][4];  // value words of the lane's tokens c, c + 4, c + 8, c + 12, unit j
+  uint32_t wt[NT][NG][2];
+  Words<NG> v[4];  // value words of the lane's tokens c, c + 4, c + 8, c + 12, unit j
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    if (hf >= halves) continue;
+  for (int q = 0; q < 4; ++q)
+    v[q] = lds_words<NG>(st + R::kV + (c + 4 * q) * R::kRow +
+                         ((j ^ row_swz(c + 4 * q)) * NG) * 4);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float sc = bf16_lo(vp[hf][r].w[g]);
-          wt[hf][nt][g][r] =
-              transpose8x8(pack_f16(x[hf][nt][2 * r] * sc, x[hf][nt][2 * r + 1] * sc));
-        }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      v[hf][q] = lds_words<NG>(st + C::kOffV + (16 * hf + c + 4 * q) * C::kRow +
-                               ((j ^ row_swz(c + 4 * q)) * NG) * 4);
-  }
+      for (int r = 0; r < 2; ++r) {
+        const float sc = bf16_lo(vp[r].w[g]);
+        wt[nt][g][r] = transpose8x8(pack_f16(x[nt][2 * r] * sc, x[nt][2 * r + 1] * sc));
+      }
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const uint32_t sel = part ? 0x7632u : 0x5410u;
-      // The tile's sum starts from zero and joins the running one by a rounded addition: the
-      // MMA's own additions truncate, and over thousands of tiles of nonnegative codes that
-      // would pull the code part down against the bias part that it nearly cancels.
-      float t[NT][2][4];
+      uint32_t u0 = __byte_perm(v[0].w[g], v[1].w[g], sel);
+      uint32_t u1 = __byte_perm(v[2].w[g], v[3].w[g], sel);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[nt][0][e] = t[nt][1][e] = 0.f;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (hf >= halves) continue;
-        uint32_t u0 = __byte_perm(v[hf][0].w[g], v[hf][1].w[g], sel);
-        uint32_t u1 = __byte_perm(v[hf][2].w[g], v[hf][3].w[g], sel);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(t[nt][k], u0 & kNib0, u0 & kNib1, u1 & kNib0, u1 & kNib1, wt[hf][nt][g][0],
-                    wt[hf][nt][g][1]);
-          u0 >>= 8;
-          u1 >>= 8;
+        for (int nt = 0; nt < NT; ++nt) {
+          // The tile's sum joins the running one by a rounded addition: the MMA's own additions
+          // truncate, and over thousands of tiles of nonnegative codes that would pull the code
+          // part down against the bias part that it nearly cancels.
+          float t[4];
+          mma_f16_first(t, u0 & kNib0, u0 & kNib1, u1 & kNib0, u1 & kNib1, wt[nt][g][0],
+                        wt[nt][g][1]);
+          float(&o)[4] = s.o[nt][g][2 * part + k];
+          add2(o[0], o[1], t[0], t[1]);
+          add2(o[2], o[3], t[2], t[3]);
         }
+        u0 >>= 8;
+        u1 >>= 8;
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          add2(s.o[nt][g][2 * part + k][0], s.o[nt][g][2 * part + k][1], t[nt][k][0], t[nt][k][1]);
-          add2(s.o[nt][g][2 * part + k][2], s.o[nt][g][2 * part + k][3], t[nt][k][2], t[nt][k][3]);
-        }
     }
 }
 
-// Copies of a warp's tiles into its ring, by lane 0; `pages` holds the ids of 32 tiles ahead.
-template <int D, int NT>
-struct Feed {
-  using C = Cfg<D, NT>;
-  uint8_t* ring;
-  uint64_t* bars;
-  uint64_t policy;
-
-  // pg0, pg1: pages of the tile's first and second 16 tokens
-  __device__ __forceinline__ void issue(const FwdArgs& a, int h, int tile, int kv, int stage,
-                                        int pg0, int pg1) {
-    const int P = 1 << a.d.page_shift;
-    const int tok0 = tile * kTile;
-    const int rows = kv - tok0 > 16 ? 32 : 16;
-    uint8_t* dst = ring + stage * C::kStage;
-    uint64_t* bar = bars + stage;
-    mbar_arrive_expect_tx(bar, rows * 2 * (C::kRow + C::kPar));
-    const int step = P < kTile ? 16 : rows;
-    for (int r = 0; r < rows; r += step) {
-      const int pg = r ? pg1 : pg0;
-      const int64_t at = ((int64_t)pg * a.d.Hkv + h) * P + ((tok0 + r) & (P - 1));
-      bulk_load(dst + r * C::kRow, a.c.kc + at * C::kRow, step * C::kRow, bar, policy);
-      bulk_load(dst + C::kOffKp + r * C::kPar, reinterpret_cast<uint8_t*>(a.c.kp) + at * C::kPar,
-                step * C::kPar, bar, policy);
-      bulk_load(dst + C::kOffV + r * C::kRow, a.c.vc + at * C::kRow, step * C::kRow, bar, policy);
-      bulk_load(dst + C::kOffVp + r * C::kPar, reinterpret_cast<uint8_t*>(a.c.vp) + at * C::kPar,
-                step * C::kPar, bar, policy);
-    }
+// Record of `tile` of request b's context, head h; a page id out of range reads page 0 and is
+// recorded.  (32 bits: 2^32 records are more than 5 TB.)
+__device__ __forceinline__ uint32_t tile_record(const FwdArgs& a, int b, int h, int tile) {
+  const int shift = a.d.page_shift - 4;  // tiles per page
+  int id = a.table[(int64_t)b * a.table_width + (tile >> shift)];
+  if (id < 0 || id >= a.d.n_pages) {
+    record_error(a.err, kDevErrState);
+    id = 0;
   }
-};
-
-// Page ids of the 16-token halves of `tile`; an id out of range reads page 0 and is recorded.
-__device__ __forceinline__ int2 tile_pages(const FwdArgs& a, int b, int tile, int kv) {
-  int id[2] = {0, 0};
-  const int P = 1 << a.d.page_shift;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int tok = tile * kTile + 16 * i;
-    if (tok < kv && (i == 0 || P < kTile)) {
-      id[i] = a.table[(int64_t)b * a.table_width + (tok >> a.d.page_shift)];
-      if (id[i] < 0 || id[i] >= a.d.n_pages) {
-        record_error(a.err, kDevErrState);
-        id[i] = 0;
-      }
-    }
-  }
-  return make_int2(id[0], id[1]);
+  return (((uint32_t)id * a.d.Hkv + h) << shift) + (tile & ((1 << shift) - 1));
 }
 
+// The part that holds work w of the block's [w, w1).
+__device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, int cols, int64_t w,
+                                       int64_t w1) {
+  Part p;
+  p.some = false;
+  while (w < w1) {
+    int lo = 0, hi = a.B;  // first[lo] <= w < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= w) lo = mid;
+      else hi = mid;
+    }
+    p.b = lo;
+    p.r = load_req(a, lo);
+    p.tiles = kv_tiles(p.r.kv);
+    const int rts = row_tiles(a, p.r.qn, cols);
+    const int k = (int)divide(w - first[lo], p.tiles + kPartCost);
+    p.h = k / rts;
+    p.rt = k % rts;
+    p.start = first[lo] + (int64_t)k * (p.tiles + kPartCost) + kPartCost;
+    p.t0 = (int)max(w - p.start, (int64_t)0);
+    p.t1 = (int)min(w1 - p.start, (int64_t)p.tiles);
+    w = p.next = min(p.start + p.tiles, w1);
+    if (p.t1 > 0) {  // else the context's tiles begin in the next block
+      p.some = true;
+      break;
+    }
+  }
+  return p;
+}
+
+__device__ __forceinline__ float part_weight(float m_part, float l_part, float m) {
+  // a part that saw nothing has m = -inf and l = 0; one of NaN scores m = -inf and l = NaN
+  return m_part == -INFINITY ? (l_part == 0.f ? 0.f : 1.f) : exp2_fast(m_part - m);
+}
+
+// Outputs are joined in the order in which the lanes hold them: float4 i of a column is channels
+// out_channel(i) .. + 3.
+__device__ __forceinline__ int out_channel(int i) {
+  return (i >> 4) * 64 + (i & 7) * 8 + ((i >> 3) & 1) * 4;
+}
+
+__device__ __forceinline__ void store_out4(const FwdArgs& a, const Part& p, int row, int D, int i,
+                                           float4 o, float l) {
+  if (row >= p.r.qn * a.d.G) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
+                       (int64_t)(p.h * a.d.G + row % a.d.G) * D + out_channel(i);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                              *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+__device__ __forceinline__ void fma4(float4& o, const float4& v, float f) {
+  o.x = fmaf(v.x, f, o.x);
+  o.y = fmaf(v.y, f, o.y);
+  o.z = fmaf(v.z, f, o.z);
+  o.w = fmaf(v.w, f, o.w);
+}
+
+// Slot of part i of a context whose first part is block b0's: that block's second slot, then the
+// first slots of the blocks behind it.
+__device__ __forceinline__ int part_slot(int b0, int i) { return 2 * (b0 + i) + (i == 0); }
+
+// One block per SM.  While a part is worked on, the next part's queries and, as ring stages fall
+// free, its first tiles are copied, so the joins between parts leave no gap in the stream.
 template <int D, int NT, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   using C = Cfg<D, NT>;
   constexpr int NG = C::NG;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kWarps * C::kStages];
-  __shared__ int64_t sums[kWarps], found[2];
-  __shared__ float join_m[kWarps][C::kCols], join_l[kWarps][C::kCols];
+  __shared__ QueryShared<D, NT> S;
+  __shared__ float2 join_ml[C::kCols][kWarps], join_sum[C::kCols];  // (m, l) of each warp, of all
+  __shared__ float join_f[C::kCols][kWarps];                  // the warps' weights
+  __shared__ float join_b[C::kCols][NG][kWarps], join_bias[C::kCols][NG];  // bias parts
+  __shared__ Part parts[2];
+  __shared__ Cut cut_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int j = lane >> 2, c = lane & 3;
-  Feed<D, NT> feed;
-  feed.ring = smem + warp * C::kStages * C::kStage;
-  feed.bars = bars + warp * C::kStages;
-  feed.policy = policy_evict_first();
+  uint8_t* ring = smem + warp * C::kStages * C::kStage;
+  uint64_t* full = bars + warp * C::kStages;
+  float* join = reinterpret_cast<float*>(smem + C::kJoin);
+  const uint64_t policy = policy_evict_first();
   if (lane == 0)
-    for (int i = 0; i < C::kStages; ++i) mbar_init(feed.bars + i, 1);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
   fence_mbar_init();
   pdl_wait();
   pdl_trigger();
 
-  Range R;
-  int rts_max = 0;
-  if (WHOLE) {
-    rts_max = row_tiles(a, a.max_q, C::kCols);
-    R.b = blockIdx.x / (a.d.Hkv * rts_max);
-    R.w0 = 0;
-    R.w1 = 1;
-    R.before = 0;
-    R.blocks = 0;
-    if (tid == 0 && blockIdx.x % (a.d.Hkv * rts_max) == 0 && req_out_of_range(a, R.b))
-      record_error(a.err, kDevErrState);
-  } else {
-    R = find_range(a, C::kCols, sums, found);
-    if (tid == 0 && a.desc) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);  // [B + 1]
+  int64_t w1 = 0;  // end of the block's work
+  if (warp == 0) {
+    Part p;
+    p.some = false;
+    if (WHOLE) {
+      const int rts_max = row_tiles(a, a.max_q, C::kCols);
+      const int k = blockIdx.x % (a.d.Hkv * rts_max);
+      p.b = blockIdx.x / (a.d.Hkv * rts_max);
+      p.h = k / rts_max;
+      p.rt = k % rts_max;
+      p.r = load_req(a, p.b);
+      p.t0 = 0;
+      p.t1 = p.tiles = kv_tiles(p.r.kv);
+      p.some = p.rt < row_tiles(a, p.r.qn, C::kCols);
+      if (lane == 0 && k == 0 && req_out_of_range(a, p.b)) record_error(a.err, kDevErrState);
+    } else {
+      const Cut cut = cut_contexts(a, C::kCols, first);
+      if ((int)blockIdx.x < cut.blocks)
+        p = locate(a, first, C::kCols, cut.bound(blockIdx.x), cut.bound(blockIdx.x + 1));
+      if (lane == 0) cut_s = cut;
+    }
+    if (lane == 0) parts[0] = p;
   }
   __syncthreads();
+  if (!WHOLE && tid == 0) a.desc[2 * blockIdx.x].x = 0;
+  if (!parts[0].some) return;
+  if (!WHOLE) w1 = cut_s.bound(blockIdx.x + 1);
+  fetch_query<D, NT>(a, parts[0], smem + C::kQuery);
 
-  int used = 0;  // stages this warp has taken so far
-  int64_t w = R.w0, before = R.before;
+  // the warp's tiles of a part: t0 + warp, + kWarps, ... below the end of the context
+  auto lead_of = [&](const Part& p) { return p.t0 + warp; };
+  auto tiles_of = [&](const Part& p) {
+    const int n = min(p.t1, (p.r.kv + kTile - 1) / kTile) - lead_of(p);
+    return n > 0 ? (n + kWarps - 1) / kWarps : 0;
+  };
+  int head = 0, used = 0;  // ring stages filled and emptied so far
+  auto load = [&](uint32_t rec) {
+    const int stage = head % C::kStages;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(full + stage, C::kStage);
+      bulk_load(ring + stage * C::kStage, a.cache + (uint64_t)rec * C::kStage, C::kStage,
+                full + stage, policy);
+    }
+    ++head;
+  };
+
+  int mine = tiles_of(parts[0]);
+  uint32_t record = 0, record_more = 0;  // of 32 tiles ahead, one a lane
+  if (lane < mine)
+    record = tile_record(a, parts[0].b, parts[0].h, lead_of(parts[0]) + lane * kWarps);
+  int issued = min(mine, C::kStages);  // tiles of the part
+  for (int i = 0; i < issued; ++i) load(__shfl_sync(~0u, record, i));
+
   bool ok = true;
-  for (int b = R.b; w < R.w1; ) {
-    const Req r = load_req(a, b);
-    const int rts = row_tiles(a, r.qn, C::kCols);
-    const int nt_kv = kv_tiles(r.kv);
-    int h, rt, t0, t1;
-    if (WHOLE) {
-      const int k = blockIdx.x % (a.d.Hkv * rts_max);
-      h = k / rts_max;
-      rt = k % rts_max;
-      t0 = 0;
-      t1 = nt_kv;
-      w = R.w1;
-      if (rt >= rts) break;
-    } else {
-      const int64_t n = r.qn > 0 ? (int64_t)a.d.Hkv * rts * nt_kv : 0;
-      if (w >= before + n) {
-        before += n;
-        ++b;
-        continue;
-      }
-      const int64_t k = (w - before) / nt_kv;
-      h = (int)(k / rts);
-      rt = (int)(k % rts);
-      t0 = (int)((w - before) % nt_kv);
-      const int64_t left = R.w1 - w;
-      t1 = (int)(left < nt_kv - t0 ? t0 + left : nt_kv);
+  for (int cur = 0;; cur ^= 1) {
+    const Part& p = parts[cur];
+    Part& next = parts[cur ^ 1];
+    wait_copies();
+    __syncthreads();
+    if (warp < NT * NG)
+      prepare_query<D, NT>(a, p, smem + C::kQuery + cur * C::kCols * C::kQPitch, warp / NG,
+                           warp % NG, S);
+    if (tid == kThreads - 1) {
+      if (WHOLE) next.some = false;
+      else next = locate(a, first, C::kCols, p.next, w1);
     }
-    // the warp's tiles: t0 + warp, + kWarps, ... below the end of the context
-    const int last = min(t1, (r.kv + kTile - 1) / kTile);
-    const int first = t0 + warp;
-    const int mine = last > first ? (last - first + kWarps - 1) / kWarps : 0;
-    int2 pages = make_int2(0, 0), pages_next = pages;
-    if (lane < mine) pages = tile_pages(a, b, first + lane * kWarps, r.kv);
-    const int start = min(mine, C::kStages);
-    int issued = ok ? start : 0;
-    for (int i = 0; i < issued; ++i) {
-      const int pg0 = __shfl_sync(~0u, pages.x, i), pg1 = __shfl_sync(~0u, pages.y, i);
-      if (lane == 0)
-        feed.issue(a, h, first + i * kWarps, r.kv, (used + i) % C::kStages, pg0, pg1);
+    __syncthreads();
+    Query<NT> Q;
+    load_query<D, NT>(S, Q);
+    int mine_next = 0, issued_next = 0;
+    uint32_t record_next = 0;
+    if (next.some) {
+      fetch_query<D, NT>(a, next, smem + C::kQuery + (cur ^ 1) * C::kCols * C::kQPitch);
+      mine_next = tiles_of(next);
+      if (lane < mine_next)
+        record_next = tile_record(a, next.b, next.h, lead_of(next) + lane * kWarps);
     }
-    Query<D, NT> Q;
-    load_query<D, NT>(a, r, h, rt, Q);
     State<D, NT> s;
     clear(s);
-    for (int i = 0; i < mine; ++i) {
+    const int kv = p.r.kv;
+    int tok0 = lead_of(p) * kTile;
+    for (int i = 0; i < mine; ++i, tok0 += kWarps * kTile) {
       const int stage = used % C::kStages;
       // after a wait that ran out nothing more is copied, but what is under way still lands
-      if (i < issued) ok = mbar_wait(feed.bars + stage, (used / C::kStages) & 1, a.err) && ok;
+      if (used < head) ok = mbar_wait(full + stage, (used / C::kStages) & 1, a.err) && ok;
       ok = __all_sync(~0u, ok);
+      if (!ok && used >= head) continue;
       if (ok)
-        tile_step<D, NT>(smem_u32(feed.ring + stage * C::kStage), (first + i * kWarps) * kTile,
-                         r.kv, Q, s);
+        tile_step<D, NT>(smem_u32(ring + stage * C::kStage), smem_u32(S.frags), tok0, kv, Q, s);
       ++used;
       __syncwarp();
-      const int nx = i + C::kStages;
-      if ((nx & 31) == 0) pages = pages_next;
-      if ((nx & 31) == 16) {  // the ids of the following 32 tiles, half a batch ahead
-        const int f = nx + 16 + lane;
-        if (f < mine) pages_next = tile_pages(a, b, first + f * kWarps, r.kv);
-      }
-      if (nx < mine && ok) {
-        issued = nx + 1;
-        const int pg0 = __shfl_sync(~0u, pages.x, nx & 31);
-        const int pg1 = __shfl_sync(~0u, pages.y, nx & 31);
-        if (lane == 0) feed.issue(a, h, first + nx * kWarps, r.kv, stage, pg0, pg1);
+      if (!ok) continue;
+      if (issued < mine) {
+        if ((issued & 31) == 0) record = record_more;
+        if ((issued & 31) == 16) {  // the following 32 tiles, half a batch ahead
+          const int f = issued + 16 + lane;
+          if (f < mine) record_more = tile_record(a, p.b, p.h, lead_of(p) + f * kWarps);
+        }
+        load(__shfl_sync(~0u, record, issued & 31));
+        ++issued;
+      } else if (issued_next < min(mine_next, C::kStages)) {
+        load(__shfl_sync(~0u, record_next, issued_next));
+        ++issued_next;
       }
     }
+    while (ok && head - used < C::kStages && issued_next < mine_next) {
+      load(__shfl_sync(~0u, record_next, issued_next));
+      ++issued_next;
+    }
 
-    // join the warps
-    __syncthreads();  // every warp is done with its ring
-    float* join = reinterpret_cast<float*>(smem);
+    // join the warps: a common reference for each column, then kJoinWarps warps at a time
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        const int col = 8 * nt + 2 * c + cc;
         float l = s.l[nt][cc];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(~0u, l, o);
-        if (j == 0) {
-          join_m[warp][col] = s.m[nt][cc];
-          join_l[warp][col] = l;
-        }
+        if (j == 0) join_ml[8 * nt + 2 * c + cc][warp] = make_float2(s.m[nt][cc], l);
+      }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float ob = s.ob[nt][cc][g];
+    for (int nt = 0; nt < NT; ++nt) {
+      // bias parts, 2 NG values over 8 lanes: each exchange halves what a lane still sums
+      float v[2 * NG];
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) ob += __shfl_xor_sync(~0u, ob, o);
-          float v[8];
+      for (int i = 0; i < 2 * NG; ++i) v[i] = s.ob[nt][i / NG][i % NG];
+      int at = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[2 * i] = fmaf(s.o[nt][g][i][cc], 16777216.f, ob);
-            v[2 * i + 1] = fmaf(s.o[nt][g][i][2 + cc], 1048576.f, ob);
+      for (int o = 4, n = 2 * NG; o < 32; o <<= 1) {
+        if (n > 1) {
+          const bool up = lane & o;
+#pragma unroll
+          for (int i = 0; i < n / 2; ++i) {
+            const float give = up ? v[i] : v[i + n / 2];
+            const float keep = up ? v[i + n / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(~0u, give, o);
           }
-          float4* dst = reinterpret_cast<float4*>(
-              join + (warp * C::kCols + col) * C::kPitch + 64 * g + 8 * j);
-          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          n >>= 1;
+          at = at * 2 + up;
+        } else {
+          v[0] += __shfl_xor_sync(~0u, v[0], o);
         }
       }
+      // lanes that share a value write the same one
+      join_b[8 * nt + 2 * c + at / NG][at % NG][warp] = v[0];
+    }
     __syncthreads();
-    const bool whole = WHOLE || (t0 == 0 && t1 == nt_kv);
-    const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-    for (int i = tid; i < C::kCols * (D / 4); i += kThreads) {
-      const int col = i / (D / 4), ch = 4 * (i % (D / 4));
-      float m = join_m[0][col];
+    if (tid < C::kCols * NG) {
+      const int col = tid / NG, g = tid % NG;
+      float m = -INFINITY, l = 0.f, bias = 0.f;
 #pragma unroll
-      for (int k = 1; k < kWarps; ++k) m = fmaxf(m, join_m[k][col]);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < kWarps; ++k) m = fmaxf(m, join_ml[col][k].x);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        const float mk = join_m[k][col];
-        const float f = mk == -INFINITY ? (join_l[k][col] == 0.f ? 0.f : 1.f) : exp2_fast(mk - m);
-        const float4 v =
-            *reinterpret_cast<const float4*>(join + (k * C::kCols + col) * C::kPitch + ch);
-        l = fmaf(join_l[k][col], f, l);
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
+        const float2 x = join_ml[col][k];
+        const float f = part_weight(x.x, x.y, m);
+        l = fmaf(x.y, f, l);
+        bias = fmaf(join_b[col][g][k], f, bias);
+        if (g == 0) join_f[col][k] = f;
       }
-      if (whole) {
-        const int row = rt * C::kCols + col;
-        if (row < r.qn * a.d.G) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          __nv_bfloat16* dst = a.out + (int64_t)(r.q0 + row / a.d.G) * a.out_stride +
-                               (int64_t)(h * a.d.G + row % a.d.G) * D + ch;
-          __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-          __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-          *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&lo),
-                                                      *reinterpret_cast<uint32_t*>(&hi));
-        }
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * C::kCols + col) * D + ch) = o;
-        if (ch == 0) a.part_ml[slot * C::kCols + col] = make_float2(m, l);
-      }
+      join_bias[col][g] = bias;
+      if (g == 0) join_sum[col] = make_float2(m, l);
     }
-    if (!WHOLE) {
-      if (!whole && t0 == 0 && tid == 0) {
-        // this block has the context's first part: it names the join
-        const int64_t end = w + nt_kv;
-        // the last block that starts before the end
-        const int last_block = (int)((end * R.blocks + R.total - 1) / R.total) - 1;
-        a.desc[blockIdx.x] = make_int4(last_block - blockIdx.x + 1, b, h, rt);
-      }
-      w += t1 - t0;
-    }
-    fence_proxy_async_smem();  // the ring is written by copies again
     __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const float f = join_f[8 * nt + 2 * c + cc][warp];
+        const float f24 = f * 16777216.f, f20 = f * 1048576.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s.o[nt][g][i][cc] *= f24;
+            s.o[nt][g][i][2 + cc] *= f20;
+          }
+      }
+    const int own_col = tid / C::kLanes, own_ln = tid % C::kLanes;
+    float4 own[C::kVec];
+#pragma unroll
+    for (int k = 0; k < C::kVec; ++k) {
+      const float x = tid < C::kOwners ? join_bias[own_col][(own_ln + k * C::kLanes) / 16] : 0.f;
+      own[k] = make_float4(x, x, x, x);
+    }
+#pragma unroll 1
+    for (int round = 0; round < kWarps / kJoinWarps; ++round) {
+      if (warp / kJoinWarps == round) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            float* dst = join + ((warp % kJoinWarps) * C::kCols + 8 * nt + 2 * c + cc) * C::kPitch +
+                         4 * j;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float(&o0)[4] = s.o[nt][g][2 * k];
+                const float(&o1)[4] = s.o[nt][g][2 * k + 1];
+                *reinterpret_cast<float4*>(dst + 64 * g + 32 * k) =
+                    make_float4(o0[cc], o0[2 + cc], o1[cc], o1[2 + cc]);
+              }
+          }
+      }
+      __syncthreads();
+      if (tid < C::kOwners) {
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) {
+          const float4* src = reinterpret_cast<const float4*>(
+              join + (k * C::kCols + own_col) * C::kPitch);
+#pragma unroll
+          for (int v = 0; v < C::kVec; ++v) {
+            const float4 x = src[own_ln + v * C::kLanes];
+            own[v].x += x.x;
+            own[v].y += x.y;
+            own[v].z += x.z;
+            own[v].w += x.w;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    const bool whole = p.t1 - p.t0 == p.tiles;
+    if (tid < C::kOwners) {
+      const float2 ml = join_sum[own_col];
+      if (whole) {
+#pragma unroll
+        for (int v = 0; v < C::kVec; ++v)
+          store_out4(a, p, p.rt * C::kCols + own_col, D, own_ln + v * C::kLanes, own[v], ml.y);
+      } else {
+        const int64_t at = (2 * blockIdx.x + (p.t0 == 0)) * C::kCols + own_col;
+        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D) + own_ln;
+#pragma unroll
+        for (int v = 0; v < C::kVec; ++v) dst[v * C::kLanes] = own[v];
+        if (own_ln == 0) a.part_ml[at] = ml;
+      }
+    }
+    if (WHOLE) return;
+    if (!whole && p.t0 == 0 && tid == 0) {
+      // the block of a shared context's first part names it for the joins
+      const int n = cut_s.block_of(p.start + p.tiles - 1) - blockIdx.x + 1;
+      a.desc[2 * blockIdx.x] = make_int4(n, p.h, p.rt, p.r.q0);
+      a.desc[2 * blockIdx.x + 1].x = p.r.qn;
+    }
+    if (!next.some) return;
+    mine = mine_next;
+    issued = issued_next;
+    record = record_next;
   }
 }
 
-// Joins the parts of a context that several blocks share: block x names it (its own second part,
-// then the first parts of the following blocks), y is the column.
+// Joins the parts of the contexts that several blocks share, in block order.  Contexts of few
+// parts take one warp per column; contexts of many a block per column and 64 channels, with 16
+// groups of lanes over the parts, so that one long context (76 parts of 8 KB) is spread over 32
+// blocks and its parts are read in one round trip.
+constexpr int kJoinThreads = 256;
+constexpr int kFewParts = 8;
+constexpr int kMaxBlocks = 256;  // of the attention launch
+
+template <int N>
+__device__ __forceinline__ void add_scaled(float (&o)[N], const float* src, float f) {
+  if constexpr (N == 2) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+    o[0] = fmaf(v.x, f, o[0]);
+    o[1] = fmaf(v.y, f, o[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i));
+      o[i] = fmaf(v.x, f, o[i]);
+      o[i + 1] = fmaf(v.y, f, o[i + 1]);
+      o[i + 2] = fmaf(v.z, f, o[i + 2]);
+      o[i + 3] = fmaf(v.w, f, o[i + 3]);
+    }
+  }
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(128) attn_join_kernel(FwdArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(FwdArgs a, int blocks) {
   constexpr int kCols = 8 * NT;
-  constexpr int kLanes = D / 4;            // threads over the channels
-  constexpr int kGroups = 128 / kLanes;    // over the parts
-  __shared__ float4 acc[kGroups][kLanes];
-  __shared__ float red[4], ls[kGroups];
-  const int tid = threadIdx.x, col = blockIdx.y;
+  constexpr int kWarpsJ = kJoinThreads / 32;
+  __shared__ short few[kMaxBlocks], many[kMaxBlocks];
+  __shared__ int2 counts[kWarpsJ];
+  __shared__ float weight[kMaxBlocks];
+  __shared__ float2 red[kWarpsJ];
+  __shared__ float acc[16][64];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
-  const int4 d = a.desc[blockIdx.x];
-  if (d.x == 0) return;
-  const Req r = load_req(a, d.y);
-  const int row = d.w * kCols + col;
-  if (row >= r.qn * a.d.G) return;
-  const int base = 2 * blockIdx.x;
-  float m = -INFINITY;
-  for (int i = tid; i < d.x; i += 128)
-    m = fmaxf(m, a.part_ml[(base + (i ? 2 * i : 1)) * kCols + col].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  if ((tid & 31) == 0) red[tid >> 5] = m;
+  // the lists of shared contexts, in the same order in every block
+  const int n_mine = tid < blocks ? a.desc[2 * tid].x : 0;
+  const unsigned f_mask = __ballot_sync(~0u, n_mine > 0 && n_mine <= kFewParts);
+  const unsigned m_mask = __ballot_sync(~0u, n_mine > kFewParts);
+  if (lane == 0) counts[warp] = make_int2(__popc(f_mask), __popc(m_mask));
   __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const int ln = tid % kLanes, grp = tid / kLanes;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = grp; i < d.x; i += kGroups) {
-    const int slot = base + (i ? 2 * i : 1);
-    const float2 ml = a.part_ml[slot * kCols + col];
-    const float4 v =
-        *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * kCols + col) * D + 4 * ln);
-    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2_fast(ml.x - m);
-    l = fmaf(ml.y, f, l);
-    o.x = fmaf(v.x, f, o.x);
-    o.y = fmaf(v.y, f, o.y);
-    o.z = fmaf(v.z, f, o.z);
-    o.w = fmaf(v.w, f, o.w);
+  int nf = 0, nm = 0, f0 = 0, m0 = 0;
+#pragma unroll
+  for (int w = 0; w < kWarpsJ; ++w) {
+    if (w == warp) f0 = nf, m0 = nm;
+    nf += counts[w].x;
+    nm += counts[w].y;
   }
-  acc[grp][ln] = o;
-  if (ln == 0) ls[grp] = l;
+  const unsigned below = (1u << lane) - 1;
+  if (f_mask >> lane & 1) few[f0 + __popc(f_mask & below)] = (short)tid;
+  if (m_mask >> lane & 1) many[m0 + __popc(m_mask & below)] = (short)tid;
   __syncthreads();
-  if (grp == 0) {
-    float sum = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  Part p;
+  for (int u = blockIdx.x; u < nm * kCols * (D / 64); u += gridDim.x) {
+    const int piece = u % (D / 64), col = u / (D / 64) % kCols;
+    const int b0 = many[u / (D / 64) / kCols];
+    const int4 d = a.desc[2 * b0];
+    p.r.qn = a.desc[2 * b0 + 1].x;
+    p.h = d.y;
+    p.rt = d.z;
+    p.r.q0 = d.w;
+    const int n = d.x;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (tid < n) ml = __ldcg(a.part_ml + part_slot(b0, tid) * kCols + col);
+    float m = ml.x;
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      sum += ls[k];
-      o.x += acc[k][ln].x;
-      o.y += acc[k][ln].y;
-      o.z += acc[k][ln].z;
-      o.w += acc[k][ln].w;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    if (lane == 0) red[warp].x = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarpsJ; ++k) m = fmaxf(m, red[k].x);
+    const float f = part_weight(ml.x, ml.y, m);
+    weight[tid] = f;
+    float l = ml.y * f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    if (lane == 0) red[warp].y = l;
+    __syncthreads();
+    const int ln = tid & 15, grp = tid >> 4;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 5
+    for (int i = grp; i < n; i += 16)
+      add_scaled(o, a.part_o + ((int64_t)part_slot(b0, i) * kCols + col) * D + 64 * piece + 4 * ln,
+                 weight[i]);
+    *reinterpret_cast<float4*>(&acc[grp][4 * ln]) = make_float4(o[0], o[1], o[2], o[3]);
+    __syncthreads();
+    if (tid < 16) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarpsJ; ++k) sum += red[k].y;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) fma4(x, *reinterpret_cast<const float4*>(&acc[k][4 * tid]), 1.f);
+      store_out4(a, p, p.rt * kCols + col, D, 16 * piece + tid, x, sum);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    __nv_bfloat16* dst = a.out + (int64_t)(r.q0 + row / a.d.G) * a.out_stride +
-                         (int64_t)(d.z * a.d.G + row % a.d.G) * D + 4 * ln;
-    __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+    __syncthreads();
+  }
+
+  constexpr int kCh = D / 32;  // channels of a lane
+  for (int u = blockIdx.x * kWarpsJ + warp; u < nf * kCols; u += gridDim.x * kWarpsJ) {
+    const int col = u % kCols, b0 = few[u / kCols];
+    const int4 d = a.desc[2 * b0];
+    p.r.qn = a.desc[2 * b0 + 1].x;
+    p.h = d.y;
+    p.rt = d.z;
+    p.r.q0 = d.w;
+    const int row = p.rt * kCols + col;
+    if (row >= p.r.qn * a.d.G) continue;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < d.x) ml = __ldcg(a.part_ml + part_slot(b0, lane) * kCols + col);
+    float m = ml.x;
+#pragma unroll
+    for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    const float f = part_weight(ml.x, ml.y, m);
+    float l = ml.y * f;
+#pragma unroll
+    for (int o = 4; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    l = __shfl_sync(~0u, l, 0);
+    float o[kCh];
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) o[e] = 0.f;
+    const int last = d.x - 1;
+#pragma unroll
+    for (int i = 0; i < kFewParts; ++i)  // parts beyond the last read it again, with weight 0
+      add_scaled(o, a.part_o + ((int64_t)part_slot(b0, min(i, last)) * kCols + col) * D + lane * kCh,
+                 i <= last ? __shfl_sync(~0u, f, i) : 0.f);
+    if constexpr (kCh == 2) {
+      // two lanes hold the four channels that are stored at once
+      const float x = __shfl_down_sync(~0u, o[0], 1), y = __shfl_down_sync(~0u, o[1], 1);
+      if ((lane & 1) == 0)
+        store_out4(a, p, row, D, lane / 2, make_float4(o[0], o[1], x, y), l);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kCh; e += 4)
+        store_out4(a, p, row, D, (lane * kCh + e) / 4,
+                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]), l);
+    }
   }
 }
 
 template <int D, int NT>
-cudaError_t prepare() {
+cudaError_t prepare(int max_requests) {
   cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NT>::kSmem);
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg<D, NT>::kSmem + (max_requests + 1) * (int)sizeof(int64_t));
 }
 
 template <int D, int NT>
@@ -831,26 +1040,28 @@ cudaError_t launch(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
       return launch_pdl(attn_decode_kernel<D, NT, true>, dim3((unsigned)grid), dim3(kThreads),
                         C::kSmem, s, a);
   }
-  const int blocks = attn_decode_blocks(sms);
-  cudaError_t e = launch_pdl(attn_decode_kernel<D, NT, false>, dim3(blocks), dim3(kThreads),
-                             C::kSmem, s, a);
+  const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
+  const cudaError_t e =
+      launch_pdl(attn_decode_kernel<D, NT, false>, dim3(blocks), dim3(kThreads),
+                 C::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_join_kernel<D, NT>, dim3(blocks, C::kCols), dim3(128), 0, s, a);
+  return launch_pdl(attn_join_kernel<D, NT>, dim3(2 * sms), dim3(kJoinThreads), 0, s, a, blocks);
 }
 
 }  // namespace
 
-int attn_decode_blocks(int sms) { return 2 * sms; }
+// A block shares at most its first and its last context with others.
+int attn_decode_slots(int sms) { return 2 * sms; }
 
 size_t attn_decode_part_floats(int D) { return (size_t)(D == 256 ? 8 : 16) * D; }
 
-cudaError_t prepare_attn_decode_kernels() {
+cudaError_t prepare_attn_decode_kernels(int max_requests) {
   cudaError_t e;
-  if ((e = prepare<64, 2>()) != cudaSuccess) return e;
-  if ((e = prepare<64, 1>()) != cudaSuccess) return e;
-  if ((e = prepare<128, 2>()) != cudaSuccess) return e;
-  if ((e = prepare<128, 1>()) != cudaSuccess) return e;
-  return prepare<256, 1>();
+  if ((e = prepare<64, 2>(max_requests)) != cudaSuccess) return e;
+  if ((e = prepare<64, 1>(max_requests)) != cudaSuccess) return e;
+  if ((e = prepare<128, 2>(max_requests)) != cudaSuccess) return e;
+  if ((e = prepare<128, 1>(max_requests)) != cudaSuccess) return e;
+  return prepare<256, 1>(max_requests);
 }
 
 cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {

@@ -155,6 +155,12 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+// Record of slot and head.
+__device__ __forceinline__ int64_t record_of(const RowsArgs& a, int slot, int h) {
+  const int64_t page = slot >> a.page_shift;
+  return ((page * a.Hkv + h) << (a.page_shift - 4)) + ((slot & ((1 << a.page_shift) - 1)) >> 4);
+}
+
 struct Coded {
   uint32_t word;    // the lane's 8 codes
   uint32_t params;  // the group's scale and bias
@@ -194,12 +200,12 @@ __device__ __forceinline__ Coded code_row(const Row8& r) {
 // non-finite channel of either marks both.  Prompts keep two rows in flight per group.
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
+  using R = Record<D>;
   constexpr int L = D / 8, NG = D / kGroup;
   constexpr int kPerBlock = kThreads / L;
   const int li = threadIdx.x % L;
   const unsigned group_mask = L == 32 ? ~0u : ((1u << L) - 1) << ((threadIdx.x & 31) - li);
   const int64_t rows = (int64_t)a.T * a.Hkv;
-  const int page = 1 << a.page_shift;
   pdl_wait();
   pdl_trigger();
   const int64_t per_round = (int64_t)gridDim.x * kPerBlock;
@@ -222,13 +228,13 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
     if (slot >= a.n_slots) {
       if (li == 0) record_error(a.err, kDevErrState);
     } else if (slot >= 0) {
-      const int64_t at = ((int64_t)(slot >> a.page_shift) * a.Hkv + h) * page + (slot & (page - 1));
-      const int word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
-      reinterpret_cast<uint32_t*>(a.c.kc)[at * (D / 8) + word] = k.word;
-      reinterpret_cast<uint32_t*>(a.c.vc)[at * (D / 8) + word] = v.word;
+      uint8_t* rec = a.cache + record_of(a, slot, h) * R::kBytes;
+      const int row = slot & 15, word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
+      reinterpret_cast<uint32_t*>(rec + row * R::kRow)[word] = k.word;
+      reinterpret_cast<uint32_t*>(rec + R::kV + row * R::kRow)[word] = v.word;
       if ((li & 7) == 0) {
-        a.c.kp[at * NG + (li >> 3)] = k.params;
-        a.c.vp[at * NG + (li >> 3)] = v.params;
+        reinterpret_cast<uint32_t*>(rec + R::kKp + row * R::kPar)[li >> 3] = k.params;
+        reinterpret_cast<uint32_t*>(rec + R::kVp + row * R::kPar)[li >> 3] = v.params;
       }
     }
   }
@@ -245,11 +251,11 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t params) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_read_kernel(RowsArgs a) {
+  using R = Record<D>;
   constexpr int L = D / 8, NG = D / kGroup;
   constexpr int kPerBlock = kThreads / L;
   const int li = threadIdx.x % L;
   const int64_t rows = (int64_t)a.T * a.Hkv;
-  const int page = 1 << a.page_shift;
   pdl_wait();
   pdl_trigger();
 #pragma unroll 2
@@ -259,12 +265,13 @@ __global__ void __launch_bounds__(kThreads) attn_read_kernel(RowsArgs a) {
     const int slot = a.slots[t];
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     if (slot >= 0 && slot < a.n_slots) {
-      const int64_t at = ((int64_t)(slot >> a.page_shift) * a.Hkv + h) * page + (slot & (page - 1));
-      const int word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
-      k = decode_word(reinterpret_cast<const uint32_t*>(a.c.kc)[at * (D / 8) + word],
-                      a.c.kp[at * NG + (li >> 3)]);
-      v = decode_word(reinterpret_cast<const uint32_t*>(a.c.vc)[at * (D / 8) + word],
-                      a.c.vp[at * NG + (li >> 3)]);
+      const uint8_t* rec = a.cache + record_of(a, slot, h) * R::kBytes;
+      const int row = slot & 15, word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
+      k = decode_word(reinterpret_cast<const uint32_t*>(rec + row * R::kRow)[word],
+                      reinterpret_cast<const uint32_t*>(rec + R::kKp + row * R::kPar)[li >> 3]);
+      v = decode_word(
+          reinterpret_cast<const uint32_t*>(rec + R::kV + row * R::kRow)[word],
+          reinterpret_cast<const uint32_t*>(rec + R::kVp + row * R::kPar)[li >> 3]);
     } else if (slot >= a.n_slots && li == 0) {
       record_error(a.err, kDevErrState);
     }

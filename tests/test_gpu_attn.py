@@ -284,8 +284,7 @@ def test_cached_rows_equal_the_definition(T, Hq, Hkv, D, P, scale):
     n_pages = -(-T // P) + 3
     attn = moe.PagedAttention(Hq, Hkv, D, P, n_pages, 1)
     cache = attn.new_cache()
-    for t in (cache.k_codes, cache.v_codes, cache.k_params, cache.v_params):
-        t.fill_(77)
+    cache.data.fill_(77)
     kv = (randn(g, T, 2, Hkv, D) * scale).bfloat16()
     kv[0, 0, 0, :64] = 3.0            # a constant group: step 0
     kv[0, 1, 0, :64] = 0.0
@@ -307,7 +306,8 @@ def test_cached_rows_equal_the_definition(T, Hq, Hkv, D, P, scale):
     # the documented layout: word j of group g at (j ^ f(s)) * (D / 64) + g, lowest nibble first
     s = int(slots[0])
     f = ((s & 3) << 1) ^ (s & 4)
-    words = cache.k_codes[s // P, Hkv - 1, s % P].cpu().numpy().view(np.uint32)
+    record = cache.data[s // P, Hkv - 1, s % P // 16]
+    words = record[s % 16 * D // 2:][:D // 2].cpu().numpy().view(np.uint32)
     _, code = code_reference(k[0, Hkv - 1].float().cpu().numpy())
     for j in range(8):
         for grp in range(D // 64):
@@ -317,7 +317,8 @@ def test_cached_rows_equal_the_definition(T, Hq, Hkv, D, P, scale):
     # rows that no slot names are left alone
     rest = torch.ones(n_pages * P, dtype=torch.bool, device=DEV)
     rest[slots[:n].long()] = False
-    flat = cache.k_codes.transpose(1, 2).reshape(n_pages * P, -1)
+    codes = cache.data[..., 9 * D:17 * D].unflatten(-1, (16, D // 2))  # of the values
+    flat = codes.flatten(2, 3).transpose(1, 2).reshape(n_pages * P, -1)
     assert bool((flat[rest] == 77).all())
     attn.close()
 
@@ -359,9 +360,7 @@ class Setup:
         self.scale = scale or D ** -0.5
         self.attn = moe.PagedAttention(Hq, Hkv, D, P, self.n_pages, max(B, 1), scale=scale)
         self.cache = self.attn.new_cache()
-        for t in (self.cache.k_codes, self.cache.v_codes, self.cache.k_params,
-                  self.cache.v_params):
-            t.fill_(255 if t.dtype == torch.uint8 else -1)
+        self.cache.data.fill_(255)
         ids = first_page + torch.randperm(self.n_pages - first_page, generator=g, device=DEV)
         self.table = torch.full((B, self.width), 1 << 30, dtype=torch.int32, device=DEV)
         slots, used = [], 0
@@ -594,11 +593,11 @@ def test_many_requests_and_rows_of_nobody():
 
 def test_a_cache_beyond_32_bit_offsets():
     # the last pages of a cache whose arrays pass 4 GiB
-    n_pages = (5 << 30) // (64 * 2 * 128)
+    n_pages = (10 << 30) // (64 * 2 * 288)
     for new in ([1, 1], [1, 90]):
         s = Setup(16, 2, 256, 64, new, [700, 100], seed=15, n_pages=n_pages,
                   first_page=n_pages - 20)
-        assert s.cache.k_codes.numel() > 5e9
+        assert s.cache.data.numel() > 5e9
         s.check(s.forward())
         s.attn.close()
         del s
@@ -647,7 +646,7 @@ def test_arguments_are_refused_on_the_host():
     import torch
     s = Setup(16, 2, 256, 64, [1], [100], seed=17)
     A = 0x100000  # never dereferenced: every call below fails in the argument checks
-    h, c = s.attn.handle, s.cache.struct
+    h, c = s.attn.handle, s.cache.ptr
     OK, INV, UNS, ALI = (moe.MOE_OK, moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED,
                          moe.MOE_ERR_ALIGNMENT)
 
@@ -663,8 +662,7 @@ def test_arguments_are_refused_on_the_host():
     assert fwd(B=2) == UNS and fwd(T=(1 << 20) + 1) == UNS
     assert fwd(q=A + 8) == ALI and fwd(out=A + 2) == ALI and fwd(qs=4100) == ALI
     assert fwd(table=A + 2) == ALI and fwd(qo=A + 1) == ALI and fwd(kv=A + 2) == ALI
-    assert fwd(cache=moe.attn_kv4_cache(A, A, None, A)) == INV
-    assert fwd(cache=moe.attn_kv4_cache(A, A + 8, A, A)) == ALI
+    assert fwd(cache=A + 64) == ALI
 
     def rope(q=A, qs=4096, k=A, ks=512, pos=A, qw=A, kw=A, eps=1e-6, cs=A, n=4, rot=64, T=1,
              qo=A, qos=4096, ko=A, kos=512):
