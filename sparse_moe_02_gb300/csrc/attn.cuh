@@ -13,6 +13,9 @@
 namespace moe {
 
 constexpr int kGroup = 64;        // channels per scale and bias
+// Cached rows hold magnitudes below this only (larger ones count as not finite): the kernels'
+// powers of two of a record's bound, 2^118 at most, stay normal fp32 numbers.
+constexpr float kLargest = 8.307675e34f;  // 2^116
 constexpr int kDevErrNoMemory = 7;
 constexpr int kDevErrArg = 1;
 
@@ -138,5 +141,10 @@ cudaError_t prepare_attn_decode_kernels(int max_requests);
 int attn_decode_slots(int sms);         // partial results of a launch
 size_t attn_decode_part_floats(int D);  // fp32 of one partial result
 cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s);
+
+// Attention of more rows, and of batches that hold any such request: attn_prefill.cu.
+cudaError_t prepare_attn_prefill_kernels(int max_requests);
+size_t attn_prefill_part_floats(int D);
+cudaError_t launch_attn_prefill(const FwdArgs& a, int sms, cudaStream_t s);
 
 }  // namespace moe

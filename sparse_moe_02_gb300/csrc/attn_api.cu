@@ -91,6 +91,7 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
     return st;
   if ((st = record_cuda_status(moe::prepare_attn_plan_kernel(cfg->max_requests)))) return st;
   if ((st = record_cuda_status(moe::prepare_attn_decode_kernels(cfg->max_requests)))) return st;
+  if ((st = record_cuda_status(moe::prepare_attn_prefill_kernels(cfg->max_requests)))) return st;
 
   attn_handle h = new (std::nothrow) attn_handle_s;
   if (!h) return MOE_ERR_NO_MEMORY;
@@ -108,8 +109,8 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
 
   const size_t slots = moe::attn_decode_slots(sms);
   const size_t o_bytes =
-      round256(slots * moe::attn_decode_part_floats(cfg->head_dim) * sizeof(float));
-  const size_t ml_bytes = round256(slots * moe::kDecodeRows * sizeof(float2));
+      round256(slots * moe::attn_prefill_part_floats(cfg->head_dim) * sizeof(float));
+  const size_t ml_bytes = round256(slots * 128 * sizeof(float2));
   const size_t desc_bytes = round256(slots * sizeof(int4));
   const size_t zeroed = 2 * sizeof(int);  // the plan's ticket, the error word
   const size_t bytes = o_bytes + ml_bytes + desc_bytes + zeroed;
@@ -305,8 +306,10 @@ int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void*
   a.part_ml = h->part_ml;
   a.desc = h->desc;
   a.err = h->err;
-  return record_cuda_status(
-      moe::launch_attn_decode(a, max_kv_len, h->sms, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return record_cuda_status(a.max_q * h->d.G <= moe::kDecodeRows
+                                ? moe::launch_attn_decode(a, max_kv_len, h->sms, s)
+                                : moe::launch_attn_prefill(a, h->sms, s));
 }
 
 }  // extern "C"

@@ -28,6 +28,7 @@
 #include <climits>
 
 #include "attn.cuh"
+#include "attn_join.cuh"
 
 namespace moe {
 namespace {
@@ -100,12 +101,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // (a, b) += (x, y), one packed instruction
 __device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
   asm("{\n\t.reg .b64 p, q;\n\t"
@@ -153,23 +148,6 @@ __device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1)
 constexpr int kPartCost = 40;
 constexpr int kLeastWork = 32;  // of a block
 
-// a / b of nonnegative numbers, in 32 bits where they fit (a 64-bit division is a long routine)
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
-struct Cut {
-  int64_t share;  // work of a block, one more in the first `rest` blocks
-  int rest;
-  int blocks;
-  __device__ __forceinline__ int64_t bound(int i) const { return share * i + min(i, rest); }
-  // the block that does unit x
-  __device__ __forceinline__ int block_of(int64_t x) const {
-    const int64_t wide = (share + 1) * rest;
-    return x < wide ? (int)divide(x, share + 1) : rest + (int)divide(x - wide, share);
-  }
-};
-
 // Fills first[b], b = 0 .. B: the work before request b.  One warp.
 __device__ __forceinline__ Cut cut_contexts(const FwdArgs& a, int cols, int64_t* first) {
   const int lane = threadIdx.x & 31;
@@ -184,23 +162,13 @@ __device__ __forceinline__ Cut cut_contexts(const FwdArgs& a, int cols, int64_t*
       if (r.qn > 0)
         n = (int64_t)(a.d.Hkv * row_tiles(a, r.qn, cols)) * (kv_tiles(r.kv) + kPartCost);
     }
-    int64_t end = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(~0u, end, o);
-      if (lane >= o) end += u;
-    }
+    const int64_t end = warp_scan(n);
     if (b < a.B) first[b] = total + end - n;
     total += __shfl_sync(~0u, end, 31);
   }
   if (lane == 0) first[a.B] = total;
   __syncwarp();
-  const int64_t most = (total + kLeastWork - 1) / kLeastWork;
-  Cut c;
-  c.blocks = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
-  c.share = c.blocks ? divide(total, c.blocks) : 0;
-  c.rest = (int)(total - c.share * c.blocks);
-  return c;
+  return make_cut(total, kLeastWork, gridDim.x);
 }
 
 // What a lane keeps of the query rows (columns) of one context; their MMA B fragments lie in
@@ -220,16 +188,6 @@ struct QueryShared {
   float sum[8 * NT][D / kGroup];
   float scale[8 * NT];
   int lim[8 * NT];
-};
-
-// The part of a context that a block works on.
-struct Part {
-  int b, h, rt;
-  int t0, t1, tiles;  // its tiles, and the context's
-  Req r;
-  int64_t start;  // work before the context's first tile
-  int64_t next;   // the block's work after this part
-  bool some;
 };
 
 // Starts copying the part's query rows [column][D] into shared memory.
@@ -434,7 +392,7 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
 #pragma unroll
     for (int g = 0; g < NG; ++g) big = __vmaxu2(big, vp[r].w[g]);
   big = __reduce_max_sync(~0u, big & 0x7fffu);
-  const float ev = (float)max((int)(big >> 7) - 126, -60);
+  const float ev = (float)max((int)(big >> 7) - 126, -90);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float top[2];
@@ -519,38 +477,20 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
     }
 }
 
-// Record of `tile` of request b's context, head h; a page id out of range reads page 0 and is
-// recorded.  (32 bits: 2^32 records are more than 5 TB.)
-__device__ __forceinline__ uint32_t tile_record(const FwdArgs& a, int b, int h, int tile) {
-  const int shift = a.d.page_shift - 4;  // tiles per page
-  int id = a.table[(int64_t)b * a.table_width + (tile >> shift)];
-  if (id < 0 || id >= a.d.n_pages) {
-    record_error(a.err, kDevErrState);
-    id = 0;
-  }
-  return (((uint32_t)id * a.d.Hkv + h) << shift) + (tile & ((1 << shift) - 1));
-}
-
 // The part that holds work w of the block's [w, w1).
 __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, int cols, int64_t w,
                                        int64_t w1) {
   Part p;
   p.some = false;
   while (w < w1) {
-    int lo = 0, hi = a.B;  // first[lo] <= w < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= w) lo = mid;
-      else hi = mid;
-    }
-    p.b = lo;
-    p.r = load_req(a, lo);
+    p.b = find_request(first, a.B, w);
+    p.r = load_req(a, p.b);
     p.tiles = kv_tiles(p.r.kv);
     const int rts = row_tiles(a, p.r.qn, cols);
-    const int k = (int)divide(w - first[lo], p.tiles + kPartCost);
+    const int k = (int)divide(w - first[p.b], p.tiles + kPartCost);
     p.h = k / rts;
     p.rt = k % rts;
-    p.start = first[lo] + (int64_t)k * (p.tiles + kPartCost) + kPartCost;
+    p.start = first[p.b] + (int64_t)k * (p.tiles + kPartCost) + kPartCost;
     p.t0 = (int)max(w - p.start, (int64_t)0);
     p.t1 = (int)min(w1 - p.start, (int64_t)p.tiles);
     w = p.next = min(p.start + p.tiles, w1);
@@ -561,40 +501,6 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
   }
   return p;
 }
-
-__device__ __forceinline__ float part_weight(float m_part, float l_part, float m) {
-  // a part that saw nothing has m = -inf and l = 0; one of NaN scores m = -inf and l = NaN
-  return m_part == -INFINITY ? (l_part == 0.f ? 0.f : 1.f) : exp2_fast(m_part - m);
-}
-
-// Outputs are joined in the order in which the lanes hold them: float4 i of a column is channels
-// out_channel(i) .. + 3.
-__device__ __forceinline__ int out_channel(int i) {
-  return (i >> 4) * 64 + (i & 7) * 8 + ((i >> 3) & 1) * 4;
-}
-
-__device__ __forceinline__ void store_out4(const FwdArgs& a, const Part& p, int row, int D, int i,
-                                           float4 o, float l) {
-  if (row >= p.r.qn * a.d.G) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
-                       (int64_t)(p.h * a.d.G + row % a.d.G) * D + out_channel(i);
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                              *reinterpret_cast<const uint32_t*>(&hi));
-}
-
-__device__ __forceinline__ void fma4(float4& o, const float4& v, float f) {
-  o.x = fmaf(v.x, f, o.x);
-  o.y = fmaf(v.y, f, o.y);
-  o.z = fmaf(v.z, f, o.z);
-  o.w = fmaf(v.w, f, o.w);
-}
-
-// Slot of part i of a context whose first part is block b0's: that block's second slot, then the
-// first slots of the blocks behind it.
-__device__ __forceinline__ int part_slot(int b0, int i) { return 2 * (b0 + i) + (i == 0); }
 
 // One block per SM.  While a part is worked on, the next part's queries and, as ring stages fall
 // free, its first tiles are copied, so the joins between parts leave no gap in the stream.
@@ -672,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   int mine = tiles_of(parts[0]);
   uint32_t record = 0, record_more = 0;  // of 32 tiles ahead, one a lane
   if (lane < mine)
-    record = tile_record(a, parts[0].b, parts[0].h, lead_of(parts[0]) + lane * kWarps);
+    record = cache_record(a, parts[0].b, parts[0].h, lead_of(parts[0]) + lane * kWarps);
   int issued = min(mine, C::kStages);  // tiles of the part
   for (int i = 0; i < issued; ++i) load(__shfl_sync(~0u, record, i));
 
@@ -698,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
       fetch_query<D, NT>(a, next, smem + C::kQuery + (cur ^ 1) * C::kCols * C::kQPitch);
       mine_next = tiles_of(next);
       if (lane < mine_next)
-        record_next = tile_record(a, next.b, next.h, lead_of(next) + lane * kWarps);
+        record_next = cache_record(a, next.b, next.h, lead_of(next) + lane * kWarps);
     }
     State<D, NT> s;
     clear(s);
@@ -719,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
         if ((issued & 31) == 0) record = record_more;
         if ((issued & 31) == 16) {  // the following 32 tiles, half a batch ahead
           const int f = issued + 16 + lane;
-          if (f < mine) record_more = tile_record(a, p.b, p.h, lead_of(p) + f * kWarps);
+          if (f < mine) record_more = cache_record(a, p.b, p.h, lead_of(p) + f * kWarps);
         }
         load(__shfl_sync(~0u, record, issued & 31));
         ++issued;
@@ -875,150 +781,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   }
 }
 
-// Joins the parts of the contexts that several blocks share, in block order.  Contexts of few
-// parts take one warp per column; contexts of many a block per column and 64 channels, with 16
-// groups of lanes over the parts, so that one long context (76 parts of 8 KB) is spread over 32
-// blocks and its parts are read in one round trip.
-constexpr int kJoinThreads = 256;
-constexpr int kFewParts = 8;
-constexpr int kMaxBlocks = 256;  // of the attention launch
-
-template <int N>
-__device__ __forceinline__ void add_scaled(float (&o)[N], const float* src, float f) {
-  if constexpr (N == 2) {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-    o[0] = fmaf(v.x, f, o[0]);
-    o[1] = fmaf(v.y, f, o[1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i));
-      o[i] = fmaf(v.x, f, o[i]);
-      o[i + 1] = fmaf(v.y, f, o[i + 1]);
-      o[i + 2] = fmaf(v.z, f, o[i + 2]);
-      o[i + 3] = fmaf(v.w, f, o[i + 3]);
-    }
-  }
-}
-
-template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(FwdArgs a, int blocks) {
-  constexpr int kCols = 8 * NT;
-  constexpr int kWarpsJ = kJoinThreads / 32;
-  __shared__ short few[kMaxBlocks], many[kMaxBlocks];
-  __shared__ int2 counts[kWarpsJ];
-  __shared__ float weight[kMaxBlocks];
-  __shared__ float2 red[kWarpsJ];
-  __shared__ float acc[16][64];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
-  // the lists of shared contexts, in the same order in every block
-  const int n_mine = tid < blocks ? a.desc[2 * tid].x : 0;
-  const unsigned f_mask = __ballot_sync(~0u, n_mine > 0 && n_mine <= kFewParts);
-  const unsigned m_mask = __ballot_sync(~0u, n_mine > kFewParts);
-  if (lane == 0) counts[warp] = make_int2(__popc(f_mask), __popc(m_mask));
-  __syncthreads();
-  int nf = 0, nm = 0, f0 = 0, m0 = 0;
-#pragma unroll
-  for (int w = 0; w < kWarpsJ; ++w) {
-    if (w == warp) f0 = nf, m0 = nm;
-    nf += counts[w].x;
-    nm += counts[w].y;
-  }
-  const unsigned below = (1u << lane) - 1;
-  if (f_mask >> lane & 1) few[f0 + __popc(f_mask & below)] = (short)tid;
-  if (m_mask >> lane & 1) many[m0 + __popc(m_mask & below)] = (short)tid;
-  __syncthreads();
-
-  Part p;
-  for (int u = blockIdx.x; u < nm * kCols * (D / 64); u += gridDim.x) {
-    const int piece = u % (D / 64), col = u / (D / 64) % kCols;
-    const int b0 = many[u / (D / 64) / kCols];
-    const int4 d = a.desc[2 * b0];
-    p.r.qn = a.desc[2 * b0 + 1].x;
-    p.h = d.y;
-    p.rt = d.z;
-    p.r.q0 = d.w;
-    const int n = d.x;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (tid < n) ml = __ldcg(a.part_ml + part_slot(b0, tid) * kCols + col);
-    float m = ml.x;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    if (lane == 0) red[warp].x = m;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWarpsJ; ++k) m = fmaxf(m, red[k].x);
-    const float f = part_weight(ml.x, ml.y, m);
-    weight[tid] = f;
-    float l = ml.y * f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    if (lane == 0) red[warp].y = l;
-    __syncthreads();
-    const int ln = tid & 15, grp = tid >> 4;
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 5
-    for (int i = grp; i < n; i += 16)
-      add_scaled(o, a.part_o + ((int64_t)part_slot(b0, i) * kCols + col) * D + 64 * piece + 4 * ln,
-                 weight[i]);
-    *reinterpret_cast<float4*>(&acc[grp][4 * ln]) = make_float4(o[0], o[1], o[2], o[3]);
-    __syncthreads();
-    if (tid < 16) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarpsJ; ++k) sum += red[k].y;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) fma4(x, *reinterpret_cast<const float4*>(&acc[k][4 * tid]), 1.f);
-      store_out4(a, p, p.rt * kCols + col, D, 16 * piece + tid, x, sum);
-    }
-    __syncthreads();
-  }
-
-  constexpr int kCh = D / 32;  // channels of a lane
-  for (int u = blockIdx.x * kWarpsJ + warp; u < nf * kCols; u += gridDim.x * kWarpsJ) {
-    const int col = u % kCols, b0 = few[u / kCols];
-    const int4 d = a.desc[2 * b0];
-    p.r.qn = a.desc[2 * b0 + 1].x;
-    p.h = d.y;
-    p.rt = d.z;
-    p.r.q0 = d.w;
-    const int row = p.rt * kCols + col;
-    if (row >= p.r.qn * a.d.G) continue;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < d.x) ml = __ldcg(a.part_ml + part_slot(b0, lane) * kCols + col);
-    float m = ml.x;
-#pragma unroll
-    for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    const float f = part_weight(ml.x, ml.y, m);
-    float l = ml.y * f;
-#pragma unroll
-    for (int o = 4; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    l = __shfl_sync(~0u, l, 0);
-    float o[kCh];
-#pragma unroll
-    for (int e = 0; e < kCh; ++e) o[e] = 0.f;
-    const int last = d.x - 1;
-#pragma unroll
-    for (int i = 0; i < kFewParts; ++i)  // parts beyond the last read it again, with weight 0
-      add_scaled(o, a.part_o + ((int64_t)part_slot(b0, min(i, last)) * kCols + col) * D + lane * kCh,
-                 i <= last ? __shfl_sync(~0u, f, i) : 0.f);
-    if constexpr (kCh == 2) {
-      // two lanes hold the four channels that are stored at once
-      const float x = __shfl_down_sync(~0u, o[0], 1), y = __shfl_down_sync(~0u, o[1], 1);
-      if ((lane & 1) == 0)
-        store_out4(a, p, row, D, lane / 2, make_float4(o[0], o[1], x, y), l);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kCh; e += 4)
-        store_out4(a, p, row, D, (lane * kCh + e) / 4,
-                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]), l);
-    }
-  }
-}
-
 template <int D, int NT>
 cudaError_t prepare(int max_requests) {
   cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>,
@@ -1045,7 +807,7 @@ cudaError_t launch(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
       launch_pdl(attn_decode_kernel<D, NT, false>, dim3(blocks), dim3(kThreads),
                  C::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_join_kernel<D, NT>, dim3(2 * sms), dim3(kJoinThreads), 0, s, a, blocks);
+  return launch_pdl(attn_join_kernel<D, C::kCols>, dim3(2 * sms), dim3(kJoinThreads), 0, s, a, blocks);
 }
 
 }  // namespace

@@ -182,7 +182,7 @@ __device__ __forceinline__ Coded code_row(const Row8& r) {
   const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
   const float step = __bfloat162float(sb);
   Coded c;
-  c.finite = fabsf(raw) < __int_as_float(0x7f800000) && fabsf(step) < __int_as_float(0x7f800000);
+  c.finite = fabsf(lo) < kLargest && fabsf(hi) < kLargest;  // false for NaN
   c.word = 0;
   if (step > 0.f) {
 #pragma unroll
