@@ -119,9 +119,10 @@ __device__ __forceinline__ void fma4(float4& o, const float4& v, float f) {
 __device__ __forceinline__ int part_slot(int b0, int i) { return 2 * (b0 + i) + (i == 0); }
 
 // Joins the parts of the contexts that several blocks share, in block order.  Contexts of few
-// parts take one warp per column; contexts of many a block per column and 64 channels, with 16
-// groups of lanes over the parts, so that one long context (76 parts of 8 KB) is spread over 32
-// blocks and its parts are read in one round trip.
+// parts take one warp per column, as do all with many columns (row tiles); few columns of many
+// parts take a block per column and 64 channels, with 16 groups of lanes over the parts, so that
+// one long context (76 parts of 8 KB) is spread over 32 blocks and its parts are read in one round
+// trip.
 constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 8;
 constexpr int kMaxBlocks = 256;  // of the attention launch
@@ -145,7 +146,7 @@ __device__ __forceinline__ void add_scaled(float (&o)[N], const float* src, floa
 }
 
 template <int D, int kCols>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(FwdArgs a, int blocks) {
+__global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2) attn_join_kernel(FwdArgs a, int blocks) {
   constexpr int kWarpsJ = kJoinThreads / 32;
   __shared__ short few[kMaxBlocks], many[kMaxBlocks];
   __shared__ int2 counts[kWarpsJ];
@@ -157,8 +158,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(FwdArgs a, int 
   pdl_trigger();
   // the lists of shared contexts, in the same order in every block
   const int n_mine = tid < blocks ? a.desc[2 * tid].x : 0;
-  const unsigned f_mask = __ballot_sync(~0u, n_mine > 0 && n_mine <= kFewParts);
-  const unsigned m_mask = __ballot_sync(~0u, n_mine > kFewParts);
+  const bool is_few = n_mine <= kFewParts || kCols > 16;
+  const unsigned f_mask = __ballot_sync(~0u, n_mine > 0 && is_few);
+  const unsigned m_mask = __ballot_sync(~0u, n_mine > 0 && !is_few);
   if (lane == 0) counts[warp] = make_int2(__popc(f_mask), __popc(m_mask));
   __syncthreads();
   int nf = 0, nm = 0, f0 = 0, m0 = 0;
@@ -229,24 +231,33 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(FwdArgs a, int 
     p.r.q0 = d.w;
     const int row = p.rt * kCols + col;
     if (row >= p.r.qn * a.d.G) continue;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < d.x) ml = __ldcg(a.part_ml + part_slot(b0, lane) * kCols + col);
-    float m = ml.x;
+    float m = -INFINITY;
+    for (int i = lane; i < d.x; i += 32)
+      m = fmaxf(m, __ldcg(a.part_ml + part_slot(b0, i) * kCols + col).x);
 #pragma unroll
-    for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    const float f = part_weight(ml.x, ml.y, m);
-    float l = ml.y * f;
-#pragma unroll
-    for (int o = 4; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    l = __shfl_sync(~0u, l, 0);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    float l = 0.f;
     float o[kCh];
 #pragma unroll
     for (int e = 0; e < kCh; ++e) o[e] = 0.f;
-    const int last = d.x - 1;
+    for (int i0 = 0; i0 < d.x; i0 += kFewParts) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < kFewParts && i0 + lane < d.x)
+        ml = __ldcg(a.part_ml + part_slot(b0, i0 + lane) * kCols + col);
+      const float f = part_weight(ml.x, ml.y, m);
+      l = fmaf(ml.y, f, l);
 #pragma unroll
-    for (int i = 0; i < kFewParts; ++i)  // parts beyond the last read it again, with weight 0
-      add_scaled(o, a.part_o + ((int64_t)part_slot(b0, min(i, last)) * kCols + col) * D + lane * kCh,
-                 i <= last ? __shfl_sync(~0u, f, i) : 0.f);
+      for (int i = 0; i < kFewParts; ++i) {  // beyond the last: it again, with weight 0
+        const float fi = __shfl_sync(~0u, f, i);
+        add_scaled(o,
+                   a.part_o + ((int64_t)part_slot(b0, min(i0 + i, d.x - 1)) * kCols + col) * D +
+                       lane * kCh,
+                   i0 + i < d.x ? fi : 0.f);
+      }
+    }
+#pragma unroll
+    for (int i = 4; i; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+    l = __shfl_sync(~0u, l, 0);
     if constexpr (kCh == 2) {
       // two lanes hold the four channels that are stored at once
       const float x = __shfl_down_sync(~0u, o[0], 1), y = __shfl_down_sync(~0u, o[1], 1);

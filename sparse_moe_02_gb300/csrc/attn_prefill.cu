@@ -2,14 +2,15 @@
 // prompts, and batches that hold any of them, on the tcgen05 tensor cores.
 //
 // A block works on 128 query rows of one key/value head (row = new token * G + query head) in steps
-// of 64 cached tokens.  Fourteen warps: four hold the softmax (a thread per row), eight turn cached
-// rows into f16 MMA operands, one issues the MMAs, one copies cache records.
-//   S [128 x 64] = Q K^T      A = Q in tensor memory, B = keys [64][D] in shared memory
+// of 64 cached tokens.  Four warps hold the softmax (a thread per row), eight turn cached keys and
+// eight cached values into f16 MMA operands, one issues the MMAs, one finds the work and copies
+// cache records.
+//   S [128 x 64] = Q K^T      A = Q, B = keys [64][D], both in shared memory
 //   O [128 x D] += P V        A = P in tensor memory (over S), B = values [D][64] (channels by
 //                             tokens, so both operands are K-major)
-// S has two buffers, so the scores of step n + 1 are formed while the softmax of step n runs.  Q lies
-// in tensor memory because with 64 columns an MMA reads its A operand as often as B: from shared
-// memory the reads alone would take longer than the arithmetic.
+// S has two buffers, so the scores of step n + 1 are formed while the softmax of step n runs.  An MMA
+// whose A operand lies in tensor memory takes about 146 clocks whatever its width (measured): right
+// for the 256 channels of O, but the 64 columns of S took 2300 clocks a step with Q there.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -31,10 +32,15 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kStep = 64;            // tokens per step
 constexpr int kRecs = kStep / 16;    // cache records per step
-constexpr int kSoftWarps = 4, kDeqWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + kDeqWarps + 2);
-constexpr int kRaw = 4;              // steps of cache records in flight
-constexpr int kOps = 2;              // steps of MMA operands
+constexpr int kSoftWarps = 4;        // warps 0 .. 3
+constexpr int kKeyWarp = 4, kValueWarp = 12, kDeqWarps = 8;  // the first of eight each
+constexpr int kMmaWarp = 20, kLoadWarp = 21;
+constexpr int kThreads = 768;        // six warpgroups
+// Registers of a thread by warpgroup (softmax, four of dequantising warps, the rest): together the
+// 80 a thread that the launch grants.
+constexpr int kRegsSoft = 168, kRegsDeq = 64, kRegsRest = 56;
+static_assert(kRegsSoft + 4 * kRegsDeq + kRegsRest == 6 * 80, "the launch's registers");
+constexpr int kParts = 4;            // parts announced ahead
 constexpr float kSlack = 6.f, kLift = 9.f;  // as in the few-row kernel
 constexpr int kExps = 8;             // steps of record exponents kept
 
@@ -42,16 +48,19 @@ template <int D>
 struct Cfg {
   using R = Record<D>;
   static constexpr int NG = D / kGroup;
+  // steps of key operands, value operands and cache records held
+  static constexpr int kOpsK = 2, kOpsV = D == 256 ? 1 : 2, kRaw = D == 256 ? 2 : 4;
   static constexpr int kK = kStep * D * 2;  // bytes of a key (or value) operand
   static constexpr int kRawBytes = kRecs * R::kBytes;
-  static constexpr int kOffV = kOps * kK;
-  static constexpr int kOffRaw = 2 * kOps * kK;
-  static constexpr int kFirst = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kOffK = kRows * D * 2;  // behind Q
+  static constexpr int kOffV = kOffK + kOpsK * kK;
+  static constexpr int kOffRaw = kOffV + kOpsV * kK;
+  static constexpr int kOffStage = kOffRaw + kRaw * kRawBytes;  // 4 KB a softmax warp
+  static constexpr int kFirst = kOffStage + kSoftWarps * 4096;
   static constexpr int kSmem = kFirst + 1024;  // the operands start on a 1024-byte boundary
-  // tensor memory columns: O, Q, two score buffers
-  static constexpr int kColQ = D;
-  static constexpr int kColS = D + D / 2;
-  static constexpr int kCols = D == 64 ? 256 : 512;
+  // tensor memory columns: O, two score buffers
+  static constexpr int kColS = D;
+  static constexpr int kCols = D == 256 ? 512 : 256;
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -135,7 +144,7 @@ constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 // Work is counted in (cached token x query head) units, 128 per row tile and token position: row
 // tile rt of a request with `base` cached tokens before its new ones costs kPartCost G + base G +
 // 128 (rt + 1) units, and its step t starts at unit (kPartCost + 64 t) G of them.
-constexpr int kPartCost = 192;   // tokens: a row tile's fixed cost
+constexpr int kPartCost = 384;   // tokens: a row tile's fixed cost
 constexpr int kLeastSteps = 4;   // of a block
 
 struct Cost {
@@ -222,12 +231,25 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
 
 // ------------------------------------------------------------------- shared state
 
+template <int D>
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw];
-  uint64_t k_full[kOps], k_empty[kOps], v_full[kOps], v_empty[kOps];
+  using C = Cfg<D>;
+  uint64_t part_full[kParts], part_empty[kParts];
+  uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];
+  uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, o_free;
 };
+
+// Moves the warpgroup's threads to n registers.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Exponents of a record: keys were divided by 2^(ek + 6), values by 2^(ev + 6).
 struct __align__(16) Exps {
@@ -272,19 +294,18 @@ struct Dequant {
     return w;
   }
 
-  // tok: the first token's index in the context.  Also leaves the record's exponents in *ex and
-  // the value exponent and parameters for values().
+  // tok: the first token's index in the context.  Also leaves the record's exponents in *ex (those
+  // of the values too: the softmax needs them with the scores).
   static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int oct, int tok, int kv,
-                                              Exps* ex, uint32_t* v_params, int* v_exp) {
+                                              Exps* ex) {
     const int lane = threadIdx.x & 31;
     const int t = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
     const uint32_t rec = raw + (oct >> 1) * R::kBytes;
     const int row = 8 * (oct & 1) + t;
-    int e;
+    int e, ev;
     const uint32_t w = params(rec, R::kKp, oct, tok, kv, &e);
-    *v_params = params(rec, R::kVp, oct, tok, kv, v_exp);
-    if (lane == 0 && (oct & 1) == 0)
-      *ex = Exps{pow2(e), (float)*v_exp, pow2(-*v_exp), 0.f};
+    params(rec, R::kVp, oct, tok, kv, &ev);
+    if (lane == 0 && (oct & 1) == 0) *ex = Exps{pow2(e), (float)ev, pow2(-ev), 0.f};
     const float down = pow2(-(e + 6));
     const float s = bf16_lo(w) * down, b = bf16_hi(w) * down;
     const uint32_t s24 = pack_f16(s * 16777216.f, s * 16777216.f);
@@ -305,10 +326,12 @@ struct Dequant {
   // so that the rows of a store differ in their last three bits, which the swizzle spreads over
   // the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.
   static __device__ __forceinline__ void values(uint32_t raw, uint32_t dst, uint4* table, int oct,
-                                                uint32_t w, int e) {
+                                                int tok, int kv) {
     const int lane = threadIdx.x & 31;
     const uint32_t rec = raw + (oct >> 1) * R::kBytes;
     {
+      int e;
+      const uint32_t w = params(rec, R::kVp, oct, tok, kv, &e);
       const int t = lane & 7, g = (lane >> 3) % NG;
       const float down = pow2(-(e + 6));
       const uint32_t mate = __shfl_down_sync(~0u, w, 1);
@@ -368,26 +391,60 @@ __device__ __forceinline__ int out_column(int g, int k) {
 
 // ------------------------------------------------------------------- the kernel
 
+// Writes 16-byte pieces 0 .. 7 of the lane's row to dst(row) + 16 piece in whole lines, through 4 KB of
+// the warp's shared memory (pieces swizzled by the row).  dst returns NULL for rows that are not
+// written.
+template <typename F>
+__device__ __forceinline__ void store_pieces(uint32_t stage, const uint4 (&v)[8], F dst) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    sts128(stage + lane * 128 + ((j ^ (lane & 7)) << 4), v[j].x, v[j].y, v[j].z, v[j].w);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + (lane >> 3), j = lane & 7;
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(stage + row * 128 + ((j ^ (row & 7)) << 4)));
+    uint8_t* p = dst(row);
+    if (p) *reinterpret_cast<uint4*>(p + 16 * j) = x;
+  }
+  __syncwarp();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   using C = Cfg<D>;
   constexpr int NG = C::NG;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars bars;
+  __shared__ Bars<D> bars;
   __shared__ Exps exps[kExps][kRecs];
   __shared__ uint4 tables[kDeqWarps][4 * NG];
+  __shared__ Part parts[kParts];
+  __shared__ float units[kRows];
+  __shared__ __nv_bfloat16* rows[kRows];  // of the output
   __shared__ uint32_t tmem_base;
   __shared__ Cut cut_s;
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-  int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < kRaw; ++i) mbar_init(&bars.raw_full[i], 1), mbar_init(&bars.raw_empty[i], kDeqWarps);
-    for (int i = 0; i < kOps; ++i) {
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&bars.part_full[i], 1);
+      mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 1);
+    }
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(&bars.raw_full[i], 1);
+      mbar_init(&bars.raw_empty[i], 2 * kDeqWarps);
+    }
+    for (int i = 0; i < C::kOpsK; ++i) {
       mbar_init(&bars.k_full[i], kDeqWarps);
-      mbar_init(&bars.v_full[i], kDeqWarps);
       mbar_init(&bars.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kOpsV; ++i) {
+      mbar_init(&bars.v_full[i], kDeqWarps);
       mbar_init(&bars.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -399,122 +456,113 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     mbar_init(&bars.o_free, 32 * kSoftWarps);
     fence_mbar_init();
   }
-  constexpr int kMmaWarp = kSoftWarps + kDeqWarps, kLoadWarp = kMmaWarp + 1;
   if (warp == kMmaWarp) tmem_alloc(&tmem_base, C::kCols);
   pdl_wait();
   pdl_trigger();
-  if (warp == kLoadWarp) {
-    const Cut cut = cut_rows(a, first);
-    if (lane == 0) {
-      cut_s = cut;
-      a.desc[2 * blockIdx.x].x = 0;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const Cut cut = cut_s;
-  int64_t w0 = 0, w1 = 0;
-  if ((int)blockIdx.x < cut.blocks) w0 = cut.bound(blockIdx.x), w1 = cut.bound(blockIdx.x + 1);
   const uint32_t ops = smem_u32(smem);
   bool ok = true;
   int n = 0;  // steps so far
 
-  if (warp == kLoadWarp) {
-    for (Part p = locate(a, first, w0, w1); p.some && ok; p = locate(a, first, p.next, w1)) {
-      const int recs = (p.r.kv + 15) / 16;
-      uint32_t record = 0;
-      for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-        const int slot = (t - p.t0) & 7;
-        if (slot == 0) {  // the records of eight steps, one a lane
-          const int rec = t * kRecs + lane;
-          if (rec < recs) record = cache_record(a, p.b, p.h, rec);
-        }
-        const int st = n % kRaw;
-        ok = mbar_wait(&bars.raw_empty[st], ((n / kRaw) & 1) ^ 1, a.err);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        const int have = min(max(recs - t * kRecs, 0), kRecs);
-        const uint32_t rec = __shfl_sync(~0u, record, slot * kRecs + (lane & 3));
-        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[st], have * C::R::kBytes);
-        __syncwarp();
-        if (lane < have)
-          copy_record(smem + C::kOffRaw + st * C::kRawBytes + lane * C::R::kBytes,
-                      a.cache + (uint64_t)rec * C::R::kBytes, C::R::kBytes, &bars.raw_full[st]);
+  // The block's parts in order, as the load warp announces them: part k in parts[k % kParts].
+  auto part_ready = [&](int k) {
+    return mbar_wait(&bars.part_full[k % kParts], (k / kParts) & 1, a.err);
+  };
+  auto part_read = [&](int k) { mbar_arrive(&bars.part_empty[k % kParts]); };
+
+  if (warp >= kMmaWarp) {
+    registers_down<kRegsRest>();
+    if (warp == kLoadWarp) {
+      int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
+      const Cut cut = cut_rows(a, first);
+      if (lane == 0) {
+        cut_s = cut;
+        a.desc[2 * blockIdx.x].x = 0;
       }
-    }
-    // nothing may be in flight when the block ends
-    for (int k = max(0, n - kRaw); k < n; ++k) mbar_wait(&bars.raw_full[k % kRaw], (k / kRaw) & 1, a.err);
-  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
-    const int oct = warp - kSoftWarps;
-    for (Part p = locate(a, first, w0, w1); p.some && ok; p = locate(a, first, p.next, w1)) {
-      for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-        const int st = n % kRaw, op = n % kOps;
-        const uint32_t raw = ops + C::kOffRaw + st * C::kRawBytes;
-        const int tok = t * kStep + 8 * oct;
-        Exps* ex = &exps[n % kExps][oct >> 1];
-        const uint32_t par = ((n / kOps) & 1) ^ 1;
-        ok = mbar_wait(&bars.raw_full[st], (n / kRaw) & 1, a.err) &&
-             mbar_wait(&bars.k_empty[op], par, a.err);
+      int64_t w = 0, w1 = 0;
+      if ((int)blockIdx.x < cut.blocks) w = cut.bound(blockIdx.x), w1 = cut.bound(blockIdx.x + 1);
+      for (int k = 0; ok; ++k) {
+        const Part p = locate(a, first, w, w1);
+        ok = mbar_wait(&bars.part_empty[k % kParts], ((k / kParts) & 1) ^ 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        uint32_t v_params;
-        int v_exp;
-        Dequant<D>::keys(raw, ops + op * C::kK, oct, tok, p.r.kv, ex, &v_params, &v_exp);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.k_full[op]);
-        ok = __all_sync(~0u, mbar_wait(&bars.v_empty[op], par, a.err));
-        if (!ok) break;
-        Dequant<D>::values(raw, ops + C::kOffV + op * C::kK, tables[oct], oct, v_params, v_exp);
-        fence_proxy_async_smem();
-        __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars.v_full[op]);
-          mbar_arrive(&bars.raw_empty[st]);
+          parts[k % kParts] = p;
+          mbar_arrive(&bars.part_full[k % kParts]);
+        }
+        if (!p.some) break;
+        w = p.next;
+        const int recs = (p.r.kv + 15) / 16;
+        uint32_t record = 0;
+        for (int t = p.t0; t < p.t1; ++t, ++n) {
+          const int slot = (t - p.t0) & 7;
+          if (slot == 0) {  // the records of eight steps, one a lane
+            const int rec = t * kRecs + lane;
+            if (rec < recs) record = cache_record(a, p.b, p.h, rec);
+          }
+          const int st = n % C::kRaw;
+          ok = mbar_wait(&bars.raw_empty[st], ((n / C::kRaw) & 1) ^ 1, a.err);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          const int have = min(max(recs - t * kRecs, 0), kRecs);
+          const uint32_t rec = __shfl_sync(~0u, record, slot * kRecs + (lane & 3));
+          if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[st], have * C::R::kBytes);
+          __syncwarp();
+          if (lane < have)
+            copy_record(smem + C::kOffRaw + st * C::kRawBytes + lane * C::R::kBytes,
+                        a.cache + (uint64_t)rec * C::R::kBytes, C::R::kBytes,
+                        &bars.raw_full[st]);
         }
       }
-    }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
+      // nothing may be in flight when the block ends
+      for (int k = max(0, n - C::kRaw); k < n; ++k)
+        mbar_wait(&bars.raw_full[k % C::kRaw], (k / C::kRaw) & 1, a.err);
+    } else if (warp == kMmaWarp && lane == 0) {
       const uint32_t id_s = idesc_f16(kRows, kStep), id_o = idesc_f16(kRows, D);
       // scores of step k
       auto scores = [&](int k) {
-        if (!mbar_wait(&bars.k_full[k % kOps], (k / kOps) & 1, a.err)) return false;
+        if (!mbar_wait(&bars.k_full[k % C::kOpsK], (k / C::kOpsK) & 1, a.err)) return false;
         // the buffer's weights of step k - 2 have been used
         if (k >= 2 && !mbar_wait(&bars.pv_done[k & 1], ((k - 2) >> 1) & 1, a.err)) return false;
         tc_fence_after();
-        const uint32_t kb = ops + (k % kOps) * C::kK;
+        const uint32_t kb = ops + C::kOffK + (k % C::kOpsK) * C::kK;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_bf16_ts(tmem + C::kColS + (k & 1) * kStep, tmem + C::kColQ + 8 * i,
-                      sdesc_k128(kb + (i / 4) * (kStep * 128) + (i % 4) * 32), id_s, i > 0);
-        mma_commit(&bars.k_empty[k % kOps]);
+          mma_bf16(tmem + C::kColS + (k & 1) * kStep,
+                   sdesc_k128(ops + (i / 4) * (kRows * 128) + (i % 4) * 32),
+                   sdesc_k128(kb + (i / 4) * (kStep * 128) + (i % 4) * 32), id_s, i > 0);
+        mma_commit(&bars.k_empty[k % C::kOpsK]);
         mma_commit(&bars.s_full[k & 1]);
         return true;
       };
-      int part = 0;
-      for (Part p = locate(a, first, w0, w1); p.some && ok;
-           p = locate(a, first, p.next, w1), ++part) {
-        ok = mbar_wait(&bars.q_full, part & 1, a.err);
+      for (int k = 0; ok; ++k) {
+        ok = part_ready(k);
         if (!ok) break;
-        tc_fence_after();
+        const Part& p = parts[k % kParts];
+        const bool some = p.some;
+        const int steps = p.t1 - p.t0;
+        part_read(k);
+        if (!some) break;
+        ok = mbar_wait(&bars.q_full, k & 1, a.err);
+        if (!ok) break;
         ok = scores(n);
-        for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-          if (t + 1 < p.t1) ok = scores(n + 1);
+        for (int t = 0; t < steps && ok; ++t, ++n) {
+          if (t + 1 < steps) ok = scores(n + 1);
           if (!ok) break;
-          ok = mbar_wait(&bars.v_full[n % kOps], (n / kOps) & 1, a.err) &&
+          ok = mbar_wait(&bars.v_full[n % C::kOpsV], (n / C::kOpsV) & 1, a.err) &&
                mbar_wait(&bars.p_full[n & 1], (n >> 1) & 1, a.err) &&
-               (t > p.t0 || part == 0 || mbar_wait(&bars.o_free, (part - 1) & 1, a.err));
+               (t > 0 || k == 0 || mbar_wait(&bars.o_free, (k - 1) & 1, a.err));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t vb = ops + C::kOffV + (n % kOps) * C::kK;
+          const uint32_t vb = ops + C::kOffV + (n % C::kOpsV) * C::kK;
 #pragma unroll
           for (int i = 0; i < kStep / 16; ++i)
             mma_bf16_ts(tmem, tmem + C::kColS + (n & 1) * kStep + 8 * i, sdesc_k128(vb + i * 32),
-                        id_o, t > p.t0 || i > 0);
-          mma_commit(&bars.v_empty[n % kOps]);
+                        id_o, t > 0 || i > 0);
+          mma_commit(&bars.v_empty[n % C::kOpsV]);
           mma_commit(&bars.pv_done[n & 1]);
         }
       }
@@ -522,48 +570,107 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (n >= 1) mbar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, a.err);
     }
     __syncwarp();
+  } else if (warp >= kKeyWarp) {
+    registers_down<kRegsDeq>();
+    const bool is_key = warp < kValueWarp;
+    const int oct = warp - (is_key ? kKeyWarp : kValueWarp);
+    for (int k = 0; ok; ++k) {
+      ok = __all_sync(~0u, part_ready(k));
+      if (!ok) break;
+      const bool some = parts[k % kParts].some;
+      const int t0 = parts[k % kParts].t0, t1 = parts[k % kParts].t1, kv = parts[k % kParts].r.kv;
+      __syncwarp();
+      if (lane == 0) part_read(k);
+      if (!some) break;
+      for (int t = t0; t < t1; ++t, ++n) {
+        const int st = n % C::kRaw;
+        const uint32_t raw = ops + C::kOffRaw + st * C::kRawBytes;
+        const int tok = t * kStep + 8 * oct;
+        ok = mbar_wait(&bars.raw_full[st], (n / C::kRaw) & 1, a.err);
+        if (is_key) {
+          const int op = n % C::kOpsK;
+          ok = ok && mbar_wait(&bars.k_empty[op], ((n / C::kOpsK) & 1) ^ 1, a.err);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          Dequant<D>::keys(raw, ops + C::kOffK + op * C::kK, oct, tok, kv,
+                           &exps[n % kExps][oct >> 1]);
+        } else {
+          const int op = n % C::kOpsV;
+          ok = ok && mbar_wait(&bars.v_empty[op], ((n / C::kOpsV) & 1) ^ 1, a.err);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          Dequant<D>::values(raw, ops + C::kOffV + op * C::kK, tables[oct], oct, tok, kv);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(is_key ? &bars.k_full[n % C::kOpsK] : &bars.v_full[n % C::kOpsV]);
+          mbar_arrive(&bars.raw_empty[st]);
+        }
+      }
+    }
   } else {
+    registers_up<kRegsSoft>();
     // softmax: row `tid` of the row tile, tensor memory lane tid
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    for (Part p = locate(a, first, w0, w1); p.some && ok;) {
-      const int row = p.rt * kRows + tid;
-      const bool on = row < p.r.qn * a.d.G;
-      const int tok = row / a.d.G;
-      // the row as f16 in [2^13, 2^14) at its top, in the operands' channel order
-      float unit;
+    const uint32_t stage = ops + C::kOffStage + warp * 4096;
+    for (int k = 0; ok; ++k) {
+      ok = __all_sync(~0u, part_ready(k));
+      if (!ok) break;
+      const Part p = parts[k % kParts];
+      __syncwarp();
+      if (lane == 0) part_read(k);
+      if (!p.some) break;
+      const int row0 = p.rt * kRows + warp * 32;  // the warp's first row
+      const int rows_left = p.r.qn * a.d.G;
+      const int row = row0 + lane, tok = row / a.d.G;
+      const bool on = row < rows_left;
+      rows[tid] = on ? a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
+                           (int64_t)(p.h * a.d.G + row % a.d.G) * D
+                     : nullptr;
+      // The warp's query rows as f16 in [2^13, 2^14) at their top, in the operands' channel order:
+      // D / 8 lanes a row, 16-byte pieces, in the swizzle of the MMA's A operand.
       {
-        const __nv_bfloat16* src =
-            a.q + (int64_t)(p.r.q0 + (on ? tok : 0)) * a.q_stride +
-            (int64_t)(p.h * a.d.G + (on ? row % a.d.G : 0)) * D;
-        uint32_t top = 0;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(src + 8 * i);
-          const uint32_t x = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
-          top = __vmaxu2(top, __vmaxu2(x, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-        }
-        top = max(top & 0xffffu, top >> 16);
-        const int e = min(max((int)(top >> 7) - 127, -100), 126);
-        const float down = pow2(-e) * 8192.f;
-        unit = pow2(e) * (64.f / 8192.f) * a.d.scale_log2;
+        constexpr int kL = D / 8, kPer = 32 / kL;  // lanes a row, rows at a time
+        constexpr int kAhead = 8;
+        const int g = (lane % kL) >> 3, j = lane & 7;
 #pragma unroll 1
-        for (int g = 0; g < NG; ++g) {
-          uint32_t q[32];
+        for (int i0 = 0; i0 < 32 / kPer; i0 += kAhead) {
+          uint4 w[kAhead];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 w = on ? *reinterpret_cast<const uint4*>(src + 64 * g + 8 * j)
-                               : make_uint4(0, 0, 0, 0);
-            q[4 * j] = pack_f16(bf16_lo(w.x) * down, bf16_lo(w.z) * down);
-            q[4 * j + 1] = pack_f16(bf16_hi(w.x) * down, bf16_hi(w.z) * down);
-            q[4 * j + 2] = pack_f16(bf16_lo(w.y) * down, bf16_lo(w.w) * down);
-            q[4 * j + 3] = pack_f16(bf16_hi(w.y) * down, bf16_hi(w.w) * down);
+          for (int i = 0; i < kAhead; ++i) {
+            const int rr = row0 + (i0 + i) * kPer + lane / kL;
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (rr < rows_left)
+              w[i] = *reinterpret_cast<const uint4*>(
+                  a.q + (int64_t)(p.r.q0 + rr / a.d.G) * a.q_stride +
+                  (int64_t)(p.h * a.d.G + rr % a.d.G) * D + 8 * (lane % kL));
           }
-          tmem_st32(lane_base + C::kColQ + 32 * g, q);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int rr = (i0 + i) * kPer + lane / kL;  // of the warp's rows
+            uint32_t top = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                    __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+#pragma unroll
+            for (int o = kL / 2; o; o >>= 1)
+              top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+            top = max(top & 0xffffu, top >> 16);
+            const int e = min(max((int)(top >> 7) - 127, -100), 126);
+            const float down = pow2(-e) * 8192.f;
+            if (lane % kL == 0) units[warp * 32 + rr] = pow2(e) * (64.f / 8192.f) * a.d.scale_log2;
+            const int qr = warp * 32 + rr;
+            sts128(ops + g * (kRows * 128) + qr * 128 + ((j ^ (qr & 7)) << 4),
+                   pack_f16(bf16_lo(w[i].x) * down, bf16_lo(w[i].z) * down),
+                   pack_f16(bf16_hi(w[i].x) * down, bf16_hi(w[i].z) * down),
+                   pack_f16(bf16_lo(w[i].y) * down, bf16_lo(w[i].w) * down),
+                   pack_f16(bf16_hi(w[i].y) * down, bf16_hi(w[i].w) * down));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
         mbar_arrive(&bars.q_full);
       }
+      const float unit = units[tid];
       const int lim = on ? seen_by(p.r, tok) : p.r.kv;
       const int least = seen_by(p.r, p.rt * kRows / a.d.G);
       float m = -INFINITY, l = 0.f;
@@ -646,56 +753,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       tc_fence_after();
       const bool whole = p.t1 - p.t0 == p.tiles;
       const float inv = whole ? (l == 0.f ? 0.f : 64.f / l) : 64.f;
-      const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows + tid;
-      __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
-                           (int64_t)(p.h * a.d.G + row % a.d.G) * D;
+      const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows + warp * 32;
 #pragma unroll 1
       for (int g = 0; g < NG; ++g) {
         uint32_t o[8][8];  // [nibble][word]
 #pragma unroll
-        for (int k = 0; k < 8; ++k) tmem_ld8(lane_base + out_column<NG>(g, k), o[k]);
+        for (int i = 0; i < 8; ++i) tmem_ld8(lane_base + out_column<NG>(g, i), o[i]);
         wait_ld32(&o[0][0]);
         wait_ld32(&o[4][0]);
+        if (g == NG - 1) {
+          tc_fence_before();
+          mbar_arrive(&bars.o_free);
+        }
+        uint4 v[8];
         if (whole) {
-          if (on) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t v[4];
+          for (int j = 0; j < 8; ++j) {
+            uint32_t x[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 x =
-                    __floats2bfloat162_rn(__uint_as_float(o[2 * k][j]) * inv,
-                                          __uint_as_float(o[2 * k + 1][j]) * inv);
-                v[k] = *reinterpret_cast<const uint32_t*>(&x);
-              }
-              *reinterpret_cast<uint4*>(dst + 64 * g + 8 * j) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 y =
+                  __floats2bfloat162_rn(__uint_as_float(o[2 * i][j]) * inv,
+                                        __uint_as_float(o[2 * i + 1][j]) * inv);
+              x[i] = *reinterpret_cast<const uint32_t*>(&y);
             }
+            v[j] = make_uint4(x[0], x[1], x[2], x[3]);
           }
+          store_pieces(stage, v, [&](int rr) {
+            __nv_bfloat16* d = rows[warp * 32 + rr];
+            return reinterpret_cast<uint8_t*>(d ? d + 64 * g : nullptr);
+          });
         } else {
-          float4* part = reinterpret_cast<float4*>(a.part_o + at * D) + 16 * g;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              part[8 * k + j] = make_float4(__uint_as_float(o[4 * k][j]) * inv,
-                                            __uint_as_float(o[4 * k + 1][j]) * inv,
-                                            __uint_as_float(o[4 * k + 2][j]) * inv,
-                                            __uint_as_float(o[4 * k + 3][j]) * inv);
+            for (int j = 0; j < 8; ++j)
+              v[j] = make_uint4(__float_as_uint(__uint_as_float(o[4 * hf][j]) * inv),
+                                __float_as_uint(__uint_as_float(o[4 * hf + 1][j]) * inv),
+                                __float_as_uint(__uint_as_float(o[4 * hf + 2][j]) * inv),
+                                __float_as_uint(__uint_as_float(o[4 * hf + 3][j]) * inv));
+            store_pieces(stage, v, [&](int rr) {
+              return reinterpret_cast<uint8_t*>(a.part_o + (at + rr) * D + 64 * g + 32 * hf);
+            });
+          }
         }
       }
-      tc_fence_before();
-      mbar_arrive(&bars.o_free);
       if (!whole) {
-        a.part_ml[at] = make_float2(m, l);
+        a.part_ml[at + lane] = make_float2(m, l);
         if (p.t0 == 0 && tid == 0) {
           // the block of a shared row tile's first part names it for the joins
-          const int parts =
-              cut.block_of(p.start + (int64_t)(p.tiles - 1) * p.unit) - blockIdx.x + 1;
-          a.desc[2 * blockIdx.x] = make_int4(parts, p.h, p.rt, p.r.q0);
+          const int count =
+              cut_s.block_of(p.start + (int64_t)(p.tiles - 1) * p.unit) - blockIdx.x + 1;
+          a.desc[2 * blockIdx.x] = make_int4(count, p.h, p.rt, p.r.q0);
           a.desc[2 * blockIdx.x + 1].x = p.r.qn;
         }
       }
-      p = locate(a, first, p.next, w1);
     }
   }
   tc_fence_before();
@@ -714,7 +826,7 @@ cudaError_t launch(const FwdArgs& a, int sms, cudaStream_t s) {
       launch_pdl(attn_prefill_kernel<D>, dim3(blocks), dim3(kThreads),
                  Cfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_join_kernel<D, kRows>, dim3(2 * sms), dim3(kJoinThreads), 0, s, a, blocks);
+  return launch_pdl(attn_join_kernel<D, kRows>, dim3(8 * sms), dim3(kJoinThreads), 0, s, a, blocks);
 }
 
 template <int D>
