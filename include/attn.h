@@ -40,8 +40,8 @@
  * of 16 tokens of one head each, so that an attention kernel takes 16 tokens in one copy.  A record:
  *   key codes     uint8 [16][D/2]
  *   key params    uint32 [16][D/64]: group g's scale (bf16, lower half) and bias (upper half)
- *   value codes   uint8 [16][D/2]
  *   value params  uint32 [16][D/64]
+ *   value codes   uint8 [16][D/2]
  * Slot s = page * P + offset is row offset % 16 of record offset / 16 of its page.  Inside a row of
  * codes, 32-bit word j (0..7) of group g holds the codes of channels 64g + 8j .. 64g + 8j + 7, the
  * lowest nibble first, and lies at word (j ^ f(s)) * (D/64) + g, f(s) = 2 (s & 3) ^ (s & 4): the

@@ -32,13 +32,20 @@ struct Record {
   static constexpr int kRow = D / 2;            // code bytes of a row
   static constexpr int kPar = 4 * (D / kGroup);  // parameter bytes of a row
   static constexpr int kKp = 16 * kRow;
-  static constexpr int kV = kKp + 16 * kPar;
-  static constexpr int kVp = kV + 16 * kRow;
-  static constexpr int kBytes = kVp + 16 * kPar;
+  static constexpr int kVp = kKp + 16 * kPar;
+  static constexpr int kV = kVp + 16 * kPar;
+  static constexpr int kBytes = kV + 16 * kRow;
 };
 
 // Position (in units of D/64 words) of word j of every group in the row of slot s.
 __host__ __device__ __forceinline__ int row_swz(int s) { return ((s & 3) << 1) ^ (s & 4); }
+
+// Larger of each 16-bit half, unsigned: on the magnitudes of bf16 pairs their order.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // A device-side error: of several the largest value stays.
 __device__ __forceinline__ void record_error(int* err, int code) { atomicMax(err, code); }
@@ -132,8 +139,8 @@ struct RowsArgs {
   int* err;
 };
 
-cudaError_t launch_attn_append(const RowsArgs& a, int D, int sms, cudaStream_t s);
-cudaError_t launch_attn_read(const RowsArgs& a, int D, int sms, cudaStream_t s);
+cudaError_t launch_attn_append(const RowsArgs& a, int D, cudaStream_t s);
+cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s);
 
 // Attention of few query rows per key/value head and request (n_b G <= 16): attn_decode.cu.
 constexpr int kDecodeRows = 16;

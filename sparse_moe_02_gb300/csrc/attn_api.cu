@@ -248,7 +248,7 @@ int attn_kv4_append(attn_handle h, const void* k, int64_t k_stride, const void* 
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   return record_cuda_status(
-      moe::launch_attn_append(a, h->d.D, h->sms, static_cast<cudaStream_t>(stream)));
+      moe::launch_attn_append(a, h->d.D, static_cast<cudaStream_t>(stream)));
 }
 
 int attn_kv4_read(attn_handle h, const void* cache, const int32_t* slots, int T, void* k,
@@ -269,7 +269,7 @@ int attn_kv4_read(attn_handle h, const void* cache, const int32_t* slots, int T,
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   return record_cuda_status(
-      moe::launch_attn_read(a, h->d.D, h->sms, static_cast<cudaStream_t>(stream)));
+      moe::launch_attn_read(a, h->d.D, static_cast<cudaStream_t>(stream)));
 }
 
 int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void* cache,

@@ -225,11 +225,11 @@ __device__ __forceinline__ void prepare_query(const FwdArgs& a, const Part& p, c
 #pragma unroll
   for (int k = 0; k < 2 * NG; ++k) {
     const uint4 w = *reinterpret_cast<const uint4*>(src + 64 * k);
-    const uint32_t x = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
-    top = __vmaxu2(top, __vmaxu2(x, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+    const uint32_t x = max_u16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+    top = max_u16x2(top, max_u16x2(x, max_u16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
   }
-  top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 1));
-  top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 2));
+  top = max_u16x2(top, __shfl_xor_sync(~0u, top, 1));
+  top = max_u16x2(top, __shfl_xor_sync(~0u, top, 2));
   top = max(top & 0xffffu, top >> 16);
   // 2^-e with the row's largest entry in [2^e, 2^(e+1)), kept a normal number
   const int e = min(max((int)(top >> 7) - 127, -100), 126);
@@ -390,7 +390,7 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int g = 0; g < NG; ++g) big = __vmaxu2(big, vp[r].w[g]);
+    for (int g = 0; g < NG; ++g) big = max_u16x2(big, vp[r].w[g]);
   big = __reduce_max_sync(~0u, big & 0x7fffu);
   const float ev = (float)max((int)(big >> 7) - 126, -90);
 #pragma unroll

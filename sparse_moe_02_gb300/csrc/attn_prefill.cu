@@ -8,7 +8,8 @@
 //   S [128 x 64] = Q K^T      A = Q, B = keys [64][D], both in shared memory
 //   O [128 x D] += P V        A = P in tensor memory (over S), B = values [D][64] (channels by
 //                             tokens, so both operands are K-major)
-// S has two buffers, so the scores of step n + 1 are formed while the softmax of step n runs.  An MMA
+// S has four buffers: the scores of step n + 2 are queued behind the product of step n without
+// waiting for it, so the tensor core does not drain between steps.  An MMA
 // whose A operand lies in tensor memory takes about 146 clocks whatever its width (measured): right
 // for the 256 channels of O, but the 64 columns of S took 2300 clocks a step with Q there.
 //
@@ -34,7 +35,7 @@ constexpr int kStep = 64;            // tokens per step
 constexpr int kRecs = kStep / 16;    // cache records per step
 constexpr int kSoftWarps = 4;        // warps 0 .. 3
 constexpr int kKeyWarp = 4, kValueWarp = 12, kDeqWarps = 8;  // the first of eight each
-constexpr int kMmaWarp = 20, kLoadWarp = 21;
+constexpr int kMmaWarp = 20, kLoadWarp = 21, kValueLoadWarp = 22;
 constexpr int kThreads = 768;        // six warpgroups
 // Registers of a thread by warpgroup (softmax, four of dequantising warps, the rest): together the
 // 80 a thread that the launch grants.
@@ -42,25 +43,29 @@ constexpr int kRegsSoft = 168, kRegsDeq = 64, kRegsRest = 56;
 static_assert(kRegsSoft + 4 * kRegsDeq + kRegsRest == 6 * 80, "the launch's registers");
 constexpr int kParts = 4;            // parts announced ahead
 constexpr float kSlack = 6.f, kLift = 9.f;  // as in the few-row kernel
+constexpr int kS = 4;                // score buffers
 constexpr int kExps = 8;             // steps of record exponents kept
 
 template <int D>
 struct Cfg {
   using R = Record<D>;
   static constexpr int NG = D / kGroup;
-  // steps of key operands, value operands and cache records held
+  // steps of key operands and value operands, and of the records' key and value sides, held
   static constexpr int kOpsK = 2, kOpsV = D == 256 ? 1 : 2, kRaw = D == 256 ? 2 : 4;
+  // A record's key side (with the parameters of its values: the softmax needs their exponents with
+  // the scores) and its value side.
+  static constexpr int kSideK = R::kV, kSideV = R::kBytes - R::kVp;
   static constexpr int kK = kStep * D * 2;  // bytes of a key (or value) operand
-  static constexpr int kRawBytes = kRecs * R::kBytes;
   static constexpr int kOffK = kRows * D * 2;  // behind Q
   static constexpr int kOffV = kOffK + kOpsK * kK;
   static constexpr int kOffRaw = kOffV + kOpsV * kK;
-  static constexpr int kOffStage = kOffRaw + kRaw * kRawBytes;  // 4 KB a softmax warp
-  static constexpr int kFirst = kOffStage + kSoftWarps * 4096;
+  static constexpr int kOffRawV = kOffRaw + kRaw * kRecs * kSideK;
+  static constexpr int kOffStage = kOffRawV + kRaw * kRecs * kSideV;  // 2 KB a softmax warp
+  static constexpr int kFirst = kOffStage + kSoftWarps * 2048;
   static constexpr int kSmem = kFirst + 1024;  // the operands start on a 1024-byte boundary
-  // tensor memory columns: O, two score buffers
+  // tensor memory columns: O, the score buffers
   static constexpr int kColS = D;
-  static constexpr int kCols = D == 256 ? 512 : 256;
+  static constexpr int kCols = 512;
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -235,9 +240,9 @@ template <int D>
 struct Bars {
   using C = Cfg<D>;
   uint64_t part_full[kParts], part_empty[kParts];
-  uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];
+  uint64_t raw_full[2][C::kRaw], raw_empty[2][C::kRaw];  // [keys, values]
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[kS], p_full[kS], pv_done[kS];
   uint64_t q_full, o_free;
 };
 
@@ -272,9 +277,13 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) {
 }
 
 // One warp turns 8 cached tokens (half a record) of a step into operands: rows of the key operand
-// [64 tokens][D] and columns of the value operand [D][64 tokens], both in the 128-byte swizzle.
+// [64 tokens][D] or columns of the value operand [D][64 tokens], both in the 128-byte swizzle.  The
+// values are formed in registers first and stored once the operand's last readers are done, so
+// only the stores lie between two MMAs on the same buffer.
 template <int D>
 struct Dequant {
+  uint32_t out[2 * (D / kGroup)][4];
+
   using C = Cfg<D>;
   using R = Record<D>;
   static constexpr int NG = C::NG;
@@ -296,11 +305,10 @@ struct Dequant {
 
   // tok: the first token's index in the context.  Also leaves the record's exponents in *ex (those
   // of the values too: the softmax needs them with the scores).
-  static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int oct, int tok, int kv,
-                                              Exps* ex) {
+  __device__ __forceinline__ void keys(uint32_t raw, int oct, int tok, int kv, Exps* ex) {
     const int lane = threadIdx.x & 31;
     const int t = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
-    const uint32_t rec = raw + (oct >> 1) * R::kBytes;
+    const uint32_t rec = raw + (oct >> 1) * C::kSideK;
     const int row = 8 * (oct & 1) + t;
     int e, ev;
     const uint32_t w = params(rec, R::kKp, oct, tok, kv, &e);
@@ -312,23 +320,34 @@ struct Dequant {
     const uint32_t s20 = pack_f16(s * 1048576.f, s * 1048576.f);
     const uint32_t bb = pack_f16(b, b);
     const uint32_t src = rec + row * R::kRow + 4 * g;
-    const uint32_t out = dst + g * (kStep * 128) + (8 * oct + t) * 128;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int j = (sub * kWords + i) ^ (t >> 2);
       const uint32_t c = lds32(src + ((j ^ row_swz(t)) * NG) * 4), c8 = c >> 8;
-      sts128(out + ((j ^ t) << 4), fma_f16x2(c & kNib0, s24, bb), fma_f16x2(c & kNib1, s20, bb),
-             fma_f16x2(c8 & kNib0, s24, bb), fma_f16x2(c8 & kNib1, s20, bb));
+      out[i][0] = fma_f16x2(c & kNib0, s24, bb);
+      out[i][1] = fma_f16x2(c & kNib1, s20, bb);
+      out[i][2] = fma_f16x2(c8 & kNib0, s24, bb);
+      out[i][3] = fma_f16x2(c8 & kNib1, s20, bb);
+    }
+  }
+
+  __device__ __forceinline__ void store_keys(uint32_t dst, int oct) {
+    const int lane = threadIdx.x & 31;
+    const int t = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
+    const uint32_t at = dst + g * (kStep * 128) + (8 * oct + t) * 128;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int j = (sub * kWords + i) ^ (t >> 2);
+      sts128(at + ((j ^ t) << 4), out[i][0], out[i][1], out[i][2], out[i][3]);
     }
   }
 
   // Row i * 32 + lane of the value operand is channel 64 g + 8 j + kWords sub + i (lane = (sub, g, j)),
   // so that the rows of a store differ in their last three bits, which the swizzle spreads over
   // the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.
-  static __device__ __forceinline__ void values(uint32_t raw, uint32_t dst, uint4* table, int oct,
-                                                int tok, int kv) {
+  __device__ __forceinline__ void values(uint32_t raw, uint4* table, int oct, int tok, int kv) {
     const int lane = threadIdx.x & 31;
-    const uint32_t rec = raw + (oct >> 1) * R::kBytes;
+    const uint32_t rec = raw + (oct >> 1) * C::kSideV;
     {
       int e;
       const uint32_t w = params(rec, R::kVp, oct, tok, kv, &e);
@@ -345,7 +364,6 @@ struct Dequant {
       __syncwarp();
     }
     const int j = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
-    uint32_t out[kWords][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t = 2 * m;
@@ -375,6 +393,10 @@ struct Dequant {
       }
     }
     __syncwarp();  // the table is free for the next step
+  }
+
+  __device__ __forceinline__ void store_values(uint32_t dst, int oct) {
+    const int lane = threadIdx.x & 31, j = lane & 7;
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
       sts128(dst + (32 * i + lane) * 128 + ((oct ^ j) << 4), out[i][0], out[i][1], out[i][2],
@@ -391,27 +413,32 @@ __device__ __forceinline__ int out_column(int g, int k) {
 
 // ------------------------------------------------------------------- the kernel
 
-// Writes 16-byte pieces 0 .. 7 of the lane's row to dst(row) + 16 piece in whole lines, through 4 KB of
-// the warp's shared memory (pieces swizzled by the row).  dst returns NULL for rows that are not
-// written.
+// Writes 16-byte pieces 0 .. 7 of the lane's row to dst(row) + 16 piece in runs of 64 bytes, through 2 KB
+// of the warp's shared memory (pieces swizzled by the row).  dst returns NULL for rows that are
+// not written.
 template <typename F>
 __device__ __forceinline__ void store_pieces(uint32_t stage, const uint4 (&v)[8], F dst) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    sts128(stage + lane * 128 + ((j ^ (lane & 7)) << 4), v[j].x, v[j].y, v[j].z, v[j].w);
-  __syncwarp();
+  for (int half = 0; half < 2; ++half) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3), j = lane & 7;
-    uint4 x;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                 : "r"(stage + row * 128 + ((j ^ (row & 7)) << 4)));
-    uint8_t* p = dst(row);
-    if (p) *reinterpret_cast<uint4*>(p + 16 * j) = x;
+    for (int j = 0; j < 4; ++j) {
+      const uint4& x = v[4 * half + j];
+      sts128(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), x.x, x.y, x.z, x.w);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * i + (lane >> 2), j = lane & 3;
+      uint4 x;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                   : "r"(stage + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)));
+      uint8_t* p = dst(row);
+      if (p) *reinterpret_cast<uint4*>(p + 64 * half + 16 * j) = x;
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 template <int D>
@@ -433,11 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   if (tid == 0) {
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&bars.part_full[i], 1);
-      mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 1);
+      mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 2);
     }
-    for (int i = 0; i < C::kRaw; ++i) {
-      mbar_init(&bars.raw_full[i], 1);
-      mbar_init(&bars.raw_empty[i], 2 * kDeqWarps);
+    for (int i = 0; i < 2 * C::kRaw; ++i) {
+      mbar_init(&bars.raw_full[0][i], 1);
+      mbar_init(&bars.raw_empty[0][i], kDeqWarps);
     }
     for (int i = 0; i < C::kOpsK; ++i) {
       mbar_init(&bars.k_full[i], kDeqWarps);
@@ -447,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       mbar_init(&bars.v_full[i], kDeqWarps);
       mbar_init(&bars.v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kS; ++i) {
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.p_full[i], 32 * kSoftWarps);
       mbar_init(&bars.pv_done[i], 1);
@@ -475,6 +502,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
 
   if (warp >= kMmaWarp) {
     registers_down<kRegsRest>();
+    // copies the key (0) or value (1) sides of a part's records, a warp each
+    auto copy_sides = [&](int which, int b, int h, int kv, int t0, int t1) {
+      const int recs = (kv + 15) / 16;
+      uint32_t record = 0;
+      for (int t = t0; t < t1; ++t, ++n) {
+        const int slot = (t - t0) & 7;
+        if (slot == 0) {  // the records of eight steps, one a lane
+          const int rec = t * kRecs + lane;
+          if (rec < recs) record = cache_record(a, b, h, rec);
+        }
+        const int st = n % C::kRaw;
+        uint64_t* full = &bars.raw_full[which][st];
+        ok = mbar_wait(&bars.raw_empty[which][st], ((n / C::kRaw) & 1) ^ 1, a.err);
+        ok = __all_sync(~0u, ok);
+        if (!ok) return;
+        const int have = min(max(recs - t * kRecs, 0), kRecs);
+        const uint32_t rec = __shfl_sync(~0u, record, slot * kRecs + (lane & 3));
+        const int side = which ? C::kSideV : C::kSideK;
+        if (lane == 0) mbar_arrive_expect_tx(full, have * side);
+        __syncwarp();
+        if (lane < have)
+          copy_record(smem + (which ? C::kOffRawV : C::kOffRaw) + (st * kRecs + lane) * side,
+                      a.cache + (uint64_t)rec * C::R::kBytes + (which ? C::R::kVp : 0), side, full);
+      }
+    };
+    // nothing may be in flight when the block ends
+    auto drain = [&](int which) {
+      for (int k = max(0, n - C::kRaw); k < n; ++k)
+        mbar_wait(&bars.raw_full[which][k % C::kRaw], (k / C::kRaw) & 1, a.err);
+    };
     if (warp == kLoadWarp) {
       int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
       const Cut cut = cut_rows(a, first);
@@ -495,47 +552,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
         if (!p.some) break;
         w = p.next;
-        const int recs = (p.r.kv + 15) / 16;
-        uint32_t record = 0;
-        for (int t = p.t0; t < p.t1; ++t, ++n) {
-          const int slot = (t - p.t0) & 7;
-          if (slot == 0) {  // the records of eight steps, one a lane
-            const int rec = t * kRecs + lane;
-            if (rec < recs) record = cache_record(a, p.b, p.h, rec);
-          }
-          const int st = n % C::kRaw;
-          ok = mbar_wait(&bars.raw_empty[st], ((n / C::kRaw) & 1) ^ 1, a.err);
-          ok = __all_sync(~0u, ok);
-          if (!ok) break;
-          const int have = min(max(recs - t * kRecs, 0), kRecs);
-          const uint32_t rec = __shfl_sync(~0u, record, slot * kRecs + (lane & 3));
-          if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[st], have * C::R::kBytes);
-          __syncwarp();
-          if (lane < have)
-            copy_record(smem + C::kOffRaw + st * C::kRawBytes + lane * C::R::kBytes,
-                        a.cache + (uint64_t)rec * C::R::kBytes, C::R::kBytes,
-                        &bars.raw_full[st]);
-        }
+        copy_sides(0, p.b, p.h, p.r.kv, p.t0, p.t1);
       }
-      // nothing may be in flight when the block ends
-      for (int k = max(0, n - C::kRaw); k < n; ++k)
-        mbar_wait(&bars.raw_full[k % C::kRaw], (k / C::kRaw) & 1, a.err);
+      drain(0);
+    } else if (warp == kValueLoadWarp) {
+      for (int k = 0; ok; ++k) {
+        ok = __all_sync(~0u, part_ready(k));
+        if (!ok) break;
+        const Part p = parts[k % kParts];
+        __syncwarp();
+        if (lane == 0) part_read(k);
+        if (!p.some) break;
+        copy_sides(1, p.b, p.h, p.r.kv, p.t0, p.t1);
+      }
+      drain(1);
     } else if (warp == kMmaWarp && lane == 0) {
       const uint32_t id_s = idesc_f16(kRows, kStep), id_o = idesc_f16(kRows, D);
       // scores of step k
       auto scores = [&](int k) {
         if (!mbar_wait(&bars.k_full[k % C::kOpsK], (k / C::kOpsK) & 1, a.err)) return false;
-        // the buffer's weights of step k - 2 have been used
-        if (k >= 2 && !mbar_wait(&bars.pv_done[k & 1], ((k - 2) >> 1) & 1, a.err)) return false;
+        // the buffer's weights of step k - kS have been used
+        if (k >= kS && !mbar_wait(&bars.pv_done[k % kS], ((k - kS) / kS) & 1, a.err)) return false;
         tc_fence_after();
         const uint32_t kb = ops + C::kOffK + (k % C::kOpsK) * C::kK;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_bf16(tmem + C::kColS + (k & 1) * kStep,
+          mma_bf16(tmem + C::kColS + (k % kS) * kStep,
                    sdesc_k128(ops + (i / 4) * (kRows * 128) + (i % 4) * 32),
                    sdesc_k128(kb + (i / 4) * (kStep * 128) + (i % 4) * 32), id_s, i > 0);
         mma_commit(&bars.k_empty[k % C::kOpsK]);
-        mma_commit(&bars.s_full[k & 1]);
+        mma_commit(&bars.s_full[k % kS]);
         return true;
       };
       for (int k = 0; ok; ++k) {
@@ -548,32 +594,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         if (!some) break;
         ok = mbar_wait(&bars.q_full, k & 1, a.err);
         if (!ok) break;
-        ok = scores(n);
+        // two steps of scores ahead of the products
+        ok = scores(n) && (steps < 2 || scores(n + 1));
         for (int t = 0; t < steps && ok; ++t, ++n) {
-          if (t + 1 < steps) ok = scores(n + 1);
-          if (!ok) break;
           ok = mbar_wait(&bars.v_full[n % C::kOpsV], (n / C::kOpsV) & 1, a.err) &&
-               mbar_wait(&bars.p_full[n & 1], (n >> 1) & 1, a.err) &&
+               mbar_wait(&bars.p_full[n % kS], (n / kS) & 1, a.err) &&
                (t > 0 || k == 0 || mbar_wait(&bars.o_free, (k - 1) & 1, a.err));
           if (!ok) break;
           tc_fence_after();
           const uint32_t vb = ops + C::kOffV + (n % C::kOpsV) * C::kK;
 #pragma unroll
           for (int i = 0; i < kStep / 16; ++i)
-            mma_bf16_ts(tmem, tmem + C::kColS + (n & 1) * kStep + 8 * i, sdesc_k128(vb + i * 32),
+            mma_bf16_ts(tmem, tmem + C::kColS + (n % kS) * kStep + 8 * i, sdesc_k128(vb + i * 32),
                         id_o, t > 0 || i > 0);
           mma_commit(&bars.v_empty[n % C::kOpsV]);
-          mma_commit(&bars.pv_done[n & 1]);
+          mma_commit(&bars.pv_done[n % kS]);
+          if (t + 2 < steps) ok = scores(n + 2);
         }
       }
       // every MMA has ended before the tensor memory is given back
-      if (n >= 1) mbar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, a.err);
+      if (n >= 1) mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err);
     }
     __syncwarp();
   } else if (warp >= kKeyWarp) {
     registers_down<kRegsDeq>();
     const bool is_key = warp < kValueWarp;
     const int oct = warp - (is_key ? kKeyWarp : kValueWarp);
+    Dequant<D> d;
     for (int k = 0; ok; ++k) {
       ok = __all_sync(~0u, part_ready(k));
       if (!ok) break;
@@ -584,36 +631,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (!some) break;
       for (int t = t0; t < t1; ++t, ++n) {
         const int st = n % C::kRaw;
-        const uint32_t raw = ops + C::kOffRaw + st * C::kRawBytes;
+        const int which = is_key ? 0 : 1;
         const int tok = t * kStep + 8 * oct;
-        ok = mbar_wait(&bars.raw_full[st], (n / C::kRaw) & 1, a.err);
-        if (is_key) {
-          const int op = n % C::kOpsK;
-          ok = ok && mbar_wait(&bars.k_empty[op], ((n / C::kOpsK) & 1) ^ 1, a.err);
-          ok = __all_sync(~0u, ok);
-          if (!ok) break;
-          Dequant<D>::keys(raw, ops + C::kOffK + op * C::kK, oct, tok, kv,
-                           &exps[n % kExps][oct >> 1]);
-        } else {
-          const int op = n % C::kOpsV;
-          ok = ok && mbar_wait(&bars.v_empty[op], ((n / C::kOpsV) & 1) ^ 1, a.err);
-          ok = __all_sync(~0u, ok);
-          if (!ok) break;
-          Dequant<D>::values(raw, ops + C::kOffV + op * C::kK, tables[oct], oct, tok, kv);
-        }
+        ok = mbar_wait(&bars.raw_full[which][st], (n / C::kRaw) & 1, a.err);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        if (is_key)
+          d.keys(ops + C::kOffRaw + st * kRecs * C::kSideK, oct, tok, kv,
+                 &exps[n % kExps][oct >> 1]);
+        else  // (a value side begins with its parameters: R::kVp from where the record would)
+          d.values(ops + C::kOffRawV + st * kRecs * C::kSideV - C::R::kVp, tables[oct], oct, tok,
+                   kv);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.raw_empty[which][st]);
+        const int op = is_key ? n % C::kOpsK : n % C::kOpsV;
+        const int turn = is_key ? n / C::kOpsK : n / C::kOpsV;
+        ok = mbar_wait(is_key ? &bars.k_empty[op] : &bars.v_empty[op], (turn & 1) ^ 1, a.err);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        if (is_key) d.store_keys(ops + C::kOffK + op * C::kK, oct);
+        else d.store_values(ops + C::kOffV + op * C::kK, oct);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(is_key ? &bars.k_full[n % C::kOpsK] : &bars.v_full[n % C::kOpsV]);
-          mbar_arrive(&bars.raw_empty[st]);
-        }
+        if (lane == 0) mbar_arrive(is_key ? &bars.k_full[op] : &bars.v_full[op]);
       }
     }
   } else {
     registers_up<kRegsSoft>();
     // softmax: row `tid` of the row tile, tensor memory lane tid
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t stage = ops + C::kOffStage + warp * 4096;
+    const uint32_t stage = ops + C::kOffStage + warp * 2048;
     for (int k = 0; ok; ++k) {
       ok = __all_sync(~0u, part_ready(k));
       if (!ok) break;
@@ -632,28 +679,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       // D / 8 lanes a row, 16-byte pieces, in the swizzle of the MMA's A operand.
       {
         constexpr int kL = D / 8, kPer = 32 / kL;  // lanes a row, rows at a time
-        constexpr int kAhead = 8;
+        constexpr int kRound = 32 / kPer < 16 ? 32 / kPer : 16;
+        // the lane's own row; the others' by shuffles
+        const uint64_t own = on ? (uint64_t)(a.q + (int64_t)(p.r.q0 + tok) * a.q_stride +
+                                             (int64_t)(p.h * a.d.G + row % a.d.G) * D)
+                                : 0;
         const int g = (lane % kL) >> 3, j = lane & 7;
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32 / kPer; i0 += kAhead) {
-          uint4 w[kAhead];
+        for (int i0 = 0; i0 < 32 / kPer; i0 += kRound) {
+          uint4 w[kRound];
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            const int rr = row0 + (i0 + i) * kPer + lane / kL;
+          for (int i = 0; i < kRound; ++i) {
+            const uint64_t src = __shfl_sync(~0u, own, (i0 + i) * kPer + lane / kL);
             w[i] = make_uint4(0, 0, 0, 0);
-            if (rr < rows_left)
-              w[i] = *reinterpret_cast<const uint4*>(
-                  a.q + (int64_t)(p.r.q0 + rr / a.d.G) * a.q_stride +
-                  (int64_t)(p.h * a.d.G + rr % a.d.G) * D + 8 * (lane % kL));
+            if (src) w[i] = reinterpret_cast<const uint4*>(src)[lane % kL];
           }
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
+          for (int i = 0; i < kRound; ++i) {
             const int rr = (i0 + i) * kPer + lane / kL;  // of the warp's rows
-            uint32_t top = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                    __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+            uint32_t top = max_u16x2(max_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                    max_u16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
 #pragma unroll
             for (int o = kL / 2; o; o >>= 1)
-              top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+              top = max_u16x2(top, __shfl_xor_sync(~0u, top, o));
             top = max(top & 0xffffu, top >> 16);
             const int e = min(max((int)(top >> 7) - 127, -100), 126);
             const float down = pow2(-e) * 8192.f;
@@ -675,10 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const int least = seen_by(p.r, p.rt * kRows / a.d.G);
       float m = -INFINITY, l = 0.f;
       for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-        ok = __all_sync(~0u, mbar_wait(&bars.s_full[n & 1], (n >> 1) & 1, a.err));
+        ok = __all_sync(~0u, mbar_wait(&bars.s_full[n % kS], (n / kS) & 1, a.err));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sb = lane_base + C::kColS + (n & 1) * kStep;
+        const uint32_t sb = lane_base + C::kColS + (n % kS) * kStep;
         uint32_t s[kStep];
         tmem_ld32(sb, s);
         tmem_ld32(sb + 32, s + 32);
@@ -710,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           l *= f;
           if (t > p.t0) {
             // the outputs so far, once the last product has landed
-            ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, a.err));
+            ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -744,11 +792,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         tmem_st32(sb, w);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars.p_full[n & 1]);
+        mbar_arrive(&bars.p_full[n % kS]);
       }
       if (!ok) break;
       // outputs: after the last product
-      ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, a.err));
+      ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err));
       if (!ok) break;
       tc_fence_after();
       const bool whole = p.t1 - p.t0 == p.tiles;

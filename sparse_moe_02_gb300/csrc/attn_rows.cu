@@ -8,6 +8,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMostHeads = 8;  // of a group of lanes, in the norm and rotation
 
 struct Row8 {
   float x[8];
@@ -32,9 +33,10 @@ __device__ __forceinline__ uint4 narrow(const Row8& r) {
 
 // ------------------------------------------------------------------- norm and rotation
 
-// A group of L = D / 8 lanes takes one token's heads first, first + step, ...: the token's cosines and
-// sines and the norm weights stay in registers for all of them.  Single tokens spread their
-// heads over as many groups as there are (heads_per = 1); prompts keep a token's heads together.
+// A group of L = D / 8 lanes takes heads_per neighbouring heads of one token: the token's cosines
+// and sines and the norm weights stay in registers for all of them.  Single tokens spread their
+// heads over as many groups as there are; prompts take up to eight heads to a group, so that the
+// rotation's table rows are read once for eight heads.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) attn_rope_kernel(RopeArgs a, int heads_per) {
   constexpr int L = D / 8;
@@ -42,19 +44,16 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(RopeArgs a, int hea
   const int li = threadIdx.x % L;
   const int ch = 8 * li;
   const int heads = a.Hq + a.Hkv;
-  const int splits = (heads + heads_per - 1) / heads_per;
-  const int64_t items = (int64_t)a.T * splits;
+  const uint32_t splits = (heads + heads_per - 1) / heads_per;
   const int half = a.rot / 2;
   const bool turn = ch < a.rot;
   pdl_wait();
   pdl_trigger();
   const Row8 wq = widen(*reinterpret_cast<const uint4*>(a.qw + ch));
   const Row8 wk = widen(*reinterpret_cast<const uint4*>(a.kw + ch));
-  // groups of one warp run the same number of rounds, so that their shuffles meet
-  const int64_t rounds = (items + (int64_t)gridDim.x * kPerBlock - 1) / ((int64_t)gridDim.x * kPerBlock);
-  for (int64_t it = 0; it < rounds; ++it) {
-    const int64_t item = (it * gridDim.x + blockIdx.x) * kPerBlock + threadIdx.x / L;
-    const bool live = item < items;
+  {
+    const uint32_t item = blockIdx.x * kPerBlock + threadIdx.x / L;
+    const bool live = item < (uint32_t)a.T * splits;
     const int t = live ? (int)(item / splits) : 0;
     const int h0 = live ? (int)(item % splits) * heads_per : heads;
     float cs[8], sn[8];
@@ -185,10 +184,27 @@ __device__ __forceinline__ Coded code_row(const Row8& r) {
   c.finite = fabsf(lo) < kLargest && fabsf(hi) < kLargest;  // false for NaN
   c.word = 0;
   if (step > 0.f) {
+    // The quotient by a product with the reciprocal is within 2^-20 of the rounded quotient, so
+    // it rounds to the same code unless it lies near a half: then, and for steps whose
+    // reciprocal is no normal number, the quotient itself decides.
+    const float inv = __frcp_rn(step);
+    float q[8];
+    bool close = step < 1e-35f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float q = rintf(__fdiv_rn(__fsub_rn(r.x[e], lo), step));
-      c.word |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (4 * e);
+      const float y = __fsub_rn(r.x[e], lo) * inv;
+      q[e] = rintf(y);
+      close |= fabsf(y - q[e]) > 0.4999f;
+    }
+    if (close) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = rintf(__fdiv_rn(__fsub_rn(r.x[e], lo), step));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // 2^23 + code: the code is in the low bits
+      const float m = __fadd_rn(fminf(fmaxf(q[e], 0.f), 15.f), 8388608.f);
+      c.word |= (__float_as_uint(m) & 15u) << (4 * e);
     }
   }
   const __nv_bfloat16 lb = __float2bfloat16_rn(lo);
@@ -197,7 +213,7 @@ __device__ __forceinline__ Coded code_row(const Row8& r) {
 }
 
 // A group of L = D / 8 lanes per (token, head): key row and value row together, since a
-// non-finite channel of either marks both.  Prompts keep two rows in flight per group.
+// non-finite channel of either marks both.  Bound by HBM for prompts.
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
   using R = Record<D>;
@@ -205,16 +221,13 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
   constexpr int kPerBlock = kThreads / L;
   const int li = threadIdx.x % L;
   const unsigned group_mask = L == 32 ? ~0u : ((1u << L) - 1) << ((threadIdx.x & 31) - li);
-  const int64_t rows = (int64_t)a.T * a.Hkv;
+  const uint32_t rows = (uint32_t)a.T * a.Hkv;  // below 2^27
   pdl_wait();
   pdl_trigger();
-  const int64_t per_round = (int64_t)gridDim.x * kPerBlock;
-  const int64_t rounds = (rows + per_round - 1) / per_round;
-#pragma unroll 2
-  for (int64_t it = 0; it < rounds; ++it) {
-    const int64_t row = (it * gridDim.x + blockIdx.x) * kPerBlock + threadIdx.x / L;
+  {
+    const uint32_t row = blockIdx.x * kPerBlock + threadIdx.x / L;
     const bool live = row < rows;
-    const int t = live ? (int)(row / a.Hkv) : 0, h = live ? (int)(row % a.Hkv) : 0;
+    const int t = live ? (int)(row / (uint32_t)a.Hkv) : 0, h = live ? (int)(row % (uint32_t)a.Hkv) : 0;
     const int slot = live ? a.slots[t] : -1;
     const uint4 kw = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + 8 * li);
     const uint4 vw = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + 8 * li);
@@ -244,8 +257,11 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t params) {
   const float step = bf16_lo(params), lo = bf16_hi(params);
   Row8 r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    r.x[e] = __fadd_rn(__fmul_rn(step, (float)((w >> (4 * e)) & 15u)), lo);
+  for (int e = 0; e < 8; ++e) {
+    // the code as a float: 2^23 + code, less 2^23 (both exact)
+    const float code = __fsub_rn(__uint_as_float(((w >> (4 * e)) & 15u) | 0x4b000000u), 8388608.f);
+    r.x[e] = __fadd_rn(__fmul_rn(step, code), lo);
+  }
   return narrow(r);
 }
 
@@ -255,13 +271,11 @@ __global__ void __launch_bounds__(kThreads) attn_read_kernel(RowsArgs a) {
   constexpr int L = D / 8, NG = D / kGroup;
   constexpr int kPerBlock = kThreads / L;
   const int li = threadIdx.x % L;
-  const int64_t rows = (int64_t)a.T * a.Hkv;
   pdl_wait();
   pdl_trigger();
-#pragma unroll 2
-  for (int64_t row = (int64_t)blockIdx.x * kPerBlock + threadIdx.x / L; row < rows;
-       row += (int64_t)gridDim.x * kPerBlock) {
-    const int t = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
+  const uint32_t row = blockIdx.x * kPerBlock + threadIdx.x / L;
+  if (row < (uint32_t)a.T * a.Hkv) {
+    const int t = (int)(row / (uint32_t)a.Hkv), h = (int)(row % (uint32_t)a.Hkv);
     const int slot = a.slots[t];
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     if (slot >= 0 && slot < a.n_slots) {
@@ -280,10 +294,9 @@ __global__ void __launch_bounds__(kThreads) attn_read_kernel(RowsArgs a) {
   }
 }
 
-int row_grid(int64_t items, int per_block, int sms) {
-  const int64_t blocks = (items + per_block - 1) / per_block;
-  const int64_t most = (int64_t)sms * (2048 / kThreads);
-  return (int)(blocks < most ? blocks : most);
+int row_grid(const RowsArgs& a, int D) {
+  const int per_block = kThreads / (D / 8);
+  return (int)(((int64_t)a.T * a.Hkv + per_block - 1) / per_block);
 }
 
 }  // namespace
@@ -292,12 +305,14 @@ cudaError_t launch_attn_qk_norm_rope(const RopeArgs& a, int D, bool inter, int s
                                      cudaStream_t s) {
   const int per_block = kThreads / (D / 8);
   const int heads = a.Hq + a.Hkv;
-  // as few heads per group as still leave one item for every group that fits the GPU
+  // as few heads per group as still leave one item for every group that fits the GPU, up to eight
   const int64_t groups = (int64_t)sms * (2048 / kThreads) * per_block;
-  int heads_per = (int)((a.T * (int64_t)heads + groups - 1) / groups);
-  if (heads_per > heads) heads_per = heads;
-  const int splits = (heads + heads_per - 1) / heads_per;
-  const dim3 grid(row_grid((int64_t)a.T * splits, per_block, sms)), block(kThreads);
+  int64_t heads_per64 = (a.T * (int64_t)heads + groups - 1) / groups;
+  if (heads_per64 > kMostHeads) heads_per64 = kMostHeads;
+  int splits = (heads + (int)heads_per64 - 1) / (int)heads_per64;
+  const int heads_per = (heads + splits - 1) / splits;  // evenly
+  splits = (heads + heads_per - 1) / heads_per;
+  const dim3 grid((unsigned)(((int64_t)a.T * splits + per_block - 1) / per_block)), block(kThreads);
   if (D == 64)
     return inter ? launch_pdl(attn_rope_kernel<64, true>, grid, block, 0, s, a, heads_per)
                  : launch_pdl(attn_rope_kernel<64, false>, grid, block, 0, s, a, heads_per);
@@ -308,15 +323,15 @@ cudaError_t launch_attn_qk_norm_rope(const RopeArgs& a, int D, bool inter, int s
                : launch_pdl(attn_rope_kernel<256, false>, grid, block, 0, s, a, heads_per);
 }
 
-cudaError_t launch_attn_append(const RowsArgs& a, int D, int sms, cudaStream_t s) {
-  const dim3 grid(row_grid((int64_t)a.T * a.Hkv, kThreads / (D / 8), sms)), block(kThreads);
+cudaError_t launch_attn_append(const RowsArgs& a, int D, cudaStream_t s) {
+  const dim3 grid(row_grid(a, D)), block(kThreads);
   if (D == 64) return launch_pdl(attn_append_kernel<64>, grid, block, 0, s, a);
   if (D == 128) return launch_pdl(attn_append_kernel<128>, grid, block, 0, s, a);
   return launch_pdl(attn_append_kernel<256>, grid, block, 0, s, a);
 }
 
-cudaError_t launch_attn_read(const RowsArgs& a, int D, int sms, cudaStream_t s) {
-  const dim3 grid(row_grid((int64_t)a.T * a.Hkv, kThreads / (D / 8), sms)), block(kThreads);
+cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s) {
+  const dim3 grid(row_grid(a, D)), block(kThreads);
   if (D == 64) return launch_pdl(attn_read_kernel<64>, grid, block, 0, s, a);
   if (D == 128) return launch_pdl(attn_read_kernel<128>, grid, block, 0, s, a);
   return launch_pdl(attn_read_kernel<256>, grid, block, 0, s, a);

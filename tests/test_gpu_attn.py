@@ -317,7 +317,7 @@ def test_cached_rows_equal_the_definition(T, Hq, Hkv, D, P, scale):
     # rows that no slot names are left alone
     rest = torch.ones(n_pages * P, dtype=torch.bool, device=DEV)
     rest[slots[:n].long()] = False
-    codes = cache.data[..., 9 * D:17 * D].unflatten(-1, (16, D // 2))  # of the values
+    codes = cache.data[..., 10 * D:].unflatten(-1, (16, D // 2))  # of the values
     flat = codes.flatten(2, 3).transpose(1, 2).reshape(n_pages * P, -1)
     assert bool((flat[rest] == 77).all())
     attn.close()
