@@ -56,6 +56,18 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(RopeArgs a, int hea
     const bool live = item < (uint32_t)a.T * splits;
     const int t = live ? (int)(item / splits) : 0;
     const int h0 = live ? (int)(item % splits) * heads_per : heads;
+    // all heads are requested before the position, which the table rows wait for
+    uint4 raw[kMostHeads];
+#pragma unroll
+    for (int i = 0; i < kMostHeads; ++i) {
+      const int h = h0 + i;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (i < heads_per && h < heads) {
+        const __nv_bfloat16* src = h < a.Hq ? a.q + t * a.q_stride + (int64_t)h * D
+                                            : a.k + t * a.k_stride + (int64_t)(h - a.Hq) * D;
+        raw[i] = *reinterpret_cast<const uint4*>(src + ch);
+      }
+    }
     float cs[8], sn[8];
     if (turn && live) {
       int pos = a.positions[t];
@@ -86,20 +98,13 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(RopeArgs a, int hea
 #pragma unroll
       for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
     }
-#pragma unroll 4
-    for (int i = 0; i < heads_per; ++i) {
+#pragma unroll
+    for (int i = 0; i < kMostHeads; ++i) {
+      if (i >= heads_per) break;
       const int h = h0 + i;
       const bool on = h < heads;
       const bool isq = h < a.Hq;
-      Row8 r;
-      if (on) {
-        const __nv_bfloat16* src = isq ? a.q + t * a.q_stride + (int64_t)h * D
-                                       : a.k + t * a.k_stride + (int64_t)(h - a.Hq) * D;
-        r = widen(*reinterpret_cast<const uint4*>(src + ch));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r.x[e] = 0.f;
-      }
+      Row8 r = widen(raw[i]);
       float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = fmaf(r.x[e], r.x[e], sum);
@@ -143,14 +148,15 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(RopeArgs a, int hea
 
 // ------------------------------------------------------------------- cached rows
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Larger and smaller of each bf16 pair, NaN if either is.
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -166,47 +172,52 @@ struct Coded {
   bool finite;
 };
 
-// Codes of the lane's 8 channels; the 8 lanes of a group share lo, step.  The division and the
-// rounding are the plain fp32 operations, so every code equals the definition's.
-__device__ __forceinline__ Coded code_row(const Row8& r) {
-  float lo = r.x[0], hi = r.x[0];
-#pragma unroll
-  for (int e = 1; e < 8; ++e) lo = min_nan(lo, r.x[e]), hi = max_nan(hi, r.x[e]);
+// Codes of the lane's 8 channels; the 8 lanes of a group share lo and step.  Every code equals the
+// one that the definition's fp32 division and rounding give.
+__device__ __forceinline__ Coded code_row(uint4 w) {
+  uint32_t lo2 = min_nan2(min_nan2(w.x, w.y), min_nan2(w.z, w.w));
+  uint32_t hi2 = max_nan2(max_nan2(w.x, w.y), max_nan2(w.z, w.w));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(~0u, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(~0u, hi, o));
+    lo2 = min_nan2(lo2, __shfl_xor_sync(~0u, lo2, o));
+    hi2 = max_nan2(hi2, __shfl_xor_sync(~0u, hi2, o));
   }
-  const float raw = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
-  const __nv_bfloat16 sb = __float2bfloat16_rn(raw);
+  const float lo = bf16_lo(min_nan2(lo2, lo2 >> 16)), hi = bf16_lo(max_nan2(hi2, hi2 >> 16));
+  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
   const float step = __bfloat162float(sb);
+  const Row8 r = widen(w);
   Coded c;
   c.finite = fabsf(lo) < kLargest && fabsf(hi) < kLargest;  // false for NaN
-  c.word = 0;
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = 0.f;
   if (step > 0.f) {
-    // The quotient by a product with the reciprocal is within 2^-20 of the rounded quotient, so
-    // it rounds to the same code unless it lies near a half: then, and for steps whose
-    // reciprocal is no normal number, the quotient itself decides.
+    // The product with the reciprocal is within 2^-20 of the rounded quotient, so it rounds to the
+    // same code (at most 15) unless it lies near a half: then, and for steps whose reciprocal is
+    // no normal number, the quotient itself decides.  2^23 is added and taken off to round.
     const float inv = __frcp_rn(step);
-    float q[8];
     bool close = step < 1e-35f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float y = __fsub_rn(r.x[e], lo) * inv;
-      q[e] = rintf(y);
-      close |= fabsf(y - q[e]) > 0.4999f;
+      const float y = __fmul_rn(__fsub_rn(r.x[e], lo), inv);
+      q[e] = __fsub_rn(__fadd_rn(y, 8388608.f), 8388608.f);
+      close |= fabsf(__fsub_rn(y, q[e])) > 0.49998f;
     }
     if (close) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = rintf(__fdiv_rn(__fsub_rn(r.x[e], lo), step));
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // 2^23 + code: the code is in the low bits
-      const float m = __fadd_rn(fminf(fmaxf(q[e], 0.f), 15.f), 8388608.f);
-      c.word |= (__float_as_uint(m) & 15u) << (4 * e);
+      for (int e = 0; e < 8; ++e)
+        q[e] = fminf(rintf(__fdiv_rn(__fsub_rn(r.x[e], lo), step)), 15.f);
     }
   }
+  // four codes as the low 16 bits of 2^23 + c0 + 16 c1 + 256 c2 + 4096 c3
+  uint32_t half[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float a = fmaf(q[4 * i + 1], 16.f, q[4 * i]);
+    const float b = fmaf(q[4 * i + 3], 16.f, q[4 * i + 2]);
+    half[i] = __float_as_uint(__fadd_rn(fmaf(b, 256.f, a), 8388608.f));
+  }
+  c.word = __byte_perm(half[0], half[1], 0x5410);
   const __nv_bfloat16 lb = __float2bfloat16_rn(lo);
   c.params = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(lb) << 16);
   return c;
@@ -231,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
     const int slot = live ? a.slots[t] : -1;
     const uint4 kw = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + 8 * li);
     const uint4 vw = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + 8 * li);
-    Coded k = code_row(widen(kw)), v = code_row(widen(vw));
+    Coded k = code_row(kw), v = code_row(vw);
     const bool good = (__ballot_sync(~0u, !(k.finite && v.finite)) & group_mask) == 0;
     if (!good) {  // queries that see the token read NaN, through its scores
       k.word = v.word = 0;
@@ -260,7 +271,7 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t params) {
   for (int e = 0; e < 8; ++e) {
     // the code as a float: 2^23 + code, less 2^23 (both exact)
     const float code = __fsub_rn(__uint_as_float(((w >> (4 * e)) & 15u) | 0x4b000000u), 8388608.f);
-    r.x[e] = __fadd_rn(__fmul_rn(step, code), lo);
+    r.x[e] = fmaf(step, code, lo);  // the product is exact: 8 bits by 4
   }
   return narrow(r);
 }
