@@ -377,19 +377,8 @@ class MoeLayer:
             pass
 
 
-def _stream_of(stream):
-    import torch
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-
-def _want(t, what, dtype, shape):
-    """Checks a tensor argument: on the GPU, of this type and shape (None: any size)."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(
-            n is not None and n != m for n, m in zip(shape, t.shape)) or not t.is_cuda:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: expected a CUDA {dtype} tensor of shape "
-                       f"{tuple('any' if n is None else n for n in shape)}, got {t.device.type} "
-                       f"{t.dtype} {tuple(t.shape)}")
-    return t
+def _refuse(status, what):
+    raise MoeError(status, what)
 
 
 class Kv4Cache:
@@ -414,6 +403,7 @@ class PagedAttention:
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
                  scale=0.0):
+        import torch
         self.handle = None
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self.page_size, self.n_pages, self.max_requests = page_size, n_pages, max_requests
@@ -421,124 +411,145 @@ class PagedAttention:
                           scale)
         st, self.handle = attn_create(cfg)
         _check(st, "attn_create")
+        self._lib = lib()
+        self._device = torch.cuda.current_device()
+        self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
+        self._torch = torch
+        # the current stream's handle without a Stream object (3 us a call), where torch has it
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
     def new_cache(self):
         return Kv4Cache(self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
 
-    def _rows(self, t, what, heads, tokens=None):
-        import torch
-        _want(t, what, torch.bfloat16, (tokens, heads, self.head_dim))
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim):
-            raise MoeError(MOE_ERR_UNSUPPORTED, f"{what}: a token's heads must be contiguous")
-        # with one token the stride says nothing
-        return t.stride(0) if t.shape[0] > 1 else heads * self.head_dim
+    def _stream(self, stream):
+        if stream is not None:
+            return stream.cuda_stream
+        if self._raw_stream is not None:
+            return self._raw_stream(self._device)
+        return self._torch.cuda.current_stream(self._device).cuda_stream
 
-    @staticmethod
-    def _ints(t, what, *shape):
-        import torch
-        _want(t, what, torch.int32, shape)
-        if not t.is_contiguous():
-            raise MoeError(MOE_ERR_UNSUPPORTED, f"{what}: must be contiguous")
+    def _rows(self, t, what, heads, tokens):
+        """(address, token stride) of bf16 rows [tokens][heads][head_dim]."""
+        D = self.head_dim
+        shape, stride = t.shape, t.stride()
+        if t.dtype is not self._bf16 or not t.is_cuda or shape != (tokens, heads, D):
+            _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected a CUDA bfloat16 tensor of shape "
+                    f"{(tokens, heads, D)}, got {t.device.type} {t.dtype} {tuple(shape)}")
+        if stride[2] != 1 or (heads > 1 and stride[1] != D):
+            _refuse(MOE_ERR_UNSUPPORTED, f"{what}: a token's heads must be contiguous")
+        # with one token the stride says nothing
+        return t.data_ptr(), stride[0] if tokens > 1 else heads * D
+
+    def _ints(self, t, what, n):
+        """Address of n contiguous int32 numbers."""
+        if (t.dtype is not self._i32 or not t.is_cuda or t.numel() != n
+                or not t.is_contiguous()):
+            _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {n} contiguous CUDA int32 numbers, "
+                    f"got {t.device.type} {t.dtype} {tuple(t.shape)}")
         return t.data_ptr()
+
+    def _new(self, shape, dtype):
+        return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self._device}")
 
     def plan(self, block_table, ctx_lens, new_lens, free_pages, cursor, q_offsets=None,
              kv_lens=None, positions=None, slots=None, cursor_out=None, T=None, stream=None):
         """Extends block_table for new_lens tokens after ctx_lens cached ones, taking pages from
         free_pages[cursor:]; returns (q_offsets, kv_lens, positions, slots, cursor_out).  Without
-        positions and slots, T gives their size."""
-        import torch
+        positions, T gives the capacity of positions and slots."""
         B, width = block_table.shape
-        like = dict(dtype=torch.int32, device=block_table.device)
+        i32 = self._i32
         if positions is not None:
-            T = positions.shape[0]
+            T = positions.numel()
         elif T is None:
-            raise MoeError(MOE_ERR_INVALID_ARG, "plan: positions or T")
+            _refuse(MOE_ERR_INVALID_ARG, "plan: positions or T")
         else:
-            positions = torch.empty(T, **like)
-        slots = torch.empty(T, **like) if slots is None else slots
-        q_offsets = torch.empty(B + 1, **like) if q_offsets is None else q_offsets
-        kv_lens = torch.empty(B, **like) if kv_lens is None else kv_lens
-        cursor_out = torch.empty(1, **like) if cursor_out is None else cursor_out
+            positions = self._new(T, i32)
+        slots = self._new(T, i32) if slots is None else slots
+        q_offsets = self._new(B + 1, i32) if q_offsets is None else q_offsets
+        kv_lens = self._new(B, i32) if kv_lens is None else kv_lens
+        cursor_out = self._new(1, i32) if cursor_out is None else cursor_out
         ints = self._ints
-        _check(lib().attn_plan(
-            self.handle, ints(block_table, "block_table", B, width), width,
+        n_free = free_pages.numel()
+        st = self._lib.attn_plan(
+            self.handle, ints(block_table, "block_table", B * width), width,
             ints(ctx_lens, "ctx_lens", B), ints(new_lens, "new_lens", B), B,
-            ints(free_pages, "free_pages", None), free_pages.shape[0],
-            ints(cursor, "cursor", 1), T, ints(q_offsets, "q_offsets", B + 1),
-            ints(kv_lens, "kv_lens", B), ints(positions, "positions", T),
-            ints(slots, "slots", T), ints(cursor_out, "cursor_out", 1), _stream_of(stream)),
-            "attn_plan")
+            ints(free_pages, "free_pages", n_free), n_free, ints(cursor, "cursor", 1), T,
+            ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B),
+            ints(positions, "positions", T), ints(slots, "slots", T),
+            ints(cursor_out, "cursor_out", 1), self._stream(stream))
+        if st:
+            _check(st, "attn_plan")
         return q_offsets, kv_lens, positions, slots, cursor_out
 
     def qk_norm_rope(self, q, k, positions, q_weight, k_weight, cos_sin, eps=1e-6,
                      interleaved=False, q_out=None, k_out=None, stream=None):
         """Norm of each query and key head and rotation by cos_sin [positions][rotary_dim] (None:
         no rotation); returns (q_out, k_out)."""
-        import torch
-        T = q.shape[0]
-        D = self.head_dim
-        qs, ks = self._rows(q, "q", self.n_q_heads), self._rows(k, "k", self.n_kv_heads, T)
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        qos = self._rows(q_out, "q_out", self.n_q_heads, T)
-        kos = self._rows(k_out, "k_out", self.n_kv_heads, T)
+        T, Hq, Hkv, D = q.shape[0], self.n_q_heads, self.n_kv_heads, self.head_dim
+        q_out = self._new((T, Hq, D), self._bf16) if q_out is None else q_out
+        k_out = self._new((T, Hkv, D), self._bf16) if k_out is None else k_out
+        rows = self._rows
+        (qp, qs), (kp, ks) = rows(q, "q", Hq, T), rows(k, "k", Hkv, T)
+        (qop, qos), (kop, kos) = rows(q_out, "q_out", Hq, T), rows(k_out, "k_out", Hkv, T)
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            _want(w, what, torch.bfloat16, (D,))
+            if w.dtype is not self._bf16 or not w.is_cuda or w.shape != (D,) or w.stride(0) != 1:
+                _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {D} contiguous CUDA bfloat16")
         n_pos = rot = 0
+        pos = table = None
         if cos_sin is not None:
-            n_pos, rot = _want(cos_sin, "cos_sin", torch.float32, (None, None)).shape
-            if not cos_sin.is_contiguous():
-                raise MoeError(MOE_ERR_UNSUPPORTED, "cos_sin: must be contiguous")
-        _check(lib().attn_qk_norm_rope(
-            self.handle, q.data_ptr(), qs, k.data_ptr(), ks,
-            None if rot == 0 else self._ints(positions, "positions", T), q_weight.data_ptr(),
-            k_weight.data_ptr(), eps, _ptr(cos_sin), n_pos, rot, int(interleaved), T,
-            q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream_of(stream)),
-            "attn_qk_norm_rope")
+            if (cos_sin.dtype is not self._f32 or not cos_sin.is_cuda or cos_sin.dim() != 2
+                    or not cos_sin.is_contiguous()):
+                _refuse(MOE_ERR_INVALID_ARG, "cos_sin: expected a contiguous CUDA float32 matrix")
+            n_pos, rot = cos_sin.shape
+            pos, table = self._ints(positions, "positions", T), cos_sin.data_ptr()
+        st = self._lib.attn_qk_norm_rope(
+            self.handle, qp, qs, kp, ks, pos, q_weight.data_ptr(), k_weight.data_ptr(), eps,
+            table, n_pos, rot, 1 if interleaved else 0, T, qop, qos, kop, kos,
+            self._stream(stream))
+        if st:
+            _check(st, "attn_qk_norm_rope")
         return q_out, k_out
 
     def append(self, k, v, slots, cache, stream=None):
         """Quantises keys and values [T][Hkv][D] into the cached rows of slots [T]."""
-        T = k.shape[0]
-        ks, vs = self._rows(k, "k", self.n_kv_heads), self._rows(v, "v", self.n_kv_heads, T)
-        _check(lib().attn_kv4_append(self.handle, k.data_ptr(), ks, v.data_ptr(), vs,
-                                     self._ints(slots, "slots", T), T, cache.ptr,
-                                     _stream_of(stream)), "attn_kv4_append")
+        T, Hkv = k.shape[0], self.n_kv_heads
+        (kp, ks), (vp, vs) = self._rows(k, "k", Hkv, T), self._rows(v, "v", Hkv, T)
+        st = self._lib.attn_kv4_append(self.handle, kp, ks, vp, vs,
+                                       self._ints(slots, "slots", T), T, cache.ptr,
+                                       self._stream(stream))
+        if st:
+            _check(st, "attn_kv4_append")
 
     def read(self, slots, cache, k_out=None, v_out=None, stream=None):
         """Cached rows of slots [T] as bf16; returns (k_out, v_out)."""
-        import torch
-        T = slots.shape[0]
-        shape = (T, self.n_kv_heads, self.head_dim)
-        like = dict(dtype=torch.bfloat16, device=slots.device)
-        k_out = torch.empty(shape, **like) if k_out is None else k_out
-        v_out = torch.empty(shape, **like) if v_out is None else v_out
-        ks = self._rows(k_out, "k_out", self.n_kv_heads, T)
-        vs = self._rows(v_out, "v_out", self.n_kv_heads, T)
-        _check(lib().attn_kv4_read(self.handle, cache.ptr, self._ints(slots, "slots", T), T,
-                                   k_out.data_ptr(), ks, v_out.data_ptr(), vs,
-                                   _stream_of(stream)), "attn_kv4_read")
+        T, Hkv = slots.shape[0], self.n_kv_heads
+        k_out = self._new((T, Hkv, self.head_dim), self._bf16) if k_out is None else k_out
+        v_out = self._new((T, Hkv, self.head_dim), self._bf16) if v_out is None else v_out
+        (kp, ks), (vp, vs) = self._rows(k_out, "k_out", Hkv, T), self._rows(v_out, "v_out", Hkv, T)
+        st = self._lib.attn_kv4_read(self.handle, cache.ptr, self._ints(slots, "slots", T), T, kp,
+                                     ks, vp, vs, self._stream(stream))
+        if st:
+            _check(st, "attn_kv4_read")
         return k_out, v_out
 
     def forward(self, q, cache, block_table, q_offsets, kv_lens, max_q_len, max_kv_len, out=None,
                 stream=None):
         """Causal attention of the requests' new tokens over their cached rows; returns out."""
-        import torch
-        T = q.shape[0]
+        T, Hq = q.shape[0], self.n_q_heads
         B, width = block_table.shape
-        qs = self._rows(q, "q", self.n_q_heads)
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
-        os_ = self._rows(out, "out", self.n_q_heads, T)
+        out = self._new((T, Hq, self.head_dim), self._bf16) if out is None else out
+        (qp, qs), (op, os_) = self._rows(q, "q", Hq, T), self._rows(out, "out", Hq, T)
         ints = self._ints
-        _check(lib().attn_kv4_forward(
-            self.handle, q.data_ptr(), qs, cache.ptr,
-            ints(block_table, "block_table", B, width), width,
+        st = self._lib.attn_kv4_forward(
+            self.handle, qp, qs, cache.ptr, ints(block_table, "block_table", B * width), width,
             ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B), B, T, max_q_len,
-            max_kv_len, out.data_ptr(), os_, _stream_of(stream)), "attn_kv4_forward")
+            max_kv_len, op, os_, self._stream(stream))
+        if st:
+            _check(st, "attn_kv4_forward")
         return out
 
     def device_error(self, stream=None):
-        return attn_get_device_error(self.handle, _stream_of(stream))
+        return attn_get_device_error(self.handle, self._stream(stream))
 
     def close(self):
         if self.handle:
