@@ -60,8 +60,7 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kOpsK * kK;
   static constexpr int kOffRaw = kOffV + kOpsV * kK;
   static constexpr int kOffRawV = kOffRaw + kRaw * kRecs * kSideK;
-  static constexpr int kOffStage = kOffRawV + kRaw * kRecs * kSideV;  // 2 KB a softmax warp
-  static constexpr int kFirst = kOffStage + kSoftWarps * 2048;
+  static constexpr int kFirst = kOffRawV + kRaw * kRecs * kSideV;
   static constexpr int kSmem = kFirst + 1024;  // the operands start on a 1024-byte boundary
   // tensor memory columns: O, the score buffers
   static constexpr int kColS = D;
@@ -114,13 +113,12 @@ __device__ __forceinline__ void wait_ld32(uint32_t* r) {
                  "+r"(r[30]), "+r"(r[31]));
 }
 
-// 32 lanes x 8 columns
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr));
+// 16 lanes x 8 columns: thread (n, c) = (i / 4, i % 4) of the warp gets columns 2c, 2c + 1 of lane n (r[0],
+// r[1]) and of lane n + 8 (r[2], r[3]).
+__device__ __forceinline__ void tmem_ld_16x8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
 }
 
 // 32 lanes x 32 columns
@@ -215,7 +213,7 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
     while (rt + 1 < rts && c.before(rt + 1) <= w - at) ++rt;
     p.rt = rt;
     const int last = min((rt + 1) * kRows, p.r.qn * a.d.G) - 1;
-    p.tiles = max(1, (seen_by(p.r, last / a.d.G) + kStep - 1) / kStep);
+    p.tiles = (seen_by(p.r, last / a.d.G) + kStep - 1) / kStep;
     const int64_t end = at + c.before(rt + 1);
     p.unit = kStep * a.d.G;
     p.start = at + c.before(rt) + c.fixed;
@@ -225,11 +223,10 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
     p.t1 = stop <= p.start
                ? 0
                : (int)min((int64_t)p.tiles, divide(stop - p.start + p.unit - 1, p.unit));
+    // a row tile that sees nothing is one part without steps
+    p.some = p.t1 > p.t0 || (p.tiles == 0 && w <= p.start && p.start < stop);
     w = p.next = stop;
-    if (p.t1 > p.t0) {
-      p.some = true;
-      break;
-    }
+    if (p.some) break;
   }
   return p;
 }
@@ -243,7 +240,7 @@ struct Bars {
   uint64_t raw_full[2][C::kRaw], raw_empty[2][C::kRaw];  // [keys, values]
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[kS], p_full[kS], pv_done[kS];
-  uint64_t q_full, o_free;
+  uint64_t q_full, q_free, o_free;
 };
 
 // Moves the warpgroup's threads to n registers.
@@ -413,31 +410,43 @@ __device__ __forceinline__ int out_column(int g, int k) {
 
 // ------------------------------------------------------------------- the kernel
 
-// Writes 16-byte pieces 0 .. 7 of the lane's row to dst(row) + 16 piece in runs of 64 bytes, through 2 KB
-// of the warp's shared memory (pieces swizzled by the row).  dst returns NULL for rows that are
-// not written.
-template <typename F>
-__device__ __forceinline__ void store_pieces(uint32_t stage, const uint4 (&v)[8], F dst) {
-  const int lane = threadIdx.x & 31;
+// One warp stages query rows row0 .. row0 + 7 of the part as f16 in [2^13, 2^14) at their top, in the
+// operands' channel order and the swizzle of the MMA's A operand: D / 8 lanes a row, 16-byte pieces.
+template <int D>
+__device__ __forceinline__ void stage_queries(const FwdArgs& a, const Part& p, uint32_t dst, int row0,
+                                              int8_t* exps) {
+  constexpr int kL = D / 8, kPer = 32 / kL;  // lanes a row, rows at a time
+  const int lane = threadIdx.x & 31, g = (lane % kL) >> 3, j = lane & 7;
+  // addresses of the eight rows, a lane each
+  const int row = p.rt * kRows + row0 + (lane & 7);
+  const uint64_t own =
+      row < p.r.qn * a.d.G
+          ? (uint64_t)(a.q + (int64_t)(p.r.q0 + row / a.d.G) * a.q_stride +
+                       (int64_t)(p.h * a.d.G + row % a.d.G) * D)
+          : 0;
+  uint4 w[8 / kPer];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int i = 0; i < 8 / kPer; ++i) {
+    const uint64_t src = __shfl_sync(~0u, own, i * kPer + lane / kL);
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (src) w[i] = reinterpret_cast<const uint4*>(src)[lane % kL];
+  }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4& x = v[4 * half + j];
-      sts128(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), x.x, x.y, x.z, x.w);
-    }
-    __syncwarp();
+  for (int i = 0; i < 8 / kPer; ++i) {
+    const int qr = row0 + i * kPer + lane / kL;
+    uint32_t top = max_u16x2(max_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                             max_u16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 8 * i + (lane >> 2), j = lane & 3;
-      uint4 x;
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                   : "r"(stage + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)));
-      uint8_t* p = dst(row);
-      if (p) *reinterpret_cast<uint4*>(p + 64 * half + 16 * j) = x;
-    }
-    __syncwarp();
+    for (int o = kL / 2; o; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(~0u, top, o));
+    top = max(top & 0xffffu, top >> 16);
+    const int e = min(max((int)(top >> 7) - 127, -100), 126);
+    const float down = pow2(-e) * 8192.f;
+    if (lane % kL == 0) exps[qr] = (int8_t)e;
+    sts128(dst + g * (kRows * 128) + qr * 128 + ((j ^ (qr & 7)) << 4),
+           pack_f16(bf16_lo(w[i].x) * down, bf16_lo(w[i].z) * down),
+           pack_f16(bf16_hi(w[i].x) * down, bf16_hi(w[i].z) * down),
+           pack_f16(bf16_lo(w[i].y) * down, bf16_lo(w[i].w) * down),
+           pack_f16(bf16_hi(w[i].y) * down, bf16_hi(w[i].w) * down));
   }
 }
 
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   __shared__ Exps exps[kExps][kRecs];
   __shared__ uint4 tables[kDeqWarps][4 * NG];
   __shared__ Part parts[kParts];
-  __shared__ float units[kRows];
+  __shared__ int8_t row_exp[kExps][kRows];  // of the queries of the last parts
   __shared__ __nv_bfloat16* rows[kRows];  // of the output
   __shared__ uint32_t tmem_base;
   __shared__ Cut cut_s;
@@ -479,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       mbar_init(&bars.p_full[i], 32 * kSoftWarps);
       mbar_init(&bars.pv_done[i], 1);
     }
-    mbar_init(&bars.q_full, 32 * kSoftWarps);
+    mbar_init(&bars.q_full, 2 * kDeqWarps);
+    mbar_init(&bars.q_free, 1);
     mbar_init(&bars.o_free, 32 * kSoftWarps);
     fence_mbar_init();
   }
@@ -568,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       drain(1);
     } else if (warp == kMmaWarp && lane == 0) {
       const uint32_t id_s = idesc_f16(kRows, kStep), id_o = idesc_f16(kRows, D);
-      // scores of step k
-      auto scores = [&](int k) {
+      // scores of step k; after a part's last ones its queries may be replaced
+      auto scores = [&](int k, bool last) {
         if (!mbar_wait(&bars.k_full[k % C::kOpsK], (k / C::kOpsK) & 1, a.err)) return false;
         // the buffer's weights of step k - kS have been used
         if (k >= kS && !mbar_wait(&bars.pv_done[k % kS], ((k - kS) / kS) & 1, a.err)) return false;
@@ -582,24 +592,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
                    sdesc_k128(kb + (i / 4) * (kStep * 128) + (i % 4) * 32), id_s, i > 0);
         mma_commit(&bars.k_empty[k % C::kOpsK]);
         mma_commit(&bars.s_full[k % kS]);
+        if (last) mma_commit(&bars.q_free);
         return true;
       };
-      for (int k = 0; ok; ++k) {
+      for (int k = 0, kq = 0; ok; ++k) {  // kq: parts with steps
         ok = part_ready(k);
         if (!ok) break;
-        const Part& p = parts[k % kParts];
-        const bool some = p.some;
-        const int steps = p.t1 - p.t0;
+        const bool some = parts[k % kParts].some;
+        const int steps = parts[k % kParts].t1 - parts[k % kParts].t0;
         part_read(k);
         if (!some) break;
-        ok = mbar_wait(&bars.q_full, k & 1, a.err);
+        if (steps == 0) continue;
+        ok = mbar_wait(&bars.q_full, kq & 1, a.err);
         if (!ok) break;
         // two steps of scores ahead of the products
-        ok = scores(n) && (steps < 2 || scores(n + 1));
+        ok = scores(n, steps == 1) && (steps < 2 || scores(n + 1, steps == 2));
         for (int t = 0; t < steps && ok; ++t, ++n) {
           ok = mbar_wait(&bars.v_full[n % C::kOpsV], (n / C::kOpsV) & 1, a.err) &&
                mbar_wait(&bars.p_full[n % kS], (n / kS) & 1, a.err) &&
-               (t > 0 || k == 0 || mbar_wait(&bars.o_free, (k - 1) & 1, a.err));
+               (t > 0 || kq == 0 || mbar_wait(&bars.o_free, (kq - 1) & 1, a.err));
           if (!ok) break;
           tc_fence_after();
           const uint32_t vb = ops + C::kOffV + (n % C::kOpsV) * C::kK;
@@ -609,8 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
                         id_o, t > 0 || i > 0);
           mma_commit(&bars.v_empty[n % C::kOpsV]);
           mma_commit(&bars.pv_done[n % kS]);
-          if (t + 2 < steps) ok = scores(n + 2);
+          if (t + 2 < steps) ok = scores(n + 2, t + 3 == steps);
         }
+        ++kq;
       }
       // every MMA has ended before the tensor memory is given back
       if (n >= 1) mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err);
@@ -621,14 +633,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     const bool is_key = warp < kValueWarp;
     const int oct = warp - (is_key ? kKeyWarp : kValueWarp);
     Dequant<D> d;
-    for (int k = 0; ok; ++k) {
+    for (int k = 0, kq = 0; ok; ++k) {  // kq: parts with steps
       ok = __all_sync(~0u, part_ready(k));
       if (!ok) break;
-      const bool some = parts[k % kParts].some;
-      const int t0 = parts[k % kParts].t0, t1 = parts[k % kParts].t1, kv = parts[k % kParts].r.kv;
+      const Part p = parts[k % kParts];
       __syncwarp();
       if (lane == 0) part_read(k);
-      if (!some) break;
+      if (!p.some) break;
+      if (p.t0 == p.t1) continue;
+      if (kq > 0) ok = __all_sync(~0u, mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
+      if (!ok) break;
+      stage_queries<D>(a, p, ops, 8 * (warp - kKeyWarp), row_exp[kq % kExps]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_full);
+      ++kq;
+      const int t0 = p.t0, t1 = p.t1, kv = p.r.kv;
       for (int t = t0; t < t1; ++t, ++n) {
         const int st = n % C::kRaw;
         const int which = is_key ? 0 : 1;
@@ -660,8 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     registers_up<kRegsSoft>();
     // softmax: row `tid` of the row tile, tensor memory lane tid
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t stage = ops + C::kOffStage + warp * 2048;
-    for (int k = 0; ok; ++k) {
+    for (int k = 0, kq = 0; ok; ++k) {  // kq: parts with steps
       ok = __all_sync(~0u, part_ready(k));
       if (!ok) break;
       const Part p = parts[k % kParts];
@@ -675,57 +694,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       rows[tid] = on ? a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
                            (int64_t)(p.h * a.d.G + row % a.d.G) * D
                      : nullptr;
-      // The warp's query rows as f16 in [2^13, 2^14) at their top, in the operands' channel order:
-      // D / 8 lanes a row, 16-byte pieces, in the swizzle of the MMA's A operand.
-      {
-        constexpr int kL = D / 8, kPer = 32 / kL;  // lanes a row, rows at a time
-        constexpr int kRound = 32 / kPer < 16 ? 32 / kPer : 16;
-        // the lane's own row; the others' by shuffles
-        const uint64_t own = on ? (uint64_t)(a.q + (int64_t)(p.r.q0 + tok) * a.q_stride +
-                                             (int64_t)(p.h * a.d.G + row % a.d.G) * D)
-                                : 0;
-        const int g = (lane % kL) >> 3, j = lane & 7;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32 / kPer; i0 += kRound) {
-          uint4 w[kRound];
-#pragma unroll
-          for (int i = 0; i < kRound; ++i) {
-            const uint64_t src = __shfl_sync(~0u, own, (i0 + i) * kPer + lane / kL);
-            w[i] = make_uint4(0, 0, 0, 0);
-            if (src) w[i] = reinterpret_cast<const uint4*>(src)[lane % kL];
-          }
-#pragma unroll
-          for (int i = 0; i < kRound; ++i) {
-            const int rr = (i0 + i) * kPer + lane / kL;  // of the warp's rows
-            uint32_t top = max_u16x2(max_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                    max_u16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-#pragma unroll
-            for (int o = kL / 2; o; o >>= 1)
-              top = max_u16x2(top, __shfl_xor_sync(~0u, top, o));
-            top = max(top & 0xffffu, top >> 16);
-            const int e = min(max((int)(top >> 7) - 127, -100), 126);
-            const float down = pow2(-e) * 8192.f;
-            if (lane % kL == 0) units[warp * 32 + rr] = pow2(e) * (64.f / 8192.f) * a.d.scale_log2;
-            const int qr = warp * 32 + rr;
-            sts128(ops + g * (kRows * 128) + qr * 128 + ((j ^ (qr & 7)) << 4),
-                   pack_f16(bf16_lo(w[i].x) * down, bf16_lo(w[i].z) * down),
-                   pack_f16(bf16_hi(w[i].x) * down, bf16_hi(w[i].z) * down),
-                   pack_f16(bf16_lo(w[i].y) * down, bf16_lo(w[i].w) * down),
-                   pack_f16(bf16_hi(w[i].y) * down, bf16_hi(w[i].w) * down));
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        mbar_arrive(&bars.q_full);
-      }
-      const float unit = units[tid];
       const int lim = on ? seen_by(p.r, tok) : p.r.kv;
       const int least = seen_by(p.r, p.rt * kRows / a.d.G);
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, unit = 0.f;
       for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
         ok = __all_sync(~0u, mbar_wait(&bars.s_full[n % kS], (n / kS) & 1, a.err));
         if (!ok) break;
         tc_fence_after();
+        if (t == p.t0)  // back from the scaled queries' units to log2 units
+          unit = pow2(row_exp[kq % kExps][tid]) * (64.f / 8192.f) * a.d.scale_log2;
         const uint32_t sb = lane_base + C::kColS + (n % kS) * kStep;
         uint32_t s[kStep];
         tmem_ld32(sb, s);
@@ -795,6 +772,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         mbar_arrive(&bars.p_full[n % kS]);
       }
       if (!ok) break;
+      if (p.tiles == 0) {  // rows that see nothing
+        __syncwarp();
+        for (int i = lane; i < 32 * (D / 8); i += 32) {
+          __nv_bfloat16* d = rows[warp * 32 + i / (D / 8)];
+          if (d) *reinterpret_cast<uint4*>(d + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+        continue;
+      }
+      ++kq;
       // outputs: after the last product
       ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err));
       if (!ok) break;
@@ -802,47 +789,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const bool whole = p.t1 - p.t0 == p.tiles;
       const float inv = whole ? (l == 0.f ? 0.f : 64.f / l) : 64.f;
       const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows + warp * 32;
+      __syncwarp();
 #pragma unroll 1
-      for (int g = 0; g < NG; ++g) {
-        uint32_t o[8][8];  // [nibble][word]
-#pragma unroll
-        for (int i = 0; i < 8; ++i) tmem_ld8(lane_base + out_column<NG>(g, i), o[i]);
-        wait_ld32(&o[0][0]);
-        wait_ld32(&o[4][0]);
-        if (g == NG - 1) {
-          tc_fence_before();
-          mbar_arrive(&bars.o_free);
-        }
-        uint4 v[8];
+      for (int hf = 0; hf < 2; ++hf) {  // rows 16 hf .. 16 hf + 15 of the warp
+        const int c = lane & 3, ra = 16 * hf + (lane >> 2), rb = ra + 8;
+        const float inv_a = __shfl_sync(~0u, inv, ra), inv_b = __shfl_sync(~0u, inv, rb);
+        uint8_t *da, *db;
         if (whole) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 y =
-                  __floats2bfloat162_rn(__uint_as_float(o[2 * i][j]) * inv,
-                                        __uint_as_float(o[2 * i + 1][j]) * inv);
-              x[i] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            v[j] = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-          store_pieces(stage, v, [&](int rr) {
-            __nv_bfloat16* d = rows[warp * 32 + rr];
-            return reinterpret_cast<uint8_t*>(d ? d + 64 * g : nullptr);
-          });
+          da = reinterpret_cast<uint8_t*>(rows[warp * 32 + ra]);
+          db = reinterpret_cast<uint8_t*>(rows[warp * 32 + rb]);
         } else {
+          da = reinterpret_cast<uint8_t*>(a.part_o + (at + ra) * D);
+          db = reinterpret_cast<uint8_t*>(a.part_o + (at + rb) * D);
+        }
+#pragma unroll 1
+        for (int g = 0; g < NG; ++g) {
+          // [nibble][row a words 2c, 2c + 1; row b words 2c, 2c + 1]
+          uint32_t o[8][4];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+          for (int i = 0; i < 8; ++i)
+            tmem_ld_16x8(lane_base + ((uint32_t)(16 * hf) << 16) + out_column<NG>(g, i), o[i]);
+          wait_ld32(&o[0][0]);
+          if (hf == 1 && g == NG - 1) {
+            tc_fence_before();
+            mbar_arrive(&bars.o_free);
+          }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              v[j] = make_uint4(__float_as_uint(__uint_as_float(o[4 * hf][j]) * inv),
-                                __float_as_uint(__uint_as_float(o[4 * hf + 1][j]) * inv),
-                                __float_as_uint(__uint_as_float(o[4 * hf + 2][j]) * inv),
-                                __float_as_uint(__uint_as_float(o[4 * hf + 3][j]) * inv));
-            store_pieces(stage, v, [&](int rr) {
-              return reinterpret_cast<uint8_t*>(a.part_o + (at + rr) * D + 64 * g + 32 * hf);
-            });
+          for (int q = 0; q < 4; ++q) {
+            const float f = q < 2 ? inv_a : inv_b;
+            uint8_t* d = q < 2 ? da : db;
+            const int j = 2 * c + (q & 1);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[i][q]) * f;
+            if (whole) {
+              uint32_t x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                x[i] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              if (d)
+                *reinterpret_cast<uint4*>(d + 128 * g + 16 * j) = make_uint4(x[0], x[1], x[2], x[3]);
+            } else {
+              float4* part = reinterpret_cast<float4*>(d) + 16 * g + j;
+              part[0] = make_float4(v[0], v[1], v[2], v[3]);
+              part[8] = make_float4(v[4], v[5], v[6], v[7]);
+            }
           }
         }
       }
