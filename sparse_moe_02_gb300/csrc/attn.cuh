@@ -142,8 +142,8 @@ struct RowsArgs {
 cudaError_t launch_attn_append(const RowsArgs& a, int D, cudaStream_t s);
 cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s);
 
-// Attention of few query rows per key/value head and request (n_b G <= 16): attn_decode.cu.
-constexpr int kDecodeRows = 16;
+// Attention of few query rows per key/value head and request (n_b G <= 32): attn_decode.cu.
+constexpr int kDecodeRows = 32;
 cudaError_t prepare_attn_decode_kernels(int max_requests);
 int attn_decode_slots(int sms);         // partial results of a launch
 size_t attn_decode_part_floats(int D);  // fp32 of one partial result

@@ -148,29 +148,6 @@ __device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1)
 constexpr int kPartCost = 40;
 constexpr int kLeastWork = 32;  // of a block
 
-// Fills first[b], b = 0 .. B: the work before request b.  One warp.
-__device__ __forceinline__ Cut cut_contexts(const FwdArgs& a, int cols, int64_t* first) {
-  const int lane = threadIdx.x & 31;
-  int64_t total = 0;
-#pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int64_t n = 0;
-    if (b < a.B) {
-      const Req r = load_req(a, b);
-      if (blockIdx.x == 0 && req_out_of_range(a, b)) record_error(a.err, kDevErrState);
-      if (r.qn > 0)
-        n = (int64_t)(a.d.Hkv * row_tiles(a, r.qn, cols)) * (kv_tiles(r.kv) + kPartCost);
-    }
-    const int64_t end = warp_scan(n);
-    if (b < a.B) first[b] = total + end - n;
-    total += __shfl_sync(~0u, end, 31);
-  }
-  if (lane == 0) first[a.B] = total;
-  __syncwarp();
-  return make_cut(total, kLeastWork, gridDim.x);
-}
-
 // What a lane keeps of the query rows (columns) of one context; their MMA B fragments lie in
 // shared memory, [column tile][group][word][lane] registers of two MMAs, for all warps.
 template <int NT>
@@ -515,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   __shared__ float join_f[C::kCols][kWarps];                  // the warps' weights
   __shared__ float join_b[C::kCols][NG][kWarps], join_bias[C::kCols][NG];  // bias parts
   __shared__ Part parts[2];
+  __shared__ int64_t sums[kWarps];
   __shared__ Cut cut_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int j = lane >> 2, c = lane & 3;
@@ -529,8 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   pdl_trigger();
 
   int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);  // [B + 1]
-  int64_t w1 = 0;  // end of the block's work
-  if (warp == 0) {
+  if (!WHOLE) {
+    const Cut cut = cut_work<kThreads>(a, first, sums, kLeastWork, [&](const Req& r) {
+      return r.qn > 0 ? (int64_t)(a.d.Hkv * row_tiles(a, r.qn, C::kCols)) *
+                            (kv_tiles(r.kv) + kPartCost)
+                      : (int64_t)0;
+    });
+    if (tid == 0) cut_s = cut;
+  }
+  if (tid == 0) {
     Part p;
     p.some = false;
     if (WHOLE) {
@@ -543,19 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
       p.t0 = 0;
       p.t1 = p.tiles = kv_tiles(p.r.kv);
       p.some = p.rt < row_tiles(a, p.r.qn, C::kCols);
-      if (lane == 0 && k == 0 && req_out_of_range(a, p.b)) record_error(a.err, kDevErrState);
-    } else {
-      const Cut cut = cut_contexts(a, C::kCols, first);
-      if ((int)blockIdx.x < cut.blocks)
-        p = locate(a, first, C::kCols, cut.bound(blockIdx.x), cut.bound(blockIdx.x + 1));
-      if (lane == 0) cut_s = cut;
+      if (k == 0 && req_out_of_range(a, p.b)) record_error(a.err, kDevErrState);
+    } else if ((int)blockIdx.x < cut_s.blocks) {
+      p = locate(a, first, C::kCols, cut_s.bound(blockIdx.x), cut_s.bound(blockIdx.x + 1));
     }
-    if (lane == 0) parts[0] = p;
+    parts[0] = p;
   }
   __syncthreads();
   if (!WHOLE && tid == 0) a.desc[2 * blockIdx.x].x = 0;
   if (!parts[0].some) return;
-  if (!WHOLE) w1 = cut_s.bound(blockIdx.x + 1);
   fetch_query<D, NT>(a, parts[0], smem + C::kQuery);
 
   // the warp's tiles of a part: t0 + warp, + kWarps, ... below the end of the context
@@ -593,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
                            warp % NG, S);
     if (tid == kThreads - 1) {
       if (WHOLE) next.some = false;
-      else next = locate(a, first, C::kCols, p.next, w1);
+      else next = locate(a, first, C::kCols, p.next, cut_s.bound(blockIdx.x + 1));
     }
     __syncthreads();
     Query<NT> Q;

@@ -50,6 +50,41 @@ __device__ __forceinline__ Cut make_cut(int64_t total, int64_t least, int blocks
   return c;
 }
 
+// Fills first[b], b = 0 .. B, with the work before request b (work(b) of each) and returns the cut of
+// all work into shares of `least` at least.  Whole block; `sums` holds a value per warp.
+template <int kThreads, typename F>
+__device__ __forceinline__ Cut cut_work(const FwdArgs& a, int64_t* first, int64_t* sums,
+                                        int64_t least, F work) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t total = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t n = 0;
+    if (b0 + (int)(threadIdx.x & ~31u) < a.B) {  // warps behind the last request have nothing
+      if (b < a.B) {
+        const Req r = load_req(a, b);
+        if (blockIdx.x == 0 && req_out_of_range(a, b)) record_error(a.err, kDevErrState);
+        n = work(r);
+      }
+    }
+    const int64_t end = warp_scan(n);
+    if (lane == 31) sums[warp] = end;
+    __syncthreads();
+    int64_t before = total;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int64_t x = sums[w];
+      if (w < warp) before += x;
+      total += x;
+    }
+    if (b < a.B) first[b] = before + end - n;
+    if (b == a.B - 1) first[a.B] = total;
+    __syncthreads();
+  }
+  return make_cut(total, least, gridDim.x);
+}
+
 // The request whose work holds unit w: first[b] <= w < first[b + 1].
 __device__ __forceinline__ int find_request(const int64_t* first, int B, int64_t w) {
   int lo = 0, hi = B;

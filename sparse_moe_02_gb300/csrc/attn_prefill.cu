@@ -146,19 +146,23 @@ constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 
 // Work is counted in (cached token x query head) units, 128 per row tile and token position: row
 // tile rt of a request with `base` cached tokens before its new ones costs kPartCost G + base G +
-// 128 (rt + 1) units, and its step t starts at unit (kPartCost + 64 t) G of them.
-constexpr int kPartCost = 384;   // tokens: a row tile's fixed cost
+// 128 (rt + 1) units, and its step t starts at unit (kPartCost + 64 t) G of them.  Row tiles of a
+// request without cached tokens, whose rows are only zeroed, cost kZeroCost G each.
+constexpr int kPartCost = 320;   // tokens: a row tile's fixed cost
+constexpr int kZeroCost = 96;
 constexpr int kLeastSteps = 4;   // of a block
 
 struct Cost {
   int64_t fixed, base;  // per row tile, in units
+  int grow;             // 64: the work of half a row tile more for each
   __device__ __forceinline__ int64_t before(int64_t rt) const {
-    return rt * (fixed + base) + 64 * rt * (rt + 1);
+    return rt * (fixed + base) + grow * rt * (rt + 1);
   }
 };
 
 __device__ __forceinline__ Cost cost_of(const FwdArgs& a, const Req& r) {
-  return Cost{(int64_t)kPartCost * a.d.G, (int64_t)max(r.kv - r.qn, 0) * a.d.G};
+  if (r.kv == 0) return Cost{(int64_t)kZeroCost * a.d.G, 0, 0};
+  return Cost{(int64_t)kPartCost * a.d.G, (int64_t)max(r.kv - r.qn, 0) * a.d.G, 64};
 }
 
 __device__ __forceinline__ int row_tiles(const FwdArgs& a, const Req& r) {
@@ -168,28 +172,6 @@ __device__ __forceinline__ int row_tiles(const FwdArgs& a, const Req& r) {
 // Cached tokens that new token `tok` of the request sees.
 __device__ __forceinline__ int seen_by(const Req& r, int tok) {
   return min(max(r.kv - r.qn + tok + 1, 0), r.kv);
-}
-
-// Fills first[b], b = 0 .. B: the work before request b.  One warp.
-__device__ __forceinline__ Cut cut_rows(const FwdArgs& a, int64_t* first) {
-  const int lane = threadIdx.x & 31;
-  int64_t total = 0;
-#pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int64_t n = 0;
-    if (b < a.B) {
-      const Req r = load_req(a, b);
-      if (blockIdx.x == 0 && req_out_of_range(a, b)) record_error(a.err, kDevErrState);
-      n = a.d.Hkv * cost_of(a, r).before(row_tiles(a, r));
-    }
-    const int64_t end = warp_scan(n);
-    if (b < a.B) first[b] = total + end - n;
-    total += __shfl_sync(~0u, end, 31);
-  }
-  if (lane == 0) first[a.B] = total;
-  __syncwarp();
-  return make_cut(total, (int64_t)kLeastSteps * kStep * a.d.G, gridDim.x);
 }
 
 // The part that holds work w of the block's [w, w1).
@@ -205,12 +187,17 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
     const int64_t head = c.before(rts);
     p.h = (int)divide(w - first[p.b], head);
     const int64_t at = first[p.b] + p.h * head;
-    // 64 rt^2 + (fixed + base + 64) rt = w - at
-    const double q = (double)(c.fixed + c.base + 64);
-    int rt = (int)((sqrt(q * q + 256.0 * (double)(w - at)) - q) / 128.0);
-    rt = min(max(rt, 0), rts - 1);
-    while (rt > 0 && c.before(rt) > w - at) --rt;
-    while (rt + 1 < rts && c.before(rt + 1) <= w - at) ++rt;
+    int rt;
+    if (c.grow) {
+      // 64 rt^2 + (fixed + base + 64) rt = w - at, then the exact tile beside the rounded root
+      const float q = (float)(c.fixed + c.base + 64), x = (float)(w - at);
+      rt = (int)(2.f * x / (q + sqrtf(fmaf(q, q, 256.f * x))));
+      rt = min(max(rt, 0), rts - 1);
+      while (rt > 0 && c.before(rt) > w - at) --rt;
+      while (rt + 1 < rts && c.before(rt + 1) <= w - at) ++rt;
+    } else {
+      rt = (int)divide(w - at, c.fixed);
+    }
     p.rt = rt;
     const int last = min((rt + 1) * kRows, p.r.qn * a.d.G) - 1;
     p.tiles = (seen_by(p.r, last / a.d.G) + kStep - 1) / kStep;
@@ -223,8 +210,8 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
     p.t1 = stop <= p.start
                ? 0
                : (int)min((int64_t)p.tiles, divide(stop - p.start + p.unit - 1, p.unit));
-    // a row tile that sees nothing is one part without steps
-    p.some = p.t1 > p.t0 || (p.tiles == 0 && w <= p.start && p.start < stop);
+    // a row tile that sees nothing is one part without steps, where its work begins
+    p.some = p.t1 > p.t0 || (p.tiles == 0 && w <= at + c.before(rt));
     w = p.next = stop;
     if (p.some) break;
   }
@@ -462,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   __shared__ int8_t row_exp[kExps][kRows];  // of the queries of the last parts
   __shared__ __nv_bfloat16* rows[kRows];  // of the output
   __shared__ uint32_t tmem_base;
+  __shared__ int64_t sums[kThreads / 32];
   __shared__ Cut cut_s;
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -496,6 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   if (warp == kMmaWarp) tmem_alloc(&tmem_base, C::kCols);
   pdl_wait();
   pdl_trigger();
+  int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
+  {
+    const Cut cut =
+        cut_work<kThreads>(a, first, sums, (int64_t)kLeastSteps * kStep * a.d.G, [&](const Req& r) {
+          return a.d.Hkv * cost_of(a, r).before(row_tiles(a, r));
+        });
+    if (tid == 0) {
+      cut_s = cut;
+      a.desc[2 * blockIdx.x].x = 0;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -543,14 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         mbar_wait(&bars.raw_full[which][k % C::kRaw], (k / C::kRaw) & 1, a.err);
     };
     if (warp == kLoadWarp) {
-      int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
-      const Cut cut = cut_rows(a, first);
-      if (lane == 0) {
-        cut_s = cut;
-        a.desc[2 * blockIdx.x].x = 0;
-      }
       int64_t w = 0, w1 = 0;
-      if ((int)blockIdx.x < cut.blocks) w = cut.bound(blockIdx.x), w1 = cut.bound(blockIdx.x + 1);
+      if ((int)blockIdx.x < cut_s.blocks)
+        w = cut_s.bound(blockIdx.x), w1 = cut_s.bound(blockIdx.x + 1);
       for (int k = 0; ok; ++k) {
         const Part p = locate(a, first, w, w1);
         ok = mbar_wait(&bars.part_empty[k % kParts], ((k / kParts) & 1) ^ 1, a.err);
