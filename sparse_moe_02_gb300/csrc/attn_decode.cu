@@ -37,7 +37,7 @@ constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens per ring stage: the MMA's M side, and a whole number per page
 // One block per context, no partial results, up to this many tokens.
-constexpr int kWholeKv = 512;
+constexpr int kWholeKv = 768;
 constexpr float kSlack = 6.f;  // growth of the reference a tile may bring before a rescale
 constexpr float kLift = 9.f;   // w <= 2^(kLift + kSlack) at the reference
 constexpr int kJoinWarps = 4;  // warps whose outputs the join buffer holds at once
@@ -146,7 +146,7 @@ __device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1)
 // Work of a context: its tiles, and kPartCost tiles' worth for what a part costs besides (queries,
 // page ids, first copies, joins), so that blocks of many short contexts get fewer tiles.
 constexpr int kPartCost = 40;
-constexpr int kLeastWork = 32;  // of a block
+constexpr int kLeastWork = 12;  // of a block
 
 // What a lane keeps of the query rows (columns) of one context; their MMA B fragments lie in
 // shared memory, [column tile][group][word][lane] registers of two MMAs, for all warps.

@@ -9,9 +9,10 @@
 //   O [128 x D] += P V        A = P in tensor memory (over S), B = values [D][64] (channels by
 //                             tokens, so both operands are K-major)
 // S has four buffers: the scores of step n + 2 are queued behind the product of step n without
-// waiting for it, so the tensor core does not drain between steps.  An MMA
-// whose A operand lies in tensor memory takes about 146 clocks whatever its width (measured): right
-// for the 256 channels of O, but the 64 columns of S took 2300 clocks a step with Q there.
+// waiting for it, so the tensor core does not drain between steps.  One thread issues everything:
+// an MMA of 64 columns takes 49 clocks, of 128 columns 65, of 256 columns 129 (measured, either
+// place of A), so its operand descriptors are formed once and stepped by constants; forming each
+// anew took about 80 clocks an MMA and bound the kernel.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -572,18 +573,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       drain(1);
     } else if (warp == kMmaWarp && lane == 0) {
       const uint32_t id_s = idesc_f16(kRows, kStep), id_o = idesc_f16(kRows, D);
+      const uint64_t q_desc = sdesc_k128(ops), k_desc = sdesc_k128(ops + C::kOffK),
+                     v_desc = sdesc_k128(ops + C::kOffV);
       // scores of step k; after a part's last ones its queries may be replaced
       auto scores = [&](int k, bool last) {
         if (!mbar_wait(&bars.k_full[k % C::kOpsK], (k / C::kOpsK) & 1, a.err)) return false;
         // the buffer's weights of step k - kS have been used
         if (k >= kS && !mbar_wait(&bars.pv_done[k % kS], ((k - kS) / kS) & 1, a.err)) return false;
         tc_fence_after();
-        const uint32_t kb = ops + C::kOffK + (k % C::kOpsK) * C::kK;
+        const uint64_t kd = k_desc + (k % C::kOpsK) * (C::kK / 16);
+        const uint32_t d = tmem + C::kColS + (k % kS) * kStep;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_bf16(tmem + C::kColS + (k % kS) * kStep,
-                   sdesc_k128(ops + (i / 4) * (kRows * 128) + (i % 4) * 32),
-                   sdesc_k128(kb + (i / 4) * (kStep * 128) + (i % 4) * 32), id_s, i > 0);
+          mma_bf16(d, q_desc + ((i / 4) * (kRows * 8) + (i % 4) * 2),
+                   kd + ((i / 4) * (kStep * 8) + (i % 4) * 2), id_s, i > 0);
         mma_commit(&bars.k_empty[k % C::kOpsK]);
         mma_commit(&bars.s_full[k % kS]);
         if (last) mma_commit(&bars.q_free);
@@ -607,11 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
                (t > 0 || kq == 0 || mbar_wait(&bars.o_free, (kq - 1) & 1, a.err));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t vb = ops + C::kOffV + (n % C::kOpsV) * C::kK;
+          const uint64_t vd = v_desc + (n % C::kOpsV) * (C::kK / 16);
+          const uint32_t w = tmem + C::kColS + (n % kS) * kStep;
+          const uint32_t more = t > 0;
 #pragma unroll
           for (int i = 0; i < kStep / 16; ++i)
-            mma_bf16_ts(tmem, tmem + C::kColS + (n % kS) * kStep + 8 * i, sdesc_k128(vb + i * 32),
-                        id_o, t > 0 || i > 0);
+            mma_bf16_ts(tmem, w + 8 * i, vd + 2 * i, id_o, i > 0 ? 1u : more);
           mma_commit(&bars.v_empty[n % C::kOpsV]);
           mma_commit(&bars.pv_done[n % kS]);
           if (t + 2 < steps) ok = scores(n + 2, t + 3 == steps);
