@@ -5,14 +5,14 @@
 // of 64 cached tokens.  Four warps hold the softmax (a thread per row), eight turn cached keys and
 // eight cached values into f16 MMA operands, one issues the MMAs, one finds the work and copies
 // cache records.
-//   S [128 x 64] = Q K^T      A = Q, B = keys [64][D], both in shared memory
+//   S [128 x 64] = Q K^T      A = Q in tensor memory, B = keys [64][D] in shared memory
 //   O [128 x D] += P V        A = P in tensor memory (over S), B = values [D][64] (channels by
 //                             tokens, so both operands are K-major)
-// S has four buffers: the scores of step n + 2 are queued behind the product of step n without
-// waiting for it, so the tensor core does not drain between steps.  One thread issues everything:
-// an MMA of 64 columns takes 49 clocks, of 128 columns 65, of 256 columns 129 (measured, either
-// place of A), so its operand descriptors are formed once and stepped by constants; forming each
-// anew took about 80 clocks an MMA and bound the kernel.
+// Scores run ahead: those of step n + 2 are queued behind the product of step n.  With 256 channels
+// a step of 64 tokens takes 1300 clocks of MMAs (64 columns: 49 clocks each, 256 columns: 129,
+// measured alone) and moves 168 KB through shared memory (operands written and read, records), which
+// is its tightest resource; Q in shared memory would add 64 KB.  One thread issues the MMAs, from
+// descriptors that are formed once and stepped by constants: forming each anew took 80 clocks.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -44,27 +44,30 @@ constexpr int kRegsSoft = 168, kRegsDeq = 64, kRegsRest = 56;
 static_assert(kRegsSoft + 4 * kRegsDeq + kRegsRest == 6 * 80, "the launch's registers");
 constexpr int kParts = 4;            // parts announced ahead
 constexpr float kSlack = 6.f, kLift = 9.f;  // as in the few-row kernel
-constexpr int kS = 4;                // score buffers
 constexpr int kExps = 8;             // steps of record exponents kept
 
 template <int D>
 struct Cfg {
   using R = Record<D>;
   static constexpr int NG = D / kGroup;
-  // steps of key operands and value operands, and of the records' key and value sides, held
-  static constexpr int kOpsK = 2, kOpsV = D == 256 ? 1 : 2, kRaw = D == 256 ? 2 : 4;
+  // steps of key operands, value operands, and the records' key and value sides held
+  static constexpr int kOpsK = 2, kOpsV = 2, kRawK = D == 256 ? 3 : 4, kRawV = D == 256 ? 2 : 4;
+  static constexpr int kS = D == 256 ? 2 : 4;  // score buffers: what tensor memory holds
   // A record's key side (with the parameters of its values: the softmax needs their exponents with
   // the scores) and its value side.
   static constexpr int kSideK = R::kV, kSideV = R::kBytes - R::kVp;
   static constexpr int kK = kStep * D * 2;  // bytes of a key (or value) operand
-  static constexpr int kOffK = kRows * D * 2;  // behind Q
+  // queries pass through shared memory two groups at a time
+  static constexpr int kQGroups = NG < 2 ? NG : 2, kQPasses = NG / kQGroups;
+  static constexpr int kOffK = kQGroups * kRows * 128;
   static constexpr int kOffV = kOffK + kOpsK * kK;
   static constexpr int kOffRaw = kOffV + kOpsV * kK;
-  static constexpr int kOffRawV = kOffRaw + kRaw * kRecs * kSideK;
-  static constexpr int kFirst = kOffRawV + kRaw * kRecs * kSideV;
+  static constexpr int kOffRawV = kOffRaw + kRawK * kRecs * kSideK;
+  static constexpr int kFirst = kOffRawV + kRawV * kRecs * kSideV;
   static constexpr int kSmem = kFirst + 1024;  // the operands start on a 1024-byte boundary
-  // tensor memory columns: O, the score buffers
-  static constexpr int kColS = D;
+  // tensor memory columns: O, Q, the score buffers
+  static constexpr int kColQ = D;
+  static constexpr int kColS = D + D / 2;
   static constexpr int kCols = 512;
 };
 
@@ -225,10 +228,10 @@ template <int D>
 struct Bars {
   using C = Cfg<D>;
   uint64_t part_full[kParts], part_empty[kParts];
-  uint64_t raw_full[2][C::kRaw], raw_empty[2][C::kRaw];  // [keys, values]
+  uint64_t raw_full[2][4], raw_empty[2][4];  // [keys, values]
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
-  uint64_t s_full[kS], p_full[kS], pv_done[kS];
-  uint64_t q_full, q_free, o_free;
+  uint64_t s_full[C::kS], p_full[C::kS], pv_done[C::kS];
+  uint64_t q_staged, q_copied, q_full, q_free, o_free;
 };
 
 // Moves the warpgroup's threads to n registers.
@@ -398,44 +401,75 @@ __device__ __forceinline__ int out_column(int g, int k) {
 
 // ------------------------------------------------------------------- the kernel
 
-// One warp stages query rows row0 .. row0 + 7 of the part as f16 in [2^13, 2^14) at their top, in the
-// operands' channel order and the swizzle of the MMA's A operand: D / 8 lanes a row, 16-byte pieces.
+// Query rows row0 .. row0 + 7 of a part as f16 in [2^13, 2^14) at their top, in the operands' channel
+// order: D / 8 lanes a row, 16-byte pieces, held by one warp.
 template <int D>
-__device__ __forceinline__ void stage_queries(const FwdArgs& a, const Part& p, uint32_t dst, int row0,
-                                              int8_t* exps) {
-  constexpr int kL = D / 8, kPer = 32 / kL;  // lanes a row, rows at a time
-  const int lane = threadIdx.x & 31, g = (lane % kL) >> 3, j = lane & 7;
-  // addresses of the eight rows, a lane each
-  const int row = p.rt * kRows + row0 + (lane & 7);
-  const uint64_t own =
-      row < p.r.qn * a.d.G
-          ? (uint64_t)(a.q + (int64_t)(p.r.q0 + row / a.d.G) * a.q_stride +
-                       (int64_t)(p.h * a.d.G + row % a.d.G) * D)
-          : 0;
+struct QueryRows {
+  static constexpr int kL = D / 8, kPer = 32 / kL;  // lanes a row, rows at a time
   uint4 w[8 / kPer];
+
+  __device__ __forceinline__ void load(const FwdArgs& a, const Part& p, int row0, int8_t* exps) {
+    const int lane = threadIdx.x & 31;
+    // addresses of the eight rows, a lane each
+    const int row = p.rt * kRows + row0 + (lane & 7);
+    const uint64_t own =
+        row < p.r.qn * a.d.G
+            ? (uint64_t)(a.q + (int64_t)(p.r.q0 + row / a.d.G) * a.q_stride +
+                         (int64_t)(p.h * a.d.G + row % a.d.G) * D)
+            : 0;
 #pragma unroll
-  for (int i = 0; i < 8 / kPer; ++i) {
-    const uint64_t src = __shfl_sync(~0u, own, i * kPer + lane / kL);
-    w[i] = make_uint4(0, 0, 0, 0);
-    if (src) w[i] = reinterpret_cast<const uint4*>(src)[lane % kL];
+    for (int i = 0; i < 8 / kPer; ++i) {
+      const uint64_t src = __shfl_sync(~0u, own, i * kPer + lane / kL);
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (src) w[i] = reinterpret_cast<const uint4*>(src)[lane % kL];
+    }
+#pragma unroll
+    for (int i = 0; i < 8 / kPer; ++i) {
+      uint32_t top = max_u16x2(max_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                               max_u16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+#pragma unroll
+      for (int o = kL / 2; o; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(~0u, top, o));
+      top = max(top & 0xffffu, top >> 16);
+      const int e = min(max((int)(top >> 7) - 127, -100), 126);
+      const float down = pow2(-e) * 8192.f;
+      if (lane % kL == 0) exps[row0 + i * kPer + lane / kL] = (int8_t)e;
+      w[i] = make_uint4(pack_f16(bf16_lo(w[i].x) * down, bf16_lo(w[i].z) * down),
+                        pack_f16(bf16_hi(w[i].x) * down, bf16_hi(w[i].z) * down),
+                        pack_f16(bf16_lo(w[i].y) * down, bf16_lo(w[i].w) * down),
+                        pack_f16(bf16_hi(w[i].y) * down, bf16_hi(w[i].w) * down));
+    }
   }
+
+  // Groups g0 .. g0 + kQGroups - 1 into shared memory: [group][row] of 128 bytes, pieces swizzled.
+  __device__ __forceinline__ void store(uint32_t dst, int row0, int g0) {
+    const int lane = threadIdx.x & 31, g = ((lane % kL) >> 3) - g0, j = lane & 7;
+    if (g < 0 || g >= Cfg<D>::kQGroups) return;
 #pragma unroll
-  for (int i = 0; i < 8 / kPer; ++i) {
-    const int qr = row0 + i * kPer + lane / kL;
-    uint32_t top = max_u16x2(max_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                             max_u16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-#pragma unroll
-    for (int o = kL / 2; o; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(~0u, top, o));
-    top = max(top & 0xffffu, top >> 16);
-    const int e = min(max((int)(top >> 7) - 127, -100), 126);
-    const float down = pow2(-e) * 8192.f;
-    if (lane % kL == 0) exps[qr] = (int8_t)e;
-    sts128(dst + g * (kRows * 128) + qr * 128 + ((j ^ (qr & 7)) << 4),
-           pack_f16(bf16_lo(w[i].x) * down, bf16_lo(w[i].z) * down),
-           pack_f16(bf16_hi(w[i].x) * down, bf16_hi(w[i].z) * down),
-           pack_f16(bf16_lo(w[i].y) * down, bf16_lo(w[i].w) * down),
-           pack_f16(bf16_hi(w[i].y) * down, bf16_hi(w[i].w) * down));
+    for (int i = 0; i < 8 / kPer; ++i) {
+      const int row = row0 + i * kPer + lane / kL;
+      sts128(dst + g * (kRows * 128) + row * 128 + ((j ^ (row & 7)) << 4), w[i].x, w[i].y, w[i].z,
+             w[i].w);
+    }
   }
+};
+
+// The warp's 32 rows (tensor memory lanes 32 (warp % 4) ..) of those groups into tensor memory.
+template <int D>
+__device__ __forceinline__ void copy_queries(uint32_t src, uint32_t tmem, int g0) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = 32 * quarter + lane;
+#pragma unroll 1
+  for (int g = 0; g < C::kQGroups; ++g) {
+    uint32_t q[32];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(q[4 * j]), "=r"(q[4 * j + 1]), "=r"(q[4 * j + 2]), "=r"(q[4 * j + 3])
+                   : "r"(src + g * (kRows * 128) + row * 128 + ((j ^ (row & 7)) << 4)));
+    tmem_st32(tmem + ((uint32_t)(32 * quarter) << 16) + C::kColQ + 32 * (g0 + g), q);
+  }
+  tmem_wait_st();
+  tc_fence_before();
 }
 
 template <int D>
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       mbar_init(&bars.part_full[i], 1);
       mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 2);
     }
-    for (int i = 0; i < 2 * C::kRaw; ++i) {
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&bars.raw_full[0][i], 1);
       mbar_init(&bars.raw_empty[0][i], kDeqWarps);
     }
@@ -472,12 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       mbar_init(&bars.v_full[i], kDeqWarps);
       mbar_init(&bars.v_empty[i], 1);
     }
-    for (int i = 0; i < kS; ++i) {
+    for (int i = 0; i < C::kS; ++i) {
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.p_full[i], 32 * kSoftWarps);
       mbar_init(&bars.pv_done[i], 1);
     }
-    mbar_init(&bars.q_full, 2 * kDeqWarps);
+    mbar_init(&bars.q_staged, 2 * kDeqWarps);
+    mbar_init(&bars.q_copied, 4);
+    mbar_init(&bars.q_full, 4);
     mbar_init(&bars.q_free, 1);
     mbar_init(&bars.o_free, 32 * kSoftWarps);
     fence_mbar_init();
@@ -514,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     registers_down<kRegsRest>();
     // copies the key (0) or value (1) sides of a part's records, a warp each
     auto copy_sides = [&](int which, int b, int h, int kv, int t0, int t1) {
-      const int recs = (kv + 15) / 16;
+      const int recs = (kv + 15) / 16, ring = which ? C::kRawV : C::kRawK;
       uint32_t record = 0;
       for (int t = t0; t < t1; ++t, ++n) {
         const int slot = (t - t0) & 7;
@@ -522,9 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           const int rec = t * kRecs + lane;
           if (rec < recs) record = cache_record(a, b, h, rec);
         }
-        const int st = n % C::kRaw;
+        const int st = n % ring;
         uint64_t* full = &bars.raw_full[which][st];
-        ok = mbar_wait(&bars.raw_empty[which][st], ((n / C::kRaw) & 1) ^ 1, a.err);
+        ok = mbar_wait(&bars.raw_empty[which][st], ((n / ring) & 1) ^ 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) return;
         const int have = min(max(recs - t * kRecs, 0), kRecs);
@@ -539,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     };
     // nothing may be in flight when the block ends
     auto drain = [&](int which) {
-      for (int k = max(0, n - C::kRaw); k < n; ++k)
-        mbar_wait(&bars.raw_full[which][k % C::kRaw], (k / C::kRaw) & 1, a.err);
+      const int ring = which ? C::kRawV : C::kRawK;
+      for (int k = max(0, n - ring); k < n; ++k)
+        mbar_wait(&bars.raw_full[which][k % ring], (k / ring) & 1, a.err);
     };
     if (warp == kLoadWarp) {
       int64_t w = 0, w1 = 0;
@@ -573,22 +610,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       drain(1);
     } else if (warp == kMmaWarp && lane == 0) {
       const uint32_t id_s = idesc_f16(kRows, kStep), id_o = idesc_f16(kRows, D);
-      const uint64_t q_desc = sdesc_k128(ops), k_desc = sdesc_k128(ops + C::kOffK),
-                     v_desc = sdesc_k128(ops + C::kOffV);
+      const uint64_t k_desc = sdesc_k128(ops + C::kOffK), v_desc = sdesc_k128(ops + C::kOffV);
       // scores of step k; after a part's last ones its queries may be replaced
       auto scores = [&](int k, bool last) {
         if (!mbar_wait(&bars.k_full[k % C::kOpsK], (k / C::kOpsK) & 1, a.err)) return false;
-        // the buffer's weights of step k - kS have been used
-        if (k >= kS && !mbar_wait(&bars.pv_done[k % kS], ((k - kS) / kS) & 1, a.err)) return false;
+        // the buffer's weights of step k - C::kS have been used
+        if (k >= C::kS && !mbar_wait(&bars.pv_done[k % C::kS], ((k - C::kS) / C::kS) & 1, a.err)) return false;
         tc_fence_after();
         const uint64_t kd = k_desc + (k % C::kOpsK) * (C::kK / 16);
-        const uint32_t d = tmem + C::kColS + (k % kS) * kStep;
+        const uint32_t d = tmem + C::kColS + (k % C::kS) * kStep;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_bf16(d, q_desc + ((i / 4) * (kRows * 8) + (i % 4) * 2),
-                   kd + ((i / 4) * (kStep * 8) + (i % 4) * 2), id_s, i > 0);
+          mma_bf16_ts(d, tmem + C::kColQ + 8 * i, kd + ((i / 4) * (kStep * 8) + (i % 4) * 2), id_s,
+                      i > 0);
         mma_commit(&bars.k_empty[k % C::kOpsK]);
-        mma_commit(&bars.s_full[k % kS]);
+        mma_commit(&bars.s_full[k % C::kS]);
         if (last) mma_commit(&bars.q_free);
         return true;
       };
@@ -606,24 +642,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         ok = scores(n, steps == 1) && (steps < 2 || scores(n + 1, steps == 2));
         for (int t = 0; t < steps && ok; ++t, ++n) {
           ok = mbar_wait(&bars.v_full[n % C::kOpsV], (n / C::kOpsV) & 1, a.err) &&
-               mbar_wait(&bars.p_full[n % kS], (n / kS) & 1, a.err) &&
+               mbar_wait(&bars.p_full[n % C::kS], (n / C::kS) & 1, a.err) &&
                (t > 0 || kq == 0 || mbar_wait(&bars.o_free, (kq - 1) & 1, a.err));
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = v_desc + (n % C::kOpsV) * (C::kK / 16);
-          const uint32_t w = tmem + C::kColS + (n % kS) * kStep;
+          const uint32_t w = tmem + C::kColS + (n % C::kS) * kStep;
           const uint32_t more = t > 0;
 #pragma unroll
           for (int i = 0; i < kStep / 16; ++i)
             mma_bf16_ts(tmem, w + 8 * i, vd + 2 * i, id_o, i > 0 ? 1u : more);
           mma_commit(&bars.v_empty[n % C::kOpsV]);
-          mma_commit(&bars.pv_done[n % kS]);
+          mma_commit(&bars.pv_done[n % C::kS]);
           if (t + 2 < steps) ok = scores(n + 2, t + 3 == steps);
         }
         ++kq;
       }
       // every MMA has ended before the tensor memory is given back
-      if (n >= 1) mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err);
+      if (n >= 1) mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err);
     }
     __syncwarp();
   } else if (warp >= kKeyWarp) {
@@ -641,17 +677,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (p.t0 == p.t1) continue;
       if (kq > 0) ok = __all_sync(~0u, mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
       if (!ok) break;
-      stage_queries<D>(a, p, ops, 8 * (warp - kKeyWarp), row_exp[kq % kExps]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q_full);
+      // queries: every warp scales eight rows, four warps (one for each 32 lanes) move them on
+      QueryRows<D> q;
+      q.load(a, p, 8 * (warp - kKeyWarp), row_exp[kq % kExps]);
+#pragma unroll
+      for (int pass = 0; pass < C::kQPasses && ok; ++pass) {
+        const int turn = kq * C::kQPasses + pass;
+        if (pass > 0)
+          ok = __all_sync(~0u, mbar_wait(&bars.q_copied, (turn - 1) & 1, a.err));
+        if (!ok) break;
+        q.store(ops, 8 * (warp - kKeyWarp), pass * C::kQGroups);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.q_staged);
+        if (warp < kKeyWarp + 4) {
+          ok = __all_sync(~0u, mbar_wait(&bars.q_staged, turn & 1, a.err));
+          if (!ok) break;
+          copy_queries<D>(ops, tmem, pass * C::kQGroups);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars.q_copied);
+            if (pass == C::kQPasses - 1) mbar_arrive(&bars.q_full);
+          }
+        }
+      }
+      if (!ok) break;
       ++kq;
       const int t0 = p.t0, t1 = p.t1, kv = p.r.kv;
       for (int t = t0; t < t1; ++t, ++n) {
-        const int st = n % C::kRaw;
-        const int which = is_key ? 0 : 1;
+        const int which = is_key ? 0 : 1, ring = is_key ? C::kRawK : C::kRawV;
+        const int st = n % ring;
         const int tok = t * kStep + 8 * oct;
-        ok = mbar_wait(&bars.raw_full[which][st], (n / C::kRaw) & 1, a.err);
+        ok = mbar_wait(&bars.raw_full[which][st], (n / ring) & 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         if (is_key)
@@ -696,12 +752,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const int least = seen_by(p.r, p.rt * kRows / a.d.G);
       float m = -INFINITY, l = 0.f, unit = 0.f;
       for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-        ok = __all_sync(~0u, mbar_wait(&bars.s_full[n % kS], (n / kS) & 1, a.err));
+        ok = __all_sync(~0u, mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err));
         if (!ok) break;
         tc_fence_after();
         if (t == p.t0)  // back from the scaled queries' units to log2 units
           unit = pow2(row_exp[kq % kExps][tid]) * (64.f / 8192.f) * a.d.scale_log2;
-        const uint32_t sb = lane_base + C::kColS + (n % kS) * kStep;
+        const uint32_t sb = lane_base + C::kColS + (n % C::kS) * kStep;
         uint32_t s[kStep];
         tmem_ld32(sb, s);
         tmem_ld32(sb + 32, s + 32);
@@ -733,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           l *= f;
           if (t > p.t0) {
             // the outputs so far, once the last product has landed
-            ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err));
+            ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -767,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         tmem_st32(sb, w);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars.p_full[n % kS]);
+        mbar_arrive(&bars.p_full[n % C::kS]);
       }
       if (!ok) break;
       if (p.tiles == 0) {  // rows that see nothing
@@ -781,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       }
       ++kq;
       // outputs: after the last product
-      ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % kS], ((n - 1) / kS) & 1, a.err));
+      ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err));
       if (!ok) break;
       tc_fence_after();
       const bool whole = p.t1 - p.t0 == p.tiles;
