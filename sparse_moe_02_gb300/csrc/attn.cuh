@@ -145,13 +145,12 @@ cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s);
 // Attention of few query rows per key/value head and request (n_b G <= 32): attn_decode.cu.
 constexpr int kDecodeRows = 32;
 cudaError_t prepare_attn_decode_kernels(int max_requests);
-int attn_decode_slots(int sms);         // partial results of a launch
-size_t attn_decode_part_floats(int D);  // fp32 of one partial result
+int attn_part_slots(int sms);  // partial results of a launch, of either kernel
 cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s);
 
 // Attention of more rows, and of batches that hold any such request: attn_prefill.cu.
 cudaError_t prepare_attn_prefill_kernels(int max_requests);
-size_t attn_prefill_part_floats(int D);
+size_t attn_prefill_part_floats(int D);  // fp32 of a partial result, the larger of the kernels'
 cudaError_t launch_attn_prefill(const FwdArgs& a, int sms, cudaStream_t s);
 
 }  // namespace moe

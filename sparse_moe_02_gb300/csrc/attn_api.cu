@@ -107,7 +107,7 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
   const double scale = cfg->scale > 0.f ? cfg->scale : 1.0 / std::sqrt((double)cfg->head_dim);
   h->d.scale_log2 = (float)(scale * 1.4426950408889634);
 
-  const size_t slots = moe::attn_decode_slots(sms);
+  const size_t slots = moe::attn_part_slots(sms);
   const size_t o_bytes =
       round256(slots * moe::attn_prefill_part_floats(cfg->head_dim) * sizeof(float));
   const size_t ml_bytes = round256(slots * 128 * sizeof(float2));

@@ -1,5 +1,5 @@
 // Attention of few query rows over the paged 4-bit cache (include/attn.h): single tokens and
-// short drafts, n_b G <= 16 rows per request and key/value head.
+// short drafts, n_b G <= kDecodeRows rows per request and key/value head.
 //
 // Mathematics.  A key row of group g is k_c = s_g code_c + b_g, so a score is
 //   q . k = sum_g s_g (sum_c q_c code_c) + b_g (sum_c q_c):
@@ -794,9 +794,7 @@ cudaError_t launch(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
 }  // namespace
 
 // A block shares at most its first and its last context with others.
-int attn_decode_slots(int sms) { return 2 * sms; }
-
-size_t attn_decode_part_floats(int D) { return (size_t)(D == 256 ? 8 : 16) * D; }
+int attn_part_slots(int sms) { return 2 * sms; }
 
 cudaError_t prepare_attn_decode_kernels(int max_requests) {
   cudaError_t e;

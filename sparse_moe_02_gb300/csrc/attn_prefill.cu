@@ -10,9 +10,19 @@
 //                             tokens, so both operands are K-major)
 // Scores run ahead: those of step n + 2 are queued behind the product of step n.  With 256 channels
 // a step of 64 tokens takes 1300 clocks of MMAs (64 columns: 49 clocks each, 256 columns: 129,
-// measured alone) and moves 168 KB through shared memory (operands written and read, records), which
-// is its tightest resource; Q in shared memory would add 64 KB.  One thread issues the MMAs, from
-// descriptors that are formed once and stepped by constants: forming each anew took 80 clocks.
+// measured alone).  One thread issues the MMAs, from descriptors that are formed once and stepped by
+// constants: forming each anew took 80 clocks.
+//
+// What bounds it is the dequantising: a step takes 2800 clocks, in which the block issues some 7400
+// warp instructions (67% of the issue slots) and the key warps never wait; the tensor pipe is busy
+// for 37% of them.  Every 128 rows dequantise their context anew, so the rate rises with neither
+// rows nor context beyond this.  Where queries are (tensor or shared memory) changes a long context
+// by less than 1%; in tensor memory they leave room for two steps of value operands, which is worth
+// 7% on chunks and 20% with 64 channels, and costs 4% on a prompt of 4096.
+//
+// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 247 us (555 TFLOP/s),
+// 2048 over a context of 32K 1177 us (884 TFLOP/s, 46% of a bf16 product's rate); ragged chunks
+// 102 us; 4096 tokens of 32 heads over 8 of 128 channels 277 us, of 64 channels 240 us.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -144,6 +154,29 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Packed fp32 pairs: half the issue slots of the softmax's multiplications and additions.
+__device__ __forceinline__ uint64_t pair(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void fma_pair(float& a, float& b, uint32_t x, uint32_t y, uint64_t mul,
+                                         uint64_t add) {
+  asm("{\n\t.reg .b64 p;\n\t"
+      "mov.b64 p, {%2, %3};\n\t"
+      "fma.rn.f32x2 p, p, %4, %5;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "r"(x), "r"(y), "l"(mul), "l"(add));
+}
+__device__ __forceinline__ void add_pair(uint64_t& sum, float x, float y) {
+  asm("{\n\t.reg .b64 p;\n\t"
+      "mov.b64 p, {%1, %2};\n\t"
+      "add.rn.f32x2 %0, %0, p;\n\t}"
+      : "+l"(sum)
+      : "f"(x), "f"(y));
+}
+
 constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 
 // ------------------------------------------------------------------- the work of a block
@@ -231,7 +264,7 @@ struct Bars {
   uint64_t raw_full[2][4], raw_empty[2][4];  // [keys, values]
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[C::kS], p_full[C::kS], pv_done[C::kS];
-  uint64_t q_staged, q_copied, q_full, q_free, o_free;
+  uint64_t q_staged, q_copied, q_full, q_free, o_free, ended;
 };
 
 // Moves the warpgroup's threads to n registers.
@@ -254,14 +287,17 @@ struct __align__(16) Exps {
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Bound of |bias| + 15 |step| as bits of a nonnegative float, 0 if it is not finite.
-__device__ __forceinline__ uint32_t magnitude(uint32_t params) {
-  const float v = fmaf(15.f, fabsf(bf16_lo(params)), fabsf(bf16_hi(params)));
-  return v < __int_as_float(0x7f800000) ? __float_as_uint(v) : 0u;
+// Magnitudes of a parameter word (step below, bias above) as packed bf16 bits; those of a token that
+// is marked as not finite count as nothing.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t params) {
+  return params == 0x7fc00000u ? 0u : params & 0x7fff7fffu;
 }
 
-__device__ __forceinline__ int exponent_of(uint32_t bits) {
-  return max((int)(bits >> 23) - 126, -90);  // at most 118: see kLargest
+// e with |bias| + 15 |step| < 2^e for the largest of either over the warp; at most 118 (kLargest).
+__device__ __forceinline__ int exponent_of(uint32_t packed) {
+  const int s = (int)(__reduce_max_sync(~0u, packed & 0xffffu) >> 7);
+  const int b = (int)(__reduce_max_sync(~0u, packed >> 16) >> 7);
+  return max(max(s + 4, b) - 125, -90);  // 15 step < 2^(4 + its exponent + 1)
 }
 
 // One warp turns 8 cached tokens (half a record) of a step into operands: rows of the key operand
@@ -287,7 +323,7 @@ struct Dequant {
     uint32_t w = lds32(par), w2 = lds32(par + other * R::kPar);
     if (tok + t >= kv) w = 0;
     if (tok + t + other >= kv) w2 = 0;
-    *e = exponent_of(__reduce_max_sync(~0u, max(magnitude(w), magnitude(w2))));
+    *e = exponent_of(max_u16x2(magnitudes(w), magnitudes(w2)));
     return w;
   }
 
@@ -516,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     mbar_init(&bars.q_full, 4);
     mbar_init(&bars.q_free, 1);
     mbar_init(&bars.o_free, 32 * kSoftWarps);
+    mbar_init(&bars.ended, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&tmem_base, C::kCols);
@@ -658,8 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
         ++kq;
       }
-      // every MMA has ended before the tensor memory is given back
-      if (n >= 1) mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err);
+      // every MMA, those of a run that a wait cut short too, has ended before the tensor memory is
+      // given back
+      mma_commit(&bars.ended);
+      mbar_wait(&bars.ended, 0, a.err);
     }
     __syncwarp();
   } else if (warp >= kKeyWarp) {
@@ -808,17 +847,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         uint32_t w[kStep / 2];
 #pragma unroll
         for (int r = 0; r < kRecs; ++r) {
-          const float add = ref + ex[r].ev;
-          float sum0 = 0.f, sum1 = 0.f;
+          const uint64_t add = pair(ref + ex[r].ev), mul = pair(ex[r].up_k);
+          uint64_t sum = 0;  // two fp32 zeros
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float p0 = exp2_fast(fmaf(__uint_as_float(s[16 * r + i]), ex[r].up_k, add));
-            const float p1 = exp2_fast(fmaf(__uint_as_float(s[16 * r + i + 1]), ex[r].up_k, add));
-            sum0 += p0;
-            sum1 += p1;
+            float x0, x1;
+            fma_pair(x0, x1, s[16 * r + i], s[16 * r + i + 1], mul, add);
+            const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
+            add_pair(sum, p0, p1);
             w[8 * r + i / 2] = pack_f16(p0, p1);
           }
-          l = fmaf(sum0 + sum1, ex[r].down_v, l);
+          l = fmaf(__uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32)),
+                   ex[r].down_v, l);
         }
         tmem_st32(sb, w);
         tmem_wait_st();
