@@ -390,6 +390,7 @@ class Kv4Cache:
         self.data = torch.zeros((n_pages, n_kv_heads, page_size // 16, 18 * head_dim),
                                 dtype=torch.uint8, device=device)
         self.ptr = self.data.data_ptr()
+        self.layout = (n_pages, n_kv_heads, page_size, head_dim)
 
 
 class PagedAttention:
@@ -407,6 +408,7 @@ class PagedAttention:
         self.handle = None
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self.page_size, self.n_pages, self.max_requests = page_size, n_pages, max_requests
+        self._layout = (n_pages, n_kv_heads, page_size, head_dim)
         cfg = attn_config(n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
                           scale)
         st, self.handle = attn_create(cfg)
@@ -447,6 +449,12 @@ class PagedAttention:
             _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {n} contiguous CUDA int32 numbers, "
                     f"got {t.device.type} {t.dtype} {tuple(t.shape)}")
         return t.data_ptr()
+
+    def _cache(self, cache):
+        if cache.layout != self._layout:
+            _refuse(MOE_ERR_INVALID_ARG, f"cache: expected (pages, heads, page, channels) "
+                    f"{self._layout}, got {cache.layout}")
+        return cache.ptr
 
     def _new(self, shape, dtype):
         return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self._device}")
@@ -515,7 +523,7 @@ class PagedAttention:
         T, Hkv = k.shape[0], self.n_kv_heads
         (kp, ks), (vp, vs) = self._rows(k, "k", Hkv, T), self._rows(v, "v", Hkv, T)
         st = self._lib.attn_kv4_append(self.handle, kp, ks, vp, vs,
-                                       self._ints(slots, "slots", T), T, cache.ptr,
+                                       self._ints(slots, "slots", T), T, self._cache(cache),
                                        self._stream(stream))
         if st:
             _check(st, "attn_kv4_append")
@@ -526,8 +534,9 @@ class PagedAttention:
         k_out = self._new((T, Hkv, self.head_dim), self._bf16) if k_out is None else k_out
         v_out = self._new((T, Hkv, self.head_dim), self._bf16) if v_out is None else v_out
         (kp, ks), (vp, vs) = self._rows(k_out, "k_out", Hkv, T), self._rows(v_out, "v_out", Hkv, T)
-        st = self._lib.attn_kv4_read(self.handle, cache.ptr, self._ints(slots, "slots", T), T, kp,
-                                     ks, vp, vs, self._stream(stream))
+        st = self._lib.attn_kv4_read(self.handle, self._cache(cache),
+                                     self._ints(slots, "slots", T), T, kp, ks, vp, vs,
+                                     self._stream(stream))
         if st:
             _check(st, "attn_kv4_read")
         return k_out, v_out
@@ -541,9 +550,9 @@ class PagedAttention:
         (qp, qs), (op, os_) = self._rows(q, "q", Hq, T), self._rows(out, "out", Hq, T)
         ints = self._ints
         st = self._lib.attn_kv4_forward(
-            self.handle, qp, qs, cache.ptr, ints(block_table, "block_table", B * width), width,
-            ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B), B, T, max_q_len,
-            max_kv_len, op, os_, self._stream(stream))
+            self.handle, qp, qs, self._cache(cache), ints(block_table, "block_table", B * width),
+            width, ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B), B, T,
+            max_q_len, max_kv_len, op, os_, self._stream(stream))
         if st:
             _check(st, "attn_kv4_forward")
         return out
