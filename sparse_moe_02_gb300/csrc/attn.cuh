@@ -70,6 +70,12 @@ struct FwdArgs {
   float* part_o;     // partial outputs: [slots][columns][D] fp32
   float2* part_ml;   // their softmax reference and sum: [slots][columns]
   int4* desc;        // [2 * blocks]: (parts, head, row tile, first row), (rows) of shared contexts
+  // Contexts as MMA operands (attn_prefill.cu): whether they are there and, from [1] on, each
+  // request's first step; room for prep_cap steps, 0 where a call does not form them.
+  int* prep_at;
+  int prep_cap;
+  uint8_t* prep;      // [steps]: a step's key operand, then its value operand
+  uint4* prep_exps;   // [steps][4]: exponents of the records
   int* err;
 };
 
@@ -151,6 +157,8 @@ cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream
 // Attention of more rows, and of batches that hold any such request: attn_prefill.cu.
 cudaError_t prepare_attn_prefill_kernels(int max_requests);
 size_t attn_prefill_part_floats(int D);  // fp32 of a partial result, the larger of the kernels'
+int attn_prep_steps(const AttnDims& d, int max_requests);  // of contexts held as operands
+size_t attn_prep_step_bytes(int D);                        // of one, without its exponents
 cudaError_t launch_attn_prefill(const FwdArgs& a, int sms, cudaStream_t s);
 
 }  // namespace moe

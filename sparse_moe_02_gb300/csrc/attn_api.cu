@@ -17,6 +17,10 @@ struct attn_handle_s {
   float* part_o = nullptr;
   float2* part_ml = nullptr;
   int4* desc = nullptr;
+  uint8_t* prep = nullptr;
+  uint4* prep_exps = nullptr;
+  int* prep_at = nullptr;
+  int prep_cap = 0;
   int* ticket = nullptr;
   int* err = nullptr;
 };
@@ -112,8 +116,13 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
       round256(slots * moe::attn_prefill_part_floats(cfg->head_dim) * sizeof(float));
   const size_t ml_bytes = round256(slots * 128 * sizeof(float2));
   const size_t desc_bytes = round256(slots * sizeof(int4));
+  h->prep_cap = moe::attn_prep_steps(h->d, cfg->max_requests);
+  const size_t prep_bytes = round256(h->prep_cap * moe::attn_prep_step_bytes(cfg->head_dim));
+  const size_t exps_bytes = round256(h->prep_cap * 4 * sizeof(uint4));
+  const size_t at_bytes = round256((1 + (size_t)cfg->max_requests) * sizeof(int));
   const size_t zeroed = 2 * sizeof(int);  // the plan's ticket, the error word
-  const size_t bytes = o_bytes + ml_bytes + desc_bytes + zeroed;
+  const size_t bytes =
+      o_bytes + ml_bytes + desc_bytes + prep_bytes + exps_bytes + at_bytes + zeroed;
   cudaError_t e = cudaMalloc(&h->ws, bytes);
   if (e == cudaErrorMemoryAllocation) {
     cudaGetLastError();
@@ -123,9 +132,12 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
   if (e == cudaSuccess) {
     char* p = static_cast<char*>(h->ws);
     h->part_o = reinterpret_cast<float*>(p);
-    h->part_ml = reinterpret_cast<float2*>(p + o_bytes);
-    h->desc = reinterpret_cast<int4*>(p + o_bytes + ml_bytes);
-    h->ticket = reinterpret_cast<int*>(p + o_bytes + ml_bytes + desc_bytes);
+    h->part_ml = reinterpret_cast<float2*>(p += o_bytes);
+    h->desc = reinterpret_cast<int4*>(p += ml_bytes);
+    h->prep = reinterpret_cast<uint8_t*>(p += desc_bytes);
+    h->prep_exps = reinterpret_cast<uint4*>(p += prep_bytes);
+    h->prep_at = reinterpret_cast<int*>(p += exps_bytes);
+    h->ticket = reinterpret_cast<int*>(p += at_bytes);
     h->err = h->ticket + 1;
     e = cudaMemset(h->ticket, 0, zeroed);
     // the handle may be used on a stream that does not order itself behind the default one
@@ -305,6 +317,10 @@ int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void*
   a.part_o = h->part_o;
   a.part_ml = h->part_ml;
   a.desc = h->desc;
+  a.prep_at = h->prep_at;
+  a.prep_cap = h->prep_cap;
+  a.prep = h->prep;
+  a.prep_exps = h->prep_exps;
   a.err = h->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return record_cuda_status(a.max_q * h->d.G <= moe::kDecodeRows

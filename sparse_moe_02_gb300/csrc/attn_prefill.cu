@@ -35,6 +35,9 @@
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
 // in the few-row kernel; shared row tiles are joined by its second launch.
+#include <algorithm>
+#include <climits>
+
 #include "attn.cuh"
 #include "attn_join.cuh"
 
@@ -187,6 +190,7 @@ constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 // request without cached tokens, whose rows are only zeroed, cost kZeroCost G each.
 constexpr int kPartCost = 320;   // tokens: a row tile's fixed cost
 constexpr int kZeroCost = 96;
+constexpr int kPartCostPrep = 640;  // the same, of prepared contexts, whose steps are shorter
 constexpr int kLeastSteps = 4;   // of a block
 
 struct Cost {
@@ -197,9 +201,9 @@ struct Cost {
   }
 };
 
-__device__ __forceinline__ Cost cost_of(const FwdArgs& a, const Req& r) {
+__device__ __forceinline__ Cost cost_of(const FwdArgs& a, const Req& r, int part_cost) {
   if (r.kv == 0) return Cost{(int64_t)kZeroCost * a.d.G, 0, 0};
-  return Cost{(int64_t)kPartCost * a.d.G, (int64_t)max(r.kv - r.qn, 0) * a.d.G, 64};
+  return Cost{(int64_t)part_cost * a.d.G, (int64_t)max(r.kv - r.qn, 0) * a.d.G, 64};
 }
 
 __device__ __forceinline__ int row_tiles(const FwdArgs& a, const Req& r) {
@@ -212,14 +216,14 @@ __device__ __forceinline__ int seen_by(const Req& r, int tok) {
 }
 
 // The part that holds work w of the block's [w, w1).
-__device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, int64_t w,
-                                       int64_t w1) {
+__device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, int part_cost,
+                                       int64_t w, int64_t w1) {
   Part p;
   p.some = false;
   while (w < w1) {
     p.b = find_request(first, a.B, w);
     p.r = load_req(a, p.b);
-    const Cost c = cost_of(a, p.r);
+    const Cost c = cost_of(a, p.r, part_cost);
     const int rts = row_tiles(a, p.r);
     const int64_t head = c.before(rts);
     p.h = (int)divide(w - first[p.b], head);
@@ -264,8 +268,17 @@ struct Bars {
   uint64_t raw_full[2][4], raw_empty[2][4];  // [keys, values]
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[C::kS], p_full[C::kS], pv_done[C::kS];
+  uint64_t x_full[kExps];  // exponents of prepared steps
   uint64_t q_staged, q_copied, q_full, q_free, o_free, ended;
 };
+
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
 
 // Moves the warpgroup's threads to n registers.
 template <int N>
@@ -547,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       mbar_init(&bars.p_full[i], 32 * kSoftWarps);
       mbar_init(&bars.pv_done[i], 1);
     }
+    for (int i = 0; i < kExps; ++i) mbar_init(&bars.x_full[i], 1);
     mbar_init(&bars.q_staged, 2 * kDeqWarps);
     mbar_init(&bars.q_copied, 4);
     mbar_init(&bars.q_full, 4);
@@ -559,10 +573,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   pdl_wait();
   pdl_trigger();
   int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
+  const bool prepared = a.prep_cap > 0 && a.prep_at[0];
+  const int part_cost = prepared ? kPartCostPrep : kPartCost;
   {
     const Cut cut =
         cut_work<kThreads>(a, first, sums, (int64_t)kLeastSteps * kStep * a.d.G, [&](const Req& r) {
-          return a.d.Hkv * cost_of(a, r).before(row_tiles(a, r));
+          return a.d.Hkv * cost_of(a, r, part_cost).before(row_tiles(a, r));
         });
     if (tid == 0) {
       cut_s = cut;
@@ -610,8 +626,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
                       a.cache + (uint64_t)rec * C::R::kBytes + (which ? C::R::kVp : 0), side, full);
       }
     };
+    // copies the prepared key (0) or value (1) operands of steps t0 .. t1 - 1 of a context whose
+    // first is `at`, a warp each: eight arrivals a step, as from the dequantising warps
+    auto copy_prepared = [&](int which, int at, int t0, int t1) {
+      constexpr int kRing = C::kOpsK;
+      static_assert(C::kOpsK == C::kOpsV && kDeqWarps == 8, "one rule for both");
+      for (int t = t0; t < t1; ++t, ++n) {
+        const int op = n % kRing;
+        uint64_t* full = which ? &bars.v_full[op] : &bars.k_full[op];
+        ok = mbar_wait(which ? &bars.v_empty[op] : &bars.k_empty[op], ((n / kRing) & 1) ^ 1, a.err);
+        ok = __all_sync(~0u, ok);
+        if (!ok) return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, C::kK);
+          copy_record(smem + (which ? C::kOffV : C::kOffK) + op * C::kK,
+                      a.prep + ((int64_t)(at + t) * 2 + which) * C::kK, C::kK, full);
+        } else if (lane < kDeqWarps) {
+          mbar_arrive(full);
+        } else if (lane == kDeqWarps && which == 0) {
+          mbar_arrive_expect_tx(&bars.x_full[n % kExps], sizeof(exps[0]));
+          copy_record(exps[n % kExps], a.prep_exps + (int64_t)(at + t) * kRecs, sizeof(exps[0]),
+                      &bars.x_full[n % kExps]);
+        }
+        __syncwarp();
+      }
+    };
+    // first prepared step of a part's context
+    auto prepared_at = [&](const Part& p) {
+      return a.prep_at[1 + p.b] + p.h * ((p.r.kv + kStep - 1) / kStep);
+    };
     // nothing may be in flight when the block ends
     auto drain = [&](int which) {
+      if (prepared) {
+        for (int k = max(0, n - C::kOpsK); k < n; ++k)
+          mbar_wait(which ? &bars.v_full[k % C::kOpsK] : &bars.k_full[k % C::kOpsK],
+                    (k / C::kOpsK) & 1, a.err);
+        for (int k = max(0, n - kExps); which == 0 && k < n; ++k)
+          mbar_wait(&bars.x_full[k % kExps], (k / kExps) & 1, a.err);
+        return;
+      }
       const int ring = which ? C::kRawV : C::kRawK;
       for (int k = max(0, n - ring); k < n; ++k)
         mbar_wait(&bars.raw_full[which][k % ring], (k / ring) & 1, a.err);
@@ -621,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if ((int)blockIdx.x < cut_s.blocks)
         w = cut_s.bound(blockIdx.x), w1 = cut_s.bound(blockIdx.x + 1);
       for (int k = 0; ok; ++k) {
-        const Part p = locate(a, first, w, w1);
+        const Part p = locate(a, first, part_cost, w, w1);
         ok = mbar_wait(&bars.part_empty[k % kParts], ((k / kParts) & 1) ^ 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
@@ -631,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
         if (!p.some) break;
         w = p.next;
-        copy_sides(0, p.b, p.h, p.r.kv, p.t0, p.t1);
+        if (prepared) copy_prepared(0, prepared_at(p), p.t0, p.t1);
+        else copy_sides(0, p.b, p.h, p.r.kv, p.t0, p.t1);
       }
       drain(0);
     } else if (warp == kValueLoadWarp) {
@@ -642,62 +696,78 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         __syncwarp();
         if (lane == 0) part_read(k);
         if (!p.some) break;
-        copy_sides(1, p.b, p.h, p.r.kv, p.t0, p.t1);
+        if (prepared) copy_prepared(1, prepared_at(p), p.t0, p.t1);
+        else copy_sides(1, p.b, p.h, p.r.kv, p.t0, p.t1);
       }
       drain(1);
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
+      // the whole warp walks through the steps, so that all that the MMAs take is uniform; one of
+      // its threads issues them
+      const bool lead = elect_one();
       const uint32_t id_s = idesc_f16(kRows, kStep), id_o = idesc_f16(kRows, D);
       const uint64_t k_desc = sdesc_k128(ops + C::kOffK), v_desc = sdesc_k128(ops + C::kOffV);
       // scores of step k; after a part's last ones its queries may be replaced
       auto scores = [&](int k, bool last) {
-        if (!mbar_wait(&bars.k_full[k % C::kOpsK], (k / C::kOpsK) & 1, a.err)) return false;
-        // the buffer's weights of step k - C::kS have been used
-        if (k >= C::kS && !mbar_wait(&bars.pv_done[k % C::kS], ((k - C::kS) / C::kS) & 1, a.err)) return false;
+        const int op = k % C::kOpsK, sb = k % C::kS;
+        // (the buffer's weights of step k - C::kS have been used)
+        const bool go = mbar_wait(&bars.k_full[op], (k / C::kOpsK) & 1, a.err) &&
+                        (k < C::kS || mbar_wait(&bars.pv_done[sb], ((k - C::kS) / C::kS) & 1, a.err));
+        if (!__all_sync(~0u, go)) return false;
         tc_fence_after();
-        const uint64_t kd = k_desc + (k % C::kOpsK) * (C::kK / 16);
-        const uint32_t d = tmem + C::kColS + (k % C::kS) * kStep;
+        if (lead) {
+          const uint64_t kd = k_desc + op * (C::kK / 16);
+          const uint32_t d = tmem + C::kColS + sb * kStep;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          mma_bf16_ts(d, tmem + C::kColQ + 8 * i, kd + ((i / 4) * (kStep * 8) + (i % 4) * 2), id_s,
-                      i > 0);
-        mma_commit(&bars.k_empty[k % C::kOpsK]);
-        mma_commit(&bars.s_full[k % C::kS]);
-        if (last) mma_commit(&bars.q_free);
+          for (int i = 0; i < D / 16; ++i)
+            mma_bf16_ts(d, tmem + C::kColQ + 8 * i, kd + ((i / 4) * (kStep * 8) + (i % 4) * 2), id_s,
+                        i > 0);
+          mma_commit(&bars.k_empty[op]);
+          mma_commit(&bars.s_full[sb]);
+          if (last) mma_commit(&bars.q_free);
+        }
+        __syncwarp();
         return true;
       };
       for (int k = 0, kq = 0; ok; ++k) {  // kq: parts with steps
-        ok = part_ready(k);
+        ok = __all_sync(~0u, part_ready(k));
         if (!ok) break;
-        const bool some = parts[k % kParts].some;
-        const int steps = parts[k % kParts].t1 - parts[k % kParts].t0;
-        part_read(k);
+        const bool some = __shfl_sync(~0u, parts[k % kParts].some, 0);
+        const int steps = __shfl_sync(~0u, parts[k % kParts].t1 - parts[k % kParts].t0, 0);
+        __syncwarp();
+        if (lane == 0) part_read(k);
         if (!some) break;
         if (steps == 0) continue;
-        ok = mbar_wait(&bars.q_full, kq & 1, a.err);
+        ok = __all_sync(~0u, mbar_wait(&bars.q_full, kq & 1, a.err));
         if (!ok) break;
         // two steps of scores ahead of the products
         ok = scores(n, steps == 1) && (steps < 2 || scores(n + 1, steps == 2));
         for (int t = 0; t < steps && ok; ++t, ++n) {
-          ok = mbar_wait(&bars.v_full[n % C::kOpsV], (n / C::kOpsV) & 1, a.err) &&
-               mbar_wait(&bars.p_full[n % C::kS], (n / C::kS) & 1, a.err) &&
+          const int op = n % C::kOpsV, sb = n % C::kS;
+          ok = mbar_wait(&bars.v_full[op], (n / C::kOpsV) & 1, a.err) &&
+               mbar_wait(&bars.p_full[sb], (n / C::kS) & 1, a.err) &&
                (t > 0 || kq == 0 || mbar_wait(&bars.o_free, (kq - 1) & 1, a.err));
+          ok = __all_sync(~0u, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vd = v_desc + (n % C::kOpsV) * (C::kK / 16);
-          const uint32_t w = tmem + C::kColS + (n % C::kS) * kStep;
-          const uint32_t more = t > 0;
+          if (lead) {
+            const uint64_t vd = v_desc + op * (C::kK / 16);
+            const uint32_t w = tmem + C::kColS + sb * kStep;
+            const uint32_t more = t > 0;
 #pragma unroll
-          for (int i = 0; i < kStep / 16; ++i)
-            mma_bf16_ts(tmem, w + 8 * i, vd + 2 * i, id_o, i > 0 ? 1u : more);
-          mma_commit(&bars.v_empty[n % C::kOpsV]);
-          mma_commit(&bars.pv_done[n % C::kS]);
+            for (int i = 0; i < kStep / 16; ++i)
+              mma_bf16_ts(tmem, w + 8 * i, vd + 2 * i, id_o, i > 0 ? 1u : more);
+            mma_commit(&bars.v_empty[op]);
+            mma_commit(&bars.pv_done[sb]);
+          }
+          __syncwarp();
           if (t + 2 < steps) ok = scores(n + 2, t + 3 == steps);
         }
         ++kq;
       }
       // every MMA, those of a run that a wait cut short too, has ended before the tensor memory is
       // given back
-      mma_commit(&bars.ended);
+      if (lead) mma_commit(&bars.ended);
+      __syncwarp();
       mbar_wait(&bars.ended, 0, a.err);
     }
     __syncwarp();
@@ -714,23 +784,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (lane == 0) part_read(k);
       if (!p.some) break;
       if (p.t0 == p.t1) continue;
-      if (kq > 0) ok = __all_sync(~0u, mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
-      if (!ok) break;
-      // queries: every warp scales eight rows, four warps (one for each 32 lanes) move them on
+      // queries: every warp scales eight rows, four warps (one for each 32 lanes) move them on once
+      // the part before has used its own
       QueryRows<D> q;
       q.load(a, p, 8 * (warp - kKeyWarp), row_exp[kq % kExps]);
 #pragma unroll
       for (int pass = 0; pass < C::kQPasses && ok; ++pass) {
         const int turn = kq * C::kQPasses + pass;
-        if (pass > 0)
+        if (turn > 0)
           ok = __all_sync(~0u, mbar_wait(&bars.q_copied, (turn - 1) & 1, a.err));
         if (!ok) break;
         q.store(ops, 8 * (warp - kKeyWarp), pass * C::kQGroups);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.q_staged);
         if (warp < kKeyWarp + 4) {
-          ok = __all_sync(~0u, mbar_wait(&bars.q_staged, turn & 1, a.err));
+          ok = mbar_wait(&bars.q_staged, turn & 1, a.err) &&
+               (pass > 0 || kq == 0 || mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
+          ok = __all_sync(~0u, ok);
           if (!ok) break;
+          tc_fence_after();
           copy_queries<D>(ops, tmem, pass * C::kQGroups);
           __syncwarp();
           if (lane == 0) {
@@ -741,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       }
       if (!ok) break;
       ++kq;
+      if (prepared) continue;  // (steps are counted by those who use them)
       const int t0 = p.t0, t1 = p.t1, kv = p.r.kv;
       for (int t = t0; t < t1; ++t, ++n) {
         const int which = is_key ? 0 : 1, ring = is_key ? C::kRawK : C::kRawV;
@@ -791,7 +864,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const int least = seen_by(p.r, p.rt * kRows / a.d.G);
       float m = -INFINITY, l = 0.f, unit = 0.f;
       for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-        ok = __all_sync(~0u, mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err));
+        ok = mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err) &&
+             (!prepared || mbar_wait(&bars.x_full[n % kExps], (n / kExps) & 1, a.err));
+        ok = __all_sync(~0u, ok);
         if (!ok) break;
         tc_fence_after();
         if (t == p.t0)  // back from the scaled queries' units to log2 units
@@ -954,8 +1029,111 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   }
 }
 
+// ------------------------------------------------------------------- contexts as operands
+
+// Forms the MMA operands of every step of every context once, for calls whose contexts many row
+// tiles read.
+constexpr int kPrepThreads = 512;
+constexpr int kPrepTiles = 3;  // row tiles per context, on average, from which it pays
+constexpr int64_t kMostPrep = 512ll << 20;  // bytes of operands held
+
 template <int D>
-cudaError_t launch(const FwdArgs& a, int sms, cudaStream_t s) {
+struct PrepCfg {
+  using C = Cfg<D>;
+  static constexpr int kRaw = 2 * C::kK;
+  static constexpr int kRawV = kRaw + kRecs * C::kSideK;
+  static constexpr int kFirst = kRawV + kRecs * C::kSideV;
+  static constexpr int kSmem = kFirst;
+};
+
+__device__ __forceinline__ void store_operands(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a) {
+  using C = Cfg<D>;
+  using P = PrepCfg<D>;
+  using R = Record<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint4 tables[kDeqWarps][4 * C::NG];
+  __shared__ Exps exps[kRecs];
+  __shared__ int64_t sums[kPrepThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  int64_t* first = reinterpret_cast<int64_t*>(smem + P::kFirst);
+  pdl_wait();
+  pdl_trigger();
+  // Steps of each context in the lower half, steps of its row tiles (a causal prompt's on average)
+  // in the upper one; both capped far above what is ever taken.
+  constexpr int64_t kCap = 1 << 20;
+  cut_work<kPrepThreads>(a, first, sums, 1, [&](const Req& r) {
+    if (r.qn == 0) return (int64_t)0;
+    const int64_t steps = a.d.Hkv * (int64_t)((r.kv + kStep - 1) / kStep);
+    const int64_t mean = a.d.Hkv * (int64_t)((max(r.kv - r.qn / 2, 0) + kStep - 1) / kStep);
+    return min(steps, kCap) | min(mean * row_tiles(a, r), kCap) << 32;
+  });
+  const int64_t both = first[a.B];
+  const int64_t steps = both & 0xffffffff;
+  const bool prepared = steps <= a.prep_cap && (both >> 32) >= kPrepTiles * steps;
+  for (int b = tid; b <= a.B; b += kPrepThreads) {
+    first[b] &= 0xffffffff;
+    if (blockIdx.x == 0 && b < a.B) a.prep_at[1 + b] = (int)min(first[b], (int64_t)INT_MAX);
+  }
+  if (blockIdx.x == 0 && tid == 0) a.prep_at[0] = prepared;
+  if (!prepared) return;
+  __syncthreads();
+
+  const uint32_t ops = smem_u32(smem);
+  for (int u = blockIdx.x; u < (int)steps; u += gridDim.x) {
+    const int b = find_request(first, a.B, u);
+    const int kv = load_req(a, b).kv, of = (kv + kStep - 1) / kStep;
+    const int h = (u - (int)first[b]) / of, t = (u - (int)first[b]) % of;
+    const int have = min((kv + 15) / 16 - t * kRecs, kRecs);
+    constexpr int kPieces = R::kBytes / 16;
+    for (int i = tid; i < have * kPieces; i += kPrepThreads) {
+      const int rec = i / kPieces, at = i % kPieces * 16;
+      const uint4 w = *reinterpret_cast<const uint4*>(
+          a.cache + (uint64_t)cache_record(a, b, h, t * kRecs + rec) * R::kBytes + at);
+      if (at < R::kV) *reinterpret_cast<uint4*>(smem + P::kRaw + rec * C::kSideK + at) = w;
+      if (at >= R::kVp)
+        *reinterpret_cast<uint4*>(smem + P::kRawV + rec * C::kSideV + at - R::kVp) = w;
+    }
+    __syncthreads();
+    Dequant<D> d;
+    const int oct = warp & 7, tok = t * kStep + 8 * oct;
+    if (warp < kDeqWarps) {
+      d.keys(ops + P::kRaw, oct, tok, kv, &exps[oct >> 1]);
+      d.store_keys(ops, oct);
+    } else {
+      d.values(ops + P::kRawV - R::kVp, tables[oct], oct, tok, kv);
+      d.store_values(ops + C::kK, oct);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      store_operands(a.prep + (int64_t)u * 2 * C::kK, ops, 2 * C::kK);
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    } else if (tid >= 32 && tid < 32 + kRecs) {
+      a.prep_exps[(int64_t)u * kRecs + tid - 32] = *reinterpret_cast<const uint4*>(&exps[tid - 32]);
+    }
+    __syncthreads();
+  }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+template <int D>
+cudaError_t launch(const FwdArgs& args, int sms, cudaStream_t s) {
+  FwdArgs a = args;
+  if ((int64_t)a.max_q * a.d.G > (kPrepTiles - 1) * kRows) {
+    const cudaError_t e = launch_pdl(attn_prepare_kernel<D>, dim3(2 * sms), dim3(kPrepThreads),
+                                     PrepCfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
+    if (e != cudaSuccess) return e;
+  } else {
+    a.prep_cap = 0;
+  }
   const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
   const cudaError_t e =
       launch_pdl(attn_prefill_kernel<D>, dim3(blocks), dim3(kThreads),
@@ -966,6 +1144,10 @@ cudaError_t launch(const FwdArgs& a, int sms, cudaStream_t s) {
 
 template <int D>
 cudaError_t prepare(int max_requests) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      attn_prepare_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      PrepCfg<D>::kSmem + (max_requests + 1) * (int)sizeof(int64_t));
+  if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Cfg<D>::kSmem + (max_requests + 1) * (int)sizeof(int64_t));
 }
@@ -973,6 +1155,16 @@ cudaError_t prepare(int max_requests) {
 }  // namespace
 
 size_t attn_prefill_part_floats(int D) { return (size_t)kRows * D; }
+
+size_t attn_prep_step_bytes(int D) { return (size_t)2 * kStep * D * 2; }
+
+// As many as the cache's pages can make, up to kMostPrep bytes; calls with more of them (contexts
+// that share pages) are not prepared.
+int attn_prep_steps(const AttnDims& d, int max_requests) {
+  const int64_t all =
+      d.Hkv * ((((int64_t)d.n_pages << d.page_shift) + kStep - 1) / kStep + max_requests);
+  return (int)std::min(all, kMostPrep / (int64_t)attn_prep_step_bytes(d.D));
+}
 
 cudaError_t prepare_attn_prefill_kernels(int max_requests) {
   cudaError_t e;
