@@ -50,7 +50,9 @@
  * Ownership and threading: every tensor is a caller-owned device pointer; calls only enqueue
  * work on `stream` (a cudaStream_t as void*, NULL = the legacy default stream) and never
  * synchronise the host or allocate.  The handle owns a device workspace (partial results of
- * contexts that several blocks share) and an error word; use a handle on one stream at a time.
+ * contexts that several blocks share; contexts in the form that prompts read, 4 bytes for each
+ * channel that the cache's pages hold, 512 MB at most: longer ones are read as they are, more
+ * slowly) and an error word; use a handle on one stream at a time.
  * Rows are strided: a stride is the distance between tokens in elements, a multiple of 8 and at
  * least the width of a token's heads; heads are adjacent, their channels contiguous.  Row
  * pointers are 16-byte aligned, index arrays 4-byte aligned.  Outputs must not overlap inputs,

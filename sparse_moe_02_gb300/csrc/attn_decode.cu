@@ -19,8 +19,8 @@
 // Layout of the work.  The rows of a key/value head (G query heads x new tokens) are the MMA's N
 // side in tiles of 8, its 16 tokens the M side of the scores; a cached row is read once for all
 // of them.  One block of twelve warps per SM; each warp takes every twelfth tile of
-// 16 tokens of a context through a ring of its own (one bulk copy a tile, its cache record) and keeps its own softmax state and outputs; the block joins its warps through
-// shared memory.  Contexts are cut evenly over the blocks: with W units of work in all (a tile is
+// 16 tokens of a context through a ring of its own (one bulk copy a tile, its cache record) and keeps
+// its own softmax state and outputs; the block joins its warps through shared memory.  Contexts are cut evenly over the blocks: with W units of work in all (a tile is
 // one, a context's fixed cost kPartCost more), block i takes [i W / n, (i + 1) W / n) whatever
 // requests they belong to, so ragged batches balance; a second launch joins the partial results of
 // contexts that several blocks share, in block order (the same inputs give the same bits).  Short

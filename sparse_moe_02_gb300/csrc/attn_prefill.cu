@@ -2,27 +2,31 @@
 // prompts, and batches that hold any of them, on the tcgen05 tensor cores.
 //
 // A block works on 128 query rows of one key/value head (row = new token * G + query head) in steps
-// of 64 cached tokens.  Four warps hold the softmax (a thread per row), eight turn cached keys and
-// eight cached values into f16 MMA operands, one issues the MMAs, one finds the work and copies
-// cache records.
+// of 64 cached tokens.  Four warps hold the softmax (a thread per row); eight turn cached keys and
+// eight cached values into f16 MMA operands, and all sixteen stage queries and write outputs; one
+// issues the MMAs, one finds the work, two copy.
 //   S [128 x 64] = Q K^T      A = Q in tensor memory, B = keys [64][D] in shared memory
 //   O [128 x D] += P V        A = P in tensor memory (over S), B = values [D][64] (channels by
 //                             tokens, so both operands are K-major)
 // Scores run ahead: those of step n + 2 are queued behind the product of step n.  With 256 channels
 // a step of 64 tokens takes 1300 clocks of MMAs (64 columns: 49 clocks each, 256 columns: 129,
-// measured alone).  One thread issues the MMAs, from descriptors that are formed once and stepped by
-// constants: forming each anew took 80 clocks.
+// measured alone).  The MMA warp runs its loop as a whole and one elected thread issues, from
+// descriptors that are formed once and stepped by constants in uniform registers: issued from one
+// thread's branch, the second case below took 957 us instead of 767.
 //
-// What bounds it is the dequantising: a step takes 2800 clocks, in which the block issues some 7400
-// warp instructions (67% of the issue slots) and the key warps never wait; the tensor pipe is busy
-// for 37% of them.  Every 128 rows dequantise their context anew, so the rate rises with neither
-// rows nor context beyond this.  Where queries are (tensor or shared memory) changes a long context
-// by less than 1%; in tensor memory they leave room for two steps of value operands, which is worth
-// 7% on chunks and 20% with 64 channels, and costs 4% on a prompt of 4096.
+// Every 128 rows of a head read the same context, and turning it into operands takes 2800 clocks a
+// step (16 warps, two thirds of the block's issue slots), twice the MMAs.  So where contexts are read
+// by many row tiles (kPrepTiles) a first launch, attn_prepare_kernel, forms the operands of every
+// step once, in the handle's workspace, and this kernel copies them (64 KB a step from L2, 580 to 890
+// clocks with all SMs at it) while its dequantising warps only stage queries and write outputs.  A
+// step then takes 1600 clocks; what is left over the MMAs is the wait for the product whose weights
+// lie where the next scores go (a third score buffer, with half of Q in shared memory, was no
+// faster).
 //
-// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 247 us (555 TFLOP/s),
-// 2048 over a context of 32K 1177 us (884 TFLOP/s, 46% of a bf16 product's rate); ragged chunks
-// 102 us; 4096 tokens of 32 heads over 8 of 128 channels 277 us, of 64 channels 240 us.
+// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 155 us (885 TFLOP/s,
+// prepared; 215 us if not), 2048 over a context of 30000 760 us (1.37 PFLOP/s, 71% of a bf16 product's
+// rate; 1099 us); 4096 tokens of 32 heads over 8 of 128 channels 181 us, over 4 of 64 channels 164
+// us.  Of the 155 us the prepare launch takes 8, the joins 10, start and tail of the blocks 15.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -49,7 +53,7 @@ constexpr int kStep = 64;            // tokens per step
 constexpr int kRecs = kStep / 16;    // cache records per step
 constexpr int kSoftWarps = 4;        // warps 0 .. 3
 constexpr int kKeyWarp = 4, kValueWarp = 12, kDeqWarps = 8;  // the first of eight each
-constexpr int kMmaWarp = 20, kLoadWarp = 21, kValueLoadWarp = 22;
+constexpr int kMmaWarp = 20, kLoadWarp = 21, kValueLoadWarp = 22, kFindWarp = 23;
 constexpr int kThreads = 768;        // six warpgroups
 // Registers of a thread by warpgroup (softmax, four of dequantising warps, the rest): together the
 // 80 a thread that the launch grants.
@@ -63,6 +67,9 @@ template <int D>
 struct Cfg {
   using R = Record<D>;
   static constexpr int NG = D / kGroup;
+  // a row tile's fixed cost in tokens (kPartCost) over prepared contexts, whose steps are shorter:
+  // its queries and outputs
+  static constexpr int kPartCostPrep = D == 64 ? 256 : D * 5 / 2;
   // steps of key operands, value operands, and the records' key and value sides held
   static constexpr int kOpsK = 2, kOpsV = 2, kRawK = D == 256 ? 3 : 4, kRawV = D == 256 ? 2 : 4;
   static constexpr int kS = D == 256 ? 2 : 4;  // score buffers: what tensor memory holds
@@ -190,7 +197,6 @@ constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 // request without cached tokens, whose rows are only zeroed, cost kZeroCost G each.
 constexpr int kPartCost = 320;   // tokens: a row tile's fixed cost
 constexpr int kZeroCost = 96;
-constexpr int kPartCostPrep = 640;  // the same, of prepared contexts, whose steps are shorter
 constexpr int kLeastSteps = 4;   // of a block
 
 struct Cost {
@@ -269,7 +275,7 @@ struct Bars {
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[C::kS], p_full[C::kS], pv_done[C::kS];
   uint64_t x_full[kExps];  // exponents of prepared steps
-  uint64_t q_staged, q_copied, q_full, q_free, o_free, ended;
+  uint64_t q_staged, q_copied, q_full, q_free, o_scaled, o_done, o_free, ended;
 };
 
 // True in one thread of the (converged) warp.
@@ -531,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   __shared__ uint4 tables[kDeqWarps][4 * NG];
   __shared__ Part parts[kParts];
   __shared__ int8_t row_exp[kExps][kRows];  // of the queries of the last parts
-  __shared__ __nv_bfloat16* rows[kRows];  // of the output
+  __shared__ float out_scale[2][kRows];  // of the outputs of the last parts
   __shared__ uint32_t tmem_base;
   __shared__ int64_t sums[kThreads / 32];
   __shared__ Cut cut_s;
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   if (tid == 0) {
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&bars.part_full[i], 1);
-      mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 2);
+      mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 3);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(&bars.raw_full[0][i], 1);
@@ -565,7 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     mbar_init(&bars.q_copied, 4);
     mbar_init(&bars.q_full, 4);
     mbar_init(&bars.q_free, 1);
-    mbar_init(&bars.o_free, 32 * kSoftWarps);
+    mbar_init(&bars.o_scaled, kSoftWarps);
+    mbar_init(&bars.o_done, 1);
+    mbar_init(&bars.o_free, 2 * kDeqWarps);
     mbar_init(&bars.ended, 1);
     fence_mbar_init();
   }
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   pdl_trigger();
   int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
   const bool prepared = a.prep_cap > 0 && a.prep_at[0];
-  const int part_cost = prepared ? kPartCostPrep : kPartCost;
+  const int part_cost = prepared ? C::kPartCostPrep : kPartCost;
   {
     const Cut cut =
         cut_work<kThreads>(a, first, sums, (int64_t)kLeastSteps * kStep * a.d.G, [&](const Req& r) {
@@ -669,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       for (int k = max(0, n - ring); k < n; ++k)
         mbar_wait(&bars.raw_full[which][k % ring], (k / ring) & 1, a.err);
     };
-    if (warp == kLoadWarp) {
+    if (warp == kFindWarp) {
       int64_t w = 0, w1 = 0;
       if ((int)blockIdx.x < cut_s.blocks)
         w = cut_s.bound(blockIdx.x), w1 = cut_s.bound(blockIdx.x + 1);
@@ -684,11 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
         if (!p.some) break;
         w = p.next;
-        if (prepared) copy_prepared(0, prepared_at(p), p.t0, p.t1);
-        else copy_sides(0, p.b, p.h, p.r.kv, p.t0, p.t1);
       }
-      drain(0);
-    } else if (warp == kValueLoadWarp) {
+    } else if (warp == kLoadWarp || warp == kValueLoadWarp) {
+      const int which = warp == kValueLoadWarp;
       for (int k = 0; ok; ++k) {
         ok = __all_sync(~0u, part_ready(k));
         if (!ok) break;
@@ -696,10 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         __syncwarp();
         if (lane == 0) part_read(k);
         if (!p.some) break;
-        if (prepared) copy_prepared(1, prepared_at(p), p.t0, p.t1);
-        else copy_sides(1, p.b, p.h, p.r.kv, p.t0, p.t1);
+        if (prepared) copy_prepared(which, prepared_at(p), p.t0, p.t1);
+        else copy_sides(which, p.b, p.h, p.r.kv, p.t0, p.t1);
       }
-      drain(1);
+      drain(which);
     } else if (warp == kMmaWarp) {
       // the whole warp walks through the steps, so that all that the MMAs take is uniform; one of
       // its threads issues them
@@ -711,7 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         const int op = k % C::kOpsK, sb = k % C::kS;
         // (the buffer's weights of step k - C::kS have been used)
         const bool go = mbar_wait(&bars.k_full[op], (k / C::kOpsK) & 1, a.err) &&
-                        (k < C::kS || mbar_wait(&bars.pv_done[sb], ((k - C::kS) / C::kS) & 1, a.err));
+                        (k < C::kS ||
+                         mbar_wait(&bars.pv_done[sb], ((k - C::kS) / C::kS) & 1, a.err));
         if (!__all_sync(~0u, go)) return false;
         tc_fence_after();
         if (lead) {
@@ -758,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
               mma_bf16_ts(tmem, w + 8 * i, vd + 2 * i, id_o, i > 0 ? 1u : more);
             mma_commit(&bars.v_empty[op]);
             mma_commit(&bars.pv_done[sb]);
+            if (t + 1 == steps) mma_commit(&bars.o_done);
           }
           __syncwarp();
           if (t + 2 < steps) ok = scores(n + 2, t + 3 == steps);
@@ -776,14 +784,78 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     const bool is_key = warp < kValueWarp;
     const int oct = warp - (is_key ? kKeyWarp : kValueWarp);
     Dequant<D> d;
-    for (int k = 0, kq = 0; ok; ++k) {  // kq: parts with steps
+    // Outputs of part k, the kq-th with steps, from tensor memory: 16 rows of a group at a time, four
+    // warps to the 32 lanes that each of them may read.
+    auto outputs = [&](int k, int kq) {
+      const int quarter = warp & 3;
+      bool go = mbar_wait(&bars.o_done, kq & 1, a.err) && mbar_wait(&bars.o_scaled, kq & 1, a.err);
+      go = __all_sync(~0u, go);
+      if (!go) return false;
+      tc_fence_after();
+      const Part& p = parts[k % kParts];
+      const bool whole = p.t1 - p.t0 == p.tiles;
+      const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows;
+      const int c = lane & 3;
+#pragma unroll 1
+      for (int u = (warp - kKeyWarp) >> 2; u < 2 * NG; u += 4) {
+        const int hf = u & 1, g = u >> 1;
+        const int ra = 32 * quarter + 16 * hf + (lane >> 2);
+        // [nibble][row ra words 2c, 2c + 1; row ra + 8 words 2c, 2c + 1]
+        uint32_t o[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          tmem_ld_16x8(tmem + ((uint32_t)(32 * quarter + 16 * hf) << 16) + out_column<NG>(g, i),
+                       o[i]);
+        wait_ld32(&o[0][0]);
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          const int r = ra + 4 * q, row = p.rt * kRows + r;
+          const float f = out_scale[kq & 1][r];
+          uint8_t* d = nullptr;
+          if (!whole)
+            d = reinterpret_cast<uint8_t*>(a.part_o + (at + r) * D);
+          else if (row < p.r.qn * a.d.G)
+            d = reinterpret_cast<uint8_t*>(a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
+                                           (int64_t)(p.h * a.d.G + row % a.d.G) * D);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[i][q + w]) * f;
+            if (whole) {
+              uint32_t x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                x[i] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              if (d)
+                *reinterpret_cast<uint4*>(d + 128 * g + 16 * (2 * c + w)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
+            } else {
+              float4* part = reinterpret_cast<float4*>(d) + 16 * g + 2 * c + w;
+              part[0] = make_float4(v[0], v[1], v[2], v[3]);
+              part[8] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.o_free), part_read(k);
+      return true;
+    };
+    int k_last = 0, kq = 0;  // the last part with steps; how many so far
+    for (int k = 0; ok; ++k) {
       ok = __all_sync(~0u, part_ready(k));
       if (!ok) break;
       const Part p = parts[k % kParts];
-      __syncwarp();
-      if (lane == 0) part_read(k);
       if (!p.some) break;
-      if (p.t0 == p.t1) continue;
+      if (p.t0 == p.t1) {
+        __syncwarp();
+        if (lane == 0) part_read(k);
+        continue;
+      }
       // queries: every warp scales eight rows, four warps (one for each 32 lanes) move them on once
       // the part before has used its own
       QueryRows<D> q;
@@ -812,7 +884,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
       }
       if (!ok) break;
+      if (kq > 0 && !(ok = outputs(k_last, kq - 1))) break;
       ++kq;
+      k_last = k;
       if (prepared) continue;  // (steps are counted by those who use them)
       const int t0 = p.t0, t1 = p.t1, kv = p.r.kv;
       for (int t = t0; t < t1; ++t, ++n) {
@@ -842,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         if (lane == 0) mbar_arrive(is_key ? &bars.k_full[op] : &bars.v_full[op]);
       }
     }
+    if (ok && kq > 0) outputs(k_last, kq - 1);
   } else {
     registers_up<kRegsSoft>();
     // softmax: row `tid` of the row tile, tensor memory lane tid
@@ -857,9 +932,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const int rows_left = p.r.qn * a.d.G;
       const int row = row0 + lane, tok = row / a.d.G;
       const bool on = row < rows_left;
-      rows[tid] = on ? a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
-                           (int64_t)(p.h * a.d.G + row % a.d.G) * D
-                     : nullptr;
       const int lim = on ? seen_by(p.r, tok) : p.r.kv;
       const int least = seen_by(p.r, p.rt * kRows / a.d.G);
       float m = -INFINITY, l = 0.f, unit = 0.f;
@@ -942,72 +1014,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       }
       if (!ok) break;
       if (p.tiles == 0) {  // rows that see nothing
-        __syncwarp();
+        const uint64_t own =
+            on ? reinterpret_cast<uint64_t>(a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
+                                            (int64_t)(p.h * a.d.G + row % a.d.G) * D)
+               : 0;
         for (int i = lane; i < 32 * (D / 8); i += 32) {
-          __nv_bfloat16* d = rows[warp * 32 + i / (D / 8)];
-          if (d) *reinterpret_cast<uint4*>(d + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
+          const uint64_t dst = __shfl_sync(~0u, own, i / (D / 8));
+          if (dst) reinterpret_cast<uint4*>(dst)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
         }
-        __syncwarp();
         continue;
       }
-      ++kq;
-      // outputs: after the last product
-      ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err));
-      if (!ok) break;
-      tc_fence_after();
       const bool whole = p.t1 - p.t0 == p.tiles;
-      const float inv = whole ? (l == 0.f ? 0.f : 64.f / l) : 64.f;
-      const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows + warp * 32;
+      out_scale[kq & 1][tid] = whole ? (l == 0.f ? 0.f : 64.f / l) : 64.f;
       __syncwarp();
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {  // rows 16 hf .. 16 hf + 15 of the warp
-        const int c = lane & 3, ra = 16 * hf + (lane >> 2), rb = ra + 8;
-        const float inv_a = __shfl_sync(~0u, inv, ra), inv_b = __shfl_sync(~0u, inv, rb);
-        uint8_t *da, *db;
-        if (whole) {
-          da = reinterpret_cast<uint8_t*>(rows[warp * 32 + ra]);
-          db = reinterpret_cast<uint8_t*>(rows[warp * 32 + rb]);
-        } else {
-          da = reinterpret_cast<uint8_t*>(a.part_o + (at + ra) * D);
-          db = reinterpret_cast<uint8_t*>(a.part_o + (at + rb) * D);
-        }
-#pragma unroll 1
-        for (int g = 0; g < NG; ++g) {
-          // [nibble][row a words 2c, 2c + 1; row b words 2c, 2c + 1]
-          uint32_t o[8][4];
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            tmem_ld_16x8(lane_base + ((uint32_t)(16 * hf) << 16) + out_column<NG>(g, i), o[i]);
-          wait_ld32(&o[0][0]);
-          if (hf == 1 && g == NG - 1) {
-            tc_fence_before();
-            mbar_arrive(&bars.o_free);
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float f = q < 2 ? inv_a : inv_b;
-            uint8_t* d = q < 2 ? da : db;
-            const int j = 2 * c + (q & 1);
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[i][q]) * f;
-            if (whole) {
-              uint32_t x[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                x[i] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-              if (d)
-                *reinterpret_cast<uint4*>(d + 128 * g + 16 * j) = make_uint4(x[0], x[1], x[2], x[3]);
-            } else {
-              float4* part = reinterpret_cast<float4*>(d) + 16 * g + j;
-              part[0] = make_float4(v[0], v[1], v[2], v[3]);
-              part[8] = make_float4(v[4], v[5], v[6], v[7]);
-            }
-          }
-        }
-      }
+      if (lane == 0) mbar_arrive(&bars.o_scaled);
+      ++kq;
+      const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows + warp * 32;
       if (!whole) {
         a.part_ml[at + lane] = make_float2(m, l);
         if (p.t0 == 0 && tid == 0) {
@@ -1034,7 +1056,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
 // Forms the MMA operands of every step of every context once, for calls whose contexts many row
 // tiles read.
 constexpr int kPrepThreads = 512;
-constexpr int kPrepTiles = 3;  // row tiles per context, on average, from which it pays
+// From this many row tiles per context, on average, it pays (256 channels, 16 contexts of 2000 to
+// 4000 tokens, prepared against not: 4 row tiles 103 and 91 us, 6 122 and 118, 8 142 and 143, 16 (8
+// contexts) 138 and 162; 128 channels: 4 204 and 176, 8 324 and 334).
+constexpr int kPrepTiles = 8;
 constexpr int64_t kMostPrep = 512ll << 20;  // bytes of operands held
 
 template <int D>
