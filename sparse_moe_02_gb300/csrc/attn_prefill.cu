@@ -845,13 +845,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (lane == 0) mbar_arrive(&bars.o_free), part_read(k);
       return true;
     };
-    int k_last = 0, kq = 0;  // the last part with steps; how many so far
+    int due = -1, kq = 0;  // the part whose outputs are to be written; parts with steps so far
     for (int k = 0; ok; ++k) {
       ok = __all_sync(~0u, part_ready(k));
       if (!ok) break;
       const Part p = parts[k % kParts];
       if (!p.some) break;
       if (p.t0 == p.t1) {
+        // (a part's place is held until its outputs are written: not across parts without steps)
+        if (due >= 0 && !(ok = outputs(due, kq - 1))) break;
+        due = -1;
         __syncwarp();
         if (lane == 0) part_read(k);
         continue;
@@ -884,9 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
       }
       if (!ok) break;
-      if (kq > 0 && !(ok = outputs(k_last, kq - 1))) break;
+      if (due >= 0 && !(ok = outputs(due, kq - 1))) break;
       ++kq;
-      k_last = k;
+      due = k;
       if (prepared) continue;  // (steps are counted by those who use them)
       const int t0 = p.t0, t1 = p.t1, kv = p.r.kv;
       for (int t = t0; t < t1; ++t, ++n) {
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         if (lane == 0) mbar_arrive(is_key ? &bars.k_full[op] : &bars.v_full[op]);
       }
     }
-    if (ok && kq > 0) outputs(k_last, kq - 1);
+    if (ok && due >= 0) outputs(due, kq - 1);
   } else {
     registers_up<kRegsSoft>();
     // softmax: row `tid` of the row tile, tensor memory lane tid
