@@ -23,9 +23,9 @@
 // launch that joins the blocks (3 us): these are most of the time of short and middling contexts.
 // Four copies a tile (codes and parameters apart) took 55 us where one takes 50 (64 requests of 4096
 // tokens, three blocks of four warps an SM); one block of twelve warps, the even cut and copies
-// ahead into the next context make it 42.
+// ahead into the next context made it 42, a block per context where lengths are alike 38.
 // Measured, 16 query heads over 2 of 256 channels, one token: 256 cached tokens 7.2 us, 4096 10.5 us,
-// 131072 24.2 us (3.1 TB/s with everything); 48 requests of up to 16384 24.6 us, 64 of 4096 42.3 us (3.6
+// 131072 24.2 us (3.1 TB/s with everything); 48 requests of up to 16384 24.6 us, 64 of 4096 38.2 us (4.0
 // TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 26.7 us.
 //
 // Layout of the work.  The rows of a key/value head (G query heads x new tokens) are the MMA's N
@@ -37,7 +37,8 @@
 // kPartCost more), block i takes [i W / n, (i + 1) W / n) whatever requests they belong to, so ragged
 // batches balance; a second launch joins the partial results of contexts that several blocks share,
 // in block order (the same inputs give the same bits).  Short contexts (max_kv small) take one block
-// each and no second launch.
+// each and no second launch; longer ones of like lengths take one each too, and the second launch
+// finds nothing to do.
 #include <climits>
 
 #include "attn.cuh"
@@ -49,10 +50,12 @@ namespace {
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens per ring stage: the MMA's M side, and a whole number per page
-// One block per context, no partial results, up to this many tokens: the second launch costs 3 us, a
-// block's twelve warps take 64 tokens in the time of a step (1 request of 1024 tokens: 13.0 us whole,
-// 10.9 us cut).
-constexpr int kWholeKv = 768;
+// One block per context, no partial results and no second launch, up to 768 tokens and 8 more for each
+// context, at most 1536: the cut costs 3 us and a block's fixed costs per part, a whole context the time
+// of its tiles on one SM.  Whole against cut, 2 contexts of 768 tokens 10.5 and 10.8 us, of 1024 12.5 and
+// 10.9; 16 of 1024 12.6 and 12.8; 96 of 1024 12.8 and 20.0, of 1500 16.1 and 22.7, of 1 to 1500 15.7 and
+// 15.4; 256 of 1 to 1500 20.5 and 22.7.
+constexpr int kWholeKv = 768, kWholeMore = 8, kWholeMost = 1536;
 constexpr float kSlack = 6.f;  // growth of the reference a tile may bring before a rescale
 constexpr float kLift = 9.f;   // w <= 2^(kLift + kSlack) at the reference
 constexpr int kJoinWarps = 4;  // warps whose outputs the join buffer holds at once
@@ -161,6 +164,10 @@ __device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1)
 // Work of a context: its tiles, and kPartCost tiles' worth for what a part costs besides (queries,
 // page ids, first copies, joins), so that blocks of many short contexts get fewer tiles.
 constexpr int kPartCost = 40;
+// Longer contexts, seen to be of like lengths once their lengths are known, take a block each too, if
+// none has this much more work than a block's share: a cut would cost a part and a join more (128
+// contexts of 2500 tokens 26.8 and 32.5 us, of 4096 38.2 and 42.5).
+constexpr int kEachMore = 64;
 constexpr int kLeastWork = 12;  // of a block: a tile a warp (4096 tokens 10.5 us; with 32 12.5 us)
 
 // What a lane keeps of the query rows (columns) of one context; their MMA B fragments lie in
@@ -509,6 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   __shared__ Part parts[2];
   __shared__ int64_t sums[kWarps];
   __shared__ Cut cut_s;
+  __shared__ int longest;  // work of the longest context
+  __shared__ bool each;    // a block takes one context
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int j = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * C::kStages * C::kStage;
@@ -518,32 +527,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   if (lane == 0)
     for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
   fence_mbar_init();
+  if (!WHOLE) {
+    if (tid == 0) longest = 0;
+    __syncthreads();
+  }
   pdl_wait();
   pdl_trigger();
 
   int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);  // [B + 1]
   if (!WHOLE) {
     const Cut cut = cut_work<kThreads>(a, first, sums, kLeastWork, [&](const Req& r) {
-      return r.qn > 0 ? (int64_t)(a.d.Hkv * row_tiles(a, r.qn, C::kCols)) *
-                            (kv_tiles(r.kv) + kPartCost)
-                      : (int64_t)0;
+      if (r.qn == 0) return (int64_t)0;
+      const int unit = kv_tiles(r.kv) + kPartCost;
+      atomicMax(&longest, unit);
+      return (int64_t)(a.d.Hkv * row_tiles(a, r.qn, C::kCols)) * unit;
     });
     if (tid == 0) cut_s = cut;
   }
   if (tid == 0) {
     Part p;
     p.some = false;
-    if (WHOLE) {
-      const int rts_max = row_tiles(a, a.max_q, C::kCols);
+    const int rts_max = row_tiles(a, a.max_q, C::kCols);
+    if (!WHOLE)
+      each = (int64_t)a.B * a.d.Hkv * rts_max <= gridDim.x && longest <= cut_s.share + kEachMore;
+    if (WHOLE || each) {
       const int k = blockIdx.x % (a.d.Hkv * rts_max);
       p.b = blockIdx.x / (a.d.Hkv * rts_max);
       p.h = k / rts_max;
       p.rt = k % rts_max;
-      p.r = load_req(a, p.b);
-      p.t0 = 0;
-      p.t1 = p.tiles = kv_tiles(p.r.kv);
-      p.some = p.rt < row_tiles(a, p.r.qn, C::kCols);
-      if (k == 0 && req_out_of_range(a, p.b)) record_error(a.err, kDevErrState);
+      if (p.b < a.B) {
+        p.r = load_req(a, p.b);
+        p.t0 = 0;
+        p.t1 = p.tiles = kv_tiles(p.r.kv);
+        p.some = p.rt < row_tiles(a, p.r.qn, C::kCols);
+      }
+      if (WHOLE && k == 0 && req_out_of_range(a, p.b)) record_error(a.err, kDevErrState);
     } else if ((int)blockIdx.x < cut_s.blocks) {
       p = locate(a, first, C::kCols, cut_s.bound(blockIdx.x), cut_s.bound(blockIdx.x + 1));
     }
@@ -588,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
       prepare_query<D, NT>(a, p, smem + C::kQuery + cur * C::kCols * C::kQPitch, warp / NG,
                            warp % NG, S);
     if (tid == kThreads - 1) {
-      if (WHOLE) next.some = false;
+      if (WHOLE || each) next.some = false;
       else next = locate(a, first, C::kCols, p.next, cut_s.bound(blockIdx.x + 1));
     }
     __syncthreads();
@@ -792,8 +810,8 @@ template <int D, int NT>
 cudaError_t launch(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
   using C = Cfg<D, NT>;
   const int rts = (a.max_q * a.d.G + C::kCols - 1) / C::kCols;
-  if (max_kv <= kWholeKv) {
-    const int64_t grid = (int64_t)a.B * a.d.Hkv * rts;
+  const int64_t grid = (int64_t)a.B * a.d.Hkv * rts;
+  if (max_kv <= kWholeKv || (max_kv <= kWholeMost && max_kv <= kWholeKv + kWholeMore * grid)) {
     if (grid <= 0x7fffffff)
       return launch_pdl(attn_decode_kernel<D, NT, true>, dim3((unsigned)grid), dim3(kThreads),
                         C::kSmem, s, a);
