@@ -159,7 +159,8 @@ __device__ __forceinline__ int part_slot(int b0, int i) { return 2 * (b0 + i) + 
 // one long context (76 parts of 8 KB) is spread over 32 blocks and its parts are read in one round
 // trip.  Bound by latency for tokens (3 us, most of it the launch; one warp per column took 11 us
 // over a context of 1024 tokens), by the caches for row tiles (two parts of 128 KB a block, 40 MB
-// in all: 10 us).
+// in all; read eight at a time as for tokens, mostly the last one again, a prompt of 4096 took 156 us
+// instead of 148).
 constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 8;
 constexpr int kMaxBlocks = 256;  // of the attention launch
@@ -183,7 +184,8 @@ __device__ __forceinline__ void add_scaled(float (&o)[N], const float* src, floa
 }
 
 template <int D, int kCols>
-__global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2) attn_join_kernel(FwdArgs a, int blocks) {
+__global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2)
+    attn_join_kernel(FwdArgs a, int blocks) {
   constexpr int kWarpsJ = kJoinThreads / 32;
   __shared__ short few[kMaxBlocks], many[kMaxBlocks];
   __shared__ int2 counts[kWarpsJ];
@@ -213,52 +215,56 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2) attn_join_ke
   __syncthreads();
 
   Part p;
-  for (int u = blockIdx.x; u < nm * kCols * (D / 64); u += gridDim.x) {
-    const int piece = u % (D / 64), col = u / (D / 64) % kCols;
-    const int b0 = many[u / (D / 64) / kCols];
-    const int4 d = a.desc[2 * b0];
-    p.r.qn = a.desc[2 * b0 + 1].x;
-    p.h = d.y;
-    p.rt = d.z;
-    p.r.q0 = d.w;
-    const int n = d.x;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (tid < n) ml = __ldcg(a.part_ml + part_slot(b0, tid) * kCols + col);
-    float m = ml.x;
+  if constexpr (kCols <= 16) {
+    for (int u = blockIdx.x; u < nm * kCols * (D / 64); u += gridDim.x) {
+      const int piece = u % (D / 64), col = u / (D / 64) % kCols;
+      const int b0 = many[u / (D / 64) / kCols];
+      const int4 d = a.desc[2 * b0];
+      p.r.qn = a.desc[2 * b0 + 1].x;
+      p.h = d.y;
+      p.rt = d.z;
+      p.r.q0 = d.w;
+      const int n = d.x;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (tid < n) ml = __ldcg(a.part_ml + part_slot(b0, tid) * kCols + col);
+      float m = ml.x;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    if (lane == 0) red[warp].x = m;
-    __syncthreads();
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+      if (lane == 0) red[warp].x = m;
+      __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kWarpsJ; ++k) m = fmaxf(m, red[k].x);
-    const float f = part_weight(ml.x, ml.y, m);
-    weight[tid] = f;
-    float l = ml.y * f;
+      for (int k = 0; k < kWarpsJ; ++k) m = fmaxf(m, red[k].x);
+      const float f = part_weight(ml.x, ml.y, m);
+      weight[tid] = f;
+      float l = ml.y * f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    if (lane == 0) red[warp].y = l;
-    __syncthreads();
-    const int ln = tid & 15, grp = tid >> 4;
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+      if (lane == 0) red[warp].y = l;
+      __syncthreads();
+      const int ln = tid & 15, grp = tid >> 4;
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 5
-    for (int i = grp; i < n; i += 16)
-      add_scaled(o, a.part_o + ((int64_t)part_slot(b0, i) * kCols + col) * D + 64 * piece + 4 * ln,
-                 weight[i]);
-    *reinterpret_cast<float4*>(&acc[grp][4 * ln]) = make_float4(o[0], o[1], o[2], o[3]);
-    __syncthreads();
-    if (tid < 16) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
+      for (int i = grp; i < n; i += 16)
+        add_scaled(o, a.part_o + ((int64_t)part_slot(b0, i) * kCols + col) * D + 64 * piece + 4 * ln,
+                   weight[i]);
+      *reinterpret_cast<float4*>(&acc[grp][4 * ln]) = make_float4(o[0], o[1], o[2], o[3]);
+      __syncthreads();
+      if (tid < 16) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWarpsJ; ++k) sum += red[k].y;
+        for (int k = 0; k < kWarpsJ; ++k) sum += red[k].y;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) fma4(x, *reinterpret_cast<const float4*>(&acc[k][4 * tid]), 1.f);
-      store_out4(a, p, p.rt * kCols + col, D, 16 * piece + tid, x, sum);
+        for (int k = 0; k < 16; ++k) fma4(x, *reinterpret_cast<const float4*>(&acc[k][4 * tid]), 1.f);
+        store_out4(a, p, p.rt * kCols + col, D, 16 * piece + tid, x, sum);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 
   constexpr int kCh = D / 32;  // channels of a lane
+  // parts read at once: row tiles mostly have two, and their many columns keep enough in flight
+  constexpr int kAtOnce = kCols > 16 ? 2 : kFewParts;
   for (int u = blockIdx.x * kWarpsJ + warp; u < nf * kCols; u += gridDim.x * kWarpsJ) {
     const int col = u % kCols, b0 = few[u / kCols];
     const int4 d = a.desc[2 * b0];
@@ -277,14 +283,14 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2) attn_join_ke
     float o[kCh];
 #pragma unroll
     for (int e = 0; e < kCh; ++e) o[e] = 0.f;
-    for (int i0 = 0; i0 < d.x; i0 += kFewParts) {
+    for (int i0 = 0; i0 < d.x; i0 += kAtOnce) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < kFewParts && i0 + lane < d.x)
+      if (lane < kAtOnce && i0 + lane < d.x)
         ml = __ldcg(a.part_ml + part_slot(b0, i0 + lane) * kCols + col);
       const float f = part_weight(ml.x, ml.y, m);
       l = fmaf(ml.y, f, l);
 #pragma unroll
-      for (int i = 0; i < kFewParts; ++i) {  // beyond the last: it again, with weight 0
+      for (int i = 0; i < kAtOnce; ++i) {  // beyond the last: it again, with weight 0
         const float fi = __shfl_sync(~0u, f, i);
         add_scaled(o,
                    a.part_o + ((int64_t)part_slot(b0, min(i0 + i, d.x - 1)) * kCols + col) * D +
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2) attn_join_ke
       }
     }
 #pragma unroll
-    for (int i = 4; i; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+    for (int i = kAtOnce / 2; i; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
     l = __shfl_sync(~0u, l, 0);
     if constexpr (kCh == 2) {
       // two lanes hold the four channels that are stored at once

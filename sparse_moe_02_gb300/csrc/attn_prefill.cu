@@ -23,10 +23,11 @@
 // lie where the next scores go (a third score buffer, with half of Q in shared memory, was no
 // faster).
 //
-// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 155 us (885 TFLOP/s,
-// prepared; 215 us if not), 2048 over a context of 30000 760 us (1.37 PFLOP/s, 71% of a bf16 product's
-// rate; 1099 us); 4096 tokens of 32 heads over 8 of 128 channels 181 us, over 4 of 64 channels 164
-// us.  Of the 155 us the prepare launch takes 8, the joins 10, start and tail of the blocks 15.
+// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 148 us (930 TFLOP/s,
+// prepared; 205 us if not), 2048 over a context of 30000 763 us (1.36 PFLOP/s, 71% of a bf16 product's
+// rate; 1100 us); 4096 tokens of 32 heads over 8 of 128 channels 181 us (277), over 4 of 64 channels
+// 164 us (233); ragged chunks of 28 heads over 4 of 128 80 us (101).  Of the 148 us the prepare launch
+// takes 8, start and tail of the blocks and the joins 20.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -1060,8 +1061,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
 // tiles read.
 constexpr int kPrepThreads = 512;
 // From this many row tiles per context, on average, it pays (256 channels, 16 contexts of 2000 to
-// 4000 tokens, prepared against not: 4 row tiles 103 and 91 us, 6 122 and 118, 8 142 and 143, 16 (8
-// contexts) 138 and 162; 128 channels: 4 204 and 176, 8 324 and 334).
+// 4000 tokens, prepared against not: 4 row tiles 96 and 83 us, 6 113 and 109, 8 132 and 134, 16 (8
+// contexts) 130 and 152; 128 channels: 4 204 and 177, 8 324 and 337).
 constexpr int kPrepTiles = 8;
 constexpr int64_t kMostPrep = 512ll << 20;  // bytes of operands held
 
