@@ -30,7 +30,8 @@
  *     clamp(rint((x - lo) / step), 0, 15) (ties to even; 0 where step is 0), read back as
  *     step * code + lo; every operation in fp32, so the codes are the same everywhere.  If a
  *     channel of a token's key or value row of a head is not finite, or 2^116 or larger, the key
- *     row's scales become 0 and biases NaN and the value row's 0: every query that sees the token reads NaN and no other query does.
+ *     row's scales become 0 and biases NaN and the value row's 0: every query that sees the token
+ *     reads NaN and no other query does.
  *   attention: o_i = sum_t softmax_t(scale q_i . k_t) v_t over the cached tokens t <= kv_b - n_b +
  *     i of request b (kv_b = its cached tokens with the new ones); a query that sees no token
  *     gives 0.  Scores, softmax sums and outputs are held in fp32 and rounded once to bf16.

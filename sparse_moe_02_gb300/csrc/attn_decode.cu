@@ -25,8 +25,8 @@
 // tokens, three blocks of four warps an SM); one block of twelve warps, the even cut and copies
 // ahead into the next context made it 42, a block per context where lengths are alike 38.
 // Measured, 16 query heads over 2 of 256 channels, one token: 256 cached tokens 7.2 us, 4096 10.5 us,
-// 131072 24.2 us (3.1 TB/s with everything); 48 requests of up to 16384 24.6 us, 64 of 4096 38.2 us (4.0
-// TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 26.7 us.
+// 131072 24.2 us (3.1 TB/s with everything); 48 requests of up to 16384 24.6 us, 64 of 4096 38.2 us
+// (4.0 TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 26.7 us.
 //
 // Layout of the work.  The rows of a key/value head (G query heads x new tokens) are the MMA's N
 // side in tiles of 8, its 16 tokens the M side of the scores; a cached row is read once for all
@@ -50,11 +50,11 @@ namespace {
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens per ring stage: the MMA's M side, and a whole number per page
-// One block per context, no partial results and no second launch, up to 768 tokens and 8 more for each
-// context, at most 1536: the cut costs 3 us and a block's fixed costs per part, a whole context the time
-// of its tiles on one SM.  Whole against cut, 2 contexts of 768 tokens 10.5 and 10.8 us, of 1024 12.5 and
-// 10.9; 16 of 1024 12.6 and 12.8; 96 of 1024 12.8 and 20.0, of 1500 16.1 and 22.7, of 1 to 1500 15.7 and
-// 15.4; 256 of 1 to 1500 20.5 and 22.7.
+// One block per context, no partial results and no second launch, up to 768 tokens and 8 more for
+// each context, at most 1536: the cut costs 3 us and a block's fixed costs per part, a whole context
+// the time of its tiles on one SM.  Whole against cut, 2 contexts of 768 tokens 10.5 and 10.8 us, of
+// 1024 12.5 and 10.9; 16 of 1024 12.6 and 12.8; 96 of 1024 12.8 and 20.0, of 1500 16.1 and 22.7, of 1
+// to 1500 15.7 and 15.4; 256 of 1 to 1500 20.5 and 22.7.
 constexpr int kWholeKv = 768, kWholeMore = 8, kWholeMost = 1536;
 constexpr float kSlack = 6.f;  // growth of the reference a tile may bring before a rescale
 constexpr float kLift = 9.f;   // w <= 2^(kLift + kSlack) at the reference

@@ -138,8 +138,8 @@ __device__ __forceinline__ void wait_ld32(uint32_t* r) {
                  "+r"(r[30]), "+r"(r[31]));
 }
 
-// 16 lanes x 8 columns: thread (n, c) = (i / 4, i % 4) of the warp gets columns 2c, 2c + 1 of lane n (r[0],
-// r[1]) and of lane n + 8 (r[2], r[3]).
+// 16 lanes x 8 columns: thread (n, c) = (i / 4, i % 4) of the warp gets columns 2c, 2c + 1 of lane n
+// (r[0], r[1]) and of lane n + 8 (r[2], r[3]).
 __device__ __forceinline__ void tmem_ld_16x8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -979,7 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           l *= f;
           if (t > p.t0) {
             // the outputs so far, once the last product has landed
-            ok = __all_sync(~0u, mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err));
+            ok = mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err);
+            ok = __all_sync(~0u, ok);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
