@@ -276,7 +276,11 @@ struct Bars {
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[C::kS], p_full[C::kS], pv_done[C::kS];
   uint64_t x_full[kExps];  // exponents of prepared steps
-  uint64_t q_staged, q_copied, q_full, q_free, o_scaled, o_done, o_free, ended;
+  uint64_t q_staged, q_copied, q_full, q_free, o_done, o_free, ended;
+  // Two in turn: the softmax of a part needs its queries, not the outputs of the part before, so it can
+  // end while a warp has yet to look at the part before's; queries of the part after that are staged
+  // behind those outputs by every warp.
+  uint64_t o_scaled[2];
 };
 
 // True in one thread of the (converged) warp.
@@ -572,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     mbar_init(&bars.q_copied, 4);
     mbar_init(&bars.q_full, 4);
     mbar_init(&bars.q_free, 1);
-    mbar_init(&bars.o_scaled, kSoftWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.o_scaled[i], kSoftWarps);
     mbar_init(&bars.o_done, 1);
     mbar_init(&bars.o_free, 2 * kDeqWarps);
     mbar_init(&bars.ended, 1);
@@ -789,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     // warps to the 32 lanes that each of them may read.
     auto outputs = [&](int k, int kq) {
       const int quarter = warp & 3;
-      bool go = mbar_wait(&bars.o_done, kq & 1, a.err) && mbar_wait(&bars.o_scaled, kq & 1, a.err);
+      bool go = mbar_wait(&bars.o_done, kq & 1, a.err) &&
+                mbar_wait(&bars.o_scaled[kq & 1], (kq >> 1) & 1, a.err);
       go = __all_sync(~0u, go);
       if (!go) return false;
       tc_fence_after();
@@ -1032,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const bool whole = p.t1 - p.t0 == p.tiles;
       out_scale[kq & 1][tid] = whole ? (l == 0.f ? 0.f : 64.f / l) : 64.f;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.o_scaled);
+      if (lane == 0) mbar_arrive(&bars.o_scaled[kq & 1]);
       ++kq;
       const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows + warp * 32;
       if (!whole) {
