@@ -1111,6 +1111,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
     return min(steps, kCap) | min(mean * row_tiles(a, r), kCap) << 32;
   });
   const int64_t both = first[a.B];
+  __syncthreads();  // every thread has it, and decides alike, before the sums lose their upper halves
   const int64_t steps = both & 0xffffffff;
   const bool prepared = steps <= a.prep_cap && (both >> 32) >= kPrepTiles * steps;
   for (int b = tid; b <= a.B; b += kPrepThreads) {
