@@ -262,7 +262,7 @@ __device__ __forceinline__ void prepare_query(const FwdArgs& a, const Part& p, c
     S.sum[col][g] = sum * (8192.f / 16777216.f);
     if (g == 0) {
       // code * 2^-24 * q * 2^13-e  ->  log2 units
-      S.scale[col] = up * (16777216.f / 8192.f) * a.d.scale_log2;
+      S.scale[col] = fmaxf(up * (16777216.f / 8192.f) * a.d.scale_log2, kLeastUnit);
       // columns beyond the rows see everything: nothing of them is written
       const int seen = p.r.kv - p.r.qn + row / a.d.G + 1;
       S.lim[col] = row < p.r.qn * a.d.G ? min(max(seen, 0), p.r.kv) : p.r.kv;

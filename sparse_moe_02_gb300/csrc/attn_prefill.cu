@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
 #pragma unroll
         for (int r = 0; r < kRecs; ++r) {
           const float4 v = *reinterpret_cast<const float4*>(&exps[n % kExps][r]);
-          ex[r] = Exps{unit * v.x, v.y, v.z, 0.f};
+          ex[r] = Exps{fmaxf(unit * v.x, kLeastUnit), v.y, v.z, 0.f};
         }
         wait_ld32(s);
         wait_ld32(s + 32);
