@@ -13,6 +13,9 @@
 namespace moe {
 
 constexpr int kGroup = 64;        // channels per scale and bias
+// Requests of a call at most.  The kernels' shared-memory limits are set for as many whatever a handle
+// asks for: they belong to the functions, which the handles of a process share.
+constexpr int kMaxRequests = 1024;
 // Cached rows hold magnitudes below this only (larger ones count as not finite): the kernels'
 // powers of two of a record's bound, 2^118 at most, stay normal fp32 numbers.
 constexpr float kLargest = 8.307675e34f;  // 2^116
@@ -119,7 +122,6 @@ struct PlanArgs {
   int* err;
 };
 
-cudaError_t prepare_attn_plan_kernel(int max_requests);
 cudaError_t launch_attn_plan(const PlanArgs& a, int sms, cudaStream_t s);
 
 struct RopeArgs {
@@ -155,12 +157,12 @@ cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s);
 // grows with every 8 (128 and 64 channels: 16) rows, the other kernel's with every 128: 8 requests of
 // 5 tokens, G = 4, took 27 us here and 44 there, of 8 tokens 49 and 59.
 constexpr int kDecodeRows = 32;
-cudaError_t prepare_attn_decode_kernels(int max_requests);
+cudaError_t prepare_attn_decode_kernels();
 int attn_part_slots(int sms);  // partial results of a launch, of either kernel
 cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s);
 
 // Attention of more rows, and of batches that hold any such request: attn_prefill.cu.
-cudaError_t prepare_attn_prefill_kernels(int max_requests);
+cudaError_t prepare_attn_prefill_kernels();
 size_t attn_prefill_part_floats(int D);  // fp32 of a partial result, the larger of the kernels'
 int attn_prep_steps(const AttnDims& d, int max_requests);  // of contexts held as operands
 size_t attn_prep_step_bytes(int D);                        // of one, without its exponents

@@ -45,7 +45,7 @@ int check_config(const attn_config* c) {
       c->page_size != 256)
     return MOE_ERR_UNSUPPORTED;
   if ((int64_t)c->n_pages * c->page_size > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  if (c->max_requests > 1024) return MOE_ERR_UNSUPPORTED;
+  if (c->max_requests > moe::kMaxRequests) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -93,9 +93,8 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
   if ((st = record_cuda_status(
            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))))
     return st;
-  if ((st = record_cuda_status(moe::prepare_attn_plan_kernel(cfg->max_requests)))) return st;
-  if ((st = record_cuda_status(moe::prepare_attn_decode_kernels(cfg->max_requests)))) return st;
-  if ((st = record_cuda_status(moe::prepare_attn_prefill_kernels(cfg->max_requests)))) return st;
+  if ((st = record_cuda_status(moe::prepare_attn_decode_kernels()))) return st;
+  if ((st = record_cuda_status(moe::prepare_attn_prefill_kernels()))) return st;
 
   attn_handle h = new (std::nothrow) attn_handle_s;
   if (!h) return MOE_ERR_NO_MEMORY;

@@ -796,14 +796,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
 }
 
 template <int D, int NT>
-cudaError_t prepare(int max_requests) {
+cudaError_t prepare() {
   cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<D, NT>::kSmem + (max_requests + 1) * (int)sizeof(int64_t));
+                              Cfg<D, NT>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
 }
 
 template <int D, int NT>
@@ -829,13 +829,13 @@ cudaError_t launch(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
 // A block shares at most its first and its last context with others.
 int attn_part_slots(int sms) { return 2 * sms; }
 
-cudaError_t prepare_attn_decode_kernels(int max_requests) {
+cudaError_t prepare_attn_decode_kernels() {
   cudaError_t e;
-  if ((e = prepare<64, 2>(max_requests)) != cudaSuccess) return e;
-  if ((e = prepare<64, 1>(max_requests)) != cudaSuccess) return e;
-  if ((e = prepare<128, 2>(max_requests)) != cudaSuccess) return e;
-  if ((e = prepare<128, 1>(max_requests)) != cudaSuccess) return e;
-  return prepare<256, 1>(max_requests);
+  if ((e = prepare<64, 2>()) != cudaSuccess) return e;
+  if ((e = prepare<64, 1>()) != cudaSuccess) return e;
+  if ((e = prepare<128, 2>()) != cudaSuccess) return e;
+  if ((e = prepare<128, 1>()) != cudaSuccess) return e;
+  return prepare<256, 1>();
 }
 
 cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {

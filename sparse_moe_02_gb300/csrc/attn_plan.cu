@@ -149,14 +149,10 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(PlanArgs a) {
   }
 }
 
-size_t plan_smem(int B) { return (size_t)(4 * B + 1) * sizeof(int); }
+constexpr size_t plan_smem(int B) { return (size_t)(4 * B + 1) * sizeof(int); }
+static_assert(plan_smem(kMaxRequests) + 1024 <= 48 << 10, "what a kernel may have without asking");
 
 }  // namespace
-
-cudaError_t prepare_attn_plan_kernel(int max_requests) {
-  return cudaFuncSetAttribute(attn_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)plan_smem(max_requests));
-}
 
 cudaError_t launch_attn_plan(const PlanArgs& a, int sms, cudaStream_t s) {
   int grid = (a.T + kTokensPerBlock - 1) / kTokensPerBlock;

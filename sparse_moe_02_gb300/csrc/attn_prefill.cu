@@ -1179,13 +1179,13 @@ cudaError_t launch(const FwdArgs& args, int sms, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t prepare(int max_requests) {
+cudaError_t prepare() {
   const cudaError_t e = cudaFuncSetAttribute(
       attn_prepare_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      PrepCfg<D>::kSmem + (max_requests + 1) * (int)sizeof(int64_t));
+      PrepCfg<D>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<D>::kSmem + (max_requests + 1) * (int)sizeof(int64_t));
+                              Cfg<D>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
 }
 
 }  // namespace
@@ -1202,11 +1202,11 @@ int attn_prep_steps(const AttnDims& d, int max_requests) {
   return (int)std::min(all, kMostPrep / (int64_t)attn_prep_step_bytes(d.D));
 }
 
-cudaError_t prepare_attn_prefill_kernels(int max_requests) {
+cudaError_t prepare_attn_prefill_kernels() {
   cudaError_t e;
-  if ((e = prepare<64>(max_requests)) != cudaSuccess) return e;
-  if ((e = prepare<128>(max_requests)) != cudaSuccess) return e;
-  return prepare<256>(max_requests);
+  if ((e = prepare<64>()) != cudaSuccess) return e;
+  if ((e = prepare<128>()) != cudaSuccess) return e;
+  return prepare<256>();
 }
 
 cudaError_t launch_attn_prefill(const FwdArgs& a, int sms, cudaStream_t s) {
