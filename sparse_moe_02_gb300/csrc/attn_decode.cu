@@ -13,8 +13,9 @@
 // takes its codes as the MMA's A operand (channels by tokens) and w = p_t s_tg, rounded to f16
 // (11 bits; the plain fp32 form's outputs are rounded to 8), as B; the bias sum stays in fp32.
 // So that w fits f16 for any bf16 scale, the running softmax reference of a row is the maximum
-// of score + exponent(largest |s_tg|), which bounds w, instead of the score alone; it only moves
-// (and the accumulators are only rescaled) when a tile exceeds it by 2^6.
+// of score + exponent(largest |s_tg|), which bounds w, instead of the score alone (where all scales
+// are 0 or nearly so, the biases' exponent less kBiasMore); it only moves (and the accumulators are
+// only rescaled) when a tile exceeds it by 2^6.
 //
 // What bounds it.  A tile of 16 tokens (4608 bytes with 256 channels) costs about 540 warp
 // instructions for 8 rows; twelve warps an SM, each with 14 KB of copies in flight, read the cache at
@@ -58,6 +59,9 @@ constexpr int kTile = 16;  // tokens per ring stage: the MMA's M side, and a who
 constexpr int kWholeKv = 768, kWholeMore = 8, kWholeMost = 1536;
 constexpr float kSlack = 6.f;  // growth of the reference a tile may bring before a rescale
 constexpr float kLift = 9.f;   // w <= 2^(kLift + kSlack) at the reference
+// Biases may be this much larger than the bound of the scales (of groups that are nearly constant): p
+// times a bias then stays below 2^(kLift + kSlack + 1 + kBiasMore), and its sum far within fp32.
+constexpr int kBiasMore = 64;
 constexpr int kJoinWarps = 4;  // warps whose outputs the join buffer holds at once
 static_assert(kWarps % kJoinWarps == 0, "whole rounds of the join");
 
@@ -384,14 +388,15 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
       }
     }
   }
-  // 2^ev bounds the tile's scales (nonnegative bf16, the lower halves)
+  // 2^ev bounds the tile's scales (nonnegative bf16, the lower halves), 2^(ev + kBiasMore) its biases
   uint32_t big = 0;
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int g = 0; g < NG; ++g) big = max_u16x2(big, vp[r].w[g]);
-  big = __reduce_max_sync(~0u, big & 0x7fffu);
-  const float ev = (float)max((int)(big >> 7) - 126, -90);
+    for (int g = 0; g < NG; ++g) big = max_u16x2(big, vp[r].w[g] & 0x7fff7fffu);
+  const int most =
+      __reduce_max_sync(~0u, max((int)(big & 0xffffu), (int)(big >> 16) - (kBiasMore << 7)));
+  const float ev = (float)max((most >> 7) - 126, -90);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float top[2];
