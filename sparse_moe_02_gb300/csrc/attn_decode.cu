@@ -412,8 +412,9 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
       for (int cc = 0; cc < 2; ++cc) {
         const float m = fmaxf(s.m[nt][cc], top[cc]);
         const float f = m == -INFINITY ? 1.f : exp2_fast(s.m[nt][cc] - m);
+        const float root = m == -INFINITY ? 1.f : exp2_fast(0.5f * (s.m[nt][cc] - m));
         s.m[nt][cc] = m;
-        s.l[nt][cc] *= f;
+        s.l[nt][cc] = s.l[nt][cc] * root * root;  // (see part_root)
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           s.ob[nt][cc][g] *= f;
@@ -703,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float2 x = join_ml[col][k];
-        const float f = part_weight(x.x, x.y, m);
-        l = fmaf(x.y, f, l);
+        const float root = part_root(x.x, x.y, m), f = root * root;
+        l = fmaf(x.y * root, root, l);
         bias = fmaf(join_b[col][g][k], f, bias);
         if (g == 0) join_f[col][k] = f;
       }

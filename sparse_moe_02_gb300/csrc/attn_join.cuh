@@ -119,9 +119,12 @@ __device__ __forceinline__ uint32_t cache_record(const FwdArgs& a, int b, int h,
   return (((uint32_t)id * a.d.Hkv + h) << shift) + (tile & ((1 << shift) - 1));
 }
 
-__device__ __forceinline__ float part_weight(float m_part, float l_part, float m) {
+// Square root of a part's weight.  References hold the sizes of values as well as scores, so they may
+// differ by more than fp32's exponents while the sums of weights, scaled by them, are alike: sums take
+// the root twice, outputs its square, which may vanish as they do.
+__device__ __forceinline__ float part_root(float m_part, float l_part, float m) {
   // a part that saw nothing has m = -inf and l = 0; one of NaN scores m = -inf and l = NaN
-  return m_part == -INFINITY ? (l_part == 0.f ? 0.f : 1.f) : exp2_fast(m_part - m);
+  return m_part == -INFINITY ? (l_part == 0.f ? 0.f : 1.f) : exp2_fast(0.5f * (m_part - m));
 }
 
 // Outputs are joined in the order in which the lanes hold them: float4 i of a column is channels
@@ -234,9 +237,9 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2)
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < kWarpsJ; ++k) m = fmaxf(m, red[k].x);
-      const float f = part_weight(ml.x, ml.y, m);
-      weight[tid] = f;
-      float l = ml.y * f;
+      const float f = part_root(ml.x, ml.y, m);
+      weight[tid] = f * f;
+      float l = ml.y * f * f;
 #pragma unroll
       for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
       if (lane == 0) red[warp].y = l;
@@ -287,8 +290,8 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2)
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < kAtOnce && i0 + lane < d.x)
         ml = __ldcg(a.part_ml + part_slot(b0, i0 + lane) * kCols + col);
-      const float f = part_weight(ml.x, ml.y, m);
-      l = fmaf(ml.y, f, l);
+      const float root = part_root(ml.x, ml.y, m), f = root * root;
+      l = fmaf(ml.y * root, root, l);
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {  // beyond the last: it again, with weight 0
         const float fi = __shfl_sync(~0u, f, i);

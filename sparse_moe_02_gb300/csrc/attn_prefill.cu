@@ -62,6 +62,9 @@ constexpr int kRegsSoft = 168, kRegsDeq = 64, kRegsRest = 56;
 static_assert(kRegsSoft + 4 * kRegsDeq + kRegsRest == 6 * 80, "the launch's registers");
 constexpr int kParts = 4;            // parts announced ahead
 constexpr float kSlack = 6.f, kLift = 9.f;  // as in the few-row kernel
+// Values of a record this many binary orders below the largest so far: the reference may then lie so far
+// above the record's weights that they leave fp32's range.
+constexpr float kSpread = 64.f;
 constexpr int kExps = 8;             // steps of record exponents kept
 
 template <int D>
@@ -943,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const bool on = row < rows_left;
       const int lim = on ? seen_by(p.r, tok) : p.r.kv;
       const int least = seen_by(p.r, p.rt * kRows / a.d.G);
-      float m = -INFINITY, l = 0.f, unit = 0.f;
+      float m = -INFINITY, l = 0.f, unit = 0.f, most_ev = -INFINITY;
       for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
         ok = mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err) &&
              (!prepared || mbar_wait(&bars.x_full[n % kExps], (n / kExps) & 1, a.err));
@@ -980,8 +983,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         if (__any_sync(~0u, top > m + kSlack)) {
           const float m_new = fmaxf(m, top);
           const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
+          const float root = m_new == -INFINITY ? 1.f : exp2_fast(0.5f * (m - m_new));
           m = m_new;
-          l *= f;
+          l = l * root * root;  // (see part_root)
           if (t > p.t0) {
             // the outputs so far, once the last product has landed
             ok = mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err);
@@ -1001,6 +1005,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           }
         }
         const float ref = m == -INFINITY ? 0.f : kLift - m;
+        float least_ev = ex[0].ev;
+        most_ev = fmaxf(most_ev, ex[0].ev);
+#pragma unroll
+        for (int r = 1; r < kRecs; ++r)
+          least_ev = fminf(least_ev, ex[r].ev), most_ev = fmaxf(most_ev, ex[r].ev);
+        if (least_ev < most_ev - kSpread) {
+          // with 2^ev weights may vanish that count in the sum: there they enter it without
+#pragma unroll
+          for (int r = 0; r < kRecs; ++r)
+            if (ex[r].ev < most_ev - kSpread) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                l += exp2_fast(fmaf(__uint_as_float(s[16 * r + i]), ex[r].up_k, ref));
+              ex[r].down_v = 0.f;
+            }
+        }
         uint32_t w[kStep / 2];
 #pragma unroll
         for (int r = 0; r < kRecs; ++r) {
