@@ -59,7 +59,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Waits for the phase with the given parity to complete.  Gives up after kWaitLimitNs,
-// records kDevErrTimeout in *err and returns false; every caller then stops its role.
+// records kDevErrTimeout in *err unless a larger error is there, and returns false; every caller then
+// stops its role.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait(a, parity)) return true;
@@ -69,7 +70,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
     for (int i = 0; i < 256; ++i)
       if (mbar_try_wait(a, parity)) return true;
     if (global_timer_ns() - t0 > kWaitLimitNs) {
-      atomicExch(err, kDevErrTimeout);
+      atomicMax(err, kDevErrTimeout);
       return false;
     }
   }
