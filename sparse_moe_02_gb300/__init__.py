@@ -340,7 +340,8 @@ class MoeLayer:
         import torch
         T = x.shape[0]
         if y is None:
-            y = torch.empty_like(x)
+            with torch.cuda.stream(stream):  # memory of the stream that writes it
+                y = torch.empty_like(x)
         _check(moe_forward(self.handle, _ptr(x), T, _ptr(y), self._stream(stream)), "moe_forward")
         return y
 
@@ -353,10 +354,11 @@ class MoeLayer:
         import torch
         T = x.shape[0]
         dev = x.device
-        out = dict(topk_idx=torch.empty((T, 8), dtype=torch.int32, device=dev),
-                   topk_w=torch.empty((T, 8), dtype=torch.float32, device=dev),
-                   offsets=torch.empty(self.E + 1, dtype=torch.int32, device=dev),
-                   perm=torch.empty(T * 8, dtype=torch.int32, device=dev))
+        with torch.cuda.stream(stream):
+            out = dict(topk_idx=torch.empty((T, 8), dtype=torch.int32, device=dev),
+                       topk_w=torch.empty((T, 8), dtype=torch.float32, device=dev),
+                       offsets=torch.empty(self.E + 1, dtype=torch.int32, device=dev),
+                       perm=torch.empty(T * 8, dtype=torch.int32, device=dev))
         _check(moe_route(self.handle, _ptr(x), T, _ptr(out["topk_idx"]), _ptr(out["topk_w"]),
                          _ptr(out["offsets"]), _ptr(out["perm"]), self._stream(stream)),
                "moe_route")
@@ -398,8 +400,10 @@ class PagedAttention:
 
     One object serves every layer of the same shape; each layer has a cache of its own
     (new_cache).  Queries, keys, values and outputs are bf16 [T][heads][head_dim], rows may be
-    strided (views of a fused projection's output).  Outputs not given are allocated.  Calls are
-    enqueued on the current stream, or on `stream`.
+    strided (views of a fused projection's output).  Calls are enqueued on the current stream, or
+    on `stream`.  Outputs not given are allocated as memory of that stream: another one that uses
+    them waits for it first, and has them recorded (Tensor.record_stream) if they may be freed
+    before it is done.
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
@@ -456,8 +460,11 @@ class PagedAttention:
                     f"{self._layout}, got {cache.layout}")
         return cache.ptr
 
-    def _new(self, shape, dtype):
-        return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self._device}")
+    def _new(self, shape, dtype, stream):
+        if stream is None:
+            return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self._device}")
+        with self._torch.cuda.stream(stream):
+            return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self._device}")
 
     def plan(self, block_table, ctx_lens, new_lens, free_pages, cursor, q_offsets=None,
              kv_lens=None, positions=None, slots=None, cursor_out=None, T=None, stream=None):
@@ -471,11 +478,11 @@ class PagedAttention:
         elif T is None:
             _refuse(MOE_ERR_INVALID_ARG, "plan: positions or T")
         else:
-            positions = self._new(T, i32)
-        slots = self._new(T, i32) if slots is None else slots
-        q_offsets = self._new(B + 1, i32) if q_offsets is None else q_offsets
-        kv_lens = self._new(B, i32) if kv_lens is None else kv_lens
-        cursor_out = self._new(1, i32) if cursor_out is None else cursor_out
+            positions = self._new(T, i32, stream)
+        slots = self._new(T, i32, stream) if slots is None else slots
+        q_offsets = self._new(B + 1, i32, stream) if q_offsets is None else q_offsets
+        kv_lens = self._new(B, i32, stream) if kv_lens is None else kv_lens
+        cursor_out = self._new(1, i32, stream) if cursor_out is None else cursor_out
         ints = self._ints
         n_free = free_pages.numel()
         st = self._lib.attn_plan(
@@ -494,8 +501,8 @@ class PagedAttention:
         """Norm of each query and key head and rotation by cos_sin [positions][rotary_dim] (None:
         no rotation); returns (q_out, k_out)."""
         T, Hq, Hkv, D = q.shape[0], self.n_q_heads, self.n_kv_heads, self.head_dim
-        q_out = self._new((T, Hq, D), self._bf16) if q_out is None else q_out
-        k_out = self._new((T, Hkv, D), self._bf16) if k_out is None else k_out
+        q_out = self._new((T, Hq, D), self._bf16, stream) if q_out is None else q_out
+        k_out = self._new((T, Hkv, D), self._bf16, stream) if k_out is None else k_out
         rows = self._rows
         (qp, qs), (kp, ks) = rows(q, "q", Hq, T), rows(k, "k", Hkv, T)
         (qop, qos), (kop, kos) = rows(q_out, "q_out", Hq, T), rows(k_out, "k_out", Hkv, T)
@@ -531,8 +538,8 @@ class PagedAttention:
     def read(self, slots, cache, k_out=None, v_out=None, stream=None):
         """Cached rows of slots [T] as bf16; returns (k_out, v_out)."""
         T, Hkv = slots.shape[0], self.n_kv_heads
-        k_out = self._new((T, Hkv, self.head_dim), self._bf16) if k_out is None else k_out
-        v_out = self._new((T, Hkv, self.head_dim), self._bf16) if v_out is None else v_out
+        k_out = self._new((T, Hkv, self.head_dim), self._bf16, stream) if k_out is None else k_out
+        v_out = self._new((T, Hkv, self.head_dim), self._bf16, stream) if v_out is None else v_out
         (kp, ks), (vp, vs) = self._rows(k_out, "k_out", Hkv, T), self._rows(v_out, "v_out", Hkv, T)
         st = self._lib.attn_kv4_read(self.handle, self._cache(cache),
                                      self._ints(slots, "slots", T), T, kp, ks, vp, vs,
@@ -546,7 +553,7 @@ class PagedAttention:
         """Causal attention of the requests' new tokens over their cached rows; returns out."""
         T, Hq = q.shape[0], self.n_q_heads
         B, width = block_table.shape
-        out = self._new((T, Hq, self.head_dim), self._bf16) if out is None else out
+        out = self._new((T, Hq, self.head_dim), self._bf16, stream) if out is None else out
         (qp, qs), (op, os_) = self._rows(q, "q", Hq, T), self._rows(out, "out", Hq, T)
         ints = self._ints
         st = self._lib.attn_kv4_forward(
