@@ -53,7 +53,8 @@
  * synchronise the host or allocate.  The handle owns a device workspace (partial results of
  * contexts that several blocks share; contexts in the form that prompts read, 4 bytes for each
  * channel that the cache's pages hold, 512 MB at most: longer ones are read as they are, more
- * slowly) and an error word; use a handle on one stream at a time.
+ * slowly) and an error word; use a handle on one stream at a time, and every call with the device
+ * current on which it was created.
  * Rows are strided: a stride is the distance between tokens in elements, a multiple of 8 and at
  * least the width of a token's heads; heads are adjacent, their channels contiguous.  Row
  * pointers are 16-byte aligned, index arrays 4-byte aligned.  Outputs must not overlap inputs,

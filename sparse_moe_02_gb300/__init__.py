@@ -403,7 +403,8 @@ class PagedAttention:
     strided (views of a fused projection's output).  Calls are enqueued on the current stream, or
     on `stream`.  Outputs not given are allocated as memory of that stream: another one that uses
     them waits for it first, and has them recorded (Tensor.record_stream) if they may be freed
-    before it is done.
+    before it is done.  The object belongs to the device that was current when it was made: tensors
+    are on that device, and calls are made while it is current.
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
@@ -423,11 +424,18 @@ class PagedAttention:
         self._torch = torch
         # the current stream's handle without a Stream object (3 us a call), where torch has it
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
     def new_cache(self):
-        return Kv4Cache(self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
+        return Kv4Cache(self.n_pages, self.n_kv_heads, self.page_size, self.head_dim,
+                        f"cuda:{self._device}")
 
     def _stream(self, stream):
+        device = self._device
+        if self._current_device() != device or (stream is not None
+                                                and stream.device_index != device):
+            _refuse(MOE_ERR_INVALID_ARG, f"expected cuda:{device}, the device of this object, to be "
+                    "current, and a stream of it")
         if stream is not None:
             return stream.cuda_stream
         if self._raw_stream is not None:
@@ -438,9 +446,11 @@ class PagedAttention:
         """(address, token stride) of bf16 rows [tokens][heads][head_dim]."""
         D = self.head_dim
         shape, stride = t.shape, t.stride()
-        if t.dtype is not self._bf16 or not t.is_cuda or shape != (tokens, heads, D):
-            _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected a CUDA bfloat16 tensor of shape "
-                    f"{(tokens, heads, D)}, got {t.device.type} {t.dtype} {tuple(shape)}")
+        if (t.dtype is not self._bf16 or t.get_device() != self._device
+                or shape != (tokens, heads, D)):
+            _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected a bfloat16 tensor of shape "
+                    f"{(tokens, heads, D)} on cuda:{self._device}, got {t.dtype} {tuple(shape)} on "
+                    f"{t.device}")
         if stride[2] != 1 or (heads > 1 and stride[1] != D):
             _refuse(MOE_ERR_UNSUPPORTED, f"{what}: a token's heads must be contiguous")
         # with one token the stride says nothing
@@ -448,16 +458,17 @@ class PagedAttention:
 
     def _ints(self, t, what, n):
         """Address of n contiguous int32 numbers."""
-        if (t.dtype is not self._i32 or not t.is_cuda or t.numel() != n
+        if (t.dtype is not self._i32 or t.get_device() != self._device or t.numel() != n
                 or not t.is_contiguous()):
-            _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {n} contiguous CUDA int32 numbers, "
-                    f"got {t.device.type} {t.dtype} {tuple(t.shape)}")
+            _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {n} contiguous int32 numbers on "
+                    f"cuda:{self._device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
     def _cache(self, cache):
-        if cache.layout != self._layout:
+        if cache.layout != self._layout or cache.data.get_device() != self._device:
             _refuse(MOE_ERR_INVALID_ARG, f"cache: expected (pages, heads, page, channels) "
-                    f"{self._layout}, got {cache.layout}")
+                    f"{self._layout} on cuda:{self._device}, got {cache.layout} on "
+                    f"{cache.data.device}")
         return cache.ptr
 
     def _new(self, shape, dtype, stream):
@@ -507,14 +518,17 @@ class PagedAttention:
         (qp, qs), (kp, ks) = rows(q, "q", Hq, T), rows(k, "k", Hkv, T)
         (qop, qos), (kop, kos) = rows(q_out, "q_out", Hq, T), rows(k_out, "k_out", Hkv, T)
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w.dtype is not self._bf16 or not w.is_cuda or w.shape != (D,) or w.stride(0) != 1:
-                _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {D} contiguous CUDA bfloat16")
+            if (w.dtype is not self._bf16 or w.get_device() != self._device or w.shape != (D,)
+                    or w.stride(0) != 1):
+                _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {D} contiguous bfloat16 on "
+                        f"cuda:{self._device}")
         n_pos = rot = 0
         pos = table = None
         if cos_sin is not None:
-            if (cos_sin.dtype is not self._f32 or not cos_sin.is_cuda or cos_sin.dim() != 2
-                    or not cos_sin.is_contiguous()):
-                _refuse(MOE_ERR_INVALID_ARG, "cos_sin: expected a contiguous CUDA float32 matrix")
+            if (cos_sin.dtype is not self._f32 or cos_sin.get_device() != self._device
+                    or cos_sin.dim() != 2 or not cos_sin.is_contiguous()):
+                _refuse(MOE_ERR_INVALID_ARG, "cos_sin: expected a contiguous float32 matrix on "
+                        f"cuda:{self._device}")
             n_pos, rot = cos_sin.shape
             pos, table = self._ints(positions, "positions", T), cos_sin.data_ptr()
         st = self._lib.attn_qk_norm_rope(
@@ -569,7 +583,8 @@ class PagedAttention:
 
     def close(self):
         if self.handle:
-            _check(attn_destroy(self.handle), "attn_destroy")
+            with self._torch.cuda.device(self._device):
+                _check(attn_destroy(self.handle), "attn_destroy")
             self.handle = None
 
     def __del__(self):
