@@ -383,6 +383,10 @@ def _refuse(status, what):
     raise MoeError(status, what)
 
 
+def _missing(what):
+    _refuse(MOE_ERR_INVALID_ARG, f"{what}: missing")
+
+
 class Kv4Cache:
     """One layer's 4-bit cache as a torch tensor of records [n_pages][Hkv][page_size / 16][bytes]
     (layout in include/attn.h)."""
@@ -445,6 +449,8 @@ class PagedAttention:
     def _rows(self, t, what, heads, tokens):
         """(address, token stride) of bf16 rows [tokens][heads][head_dim]."""
         D = self.head_dim
+        if t is None:
+            _missing(what)
         shape, stride = t.shape, t.stride()
         if (t.dtype is not self._bf16 or t.get_device() != self._device
                 or shape != (tokens, heads, D)):
@@ -458,6 +464,8 @@ class PagedAttention:
 
     def _ints(self, t, what, n):
         """Address of n contiguous int32 numbers."""
+        if t is None:
+            _missing(what)
         if (t.dtype is not self._i32 or t.get_device() != self._device or t.numel() != n
                 or not t.is_contiguous()):
             _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {n} contiguous int32 numbers on "
@@ -465,6 +473,8 @@ class PagedAttention:
         return t.data_ptr()
 
     def _cache(self, cache):
+        if cache is None:
+            _missing("cache")
         if cache.layout != self._layout or cache.data.get_device() != self._device:
             _refuse(MOE_ERR_INVALID_ARG, f"cache: expected (pages, heads, page, channels) "
                     f"{self._layout} on cuda:{self._device}, got {cache.layout} on "
@@ -482,6 +492,8 @@ class PagedAttention:
         """Extends block_table for new_lens tokens after ctx_lens cached ones, taking pages from
         free_pages[cursor:]; returns (q_offsets, kv_lens, positions, slots, cursor_out).  Without
         positions, T gives the capacity of positions and slots."""
+        if block_table is None or free_pages is None:
+            _missing("block_table" if block_table is None else "free_pages")
         B, width = block_table.shape
         i32 = self._i32
         if positions is not None:
@@ -510,7 +522,9 @@ class PagedAttention:
     def qk_norm_rope(self, q, k, positions, q_weight, k_weight, cos_sin, eps=1e-6,
                      interleaved=False, q_out=None, k_out=None, stream=None):
         """Norm of each query and key head and rotation by cos_sin [positions][rotary_dim] (None:
-        no rotation); returns (q_out, k_out)."""
+        no rotation, and positions may be None); returns (q_out, k_out)."""
+        if q is None or q_weight is None or k_weight is None:
+            _missing("q, q_weight or k_weight")
         T, Hq, Hkv, D = q.shape[0], self.n_q_heads, self.n_kv_heads, self.head_dim
         q_out = self._new((T, Hq, D), self._bf16, stream) if q_out is None else q_out
         k_out = self._new((T, Hkv, D), self._bf16, stream) if k_out is None else k_out
@@ -541,6 +555,8 @@ class PagedAttention:
 
     def append(self, k, v, slots, cache, stream=None):
         """Quantises keys and values [T][Hkv][D] into the cached rows of slots [T]."""
+        if k is None:
+            _missing("k")
         T, Hkv = k.shape[0], self.n_kv_heads
         (kp, ks), (vp, vs) = self._rows(k, "k", Hkv, T), self._rows(v, "v", Hkv, T)
         st = self._lib.attn_kv4_append(self.handle, kp, ks, vp, vs,
@@ -551,6 +567,8 @@ class PagedAttention:
 
     def read(self, slots, cache, k_out=None, v_out=None, stream=None):
         """Cached rows of slots [T] as bf16; returns (k_out, v_out)."""
+        if slots is None:
+            _missing("slots")
         T, Hkv = slots.shape[0], self.n_kv_heads
         k_out = self._new((T, Hkv, self.head_dim), self._bf16, stream) if k_out is None else k_out
         v_out = self._new((T, Hkv, self.head_dim), self._bf16, stream) if v_out is None else v_out
@@ -565,6 +583,8 @@ class PagedAttention:
     def forward(self, q, cache, block_table, q_offsets, kv_lens, max_q_len, max_kv_len, out=None,
                 stream=None):
         """Causal attention of the requests' new tokens over their cached rows; returns out."""
+        if q is None or block_table is None:
+            _missing("q" if q is None else "block_table")
         T, Hq = q.shape[0], self.n_q_heads
         B, width = block_table.shape
         out = self._new((T, Hq, self.head_dim), self._bf16, stream) if out is None else out

@@ -1,5 +1,5 @@
 """What PagedAttention refuses before it calls the library, with stand-ins for CUDA tensors (no GPU): every
-tensor on the handle's device, every call with that device current."""
+tensor there and on the handle's device, every call with that device current."""
 import types
 
 import pytest
@@ -133,3 +133,18 @@ def test_calls_with_another_device_current_are_refused(attn, call):
 def test_streams_of_another_device_are_refused(attn, call):
     stream = types.SimpleNamespace(cuda_stream=0, device_index=1)
     refused(attn, call, dict(arguments()[call], stream=stream))
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, n in TENSORS
+                                       if not n.endswith("out") and (c, n) not in (
+                                           ("qk_norm_rope", "cos_sin"), ("plan", "q_offsets"),
+                                           ("plan", "kv_lens"), ("plan", "positions"),
+                                           ("plan", "slots"))])
+def test_missing_tensors_are_refused(attn, call, name):
+    # (positions are needed for a rotation only; outputs that are None are allocated)
+    refused(attn, call, dict(arguments()[call], **{name: None}))
+
+
+def test_positions_may_be_missing_without_a_rotation(attn):
+    attn.qk_norm_rope(**dict(arguments()["qk_norm_rope"], positions=None, cos_sin=None))
+    assert attn._lib.calls == ["attn_qk_norm_rope"]
