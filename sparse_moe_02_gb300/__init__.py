@@ -395,8 +395,11 @@ class Kv4Cache:
         import torch
         self.data = torch.zeros((n_pages, n_kv_heads, page_size // 16, 18 * head_dim),
                                 dtype=torch.uint8, device=device)
-        self.ptr = self.data.data_ptr()
         self.layout = (n_pages, n_kv_heads, page_size, head_dim)
+
+    @property
+    def ptr(self):
+        return self.data.data_ptr()
 
 
 class PagedAttention:
@@ -438,8 +441,8 @@ class PagedAttention:
         device = self._device
         if self._current_device() != device or (stream is not None
                                                 and stream.device_index != device):
-            _refuse(MOE_ERR_INVALID_ARG, f"expected cuda:{device}, the device of this object, to be "
-                    "current, and a stream of it")
+            _refuse(MOE_ERR_INVALID_ARG, f"expected cuda:{device}, the device of this object, to "
+                    "be current, and a stream of it")
         if stream is not None:
             return stream.cuda_stream
         if self._raw_stream is not None:

@@ -148,3 +148,10 @@ def test_missing_tensors_are_refused(attn, call, name):
 def test_positions_may_be_missing_without_a_rotation(attn):
     attn.qk_norm_rope(**dict(arguments()["qk_norm_rope"], positions=None, cos_sin=None))
     assert attn._lib.calls == ["attn_qk_norm_rope"]
+
+
+def test_a_cache_is_where_its_tensor_is():
+    c = moe.Kv4Cache(2, HKV, P, D, device="cpu")
+    assert c.ptr == c.data.data_ptr()
+    c.data = c.data.clone()  # as after a trip to the host and back
+    assert c.ptr == c.data.data_ptr()
