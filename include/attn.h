@@ -35,6 +35,8 @@
  *   attention: o_i = sum_t softmax_t(scale q_i . k_t) v_t over the cached tokens t <= kv_b - n_b +
  *     i of request b (kv_b = its cached tokens with the new ones); a query that sees no token
  *     gives 0.  Scores, softmax sums and outputs are held in fp32 and rounded once to bf16.
+ *     Scores are in range below 2^23 (in units of log 2): a row with larger ones may read NaN, and
+ *     from 2^28 on it does.
  *
  * Cache of one layer: one caller-owned device array of n_pages * Hkv * P * (D + D / 8) bytes (0.5625
  * bytes a channel), 128-byte aligned, written by attn_kv4_append only: records [n_pages][Hkv][P / 16]

@@ -40,6 +40,7 @@
 // in block order (the same inputs give the same bits).  Short contexts (max_kv small) take one block
 // each and no second launch; longer ones of like lengths take one each too, and the second launch
 // finds nothing to do.
+#include <cfloat>
 #include <climits>
 
 #include "attn.cuh"
@@ -266,7 +267,8 @@ __device__ __forceinline__ void prepare_query(const FwdArgs& a, const Part& p, c
     S.sum[col][g] = sum * (8192.f / 16777216.f);
     if (g == 0) {
       // code * 2^-24 * q * 2^13-e  ->  log2 units
-      S.scale[col] = fmaxf(up * (16777216.f / 8192.f) * a.d.scale_log2, kLeastUnit);
+      // (at most the largest fp32: 2^126 2^11 would be inf, and negative scores would read as masked)
+      S.scale[col] = fminf(fmaxf(up * (16777216.f / 8192.f) * a.d.scale_log2, kLeastUnit), FLT_MAX);
       // columns beyond the rows see everything: nothing of them is written
       const int seen = p.r.kv - p.r.qn + row / a.d.G + 1;
       S.lim[col] = row < p.r.qn * a.d.G ? min(max(seen, 0), p.r.kv) : p.r.kv;
@@ -778,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
       if (whole) {
 #pragma unroll
         for (int v = 0; v < C::kVec; ++v)
-          store_out4(a, p, p.rt * C::kCols + own_col, D, own_ln + v * C::kLanes, own[v], ml.y);
+          store_out4(a, p, p.rt * C::kCols + own_col, D, own_ln + v * C::kLanes, own[v],
+                     row_sum(ml.x, ml.y));
       } else {
         const int64_t at = (2 * blockIdx.x + (p.t0 == 0)) * C::kCols + own_col;
         float4* dst = reinterpret_cast<float4*>(a.part_o + at * D) + own_ln;

@@ -127,6 +127,13 @@ __device__ __forceinline__ float part_root(float m_part, float l_part, float m) 
   return m_part == -INFINITY ? (l_part == 0.f ? 0.f : 1.f) : exp2_fast(0.5f * (m_part - m));
 }
 
+// The sum that a row's outputs are divided by.  References are rounded to fp32: from 2^23 on (in units of
+// log 2) weights may leave f16 upwards (inf, and the row reads NaN), from 2^29 on downwards, which would
+// read as zeros; such rows read NaN as well.
+__device__ __forceinline__ float row_sum(float m, float l) {
+  return m != -INFINITY && fabsf(m) >= 268435456.f ? NAN : l;  // 2^28
+}
+
 // Outputs are joined in the order in which the lanes hold them: float4 i of a column is channels
 // out_channel(i) .. + 3.
 __device__ __forceinline__ int out_channel(int i) {
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2)
         for (int k = 0; k < kWarpsJ; ++k) sum += red[k].y;
 #pragma unroll
         for (int k = 0; k < 16; ++k) fma4(x, *reinterpret_cast<const float4*>(&acc[k][4 * tid]), 1.f);
-        store_out4(a, p, p.rt * kCols + col, D, 16 * piece + tid, x, sum);
+        store_out4(a, p, p.rt * kCols + col, D, 16 * piece + tid, x, row_sum(m, sum));
       }
       __syncthreads();
     }
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2)
     }
 #pragma unroll
     for (int i = kAtOnce / 2; i; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
-    l = __shfl_sync(~0u, l, 0);
+    l = row_sum(m, __shfl_sync(~0u, l, 0));
     if constexpr (kCh == 2) {
       // two lanes hold the four channels that are stored at once
       const float x = __shfl_down_sync(~0u, o[0], 1), y = __shfl_down_sync(~0u, o[1], 1);

@@ -1055,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         continue;
       }
       const bool whole = p.t1 - p.t0 == p.tiles;
-      out_scale[kq & 1][tid] = whole ? (l == 0.f ? 0.f : 64.f / l) : 64.f;
+      out_scale[kq & 1][tid] = whole ? (l == 0.f ? 0.f : 64.f / row_sum(m, l)) : 64.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.o_scaled[kq & 1]);
       ++kq;
