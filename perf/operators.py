@@ -105,7 +105,9 @@ def draw(rng):
                         q_max=q_max, ctx_min=0, ctx_max=ctx_max, mix=rng.randrange(1 << 20),
                         refused=rng.choice([0, 0, 1]) if B > 1 else 0, **heads)
         w = work(case)
-        if _size_ok(case) and all(w[k] <= top[k] for k in top):
+        # (a rotation's positions are rows of its table, which holds pos_max of them)
+        if _size_ok(case) and all(w[k] <= top[k] for k in top) \
+                and case.get("T", 0) <= case.get("pos_max", math.inf):
             return case
 
 
