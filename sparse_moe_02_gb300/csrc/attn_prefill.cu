@@ -557,10 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       mbar_init(&bars.part_full[i], 1);
       mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 3);
     }
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&bars.raw_full[0][i], 1);
-      mbar_init(&bars.raw_empty[0][i], kDeqWarps);
-    }
+    for (int side = 0; side < 2; ++side)
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&bars.raw_full[side][i], 1);
+        mbar_init(&bars.raw_empty[side][i], kDeqWarps);
+      }
     for (int i = 0; i < C::kOpsK; ++i) {
       mbar_init(&bars.k_full[i], kDeqWarps);
       mbar_init(&bars.k_empty[i], 1);
