@@ -1319,12 +1319,11 @@ int g_gateup_grid = 0, g_down_grid = 0;  // blocks that are resident at once (al
 
 cudaError_t prepare_decode_kernels(int hdim) {
   const int need = 9 * hdim * (int)sizeof(float);
-  cudaError_t e = cudaSuccess;
-  if (need > 48 * 1024) {
-    e = cudaFuncSetAttribute(dec_down_combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             need);
-    if (e != cudaSuccess) return e;
-  }
+  // the limit belongs to the kernel, which all layers share: at the largest supported shape
+  cudaError_t e = cudaFuncSetAttribute(dec_down_combine_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       9 * 2048 * (int)sizeof(float));
+  if (e != cudaSuccess) return e;
   int dev = 0, sms = 0, b1 = 0, b2 = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
