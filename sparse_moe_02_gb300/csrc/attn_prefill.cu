@@ -966,6 +966,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           const float4 v = *reinterpret_cast<const float4*>(&exps[n % kExps][r]);
           ex[r] = Exps{fmaxf(unit * v.x, kLeastUnit), v.y, v.z, 0.f};
         }
+        float least_ev = ex[0].ev;
+        most_ev = fmaxf(most_ev, ex[0].ev);
+#pragma unroll
+        for (int r = 1; r < kRecs; ++r)
+          least_ev = fminf(least_ev, ex[r].ev), most_ev = fmaxf(most_ev, ex[r].ev);
+        const bool spread = least_ev < most_ev - kSpread;
         wait_ld32(s);
         wait_ld32(s + 32);
         if ((t + 1) * kStep > least) {
@@ -1006,12 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           }
         }
         const float ref = m == -INFINITY ? 0.f : kLift - m;
-        float least_ev = ex[0].ev;
-        most_ev = fmaxf(most_ev, ex[0].ev);
-#pragma unroll
-        for (int r = 1; r < kRecs; ++r)
-          least_ev = fminf(least_ev, ex[r].ev), most_ev = fmaxf(most_ev, ex[r].ev);
-        if (least_ev < most_ev - kSpread) {
+        if (__any_sync(~0u, spread)) {
           // with 2^ev weights may vanish that count in the sum: there they enter it without
 #pragma unroll
           for (int r = 0; r < kRecs; ++r)
