@@ -66,6 +66,7 @@ constexpr float kSlack = 6.f, kLift = 9.f;  // as in the few-row kernel
 // above the record's weights that they leave fp32's range.
 constexpr float kSpread = 64.f;
 constexpr int kExps = 8;             // steps of record exponents kept
+constexpr int kNotFinite = 127;      // in place of the exponent of a query row that is not finite
 
 template <int D>
 struct Cfg {
@@ -495,7 +496,8 @@ struct QueryRows {
       top = max(top & 0xffffu, top >> 16);
       const int e = min(max((int)(top >> 7) - 127, -100), 126);
       const float down = pow2(-e) * 8192.f;
-      if (lane % kL == 0) exps[row0 + i * kPer + lane / kL] = (int8_t)e;
+      if (lane % kL == 0)
+        exps[row0 + i * kPer + lane / kL] = (int8_t)(top >= 0x7f80u ? kNotFinite : e);
       w[i] = make_uint4(pack_f16(bf16_lo(w[i].x) * down, bf16_lo(w[i].z) * down),
                         pack_f16(bf16_hi(w[i].x) * down, bf16_hi(w[i].z) * down),
                         pack_f16(bf16_lo(w[i].y) * down, bf16_lo(w[i].w) * down),
@@ -1056,6 +1058,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
         continue;
       }
+      // scores that are all -inf would read as a row that sees nothing
+      if (lim > 0 && row_exp[kq % kExps][tid] == kNotFinite) l = NAN;
       const bool whole = p.t1 - p.t0 == p.tiles;
       out_scale[kq & 1][tid] = whole ? (l == 0.f ? 0.f : 64.f / row_sum(m, l)) : 64.f;
       __syncwarp();
