@@ -431,7 +431,9 @@ class PagedAttention:
         self._torch = torch
         # the current stream's handle without a Stream object (3 us a call), where torch has it
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self._current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        # (where there is one device no other can be current)
+        self._current_device = (None if torch.cuda.device_count() == 1 else
+                                getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
 
     def new_cache(self):
         return Kv4Cache(self.n_pages, self.n_kv_heads, self.page_size, self.head_dim,
@@ -439,21 +441,25 @@ class PagedAttention:
 
     def _stream(self, stream):
         device = self._device
-        if self._current_device() != device or (stream is not None
-                                                and stream.device_index != device):
-            _refuse(MOE_ERR_INVALID_ARG, f"expected cuda:{device}, the device of this object, to "
-                    "be current, and a stream of it")
+        if self._current_device is not None and self._current_device() != device:
+            self._elsewhere()
         if stream is not None:
+            if stream.device_index != device:
+                self._elsewhere()
             return stream.cuda_stream
         if self._raw_stream is not None:
-            return self._raw_stream(self._device)
-        return self._torch.cuda.current_stream(self._device).cuda_stream
+            return self._raw_stream(device)
+        return self._torch.cuda.current_stream(device).cuda_stream
+
+    def _elsewhere(self):
+        _refuse(MOE_ERR_INVALID_ARG, f"expected cuda:{self._device}, the device of this object, "
+                "to be current, and a stream of it")
 
     def _rows(self, t, what, heads, tokens):
         """(address, token stride) of bf16 rows [tokens][heads][head_dim]."""
-        D = self.head_dim
         if t is None:
             _missing(what)
+        D = self.head_dim
         shape, stride = t.shape, t.stride()
         if (t.dtype is not self._bf16 or t.get_device() != self._device
                 or shape != (tokens, heads, D)):
@@ -478,11 +484,12 @@ class PagedAttention:
     def _cache(self, cache):
         if cache is None:
             _missing("cache")
-        if cache.layout != self._layout or cache.data.get_device() != self._device:
+        data = cache.data
+        if cache.layout != self._layout or data.get_device() != self._device:
             _refuse(MOE_ERR_INVALID_ARG, f"cache: expected (pages, heads, page, channels) "
                     f"{self._layout} on cuda:{self._device}, got {cache.layout} on "
-                    f"{cache.data.device}")
-        return cache.ptr
+                    f"{data.device}")
+        return data.data_ptr()
 
     def _new(self, shape, dtype, stream):
         if stream is None:
