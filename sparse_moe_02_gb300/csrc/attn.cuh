@@ -17,7 +17,7 @@ constexpr int kGroup = 64;        // channels per scale and bias
 // asks for: they belong to the functions, which the handles of a process share.
 constexpr int kMaxRequests = 1024;
 // Cached rows hold magnitudes below this only (larger ones count as not finite): the kernels'
-// powers of two of a record's bound, 2^118 at most, stay normal fp32 numbers.
+// powers of two of a record's bound, 2^119 at most, and their inverses stay normal fp32 numbers.
 constexpr float kLargest = 8.307675e34f;  // 2^116
 // Least unit of a score (the smallest normal fp32): masked scores are -inf times it, which a unit that
 // vanished, of a zero query row over empty or zero keys, would make NaN.

@@ -24,22 +24,23 @@
 // launch that joins the blocks (3 us): these are most of the time of short and middling contexts.
 // Four copies a tile (codes and parameters apart) took 55 us where one takes 50 (64 requests of 4096
 // tokens, three blocks of four warps an SM); one block of twelve warps, the even cut and copies
-// ahead into the next context made it 42, a block per context where lengths are alike 38.
-// Measured, 16 query heads over 2 of 256 channels, one token: 256 cached tokens 7.2 us, 4096 10.5 us,
-// 131072 24.2 us (3.1 TB/s with everything); 48 requests of up to 16384 24.6 us, 64 of 4096 38.2 us
-// (4.0 TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 26.7 us.
+// ahead into the next context made it 42, a block per context where lengths are alike 39.
+// Measured, 16 query heads over 2 of 256 channels, one token: 256 cached tokens 7.4 us, 4096 10.7 us,
+// 131072 24.6 us (3.1 TB/s with everything); 48 requests of up to 16248 24.8 us, 64 of 4096 38.8 us
+// (3.9 TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 27.1 us.
 //
 // Layout of the work.  The rows of a key/value head (G query heads x new tokens) are the MMA's N
-// side in tiles of 8, its 16 tokens the M side of the scores; a cached row is read once for all
-// of them.  One block of twelve warps per SM; each warp takes every twelfth tile of 16 tokens of a
-// context through a ring of its own (one bulk copy a tile, its cache record) and keeps its own
-// softmax state and outputs; the block joins its warps through shared memory.  Contexts are cut
-// evenly over the blocks: with W units of work in all (a tile is one, a context's fixed cost
-// kPartCost more), block i takes [i W / n, (i + 1) W / n) whatever requests they belong to, so ragged
-// batches balance; a second launch joins the partial results of contexts that several blocks share,
-// in block order (the same inputs give the same bits).  Short contexts (max_kv small) take one block
-// each and no second launch; longer ones of like lengths take one each too, and the second launch
-// finds nothing to do.
+// side in tiles of 8, its 16 tokens the M side of the scores.  A cached row is read once for 8 of
+// them (128 and 64 channels: 16, two tiles to a warp); a context with more rows is read again for
+// each further tile, a unit of work of its own.  One block of twelve warps per SM; each warp takes
+// every twelfth tile of 16 tokens of a context through a ring of its own (one bulk copy a tile, its
+// cache record) and keeps its own softmax state and outputs; the block joins its warps through
+// shared memory.  Contexts are cut evenly over the blocks: with W units of work in all (a tile is
+// one, a context's fixed cost kPartCost more), block i takes [i W / n, (i + 1) W / n) whatever
+// requests they belong to, so ragged batches balance; a second launch joins the partial results of
+// contexts that several blocks share, in block order (the same inputs give the same bits).  Short
+// contexts (max_kv small) take one block each and no second launch; longer ones of like lengths take
+// one each too, and the second launch finds nothing to do.
 #include <cfloat>
 #include <climits>
 
@@ -56,7 +57,9 @@ constexpr int kTile = 16;  // tokens per ring stage: the MMA's M side, and a who
 // each context, at most 1536: the cut costs 3 us and a block's fixed costs per part, a whole context
 // the time of its tiles on one SM.  Whole against cut, 2 contexts of 768 tokens 10.5 and 10.8 us, of
 // 1024 12.5 and 10.9; 16 of 1024 12.6 and 12.8; 96 of 1024 12.8 and 20.0, of 1500 16.1 and 22.7, of 1
-// to 1500 15.7 and 15.4; 256 of 1 to 1500 20.5 and 22.7.
+// to 1500 15.7 and 15.4; 256 of 1 to 1500 20.5 and 22.7.  128 channels: 8 contexts of 768 7.8 and 9.2,
+// of 1536 11.7 and 10.3, 128 of 1024 9.9 and 12.1, of 1500 12.3 and 14.4.  64 channels, where the cut
+// pays later: 4 of 768 6.4 and 8.5, of 1536 9.2 and 9.5, 64 of 1500 9.2 and 12.9.
 constexpr int kWholeKv = 768, kWholeMore = 8, kWholeMost = 1536;
 constexpr float kSlack = 6.f;  // growth of the reference a tile may bring before a rescale
 constexpr float kLift = 9.f;   // w <= 2^(kLift + kSlack) at the reference
@@ -167,11 +170,13 @@ __device__ __forceinline__ int row_tiles(const FwdArgs& a, int qn, int cols) {
 __device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1) / kTile); }
 
 // Work of a context: its tiles, and kPartCost tiles' worth for what a part costs besides (queries,
-// page ids, first copies, joins), so that blocks of many short contexts get fewer tiles.
+// page ids, first copies, joins), so that blocks of many short contexts get fewer tiles.  With 0, 20,
+// 40 and 80: 48 requests to 16248 tokens (256 channels) 79.6, 29.2, 24.9 and 27.1 us, 8 drafts of 2
+// to 5 tokens (128 channels) 37.3, 30.0, 27.2 and 29.7.
 constexpr int kPartCost = 40;
 // Longer contexts, seen to be of like lengths once their lengths are known, take a block each too, if
 // none has this much more work than a block's share: a cut would cost a part and a join more (128
-// contexts of 2500 tokens 26.8 and 32.5 us, of 4096 38.2 and 42.5).
+// contexts of 2500 tokens 27.4 and 33.3 us, of 4096 39.0 and 43.4).
 constexpr int kEachMore = 64;
 constexpr int kLeastWork = 12;  // of a block: a tile a warp (4096 tokens 10.5 us; with 32 12.5 us)
 

@@ -127,9 +127,9 @@ __device__ __forceinline__ float part_root(float m_part, float l_part, float m) 
   return m_part == -INFINITY ? (l_part == 0.f ? 0.f : 1.f) : exp2_fast(0.5f * (m_part - m));
 }
 
-// The sum that a row's outputs are divided by.  References are rounded to fp32: from 2^23 on (in units of
-// log 2) weights may leave f16 upwards (inf, and the row reads NaN), from 2^29 on downwards, which would
-// read as zeros; such rows read NaN as well.
+// The sum that a row's outputs are divided by.  References are rounded to fp32: from 2^23 on (in units
+// of log 2) weights may leave f16 upwards (inf, and the row reads NaN), from 2^29 on downwards, which
+// would read as zeros; such rows read NaN as well.
 __device__ __forceinline__ float row_sum(float m, float l) {
   return m != -INFINITY && fabsf(m) >= 268435456.f ? NAN : l;  // 2^28
 }

@@ -23,11 +23,11 @@
 // lie where the next scores go (a third score buffer, with half of Q in shared memory, was no
 // faster).
 //
-// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 148 us (930 TFLOP/s,
-// prepared; 205 us if not), 2048 over a context of 30000 763 us (1.36 PFLOP/s, 71% of a bf16 product's
-// rate; 1100 us); 4096 tokens of 32 heads over 8 of 128 channels 181 us (277), over 4 of 64 channels
-// 164 us (233); ragged chunks of 28 heads over 4 of 128 80 us (101).  Of the 148 us the prepare launch
-// takes 8, start and tail of the blocks and the joins 20.
+// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 149 us (920 TFLOP/s,
+// prepared; 209 us if not), 2048 over a context of 30000 755 us (1.37 PFLOP/s, 71% of a bf16 product's
+// rate; 1100 us); 4096 tokens of 32 heads over 8 of 128 channels 186 us (281), over 4 of 64 channels
+// 168 us (237); 7 ragged chunks and prompts of 28 heads over 4 of 128 85 us (106).  Of the 149 us the
+// prepare launch takes 8, start and tail of the blocks and the joins 20.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -35,8 +35,12 @@
 // 11 bits of the larger entries and 2^-18 of the record's largest for the smaller ones, against 8
 // bits of a bf16 operand.  Queries are scaled by a power of two per row.  The exponents return in
 // fp32 with the scores and, for the values, inside the weights: P = 2^(x + e - m), where the running
-// reference m bounds x + e; the softmax sum takes 2^(x - m).  Scores, sums and outputs are fp32.
-// The outputs are rescaled (in tensor memory) only when the reference grows by more than 2^6.
+// reference m bounds x + e; the softmax sum takes 2^(x - m), computed apart from P where e lies so far
+// below others that P vanishes first (looking for that costs 128 channels 3%).  Scores, sums and
+// outputs are fp32; 2^x is ex2.approx, within 2^-22.  The outputs are rescaled (in tensor memory)
+// only when the reference grows by more than 2^6.  Entries 2^18 and more below the largest of their
+// record lose bits, and weights 2^24 and more below the row's largest share of any value vanish: the
+// values of a group or a token do beside others that are 2^20 times as large and count.
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
 // in the few-row kernel; shared row tiles are joined by its second launch.
@@ -62,8 +66,8 @@ constexpr int kRegsSoft = 168, kRegsDeq = 64, kRegsRest = 56;
 static_assert(kRegsSoft + 4 * kRegsDeq + kRegsRest == 6 * 80, "the launch's registers");
 constexpr int kParts = 4;            // parts announced ahead
 constexpr float kSlack = 6.f, kLift = 9.f;  // as in the few-row kernel
-// Values of a record this many binary orders below the largest so far: the reference may then lie so far
-// above the record's weights that they leave fp32's range.
+// Values of a record this many binary orders below the largest so far: the reference may then lie so
+// far above the record's weights that they leave fp32's range.
 constexpr float kSpread = 64.f;
 constexpr int kExps = 8;             // steps of record exponents kept
 constexpr int kNotFinite = 127;      // in place of the exponent of a query row that is not finite
@@ -321,7 +325,8 @@ __device__ __forceinline__ uint32_t magnitudes(uint32_t params) {
   return params == 0x7fc00000u ? 0u : params & 0x7fff7fffu;
 }
 
-// e with |bias| + 15 |step| < 2^e for the largest of either over the warp; at most 118 (kLargest).
+// e with |bias| + 15 |step| < 2^e for the largest of either over the warp; at most 119: kLargest bounds
+// the bias below 2^116 and the step below 2^117 / 15.
 __device__ __forceinline__ int exponent_of(uint32_t packed) {
   const int s = (int)(__reduce_max_sync(~0u, packed & 0xffffu) >> 7);
   const int b = (int)(__reduce_max_sync(~0u, packed >> 16) >> 7);
@@ -1093,8 +1098,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
 // tiles read.
 constexpr int kPrepThreads = 512;
 // From this many row tiles per context, on average, it pays (256 channels, 16 contexts of 2000 to
-// 4000 tokens, prepared against not: 4 row tiles 96 and 83 us, 6 113 and 109, 8 132 and 134, 16 (8
-// contexts) 130 and 152; 128 channels: 4 204 and 177, 8 324 and 337).
+// 4000 tokens, prepared against not: 4 row tiles 97 and 87 us, 6 114 and 113, 8 133 and 138, 16 (8
+// contexts) 131 and 156; 128 channels: 4 206 and 181, 8 326 and 340).
 constexpr int kPrepTiles = 8;
 constexpr int64_t kMostPrep = 512ll << 20;  // bytes of operands held
 

@@ -1,7 +1,8 @@
 // The row kernels of the attention step (include/attn.h): norm and rotation of query and key
 // heads, quantisation of keys and values into the paged 4-bit cache, and the way back.  Each is
-// one pass over its rows, bound by HBM for prompts and by launch latency for single tokens: a
-// lane holds 8 channels (one 16-byte load), the D / 8 lanes of a row reduce by shuffles.
+// one pass over its rows, bound by launch latency for single tokens and for prompts as stated at each
+// (by loads that wait for one another, append by instruction issue): a lane holds 8 channels (one
+// 16-byte load), the D / 8 lanes of a row reduce by shuffles.
 #include "attn.cuh"
 
 namespace moe {
@@ -286,7 +287,9 @@ __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t params) {
   return narrow(r);
 }
 
-// A group of lanes per (token, head); bound by HBM (16 bytes read, 32 written per lane and tensor).
+// A group of lanes per (token, head).  A lane reads 4 bytes of codes and its group's parameter word,
+// and writes 16, for keys and for values.  Bound by latency for prompts: the slot, then the record,
+// then the stores, one row a group (4.2 TB/s, see above).
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_read_kernel(RowsArgs a) {
   using R = Record<D>;
