@@ -339,7 +339,9 @@ class MoeLayer:
     def forward(self, x, y=None, stream=None):
         import torch
         T = x.shape[0]
-        if y is None:
+        if y is None and stream is None:
+            y = torch.empty_like(x)
+        elif y is None:
             with torch.cuda.stream(stream):  # memory of the stream that writes it
                 y = torch.empty_like(x)
         _check(moe_forward(self.handle, _ptr(x), T, _ptr(y), self._stream(stream)), "moe_forward")
