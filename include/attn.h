@@ -9,6 +9,13 @@
  *   attn_kv4_forward    causal attention of the new tokens over the cached rows
  *   attn_kv4_read       cached rows back as bf16 (to move, share or inspect a prefix)
  *
+ * and, for steps that verify drafted trees and for layers that see a window of their context,
+ *
+ *   attn_tree_plan             depths and ancestor masks of drafted trees, behind attn_plan
+ *   attn_qk_norm_rope_append   norm, rotation and quantisation of a step's rows, one pass
+ *   attn_kv4_forward_masked    attention through a window with first tokens, or of a tree
+ *   attn_kv4_accept            the accepted tokens' cached rows moved to where they belong
+ *
  * Source: "Optimizing on-device inference for Apple Silicon", § "Read attention cache
  * efficiently" (16 query heads over 2 key/value heads of 256 channels; the query heads of a
  * key/value head share one pass over its cached rows) and § "Reduce intermediate and state
@@ -37,6 +44,13 @@
  *     gives 0.  Scores, softmax sums and outputs are held in fp32 and rounded once to bf16.
  *     Scores are in range below 2^23 (in units of log 2): a row with larger ones may read NaN, and
  *     from 2^28 on it does.
+ *   window and first tokens: a query at position p sees the cached tokens t <= p with t < S or t > p -
+ *     W (a window of W tokens, the query's own among them, and S first tokens).
+ *   tree: the n_b new tokens of request b are drafted, token i behind token parent_i < i, or
+ *     (parent_i = -1) behind the context.  All are appended, token i in row kv_b - n_b + i as by the
+ *     plan; its position is kv_b - n_b plus its depth, the number of its ancestors.  Token i sees all
+ *     cached tokens before the drafted ones, its ancestors and itself.  Once some are accepted,
+ *     their rows move to rows kv_b - n_b, kv_b - n_b + 1, ...; the cache is as if no other had been.
  *
  * Cache of one layer: one caller-owned device array of n_pages * Hkv * P * (D + D / 8) bytes (0.5625
  * bytes a channel), 128-byte aligned, written by attn_kv4_append only: records [n_pages][Hkv][P / 16]
@@ -158,6 +172,69 @@ int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void*
                      const int32_t* block_table, int table_width, const int32_t* q_offsets,
                      const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
                      void* out, int64_t out_stride, void* stream);
+
+/* Depths and ancestor masks of B requests' drafted trees; one launch.
+ *   parents [T] int32     index in its request of each new token's parent, below its own; -1 where it
+ *                         follows the context.  Others are recorded (MOE_ERR_INVALID_ARG) and count
+ *                         as -1.
+ *   q_offsets, kv_lens    as for attn_kv4_forward
+ *   max_q_len             1..256 and at most 32 mask_words: bounds n_b; a request beyond it is cut to it
+ *                         (MOE_ERR_DEVICE)
+ *   positions [T] int32, out: kv_b - n_b (0 where that is negative) plus the token's depth
+ *   masks [T][mask_words] uint32, out: bit j % 32 of word j / 32 for each token j of its request that
+ *                         it sees: its ancestors and itself
+ * Rows of the outputs behind the last request's tokens become 0. */
+int attn_tree_plan(attn_handle h, const int32_t* parents, const int32_t* q_offsets,
+                   const int32_t* kv_lens, int B, int T, int max_q_len, int32_t* positions,
+                   uint32_t* masks, int mask_words, void* stream);
+
+/* attn_qk_norm_rope of T tokens' queries and keys and attn_kv4_append of the turned keys and the
+ * values v [T][Hkv][D], in one launch: the keys are not written as bf16.  Arguments as there, but
+ * q_weight and k_weight may both be NULL: no norm then, the rotation alone.  q_out may be q itself.
+ * The turned key rows are rounded to bf16 and quantised.  Before, every operation is a single one
+ * in fp32, so the codes are the same everywhere: the sum of a row's squares, rounded once, times 1 / D,
+ * plus eps; 1 / sqrt of it, two operations; x times that, times the weight; a cos - b sin and b cos + a
+ * sin, three operations each.  (attn_qk_norm_rope rounds in other places, so its rows may differ in
+ * the last bit.)  Queries of tokens whose slot is negative are formed all the same. */
+int attn_qk_norm_rope_append(attn_handle h, const void* q, int64_t q_stride, const void* k,
+                             int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, const int32_t* slots, const void* q_weight,
+                             const void* k_weight, float eps, const float* cos_sin,
+                             int n_positions, int rotary_dim, int interleaved, int T, void* q_out,
+                             int64_t q_out_stride, void* cache, void* stream);
+
+/* attn_kv4_forward with a narrower view:
+ *   window      W >= 1, or 0: no window; at most 2^30
+ *   sinks       S >= 0 first tokens that stay visible behind the window (without one they mean
+ *               nothing); at most 2^30
+ *   masks       [T][mask_words] uint32, or NULL: causal.  Bit j of its row tells whether a query sees
+ *               drafted token j of its request (bits from n_b on mean nothing); the cached tokens
+ *               before the drafted ones it sees all, as far as a window lets it.  Its position is
+ *               kv_b - n_b - 1 plus the number of drafted tokens that it sees.  max_q_len is at most
+ *               256 and 32 mask_words, and at most W if there is a window (so a window never
+ *               hides drafted tokens).
+ * A query that sees no token gives 0.  Pages that hold no token which any query of the request sees are
+ * not read: their entries of block_table may be anything, such as those of pages given back
+ * behind a window. */
+int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, const void* cache,
+                            const int32_t* block_table, int table_width, const int32_t* q_offsets,
+                            const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
+                            int window, int sinks, const uint32_t* masks, int mask_words,
+                            void* out, int64_t out_stride, void* stream);
+
+/* Moves the cached rows (codes and parameters, bit for bit) of accepted tokens: of request b, row
+ * ctx_lens[b] + paths[b][i] to row ctx_lens[b] + i, for i = 0 .. path_lens[b] - 1; one launch.
+ *   ctx_lens [B] int32       cached tokens before the drafted ones
+ *   paths [B][path_width] int32   accepted tokens by their index in their request, ascending; the
+ *                            entries behind path_lens[b] are not read
+ *   path_lens [B] int32      0 .. path_width
+ * Rows behind the accepted ones keep what they hold.  Requests share none of the pages that they move
+ * rows in.  A length out of range moves nothing, an entry that is negative or not above the one
+ * before it, or a row outside the table or the cache, is left out (MOE_ERR_DEVICE; the request's moved
+ * rows are then undefined). */
+int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int table_width,
+                    const int32_t* ctx_lens, const int32_t* paths, int path_width,
+                    const int32_t* path_lens, int B, void* stream);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,9 @@ EXPORTS = ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_ge
            "moe_test_expire_waits", "gdn_scan", "moe_check_routing")
 
 ATTN_EXPORTS = ("attn_create", "attn_destroy", "attn_get_device_error", "attn_plan",
-                "attn_qk_norm_rope", "attn_kv4_append", "attn_kv4_read", "attn_kv4_forward")
+                "attn_qk_norm_rope", "attn_kv4_append", "attn_kv4_read", "attn_kv4_forward",
+                "attn_tree_plan", "attn_qk_norm_rope_append", "attn_kv4_forward_masked",
+                "attn_kv4_accept")
 
 # kernel order reported by moe_profile_end
 KERNELS_GEMM = ("router_topk", "route_plan_scatter", "experts", "combine")
@@ -131,6 +133,19 @@ def lib():
         L.attn_kv4_forward.argtypes = [_c_void_p, _c_void_p, i64, _c_void_p, _c_void_p, _c_int,
                                        _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
                                        _c_void_p, i64, _c_void_p]
+        L.attn_tree_plan.argtypes = [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int,
+                                     _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p]
+        L.attn_qk_norm_rope_append.argtypes = [_c_void_p, _c_void_p, i64, _c_void_p, i64,
+                                               _c_void_p, i64, _c_void_p, _c_void_p, _c_void_p,
+                                               _c_void_p, ctypes.c_float, _c_void_p, _c_int,
+                                               _c_int, _c_int, _c_int, _c_void_p, i64, _c_void_p,
+                                               _c_void_p]
+        L.attn_kv4_forward_masked.argtypes = [_c_void_p, _c_void_p, i64, _c_void_p, _c_void_p,
+                                              _c_int, _c_void_p, _c_void_p, _c_int, _c_int, _c_int,
+                                              _c_int, _c_int, _c_int, _c_void_p, _c_int, _c_void_p,
+                                              i64, _c_void_p]
+        L.attn_kv4_accept.argtypes = [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p,
+                                      _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p]
         for fn in ATTN_EXPORTS:
             getattr(L, fn).restype = _c_int
         for fn in ("moe_create", "moe_create_q4", "moe_read_probe", "moe_route", "moe_forward", "moe_forward_host",
@@ -246,6 +261,35 @@ def attn_kv4_forward(h, q, q_stride, cache, block_table, table_width, q_offsets,
                      max_q_len, max_kv_len, out, out_stride, stream):
     return lib().attn_kv4_forward(h, q, q_stride, cache, block_table, table_width, q_offsets,
                                   kv_lens, B, T, max_q_len, max_kv_len, out, out_stride, stream)
+
+
+def attn_tree_plan(h, parents, q_offsets, kv_lens, B, T, max_q_len, positions, masks, mask_words,
+                   stream):
+    return lib().attn_tree_plan(h, parents, q_offsets, kv_lens, B, T, max_q_len, positions, masks,
+                                mask_words, stream)
+
+
+def attn_qk_norm_rope_append(h, q, q_stride, k, k_stride, v, v_stride, positions, slots, q_weight,
+                             k_weight, eps, cos_sin, n_positions, rotary_dim, interleaved, T,
+                             q_out, q_out_stride, cache, stream):
+    return lib().attn_qk_norm_rope_append(h, q, q_stride, k, k_stride, v, v_stride, positions,
+                                          slots, q_weight, k_weight, eps, cos_sin, n_positions,
+                                          rotary_dim, interleaved, T, q_out, q_out_stride, cache,
+                                          stream)
+
+
+def attn_kv4_forward_masked(h, q, q_stride, cache, block_table, table_width, q_offsets, kv_lens, B,
+                            T, max_q_len, max_kv_len, window, sinks, masks, mask_words, out,
+                            out_stride, stream):
+    return lib().attn_kv4_forward_masked(h, q, q_stride, cache, block_table, table_width,
+                                         q_offsets, kv_lens, B, T, max_q_len, max_kv_len, window,
+                                         sinks, masks, mask_words, out, out_stride, stream)
+
+
+def attn_kv4_accept(h, cache, block_table, table_width, ctx_lens, paths, path_width, path_lens, B,
+                    stream):
+    return lib().attn_kv4_accept(h, cache, block_table, table_width, ctx_lens, paths, path_width,
+                                 path_lens, B, stream)
 
 
 def moe_test_expire_waits(h, n_calls):
@@ -493,6 +537,33 @@ class PagedAttention:
                     f"{data.device}")
         return data.data_ptr()
 
+    def _weight(self, w, what):
+        """Address of a norm's weights."""
+        if (w.dtype is not self._bf16 or w.get_device() != self._device
+                or w.shape != (self.head_dim,) or w.stride(0) != 1):
+            _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {self.head_dim} contiguous bfloat16 on "
+                    f"cuda:{self._device}")
+        return w.data_ptr()
+
+    def _turns(self, positions, cos_sin, T):
+        """(rows, rotary_dim, address of the positions, of the table); no rotation without one."""
+        if cos_sin is None:
+            return 0, 0, None, None
+        if (cos_sin.dtype is not self._f32 or cos_sin.get_device() != self._device
+                or cos_sin.dim() != 2 or not cos_sin.is_contiguous()):
+            _refuse(MOE_ERR_INVALID_ARG, "cos_sin: expected a contiguous float32 matrix on "
+                    f"cuda:{self._device}")
+        n_pos, rot = cos_sin.shape
+        return n_pos, rot, self._ints(positions, "positions", T), cos_sin.data_ptr()
+
+    def _masks(self, masks, T):
+        """(address, words) of drafted tokens' masks [T][words]."""
+        if masks.dim() != 2:
+            _refuse(MOE_ERR_INVALID_ARG, f"masks: expected int32 numbers of shape ({T}, words), got "
+                    f"{tuple(masks.shape)}")
+        words = masks.shape[1]
+        return self._ints(masks, "masks", T * words), words
+
     def _new(self, shape, dtype, stream):
         if stream is None:
             return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self._device}")
@@ -543,20 +614,9 @@ class PagedAttention:
         rows = self._rows
         (qp, qs), (kp, ks) = rows(q, "q", Hq, T), rows(k, "k", Hkv, T)
         (qop, qos), (kop, kos) = rows(q_out, "q_out", Hq, T), rows(k_out, "k_out", Hkv, T)
-        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if (w.dtype is not self._bf16 or w.get_device() != self._device or w.shape != (D,)
-                    or w.stride(0) != 1):
-                _refuse(MOE_ERR_INVALID_ARG, f"{what}: expected {D} contiguous bfloat16 on "
-                        f"cuda:{self._device}")
-        n_pos = rot = 0
-        pos = table = None
-        if cos_sin is not None:
-            if (cos_sin.dtype is not self._f32 or cos_sin.get_device() != self._device
-                    or cos_sin.dim() != 2 or not cos_sin.is_contiguous()):
-                _refuse(MOE_ERR_INVALID_ARG, "cos_sin: expected a contiguous float32 matrix on "
-                        f"cuda:{self._device}")
-            n_pos, rot = cos_sin.shape
-            pos, table = self._ints(positions, "positions", T), cos_sin.data_ptr()
+        self._weight(q_weight, "q_weight")
+        self._weight(k_weight, "k_weight")
+        n_pos, rot, pos, table = self._turns(positions, cos_sin, T)
         st = self._lib.attn_qk_norm_rope(
             self.handle, qp, qs, kp, ks, pos, q_weight.data_ptr(), k_weight.data_ptr(), eps,
             table, n_pos, rot, 1 if interleaved else 0, T, qop, qos, kop, kos,
@@ -592,9 +652,73 @@ class PagedAttention:
             _check(st, "attn_kv4_read")
         return k_out, v_out
 
+    def qk_norm_rope_append(self, q, k, v, positions, slots, q_weight, k_weight, cos_sin, cache,
+                            eps=1e-6, interleaved=False, q_out=None, stream=None):
+        """qk_norm_rope of q and k and append of the turned keys and of v in one launch (both weights
+        None: no norm); returns q_out."""
+        if q is None or k is None or v is None:
+            _missing("q, k or v")
+        if (q_weight is None) != (k_weight is None):
+            _missing("q_weight or k_weight (both or neither)")
+        T, Hq, Hkv = q.shape[0], self.n_q_heads, self.n_kv_heads
+        q_out = self._new((T, Hq, self.head_dim), self._bf16, stream) if q_out is None else q_out
+        rows = self._rows
+        (qp, qs), (kp, ks), (vp, vs) = rows(q, "q", Hq, T), rows(k, "k", Hkv, T), rows(v, "v", Hkv, T)
+        qop, qos = rows(q_out, "q_out", Hq, T)
+        qw = kw = None
+        if q_weight is not None:
+            qw, kw = self._weight(q_weight, "q_weight"), self._weight(k_weight, "k_weight")
+        n_pos, rot, pos, table = self._turns(positions, cos_sin, T)
+        st = self._lib.attn_qk_norm_rope_append(
+            self.handle, qp, qs, kp, ks, vp, vs, pos, self._ints(slots, "slots", T), qw, kw, eps,
+            table, n_pos, rot, 1 if interleaved else 0, T, qop, qos, self._cache(cache),
+            self._stream(stream))
+        if st:
+            _check(st, "attn_qk_norm_rope_append")
+        return q_out
+
+    def tree_plan(self, parents, q_offsets, kv_lens, max_q_len, positions=None, masks=None,
+                  stream=None):
+        """Positions and masks [T][words] of drafted trees: parents [T] are indices in a token's own
+        request, -1 behind the context.  Returns (positions, masks)."""
+        if parents is None or kv_lens is None:
+            _missing("parents" if parents is None else "kv_lens")
+        T, B = parents.numel(), kv_lens.numel()
+        positions = self._new(T, self._i32, stream) if positions is None else positions
+        if masks is None:
+            masks = self._new((T, max(1, (max_q_len + 31) // 32)), self._i32, stream)
+        ints = self._ints
+        mp, words = self._masks(masks, T)
+        st = self._lib.attn_tree_plan(
+            self.handle, ints(parents, "parents", T), ints(q_offsets, "q_offsets", B + 1),
+            ints(kv_lens, "kv_lens", B), B, T, max_q_len, ints(positions, "positions", T), mp, words,
+            self._stream(stream))
+        if st:
+            _check(st, "attn_tree_plan")
+        return positions, masks
+
+    def accept(self, cache, block_table, ctx_lens, paths, path_lens, stream=None):
+        """Moves cached rows ctx_lens[b] + paths[b][i] to ctx_lens[b] + i, i < path_lens[b]: the accepted
+        tokens of paths [B][width], ascending indices in their request."""
+        if block_table is None or paths is None:
+            _missing("block_table" if block_table is None else "paths")
+        if block_table.dim() != 2 or paths.dim() != 2:
+            _refuse(MOE_ERR_INVALID_ARG, "block_table and paths: expected matrices")
+        B, width = block_table.shape
+        path_width = paths.shape[1]
+        ints = self._ints
+        st = self._lib.attn_kv4_accept(
+            self.handle, self._cache(cache), ints(block_table, "block_table", B * width), width,
+            ints(ctx_lens, "ctx_lens", B), ints(paths, "paths", B * path_width), path_width,
+            ints(path_lens, "path_lens", B), B, self._stream(stream))
+        if st:
+            _check(st, "attn_kv4_accept")
+
     def forward(self, q, cache, block_table, q_offsets, kv_lens, max_q_len, max_kv_len, out=None,
-                stream=None):
-        """Causal attention of the requests' new tokens over their cached rows; returns out."""
+                stream=None, window=0, sinks=0, masks=None):
+        """Causal attention of the requests' new tokens over their cached rows; returns out.  With
+        `window`, through a window of that many tokens and `sinks` first tokens; with masks
+        [T][words] (tree_plan), of drafted trees."""
         if q is None or block_table is None:
             _missing("q" if q is None else "block_table")
         T, Hq = q.shape[0], self.n_q_heads
@@ -602,6 +726,16 @@ class PagedAttention:
         out = self._new((T, Hq, self.head_dim), self._bf16, stream) if out is None else out
         (qp, qs), (op, os_) = self._rows(q, "q", Hq, T), self._rows(out, "out", Hq, T)
         ints = self._ints
+        if window or sinks or masks is not None:
+            mp, words = (None, 0) if masks is None else self._masks(masks, T)
+            st = self._lib.attn_kv4_forward_masked(
+                self.handle, qp, qs, self._cache(cache),
+                ints(block_table, "block_table", B * width), width,
+                ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B), B, T, max_q_len,
+                max_kv_len, window, sinks, mp, words, op, os_, self._stream(stream))
+            if st:
+                _check(st, "attn_kv4_forward_masked")
+            return out
         st = self._lib.attn_kv4_forward(
             self.handle, qp, qs, self._cache(cache), ints(block_table, "block_table", B * width),
             width, ints(q_offsets, "q_offsets", B + 1), ints(kv_lens, "kv_lens", B), B, T,

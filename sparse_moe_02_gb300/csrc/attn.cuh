@@ -16,6 +16,7 @@ constexpr int kGroup = 64;        // channels per scale and bias
 // Requests of a call at most.  The kernels' shared-memory limits are set for as many whatever a handle
 // asks for: they belong to the functions, which the handles of a process share.
 constexpr int kMaxRequests = 1024;
+constexpr int kMaxDrafts = 256;  // tokens of a tree
 // Cached rows hold magnitudes below this only (larger ones count as not finite): the kernels'
 // powers of two of a record's bound, 2^119 at most, and their inverses stay normal fp32 numbers.
 constexpr float kLargest = 8.307675e34f;  // 2^116
@@ -83,6 +84,10 @@ struct FwdArgs {
   uint8_t* prep;      // [steps]: a step's key operand, then its value operand
   uint4* prep_exps;   // [steps][4]: exponents of the records
   int* err;
+  // Narrower views (attn_kv4_forward_masked): a window of 0 is none, no masks is causal.
+  int window, sinks;
+  const uint32_t* masks;
+  int mask_words;
 };
 
 __device__ __forceinline__ Req load_req(const FwdArgs& a, int b) {
@@ -124,6 +129,17 @@ struct PlanArgs {
 
 cudaError_t launch_attn_plan(const PlanArgs& a, int sms, cudaStream_t s);
 
+struct TreeArgs {
+  const int32_t *parents, *q_off, *kv_lens;
+  int B, T, max_q;
+  int32_t* positions;
+  uint32_t* masks;
+  int mask_words;
+  int* err;
+};
+
+cudaError_t launch_attn_tree_plan(const TreeArgs& a, cudaStream_t s);
+
 struct RopeArgs {
   const __nv_bfloat16 *q, *k;
   __nv_bfloat16 *q_out, *k_out;
@@ -151,6 +167,18 @@ struct RowsArgs {
 };
 
 cudaError_t launch_attn_append(const RowsArgs& a, int D, cudaStream_t s);
+// Norm (r.qw: or none), rotation and append; r.k_out is not used, a.k and a.v are.
+cudaError_t launch_attn_rope_append(const RopeArgs& r, const RowsArgs& a, int D, bool interleaved,
+                                    int sms, cudaStream_t s);
+
+struct AcceptArgs {
+  const int32_t* table;
+  int table_width;
+  const int32_t *ctx, *paths, *path_lens;
+  int path_width, B;
+};
+
+cudaError_t launch_attn_accept(const AcceptArgs& p, const RowsArgs& a, int D, cudaStream_t s);
 cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s);
 
 // Attention of few query rows per key/value head and request (n_b G <= 32): attn_decode.cu.  Its time
@@ -167,5 +195,8 @@ size_t attn_prefill_part_floats(int D);  // fp32 of a partial result, the larger
 int attn_prep_steps(const AttnDims& d, int max_requests);  // of contexts held as operands
 size_t attn_prep_step_bytes(int D);                        // of one, without its exponents
 cudaError_t launch_attn_prefill(const FwdArgs& a, int sms, cudaStream_t s);
+
+// Attention with a window or masks: attn_masked.cu.
+cudaError_t launch_attn_masked(const FwdArgs& a, int max_kv, int sms, cudaStream_t s);
 
 }  // namespace moe

@@ -77,6 +77,89 @@ moe::RowsArgs rows_args(attn_handle h, const void* cache, const int32_t* slots, 
   return a;
 }
 
+moe::RopeArgs rope_args(attn_handle h, const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const int32_t* positions, const void* q_weight,
+                        const void* k_weight, float eps, const float* cos_sin, int n_positions,
+                        int rotary_dim, int T, void* q_out, int64_t q_out_stride) {
+  moe::RopeArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.positions = positions;
+  a.qw = static_cast<const __nv_bfloat16*>(q_weight);
+  a.kw = static_cast<const __nv_bfloat16*>(k_weight);
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.n_positions = n_positions;
+  a.rot = rotary_dim;
+  a.T = T;
+  a.Hq = h->d.Hq;
+  a.Hkv = h->d.Hkv;
+  a.err = h->err;
+  return a;
+}
+
+// Masks of drafted tokens (NULL: none to check but the sizes).
+int check_masks(int max_q_len, const uint32_t* masks, int mask_words) {
+  if (max_q_len < 1 || mask_words < 1) return MOE_ERR_INVALID_ARG;
+  if (max_q_len > moe::kMaxDrafts || mask_words > moe::kMaxDrafts / 32 ||
+      max_q_len > 32 * mask_words)
+    return MOE_ERR_UNSUPPORTED;
+  return off4(masks) ? MOE_ERR_ALIGNMENT : MOE_OK;
+}
+
+constexpr int kMostTokens = 1 << 30;  // of a window: its bounds stay in 32 bits
+
+// The checks and arguments that both forms of the forward call share; *none: nothing to do.
+int forward_args(attn_handle h, const void* q, int64_t q_stride, const void* cache,
+                 const int32_t* block_table, int table_width, const int32_t* q_offsets,
+                 const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len, void* out,
+                 int64_t out_stride, moe::FwdArgs* args, bool* none) {
+  *none = false;
+  if (!h || B < 0 || table_width < 0 || max_q_len < 1 || max_kv_len < 0)
+    return MOE_ERR_INVALID_ARG;
+  int st = check_tokens(T);
+  if (st) return st;
+  if (B > h->cfg.max_requests) return MOE_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) {
+    *none = true;
+    return MOE_OK;
+  }
+  const int64_t w = (int64_t)h->d.Hq * h->d.D;
+  if ((st = check_rows(q, q_stride, w)) || (st = check_rows(out, out_stride, w)) ||
+      (st = check_cache(cache)))
+    return st;
+  if (!q_offsets || !kv_lens || (table_width > 0 && !block_table)) return MOE_ERR_INVALID_ARG;
+  if (off4(q_offsets) || off4(kv_lens) || off4(block_table)) return MOE_ERR_ALIGNMENT;
+  moe::FwdArgs& a = *args;
+  a = moe::FwdArgs{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.out_stride = out_stride;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.table = block_table;
+  a.table_width = table_width;
+  a.q_off = q_offsets;
+  a.kv_lens = kv_lens;
+  a.B = B;
+  a.T = T;
+  a.max_q = max_q_len < T ? max_q_len : T;
+  a.d = h->d;
+  a.part_o = h->part_o;
+  a.part_ml = h->part_ml;
+  a.desc = h->desc;
+  a.prep_at = h->prep_at;
+  a.prep_cap = h->prep_cap;
+  a.prep = h->prep;
+  a.prep_exps = h->prep_exps;
+  a.err = h->err;
+  return MOE_OK;
+}
+
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -217,28 +300,45 @@ int attn_qk_norm_rope(attn_handle h, const void* q, int64_t q_stride, const void
     return st;
   if (off16(q_weight) || off16(k_weight) || (rotary_dim > 0 && (off16(cos_sin) || off4(positions))))
     return MOE_ERR_ALIGNMENT;
-  moe::RopeArgs a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k = static_cast<const __nv_bfloat16*>(k);
-  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  moe::RopeArgs a = rope_args(h, q, q_stride, k, k_stride, positions, q_weight, k_weight, eps,
+                              cos_sin, n_positions, rotary_dim, T, q_out, q_out_stride);
   a.k_out = static_cast<__nv_bfloat16*>(k_out);
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.q_out_stride = q_out_stride;
   a.k_out_stride = k_out_stride;
-  a.positions = positions;
-  a.qw = static_cast<const __nv_bfloat16*>(q_weight);
-  a.kw = static_cast<const __nv_bfloat16*>(k_weight);
-  a.eps = eps;
-  a.cos_sin = cos_sin;
-  a.n_positions = n_positions;
-  a.rot = rotary_dim;
-  a.T = T;
-  a.Hq = h->d.Hq;
-  a.Hkv = h->d.Hkv;
-  a.err = h->err;
   return record_cuda_status(moe::launch_attn_qk_norm_rope(
       a, h->d.D, interleaved != 0, h->sms, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_qk_norm_rope_append(attn_handle h, const void* q, int64_t q_stride, const void* k,
+                             int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, const int32_t* slots, const void* q_weight,
+                             const void* k_weight, float eps, const float* cos_sin,
+                             int n_positions, int rotary_dim, int interleaved, int T, void* q_out,
+                             int64_t q_out_stride, void* cache, void* stream) {
+  if (!h) return MOE_ERR_INVALID_ARG;
+  int st = check_tokens(T);
+  if (st) return st;
+  if (rotary_dim < 0 || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (rotary_dim % 16 || rotary_dim > h->d.D) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!slots || !q_weight != !k_weight) return MOE_ERR_INVALID_ARG;
+  if (rotary_dim > 0 && (!positions || !cos_sin || n_positions < 1)) return MOE_ERR_INVALID_ARG;
+  const int64_t qw = (int64_t)h->d.Hq * h->d.D, kw = (int64_t)h->d.Hkv * h->d.D;
+  if ((st = check_rows(q, q_stride, qw)) || (st = check_rows(k, k_stride, kw)) ||
+      (st = check_rows(v, v_stride, kw)) || (st = check_rows(q_out, q_out_stride, qw)) ||
+      (st = check_cache(cache)))
+    return st;
+  if (off16(q_weight) || off16(k_weight) || off4(slots) ||
+      (rotary_dim > 0 && (off16(cos_sin) || off4(positions))))
+    return MOE_ERR_ALIGNMENT;
+  moe::RopeArgs r = rope_args(h, q, q_stride, k, k_stride, positions, q_weight, k_weight, eps,
+                              cos_sin, n_positions, rotary_dim, T, q_out, q_out_stride);
+  moe::RowsArgs a = rows_args(h, cache, slots, T);
+  a.k = r.k;
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  return record_cuda_status(moe::launch_attn_rope_append(
+      r, a, h->d.D, interleaved != 0, h->sms, static_cast<cudaStream_t>(stream)));
 }
 
 int attn_kv4_append(attn_handle h, const void* k, int64_t k_stride, const void* v,
@@ -287,44 +387,77 @@ int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void*
                      const int32_t* block_table, int table_width, const int32_t* q_offsets,
                      const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
                      void* out, int64_t out_stride, void* stream) {
-  if (!h || B < 0 || table_width < 0 || max_q_len < 1 || max_kv_len < 0)
-    return MOE_ERR_INVALID_ARG;
-  int st = check_tokens(T);
-  if (st) return st;
-  if (B > h->cfg.max_requests) return MOE_ERR_UNSUPPORTED;
-  if (B == 0 || T == 0) return MOE_OK;
-  const int64_t w = (int64_t)h->d.Hq * h->d.D;
-  if ((st = check_rows(q, q_stride, w)) || (st = check_rows(out, out_stride, w)) ||
-      (st = check_cache(cache)))
-    return st;
-  if (!q_offsets || !kv_lens || (table_width > 0 && !block_table)) return MOE_ERR_INVALID_ARG;
-  if (off4(q_offsets) || off4(kv_lens) || off4(block_table)) return MOE_ERR_ALIGNMENT;
-  moe::FwdArgs a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_stride = q_stride;
-  a.out = static_cast<__nv_bfloat16*>(out);
-  a.out_stride = out_stride;
-  a.cache = static_cast<const uint8_t*>(cache);
-  a.table = block_table;
-  a.table_width = table_width;
-  a.q_off = q_offsets;
-  a.kv_lens = kv_lens;
-  a.B = B;
-  a.T = T;
-  a.max_q = max_q_len < T ? max_q_len : T;
-  a.d = h->d;
-  a.part_o = h->part_o;
-  a.part_ml = h->part_ml;
-  a.desc = h->desc;
-  a.prep_at = h->prep_at;
-  a.prep_cap = h->prep_cap;
-  a.prep = h->prep;
-  a.prep_exps = h->prep_exps;
-  a.err = h->err;
+  moe::FwdArgs a;
+  bool none;
+  const int st = forward_args(h, q, q_stride, cache, block_table, table_width, q_offsets, kv_lens, B,
+                              T, max_q_len, max_kv_len, out, out_stride, &a, &none);
+  if (st || none) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return record_cuda_status(a.max_q * h->d.G <= moe::kDecodeRows
                                 ? moe::launch_attn_decode(a, max_kv_len, h->sms, s)
                                 : moe::launch_attn_prefill(a, h->sms, s));
+}
+
+int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, const void* cache,
+                            const int32_t* block_table, int table_width, const int32_t* q_offsets,
+                            const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
+                            int window, int sinks, const uint32_t* masks, int mask_words,
+                            void* out, int64_t out_stride, void* stream) {
+  if (window < 0 || sinks < 0) return MOE_ERR_INVALID_ARG;
+  if (window > kMostTokens || sinks > kMostTokens) return MOE_ERR_UNSUPPORTED;
+  if (masks) {
+    int st = check_masks(max_q_len, masks, mask_words);
+    if (st) return st;
+    if (window > 0 && max_q_len > window) return MOE_ERR_UNSUPPORTED;
+  }
+  moe::FwdArgs a;
+  bool none;
+  const int st = forward_args(h, q, q_stride, cache, block_table, table_width, q_offsets, kv_lens, B,
+                              T, max_q_len, max_kv_len, out, out_stride, &a, &none);
+  if (st || none) return st;
+  a.window = window;
+  a.sinks = sinks;
+  a.masks = masks;
+  a.mask_words = mask_words;
+  return record_cuda_status(
+      moe::launch_attn_masked(a, max_kv_len, h->sms, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_tree_plan(attn_handle h, const int32_t* parents, const int32_t* q_offsets,
+                   const int32_t* kv_lens, int B, int T, int max_q_len, int32_t* positions,
+                   uint32_t* masks, int mask_words, void* stream) {
+  if (!h || B < 0) return MOE_ERR_INVALID_ARG;
+  int st = check_tokens(T);
+  if (st) return st;
+  if (!masks && T > 0) return MOE_ERR_INVALID_ARG;
+  if ((st = check_masks(max_q_len, masks, mask_words))) return st;
+  if (B > h->cfg.max_requests) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!positions || (B > 0 && (!parents || !q_offsets || !kv_lens))) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)parents, (const void*)q_offsets, (const void*)kv_lens,
+                        (const void*)positions})
+    if (off4(p)) return MOE_ERR_ALIGNMENT;
+  moe::TreeArgs a{parents, q_offsets, kv_lens, B, T, max_q_len, positions, masks, mask_words,
+                  h->err};
+  return record_cuda_status(moe::launch_attn_tree_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int table_width,
+                    const int32_t* ctx_lens, const int32_t* paths, int path_width,
+                    const int32_t* path_lens, int B, void* stream) {
+  if (!h || B < 0 || table_width < 0 || path_width < 0) return MOE_ERR_INVALID_ARG;
+  if (B > h->cfg.max_requests || path_width > kMaxTokens) return MOE_ERR_UNSUPPORTED;
+  if (B == 0 || path_width == 0) return MOE_OK;
+  const int st = check_cache(cache);
+  if (st) return st;
+  if (!ctx_lens || !paths || !path_lens || (table_width > 0 && !block_table))
+    return MOE_ERR_INVALID_ARG;
+  if (off4(block_table) || off4(ctx_lens) || off4(paths) || off4(path_lens))
+    return MOE_ERR_ALIGNMENT;
+  const moe::RowsArgs a = rows_args(h, cache, nullptr, 0);
+  const moe::AcceptArgs p{block_table, table_width, ctx_lens, paths, path_lens, path_width, B};
+  return record_cuda_status(
+      moe::launch_attn_accept(p, a, h->d.D, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
-// attn_plan: block tables and slot maps of one step from the requests' lengths (include/attn.h
-// states the rule).
+// attn_plan: block tables and slot maps of one step from the requests' lengths, and attn_tree_plan at
+// its end (include/attn.h states the rules).
 //
 // Two prefix sums over the requests give each its first token and its first entry of the free
 // list; every token then finds its request by binary search over the first tokens.  The work is
@@ -149,6 +149,55 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(PlanArgs a) {
   }
 }
 
+// attn_tree_plan: a block per request, a thread per drafted token.  Each walks from its token to the
+// context over the parents in shared memory (they fall, so every walk ends), which sets the bits of
+// its mask and counts its depth.  Bound by latency: offsets, then parents, then a step of the walk
+// for each level of the tree.
+__global__ void __launch_bounds__(kMaxDrafts) attn_tree_plan_kernel(TreeArgs a) {
+  __shared__ int parent[kMaxDrafts];
+  const int tid = threadIdx.x, b = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  if (b < a.B) {
+    const int lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_lens[b];
+    const int q0 = min(max(lo, 0), a.T);
+    const int n = min(min(max(hi, q0), a.T) - q0, a.max_q);
+    if (tid == 0 && (lo < 0 || hi < lo || hi > a.T || hi - lo > a.max_q || kv < 0))
+      record_error(a.err, kDevErrState);
+    if (tid < n) {
+      int p = a.parents[q0 + tid];
+      if (p < -1 || p >= tid) {
+        record_error(a.err, kDevErrArg);
+        p = -1;
+      }
+      parent[tid] = p;
+    }
+    __syncthreads();
+    if (tid < n) {
+      uint32_t w[kMaxDrafts / 32] = {};
+      int depth = -1;
+      for (int j = tid; j >= 0; j = parent[j]) {
+#pragma unroll
+        for (int k = 0; k < kMaxDrafts / 32; ++k)
+          if (j >> 5 == k) w[k] |= 1u << (j & 31);
+        ++depth;
+      }
+      a.positions[q0 + tid] = max(kv - n, 0) + depth;
+      uint32_t* row = a.masks + (int64_t)(q0 + tid) * a.mask_words;
+#pragma unroll
+      for (int k = 0; k < kMaxDrafts / 32; ++k)
+        if (k < a.mask_words) row[k] = w[k];
+    }
+  }
+  if (b == (int)gridDim.x - 1) {  // behind the last request
+    const int end = a.B > 0 ? min(max(a.q_off[a.B], 0), a.T) : 0;
+    for (int t = end + tid; t < a.T; t += blockDim.x) {
+      a.positions[t] = 0;
+      for (int k = 0; k < a.mask_words; ++k) a.masks[(int64_t)t * a.mask_words + k] = 0;
+    }
+  }
+}
+
 constexpr size_t plan_smem(int B) { return (size_t)(4 * B + 1) * sizeof(int); }
 static_assert(plan_smem(kMaxRequests) + 1024 <= 48 << 10, "what a kernel may have without asking");
 
@@ -158,6 +207,11 @@ cudaError_t launch_attn_plan(const PlanArgs& a, int sms, cudaStream_t s) {
   int grid = (a.T + kTokensPerBlock - 1) / kTokensPerBlock;
   grid = grid < 1 ? 1 : grid > sms ? sms : grid;
   return launch_pdl(attn_plan_kernel, dim3(grid), dim3(kThreads), plan_smem(a.B), s, a);
+}
+
+cudaError_t launch_attn_tree_plan(const TreeArgs& a, cudaStream_t s) {
+  return launch_pdl(attn_tree_plan_kernel, dim3(a.B < 1 ? 1 : a.B), dim3((a.max_q + 31) / 32 * 32), 0,
+                    s, a);
 }
 
 }  // namespace moe

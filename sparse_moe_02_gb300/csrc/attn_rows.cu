@@ -229,6 +229,32 @@ __device__ __forceinline__ Coded code_row(uint4 w) {
   return c;
 }
 
+// Writes a token's coded key and value rows of head h to its slot, the lane's 8 channels of each.
+template <int D>
+__device__ __forceinline__ void write_rows(const RowsArgs& a, int slot, int h, int li,
+                                           unsigned group_mask, Coded k, Coded v) {
+  using R = Record<D>;
+  constexpr int NG = D / kGroup;
+  const bool good = (__ballot_sync(~0u, !(k.finite && v.finite)) & group_mask) == 0;
+  if (!good) {  // queries that see the token read NaN, through its scores
+    k.word = v.word = 0;
+    k.params = 0x7fc00000u;
+    v.params = 0;
+  }
+  if (slot >= a.n_slots) {
+    if (li == 0) record_error(a.err, kDevErrState);
+  } else if (slot >= 0) {
+    uint8_t* rec = a.cache + record_of(a, slot, h) * R::kBytes;
+    const int row = slot & 15, word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
+    reinterpret_cast<uint32_t*>(rec + row * R::kRow)[word] = k.word;
+    reinterpret_cast<uint32_t*>(rec + R::kV + row * R::kRow)[word] = v.word;
+    if ((li & 7) == 0) {
+      reinterpret_cast<uint32_t*>(rec + R::kKp + row * R::kPar)[li >> 3] = k.params;
+      reinterpret_cast<uint32_t*>(rec + R::kVp + row * R::kPar)[li >> 3] = v.params;
+    }
+  }
+}
+
 // A group of L = D / 8 lanes per (token, head): key row and value row together, since a
 // non-finite channel of either marks both.
 //
@@ -238,8 +264,7 @@ __device__ __forceinline__ Coded code_row(uint4 w) {
 // with cold caches, their reading 20 us (4.2 TB/s), both in turn 47 us; 48 tokens 3.9 us for both.
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
-  using R = Record<D>;
-  constexpr int L = D / 8, NG = D / kGroup;
+  constexpr int L = D / 8;
   constexpr int kPerBlock = kThreads / L;
   const int li = threadIdx.x % L;
   const unsigned group_mask = L == 32 ? ~0u : ((1u << L) - 1) << ((threadIdx.x & 31) - li);
@@ -253,27 +278,221 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
     const int slot = live ? a.slots[t] : -1;
     const uint4 kw = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + 8 * li);
     const uint4 vw = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + 8 * li);
-    Coded k = code_row(kw), v = code_row(vw);
-    const bool good = (__ballot_sync(~0u, !(k.finite && v.finite)) & group_mask) == 0;
-    if (!good) {  // queries that see the token read NaN, through its scores
-      k.word = v.word = 0;
-      k.params = 0x7fc00000u;
-      v.params = 0;
-    }
-    if (slot >= a.n_slots) {
-      if (li == 0) record_error(a.err, kDevErrState);
-    } else if (slot >= 0) {
-      uint8_t* rec = a.cache + record_of(a, slot, h) * R::kBytes;
-      const int row = slot & 15, word = ((li & 7) ^ row_swz(slot)) * NG + (li >> 3);
-      reinterpret_cast<uint32_t*>(rec + row * R::kRow)[word] = k.word;
-      reinterpret_cast<uint32_t*>(rec + R::kV + row * R::kRow)[word] = v.word;
-      if ((li & 7) == 0) {
-        reinterpret_cast<uint32_t*>(rec + R::kKp + row * R::kPar)[li >> 3] = k.params;
-        reinterpret_cast<uint32_t*>(rec + R::kVp + row * R::kPar)[li >> 3] = v.params;
+    write_rows<D>(a, slot, h, li, group_mask, code_row(kw), code_row(vw));
+  }
+}
+
+// ------------------------------------------------------------------- norm, rotation and append
+
+// Sum over L neighbouring lanes of the lanes' squares, as if rounded once: two floats carry it, the
+// second what the first's additions round off (exactly, Knuth's two-sum; the squares of bf16 values are
+// fp32 numbers).
+template <int L>
+__device__ __forceinline__ float sum_squares(const Row8& r) {
+  float s = __fmul_rn(r.x[0], r.x[0]), e = 0.f;
+  auto add = [&](float p) {
+    const float t = __fadd_rn(s, p), u = __fsub_rn(t, s);
+    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(p, u)));
+    s = t;
+  };
+#pragma unroll
+  for (int i = 1; i < 8; ++i) add(__fmul_rn(r.x[i], r.x[i]));
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) {
+    const float p = __shfl_xor_sync(~0u, s, o);
+    e = __fadd_rn(e, __shfl_xor_sync(~0u, e, o));
+    add(p);
+  }
+  return s < INFINITY ? __fadd_rn(s, e) : s;
+}
+
+// The cosines and sines of the lane's channels ch .. ch + 7 at a token's position, a position out of
+// range at 0.  INTER: of pairs ch / 2 .. ch / 2 + 3 (the first four of each); else of the channels, the
+// sines of the lower half negated.
+template <bool INTER>
+__device__ __forceinline__ void load_turn(const RopeArgs& a, int t, int li, int ch, float (&cs)[8],
+                                          float (&sn)[8]) {
+  int pos = a.positions[t];
+  if (pos < 0 || pos >= a.n_positions) {
+    if (li == 0) record_error(a.err, kDevErrState);
+    pos = 0;
+  }
+  const int half = a.rot / 2;
+  const float* row = a.cos_sin + (int64_t)pos * a.rot;
+  const int i = INTER ? ch / 2 : ch < half ? ch : ch - half;
+  const float sg = !INTER && ch < half ? -1.f : 1.f;
+#pragma unroll
+  for (int e = 0; e < (INTER ? 1 : 2); ++e) {
+    const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * e);
+    const float4 s = *reinterpret_cast<const float4*>(row + half + i + 4 * e);
+    cs[4 * e] = c.x; cs[4 * e + 1] = c.y; cs[4 * e + 2] = c.z; cs[4 * e + 3] = c.w;
+    sn[4 * e] = sg * s.x; sn[4 * e + 1] = sg * s.y; sn[4 * e + 2] = sg * s.z; sn[4 * e + 3] = sg * s.w;
+  }
+}
+
+// Norm (NORM) and rotation of a row, in the single operations that include/attn.h states.
+template <int D, bool INTER, bool NORM>
+__device__ __forceinline__ uint4 turn_row(const RopeArgs& a, uint4 raw, const Row8& w, int li, int ch,
+                                          const float (&cs)[8], const float (&sn)[8]) {
+  constexpr int L = D / 8;
+  Row8 r = widen(raw);
+  if (NORM) {
+    const float mean = __fadd_rn(__fmul_rn(sum_squares<L>(r), 1.f / D), a.eps);
+    const float inv = __frcp_rn(__fsqrt_rn(mean));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.x[e] = __fmul_rn(__fmul_rn(r.x[e], inv), w.x[e]);
+  }
+  if (a.rot) {
+    const bool turn = ch < a.rot;
+    if (INTER) {
+      if (turn) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = r.x[2 * e], y = r.x[2 * e + 1];
+          r.x[2 * e] = __fsub_rn(__fmul_rn(x, cs[e]), __fmul_rn(y, sn[e]));
+          r.x[2 * e + 1] = __fadd_rn(__fmul_rn(y, cs[e]), __fmul_rn(x, sn[e]));
+        }
+      }
+    } else {
+      // the pair's other half sits half / 8 lanes away
+      const int half = a.rot / 2, lane = threadIdx.x & 31;
+      const int mate = turn ? lane - li + (ch < half ? li + half / 8 : li - half / 8) : lane;
+      Row8 m;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m.x[e] = __shfl_sync(~0u, r.x[e], mate);
+      if (turn) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          r.x[e] = __fadd_rn(__fmul_rn(r.x[e], cs[e]), __fmul_rn(m.x[e], sn[e]));
       }
     }
   }
+  return narrow(r);
 }
+
+// attn_qk_norm_rope_append: a group of L = D / 8 lanes per row.  The first blocks take a key and a value
+// row each group, the others heads_per neighbouring query heads of a token, as in the norm and rotation
+// alone.
+template <int D, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kThreads) attn_rope_append_kernel(RopeArgs r, RowsArgs a,
+                                                                    int heads_per, int kv_blocks) {
+  constexpr int L = D / 8;
+  constexpr int kPerBlock = kThreads / L;
+  const int li = threadIdx.x % L;
+  const int ch = 8 * li;
+  const unsigned group_mask = L == 32 ? ~0u : ((1u << L) - 1) << ((threadIdx.x & 31) - li);
+  const bool turn = ch < r.rot;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x < kv_blocks) {
+    const uint32_t row = blockIdx.x * kPerBlock + threadIdx.x / L;
+    const bool live = row < (uint32_t)a.T * a.Hkv;  // below 2^27
+    const int t = live ? (int)(row / (uint32_t)a.Hkv) : 0, h = live ? (int)(row % (uint32_t)a.Hkv) : 0;
+    const uint4 kw = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + ch);
+    const uint4 vw = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + ch);
+    const int slot = live ? a.slots[t] : -1;
+    if (turn && live) load_turn<INTER>(r, t, li, ch, cs, sn);
+    Row8 w;
+    if (NORM) w = widen(*reinterpret_cast<const uint4*>(r.kw + ch));
+    const uint4 turned = turn_row<D, INTER, NORM>(r, kw, w, li, ch, cs, sn);
+    write_rows<D>(a, slot, h, li, group_mask, code_row(turned), code_row(vw));
+    return;
+  }
+  const uint32_t splits = (r.Hq + heads_per - 1) / heads_per;
+  const uint32_t item = (blockIdx.x - kv_blocks) * kPerBlock + threadIdx.x / L;
+  const bool live = item < (uint32_t)r.T * splits;
+  const int t = live ? (int)(item / splits) : 0;
+  const int h0 = live ? (int)(item % splits) * heads_per : r.Hq;
+  uint4 raw[kMostHeads];
+#pragma unroll
+  for (int i = 0; i < kMostHeads; ++i) {
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (i < heads_per && h0 + i < r.Hq)
+      raw[i] = *reinterpret_cast<const uint4*>(r.q + t * r.q_stride + (int64_t)(h0 + i) * D + ch);
+  }
+  if (turn && live) load_turn<INTER>(r, t, li, ch, cs, sn);
+  Row8 w;
+  if (NORM) w = widen(*reinterpret_cast<const uint4*>(r.qw + ch));
+#pragma unroll
+  for (int i = 0; i < kMostHeads; ++i) {
+    if (i >= heads_per) break;
+    const uint4 y = turn_row<D, INTER, NORM>(r, raw[i], w, li, ch, cs, sn);
+    if (h0 + i < r.Hq)
+      *reinterpret_cast<uint4*>(r.q_out + t * r.q_out_stride + (int64_t)(h0 + i) * D + ch) = y;
+  }
+}
+
+// ------------------------------------------------------------------- accepted rows
+
+// Slot of a request's cached token; -1 if the table or the cache has none.
+__device__ __forceinline__ int64_t slot_of(const AcceptArgs& p, const RowsArgs& a, int b,
+                                           int64_t tok) {
+  const int64_t page = tok >> a.page_shift;
+  if (tok < 0 || page >= p.table_width) return -1;
+  const int64_t slot = ((int64_t)p.table[(int64_t)b * p.table_width + page] << a.page_shift) +
+                       (tok & ((1 << a.page_shift) - 1));
+  return slot < a.n_slots ? slot : -1;
+}
+
+// A block per request and head, L = D / 8 lanes per accepted row, kThreads / L rows at a time: all are
+// read before any is written.  Entry i of an ascending path is i at least, so no row is written before
+// a later round reads it.  Bound by latency: lengths, path and table, rows, one after another.
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_accept_kernel(AcceptArgs p, RowsArgs a) {
+  using R = Record<D>;
+  constexpr int L = D / 8, NG = D / kGroup;
+  constexpr int kAtOnce = kThreads / L;
+  const int li = threadIdx.x % L, row = threadIdx.x / L;
+  const int b = blockIdx.x, h = blockIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  int len = p.path_lens[b];
+  const int ctx = p.ctx[b];
+  if (len < 0 || len > p.path_width || ctx < 0) {
+    if (threadIdx.x == 0) record_error(a.err, kDevErrState);
+    len = 0;
+  }
+  const int32_t* path = p.paths + (int64_t)b * p.path_width;
+  for (int i0 = 0; i0 < len; i0 += kAtOnce) {
+    const int i = i0 + row;
+    int64_t src = -1, dst = -1;
+    if (i < len) {
+      const int at = path[i], before = i ? path[i - 1] : -1;
+      if (at > before) {
+        src = slot_of(p, a, b, (int64_t)ctx + at);
+        dst = slot_of(p, a, b, (int64_t)ctx + i);
+      }
+      if ((src < 0 || dst < 0) && li == 0) record_error(a.err, kDevErrState);
+    }
+    const bool moves = src >= 0 && dst >= 0 && src != dst;
+    uint32_t kw, vw, kp, vp;
+    if (moves) {
+      const uint8_t* rec = a.cache + record_of(a, (int)src, h) * R::kBytes;
+      const int r = (int)src & 15, word = ((li & 7) ^ row_swz((int)src)) * NG + (li >> 3);
+      kw = reinterpret_cast<const uint32_t*>(rec + r * R::kRow)[word];
+      vw = reinterpret_cast<const uint32_t*>(rec + R::kV + r * R::kRow)[word];
+      kp = reinterpret_cast<const uint32_t*>(rec + R::kKp + r * R::kPar)[li >> 3];
+      vp = reinterpret_cast<const uint32_t*>(rec + R::kVp + r * R::kPar)[li >> 3];
+    }
+    __syncthreads();
+    if (moves) {
+      uint8_t* rec = a.cache + record_of(a, (int)dst, h) * R::kBytes;
+      const int r = (int)dst & 15, word = ((li & 7) ^ row_swz((int)dst)) * NG + (li >> 3);
+      reinterpret_cast<uint32_t*>(rec + r * R::kRow)[word] = kw;
+      reinterpret_cast<uint32_t*>(rec + R::kV + r * R::kRow)[word] = vw;
+      if ((li & 7) == 0) {
+        reinterpret_cast<uint32_t*>(rec + R::kKp + r * R::kPar)[li >> 3] = kp;
+        reinterpret_cast<uint32_t*>(rec + R::kVp + r * R::kPar)[li >> 3] = vp;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------- cached rows, read back
 
 __device__ __forceinline__ uint4 decode_word(uint32_t w, uint32_t params) {
   const float step = bf16_lo(params), lo = bf16_hi(params);
@@ -324,19 +543,37 @@ int row_grid(const RowsArgs& a, int D) {
   return (int)(((int64_t)a.T * a.Hkv + per_block - 1) / per_block);
 }
 
+// Items of neighbouring heads of a token: as few heads in each as still leave one item for every group of
+// lanes that fits the GPU, up to eight.
+int heads_per_item(int T, int heads, int D, int sms) {
+  const int64_t groups = (int64_t)sms * (2048 / kThreads) * (kThreads / (D / 8));
+  int64_t per = (T * (int64_t)heads + groups - 1) / groups;
+  if (per > kMostHeads) per = kMostHeads;
+  const int splits = (heads + (int)per - 1) / (int)per;
+  return (heads + splits - 1) / splits;  // evenly
+}
+
+template <int D, bool INTER>
+cudaError_t launch_rope_append(const RopeArgs& r, const RowsArgs& a, int sms, cudaStream_t s) {
+  const int per_block = kThreads / (D / 8);
+  const int heads_per = heads_per_item(r.T, r.Hq, D, sms);
+  const int splits = (r.Hq + heads_per - 1) / heads_per;
+  const int kv_blocks = row_grid(a, D);
+  const dim3 grid((unsigned)(kv_blocks + ((int64_t)r.T * splits + per_block - 1) / per_block));
+  return r.qw ? launch_pdl(attn_rope_append_kernel<D, INTER, true>, grid, dim3(kThreads), 0, s, r, a,
+                           heads_per, kv_blocks)
+              : launch_pdl(attn_rope_append_kernel<D, INTER, false>, grid, dim3(kThreads), 0, s, r, a,
+                           heads_per, kv_blocks);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_qk_norm_rope(const RopeArgs& a, int D, bool inter, int sms,
                                      cudaStream_t s) {
   const int per_block = kThreads / (D / 8);
   const int heads = a.Hq + a.Hkv;
-  // as few heads per group as still leave one item for every group that fits the GPU, up to eight
-  const int64_t groups = (int64_t)sms * (2048 / kThreads) * per_block;
-  int64_t heads_per64 = (a.T * (int64_t)heads + groups - 1) / groups;
-  if (heads_per64 > kMostHeads) heads_per64 = kMostHeads;
-  int splits = (heads + (int)heads_per64 - 1) / (int)heads_per64;
-  const int heads_per = (heads + splits - 1) / splits;  // evenly
-  splits = (heads + heads_per - 1) / heads_per;
+  const int heads_per = heads_per_item(a.T, heads, D, sms);
+  const int splits = (heads + heads_per - 1) / heads_per;
   const dim3 grid((unsigned)(((int64_t)a.T * splits + per_block - 1) / per_block)), block(kThreads);
   if (D == 64)
     return inter ? launch_pdl(attn_rope_kernel<64, true>, grid, block, 0, s, a, heads_per)
@@ -346,6 +583,25 @@ cudaError_t launch_attn_qk_norm_rope(const RopeArgs& a, int D, bool inter, int s
                  : launch_pdl(attn_rope_kernel<128, false>, grid, block, 0, s, a, heads_per);
   return inter ? launch_pdl(attn_rope_kernel<256, true>, grid, block, 0, s, a, heads_per)
                : launch_pdl(attn_rope_kernel<256, false>, grid, block, 0, s, a, heads_per);
+}
+
+cudaError_t launch_attn_rope_append(const RopeArgs& r, const RowsArgs& a, int D, bool inter, int sms,
+                                    cudaStream_t s) {
+  if (D == 64)
+    return inter ? launch_rope_append<64, true>(r, a, sms, s)
+                 : launch_rope_append<64, false>(r, a, sms, s);
+  if (D == 128)
+    return inter ? launch_rope_append<128, true>(r, a, sms, s)
+                 : launch_rope_append<128, false>(r, a, sms, s);
+  return inter ? launch_rope_append<256, true>(r, a, sms, s)
+               : launch_rope_append<256, false>(r, a, sms, s);
+}
+
+cudaError_t launch_attn_accept(const AcceptArgs& p, const RowsArgs& a, int D, cudaStream_t s) {
+  const dim3 grid(p.B, a.Hkv), block(kThreads);
+  if (D == 64) return launch_pdl(attn_accept_kernel<64>, grid, block, 0, s, p, a);
+  if (D == 128) return launch_pdl(attn_accept_kernel<128>, grid, block, 0, s, p, a);
+  return launch_pdl(attn_accept_kernel<256>, grid, block, 0, s, p, a);
 }
 
 cudaError_t launch_attn_append(const RowsArgs& a, int D, cudaStream_t s) {
