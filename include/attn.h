@@ -210,9 +210,9 @@ int attn_qk_norm_rope_append(attn_handle h, const void* q, int64_t q_stride, con
  *   masks       [T][mask_words] uint32, or NULL: causal.  Bit j of its row tells whether a query sees
  *               drafted token j of its request (bits from n_b on mean nothing); the cached tokens
  *               before the drafted ones it sees all, as far as a window lets it.  Its position is
- *               kv_b - n_b - 1 plus the number of drafted tokens that it sees.  max_q_len is at most
- *               256 and 32 mask_words, and at most W if there is a window (so a window never
- *               hides drafted tokens).
+ *               kv_b - n_b plus the number of drafted tokens that it sees besides one (itself).
+ *               max_q_len is at most 256 and 32 mask_words, and at most W if there is a window (so a
+ *               window never hides drafted tokens).
  * A query that sees no token gives 0.  Pages that hold no token which any query of the request sees are
  * not read: their entries of block_table may be anything, such as those of pages given back
  * behind a window. */

@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libmoe.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_debug.so")
 SOURCES = ["api.cu", "route.cu", "experts.cu", "decode.cu", "decode_q4.cu", "noalloc.cu", "probe.cu",
            "hostio.cu", "gdn.cu", "check.cu", "attn_api.cu", "attn_plan.cu", "attn_rows.cu",
-           "attn_decode.cu", "attn_prefill.cu", "attn_masked.cu"]
+           "attn_decode.cu", "attn_prefill.cu"]
 HEADERS = ["layer.cuh", "plan.cuh", "ptx.cuh", "select.cuh", "q4.cuh", "attn.cuh", "attn_join.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + CSRC,

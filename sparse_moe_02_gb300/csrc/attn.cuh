@@ -196,7 +196,4 @@ int attn_prep_steps(const AttnDims& d, int max_requests);  // of contexts held a
 size_t attn_prep_step_bytes(int D);                        // of one, without its exponents
 cudaError_t launch_attn_prefill(const FwdArgs& a, int sms, cudaStream_t s);
 
-// Attention with a window or masks: attn_masked.cu.
-cudaError_t launch_attn_masked(const FwdArgs& a, int max_kv, int sms, cudaStream_t s);
-
 }  // namespace moe

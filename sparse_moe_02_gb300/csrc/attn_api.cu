@@ -160,6 +160,13 @@ int forward_args(attn_handle h, const void* q, int64_t q_stride, const void* cac
   return MOE_OK;
 }
 
+int launch_forward(attn_handle h, const moe::FwdArgs& a, int max_kv_len, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return record_cuda_status(
+      a.max_q * h->d.G <= moe::kDecodeRows ? moe::launch_attn_decode(a, max_kv_len, h->sms, s)
+                                           : moe::launch_attn_prefill(a, h->sms, s));
+}
+
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -392,10 +399,7 @@ int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void*
   const int st = forward_args(h, q, q_stride, cache, block_table, table_width, q_offsets, kv_lens, B,
                               T, max_q_len, max_kv_len, out, out_stride, &a, &none);
   if (st || none) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return record_cuda_status(a.max_q * h->d.G <= moe::kDecodeRows
-                                ? moe::launch_attn_decode(a, max_kv_len, h->sms, s)
-                                : moe::launch_attn_prefill(a, h->sms, s));
+  return launch_forward(h, a, max_kv_len, stream);
 }
 
 int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, const void* cache,
@@ -419,8 +423,7 @@ int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, cons
   a.sinks = sinks;
   a.masks = masks;
   a.mask_words = mask_words;
-  return record_cuda_status(
-      moe::launch_attn_masked(a, max_kv_len, h->sms, static_cast<cudaStream_t>(stream)));
+  return launch_forward(h, a, max_kv_len, stream);
 }
 
 int attn_tree_plan(attn_handle h, const int32_t* parents, const int32_t* q_offsets,

@@ -167,7 +167,16 @@ __device__ __forceinline__ int row_tiles(const FwdArgs& a, int qn, int cols) {
   return (qn * a.d.G + cols - 1) / cols;
 }
 
-__device__ __forceinline__ int kv_tiles(int kv) { return max(1, (kv + kTile - 1) / kTile); }
+// Tiles left out of a request's context, and those that are gone over.
+template <bool MASK>
+__device__ __forceinline__ int skip_tiles(const FwdArgs& a, const Req& r) {
+  return MASK ? skipped<kTile>(a, first_start(a, r)) : 0;
+}
+
+template <bool MASK>
+__device__ __forceinline__ int kv_tiles(const FwdArgs& a, const Req& r) {
+  return max(1, (r.kv + kTile - 1) / kTile - skip_tiles<MASK>(a, r));
+}
 
 // Work of a context: its tiles, and kPartCost tiles' worth for what a part costs besides (queries,
 // page ids, first copies, joins), so that blocks of many short contexts get fewer tiles.  With 0, 20,
@@ -180,30 +189,57 @@ constexpr int kPartCost = 40;
 constexpr int kEachMore = 64;
 constexpr int kLeastWork = 12;  // of a block: a tile a warp (4096 tokens 10.5 us; with 32 12.5 us)
 
+// What a column sees.  Without masks: tokens below lim.  With: tokens below c, the cached ones before the
+// new ones, and those whose bit t - c is set (a request has at most kDecodeRows new tokens here); of all
+// these the first ones and those from lo on.
+template <bool MASK, int N, int M>
+struct Seen {
+  int lim[N][M];
+};
+template <int N, int M>
+struct Seen<true, N, M> {
+  uint32_t bits[N][M];
+  int lo[N][M];
+};
+static_assert(kDecodeRows <= 32, "a word of bits");
+
 // What a lane keeps of the query rows (columns) of one context; their MMA B fragments lie in
 // shared memory, [column tile][group][word][lane] registers of two MMAs, for all warps.
-template <int NT>
+template <int NT, bool MASK>
 struct Query {
   uint32_t sum[NT][2];  // of column lane / 4: its scaled sum over group lane % 4 as two tf32 parts
   float scale[NT][2];   // of columns 2c, 2c + 1: turns the MMA's units into log2 units
-  int lim[NT][2];       // tokens the column sees
-  int least;            // smallest lim of the columns in use
+  Seen<MASK, NT, 2> seen;
+  int least;  // tokens below it the columns in use see all (those of the window at least)
+  // with masks:
+  int c, first;  // cached tokens before the new ones; first tokens
+  int low;       // tokens from it on lie in every window
 };
 
 // The same for the block.
-template <int D, int NT>
+template <int D, int NT, bool MASK>
 struct QueryShared {
   uint4 frags[NT * (D / kGroup) * 2 * 32];
   float sum[8 * NT][D / kGroup];
   float scale[8 * NT];
-  int lim[8 * NT];
+  Seen<MASK, 8 * NT, 1> seen;
 };
 
-// Starts copying the part's query rows [column][D] into shared memory.
-template <int D, int NT>
+// Starts copying the part's query rows [column][D] into shared memory, each followed by its mask.
+template <int D, int NT, bool MASK>
 __device__ __forceinline__ void fetch_query(const FwdArgs& a, const Part& p, uint8_t* raw) {
   constexpr int kPieces = D / 8;
-  static_assert(8 * NT * kPieces <= kThreads, "one piece a thread");
+  static_assert(8 * NT * kPieces + 8 * NT <= kThreads, "one piece a thread");
+  if (MASK && a.masks) {
+    const int col = threadIdx.x - 8 * NT * kPieces, row = p.rt * 8 * NT + col;
+    if (col >= 0 && col < 8 * NT && row < p.r.qn * a.d.G) {
+      const uint32_t* src = a.masks + (int64_t)(p.r.q0 + row / a.d.G) * a.mask_words;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                       smem_u32(raw + col * Cfg<D, NT>::kQPitch + 2 * D)),
+                   "l"(src)
+                   : "memory");
+    }
+  }
   const int col = threadIdx.x / kPieces, piece = threadIdx.x % kPieces;
   if (col < 8 * NT) {
     const int row = p.rt * 8 * NT + col;
@@ -224,9 +260,9 @@ __device__ __forceinline__ void wait_copies() {
 }
 
 // One warp prepares group g of column tile nt.
-template <int D, int NT>
+template <int D, int NT, bool MASK>
 __device__ __forceinline__ void prepare_query(const FwdArgs& a, const Part& p, const uint8_t* raw,
-                                              int nt, int g, QueryShared<D, NT>& S) {
+                                              int nt, int g, QueryShared<D, NT, MASK>& S) {
   constexpr int NG = D / kGroup;
   const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
   const uint8_t* src = raw + (8 * nt + n) * Cfg<D, NT>::kQPitch + 16 * c;
@@ -275,17 +311,37 @@ __device__ __forceinline__ void prepare_query(const FwdArgs& a, const Part& p, c
       // (at most the largest fp32: 2^126 2^11 would be inf, and negative scores would read as masked)
       S.scale[col] = fminf(fmaxf(up * (16777216.f / 8192.f) * a.d.scale_log2, kLeastUnit), FLT_MAX);
       // columns beyond the rows see everything: nothing of them is written
-      const int seen = p.r.kv - p.r.qn + row / a.d.G + 1;
-      S.lim[col] = row < p.r.qn * a.d.G ? min(max(seen, 0), p.r.kv) : p.r.kv;
+      const int ctx = p.r.kv - p.r.qn, tok = row / a.d.G;
+      const bool on = row < p.r.qn * a.d.G;
+      if constexpr (MASK) {
+        uint32_t bits = 0xffffffffu >> (32 - p.r.qn);
+        int pos = ctx + tok;
+        if (on && a.masks) {
+          bits &= *reinterpret_cast<const uint32_t*>(raw + col * Cfg<D, NT>::kQPitch + 2 * D);
+          pos = ctx + max(__popc(bits) - 1, 0);
+        } else if (on) {
+          bits = 0xffffffffu >> (31 - tok);
+        }
+        S.seen.bits[col][0] = bits;
+        S.seen.lo[col][0] = on ? window_start(a, pos) : INT_MIN;
+      } else {
+        S.seen.lim[col][0] = on ? min(max(ctx + tok + 1, 0), p.r.kv) : p.r.kv;
+      }
     }
   }
 }
 
-template <int D, int NT>
-__device__ __forceinline__ void load_query(const QueryShared<D, NT>& S, Query<NT>& Q) {
+template <int D, int NT, bool MASK>
+__device__ __forceinline__ void load_query(const FwdArgs& a, const Part& p,
+                                           const QueryShared<D, NT, MASK>& S, Query<NT, MASK>& Q) {
   constexpr int NG = D / kGroup;
   const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
   Q.least = INT_MAX;
+  if constexpr (MASK) {
+    Q.c = Q.least = p.r.kv - p.r.qn;
+    Q.first = a.sinks;
+    Q.low = window_start(a, p.r.kv - 1);
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     // two tf32 parts of the sum: 22 bits of it
@@ -295,10 +351,17 @@ __device__ __forceinline__ void load_query(const QueryShared<D, NT>& S, Query<NT
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc) {
       Q.scale[nt][cc] = S.scale[8 * nt + 2 * c + cc];
-      Q.lim[nt][cc] = S.lim[8 * nt + 2 * c + cc];
+      if constexpr (MASK) {
+        Q.seen.bits[nt][cc] = S.seen.bits[8 * nt + 2 * c + cc][0];
+        Q.seen.lo[nt][cc] = S.seen.lo[8 * nt + 2 * c + cc][0];
+      } else {
+        Q.seen.lim[nt][cc] = S.seen.lim[8 * nt + 2 * c + cc][0];
+      }
     }
+    if constexpr (!MASK) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) Q.least = min(Q.least, S.lim[8 * nt + k]);
+      for (int k = 0; k < 8; ++k) Q.least = min(Q.least, S.seen.lim[8 * nt + k][0]);
+    }
   }
 }
 
@@ -329,9 +392,9 @@ __device__ __forceinline__ void clear(State<D, NT>& s) {
 }
 
 // One tile of 16 tokens at shared address `st`; tok0 is the first token's index in its context.
-template <int D, int NT>
+template <int D, int NT, bool MASK>
 __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0, int kv,
-                                          const Query<NT>& Q, State<D, NT>& s) {
+                                          const Query<NT, MASK>& Q, State<D, NT>& s) {
   using R = Record<D>;
   constexpr int NG = D / kGroup;
   const int lane = threadIdx.x & 31, j = lane >> 2, c = lane & 3;
@@ -380,15 +443,22 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
 #pragma unroll
   for (int r = 0; r < 2; ++r) vp[r] = lds_words<NG>(st + R::kVp + (8 * r + tr) * R::kPar);
   // what a row may not see, and what lies behind the context (never written: anything)
-  if (tok0 + kTile > Q.least) {
+  if (tok0 + kTile > Q.least || (MASK && tok0 < Q.low && tok0 + kTile > Q.first)) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int t = tok0 + 8 * r + tr;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc)
-          if (t >= Q.lim[nt][cc]) x[nt][2 * r + cc] = -INFINITY;
+        for (int cc = 0; cc < 2; ++cc) {
+          if constexpr (MASK) {
+            const int d = t - Q.c;  // a drafted token's index
+            const bool off = d >= 0 && !(d < 32 && (Q.seen.bits[nt][cc] >> (d & 31) & 1));
+            if (off || (t >= Q.first && t < Q.seen.lo[nt][cc])) x[nt][2 * r + cc] = -INFINITY;
+          } else {
+            if (t >= Q.seen.lim[nt][cc]) x[nt][2 * r + cc] = -INFINITY;
+          }
+        }
       if (t >= kv) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) vp[r].w[g] = 0;
@@ -490,6 +560,7 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
 }
 
 // The part that holds work w of the block's [w, w1).
+template <bool MASK>
 __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, int cols, int64_t w,
                                        int64_t w1) {
   Part p;
@@ -497,7 +568,8 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
   while (w < w1) {
     p.b = find_request(first, a.B, w);
     p.r = load_req(a, p.b);
-    p.tiles = kv_tiles(p.r.kv);
+    p.tiles = kv_tiles<MASK>(a, p.r);
+    if (MASK) p.skip = skip_tiles<MASK>(a, p.r);
     const int rts = row_tiles(a, p.r.qn, cols);
     const int k = (int)divide(w - first[p.b], p.tiles + kPartCost);
     p.h = k / rts;
@@ -516,13 +588,13 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
 
 // One block per SM.  While a part is worked on, the next part's queries and, as ring stages fall
 // free, its first tiles are copied, so the joins between parts leave no gap in the stream.
-template <int D, int NT, bool WHOLE>
+template <int D, int NT, bool WHOLE, bool MASK>
 __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   using C = Cfg<D, NT>;
   constexpr int NG = C::NG;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kWarps * C::kStages];
-  __shared__ QueryShared<D, NT> S;
+  __shared__ QueryShared<D, NT, MASK> S;
   __shared__ float2 join_ml[C::kCols][kWarps], join_sum[C::kCols];  // (m, l) of each warp, of all
   __shared__ float join_f[C::kCols][kWarps];                  // the warps' weights
   __shared__ float join_b[C::kCols][NG][kWarps], join_bias[C::kCols][NG];  // bias parts
@@ -551,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   if (!WHOLE) {
     const Cut cut = cut_work<kThreads>(a, first, sums, kLeastWork, [&](const Req& r) {
       if (r.qn == 0) return (int64_t)0;
-      const int unit = kv_tiles(r.kv) + kPartCost;
+      const int unit = kv_tiles<MASK>(a, r) + kPartCost;
       atomicMax(&longest, unit);
       return (int64_t)(a.d.Hkv * row_tiles(a, r.qn, C::kCols)) * unit;
     });
@@ -571,24 +643,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
       if (p.b < a.B) {
         p.r = load_req(a, p.b);
         p.t0 = 0;
-        p.t1 = p.tiles = kv_tiles(p.r.kv);
+        p.t1 = p.tiles = kv_tiles<MASK>(a, p.r);
+        if (MASK) p.skip = skip_tiles<MASK>(a, p.r);
         p.some = p.rt < row_tiles(a, p.r.qn, C::kCols);
       }
       if (WHOLE && k == 0 && req_out_of_range(a, p.b)) record_error(a.err, kDevErrState);
     } else if ((int)blockIdx.x < cut_s.blocks) {
-      p = locate(a, first, C::kCols, cut_s.bound(blockIdx.x), cut_s.bound(blockIdx.x + 1));
+      p = locate<MASK>(a, first, C::kCols, cut_s.bound(blockIdx.x), cut_s.bound(blockIdx.x + 1));
     }
     parts[0] = p;
   }
   __syncthreads();
   if (!WHOLE && tid == 0) a.desc[2 * blockIdx.x].x = 0;
   if (!parts[0].some) return;
-  fetch_query<D, NT>(a, parts[0], smem + C::kQuery);
+  fetch_query<D, NT, MASK>(a, parts[0], smem + C::kQuery);
 
   // the warp's tiles of a part: t0 + warp, + kWarps, ... below the end of the context
   auto lead_of = [&](const Part& p) { return p.t0 + warp; };
   auto tiles_of = [&](const Part& p) {
-    const int n = min(p.t1, (p.r.kv + kTile - 1) / kTile) - lead_of(p);
+    const int held = (p.r.kv + kTile - 1) / kTile - (MASK ? p.skip : 0);
+    const int n = min(p.t1, held) - lead_of(p);
     return n > 0 ? (n + kWarps - 1) / kWarps : 0;
   };
   int head = 0, used = 0;  // ring stages filled and emptied so far
@@ -602,10 +676,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
     ++head;
   };
 
+  // record of the warp's tile i of a part
+  auto record_of = [&](const Part& p, int i) {
+    return cache_record(a, p.b, p.h, tile_at<MASK, kTile>(a, lead_of(p) + i * kWarps, p.skip));
+  };
+
   int mine = tiles_of(parts[0]);
   uint32_t record = 0, record_more = 0;  // of 32 tiles ahead, one a lane
   if (lane < mine)
-    record = cache_record(a, parts[0].b, parts[0].h, lead_of(parts[0]) + lane * kWarps);
+    record = record_of(parts[0], lane);
   int issued = min(mine, C::kStages);  // tiles of the part
   for (int i = 0; i < issued; ++i) load(__shfl_sync(~0u, record, i));
 
@@ -616,35 +695,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
     wait_copies();
     __syncthreads();
     if (warp < NT * NG)
-      prepare_query<D, NT>(a, p, smem + C::kQuery + cur * C::kCols * C::kQPitch, warp / NG,
+      prepare_query<D, NT, MASK>(a, p, smem + C::kQuery + cur * C::kCols * C::kQPitch, warp / NG,
                            warp % NG, S);
     if (tid == kThreads - 1) {
       if (WHOLE || each) next.some = false;
-      else next = locate(a, first, C::kCols, p.next, cut_s.bound(blockIdx.x + 1));
+      else next = locate<MASK>(a, first, C::kCols, p.next, cut_s.bound(blockIdx.x + 1));
     }
     __syncthreads();
-    Query<NT> Q;
-    load_query<D, NT>(S, Q);
+    Query<NT, MASK> Q;
+    load_query<D, NT>(a, p, S, Q);
     int mine_next = 0, issued_next = 0;
     uint32_t record_next = 0;
     if (next.some) {
-      fetch_query<D, NT>(a, next, smem + C::kQuery + (cur ^ 1) * C::kCols * C::kQPitch);
+      fetch_query<D, NT, MASK>(a, next, smem + C::kQuery + (cur ^ 1) * C::kCols * C::kQPitch);
       mine_next = tiles_of(next);
       if (lane < mine_next)
-        record_next = cache_record(a, next.b, next.h, lead_of(next) + lane * kWarps);
+        record_next = record_of(next, lane);
     }
     State<D, NT> s;
     clear(s);
     const int kv = p.r.kv;
     int tok0 = lead_of(p) * kTile;
     for (int i = 0; i < mine; ++i, tok0 += kWarps * kTile) {
+      const int tok = MASK ? tile_at<MASK, kTile>(a, lead_of(p) + i * kWarps, p.skip) * kTile : tok0;
       const int stage = used % C::kStages;
       // after a wait that ran out nothing more is copied, but what is under way still lands
       if (used < head) ok = mbar_wait(full + stage, (used / C::kStages) & 1, a.err) && ok;
       ok = __all_sync(~0u, ok);
       if (!ok && used >= head) continue;
       if (ok)
-        tile_step<D, NT>(smem_u32(ring + stage * C::kStage), smem_u32(S.frags), tok0, kv, Q, s);
+        tile_step<D, NT>(smem_u32(ring + stage * C::kStage), smem_u32(S.frags), tok, kv, Q, s);
       ++used;
       __syncwarp();
       if (!ok) continue;
@@ -652,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
         if ((issued & 31) == 0) record = record_more;
         if ((issued & 31) == 16) {  // the following 32 tiles, half a batch ahead
           const int f = issued + 16 + lane;
-          if (f < mine) record_more = cache_record(a, p.b, p.h, lead_of(p) + f * kWarps);
+          if (f < mine) record_more = record_of(p, f);
         }
         load(__shfl_sync(~0u, record, issued & 31));
         ++issued;
@@ -809,33 +889,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(FwdArgs a) {
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool MASK>
 cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>,
+  cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true, MASK>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>,
+  return cudaFuncSetAttribute(attn_decode_kernel<D, NT, false, MASK>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Cfg<D, NT>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
 }
 
-template <int D, int NT>
-cudaError_t launch(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
+template <bool MASK>
+cudaError_t prepare_all() {
+  cudaError_t e;
+  if ((e = prepare<64, 2, MASK>()) != cudaSuccess) return e;
+  if ((e = prepare<64, 1, MASK>()) != cudaSuccess) return e;
+  if ((e = prepare<128, 2, MASK>()) != cudaSuccess) return e;
+  if ((e = prepare<128, 1, MASK>()) != cudaSuccess) return e;
+  return prepare<256, 1, MASK>();
+}
+
+template <int D, int NT, bool MASK>
+cudaError_t launch(const FwdArgs& a, int64_t max_kv, int sms, cudaStream_t s) {
   using C = Cfg<D, NT>;
   const int rts = (a.max_q * a.d.G + C::kCols - 1) / C::kCols;
   const int64_t grid = (int64_t)a.B * a.d.Hkv * rts;
+  if (MASK && a.window) {  // what is gone over, at most
+    const int64_t view = (int64_t)a.window + a.max_q + a.sinks + 2 * kTile;
+    max_kv = max_kv < view ? max_kv : view;
+  }
   if (max_kv <= kWholeKv || (max_kv <= kWholeMost && max_kv <= kWholeKv + kWholeMore * grid)) {
     if (grid <= 0x7fffffff)
-      return launch_pdl(attn_decode_kernel<D, NT, true>, dim3((unsigned)grid), dim3(kThreads),
+      return launch_pdl(attn_decode_kernel<D, NT, true, MASK>, dim3((unsigned)grid), dim3(kThreads),
                         C::kSmem, s, a);
   }
   const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
   const cudaError_t e =
-      launch_pdl(attn_decode_kernel<D, NT, false>, dim3(blocks), dim3(kThreads),
+      launch_pdl(attn_decode_kernel<D, NT, false, MASK>, dim3(blocks), dim3(kThreads),
                  C::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_join_kernel<D, C::kCols>, dim3(2 * sms), dim3(kJoinThreads), 0, s, a, blocks);
+}
+
+template <bool MASK>
+cudaError_t launch_any(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
+  // two column tiles per block where a context has more than 8 rows and the registers hold them
+  // (D = 256 would need 128 accumulators a lane: its second 8 rows take a block of their own)
+  const bool two = a.max_q * a.d.G > 8;
+  if (a.d.D == 256) return launch<256, 1, MASK>(a, max_kv, sms, s);
+  if (a.d.D == 128)
+    return two ? launch<128, 2, MASK>(a, max_kv, sms, s) : launch<128, 1, MASK>(a, max_kv, sms, s);
+  return two ? launch<64, 2, MASK>(a, max_kv, sms, s) : launch<64, 1, MASK>(a, max_kv, sms, s);
 }
 
 }  // namespace
@@ -844,22 +949,13 @@ cudaError_t launch(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
 int attn_part_slots(int sms) { return 2 * sms; }
 
 cudaError_t prepare_attn_decode_kernels() {
-  cudaError_t e;
-  if ((e = prepare<64, 2>()) != cudaSuccess) return e;
-  if ((e = prepare<64, 1>()) != cudaSuccess) return e;
-  if ((e = prepare<128, 2>()) != cudaSuccess) return e;
-  if ((e = prepare<128, 1>()) != cudaSuccess) return e;
-  return prepare<256, 1>();
+  const cudaError_t e = prepare_all<false>();
+  return e != cudaSuccess ? e : prepare_all<true>();
 }
 
 cudaError_t launch_attn_decode(const FwdArgs& a, int max_kv, int sms, cudaStream_t s) {
-  // two column tiles per block where a context has more than 8 rows and the registers hold them
-  // (D = 256 would need 128 accumulators a lane: its second 8 rows take a block of their own)
-  const bool two = a.max_q * a.d.G > 8;
-  if (a.d.D == 256) return launch<256, 1>(a, max_kv, sms, s);
-  if (a.d.D == 128)
-    return two ? launch<128, 2>(a, max_kv, sms, s) : launch<128, 1>(a, max_kv, sms, s);
-  return two ? launch<64, 2>(a, max_kv, sms, s) : launch<64, 1>(a, max_kv, sms, s);
+  return a.window || a.masks ? launch_any<true>(a, max_kv, sms, s)
+                             : launch_any<false>(a, max_kv, sms, s);
 }
 
 }  // namespace moe

@@ -2,6 +2,8 @@
 // results of contexts that several blocks share, and the launch that joins them.
 #pragma once
 
+#include <climits>
+
 #include "attn.cuh"
 
 namespace moe {
@@ -103,9 +105,41 @@ struct Part {
   Req r;
   int64_t start;  // work before the context's first tile
   int unit;       // work of a tile
+  int skip;       // tiles left out between the first tokens and the window
   int64_t next;   // the block's work after this part
   bool some;
 };
+
+// Narrower views (attn_kv4_forward_masked).  A kernel goes over the tiles (of kTile tokens) that hold the
+// first tokens and those from the first token of a window on: tile i of them is tile i of the context,
+// or, behind the first tokens, i + skip.
+
+// First token of the window of a query at position pos.
+__device__ __forceinline__ int window_start(const FwdArgs& a, int pos) {
+  return a.window ? pos - a.window + 1 : INT_MIN;
+}
+
+// The least window start of the request's queries: where its first one is.
+__device__ __forceinline__ int first_start(const FwdArgs& a, const Req& r) {
+  return window_start(a, r.kv - r.qn);
+}
+
+template <int kTile>
+__device__ __forceinline__ int first_tiles(const FwdArgs& a) {
+  return (a.sinks + kTile - 1) / kTile;
+}
+
+// Tiles between the first tokens and token lo.
+template <int kTile>
+__device__ __forceinline__ int skipped(const FwdArgs& a, int lo) {
+  return max(max(lo, 0) / kTile - first_tiles<kTile>(a), 0);
+}
+
+template <bool MASK, int kTile>
+__device__ __forceinline__ int tile_at(const FwdArgs& a, int i, int skip) {
+  if constexpr (!MASK) return i;
+  return i < first_tiles<kTile>(a) ? i : i + skip;
+}
 
 // Record of `tile` of request b's context, head h; a page id out of range reads page 0 and is
 // recorded.  (32 bits: 2^32 records are more than 5 TB.)

@@ -211,14 +211,35 @@ constexpr int kLeastSteps = 4;   // of a block
 struct Cost {
   int64_t fixed, base;  // per row tile, in units
   int grow;             // 64: the work of half a row tile more for each
+  // with masks: the row tiles from `bend` on cost `flat` each
+  int64_t flat;
+  int bend;
+  template <bool MASK>
   __device__ __forceinline__ int64_t before(int64_t rt) const {
+    if (MASK && rt > bend) return before<false>(bend) + (rt - bend) * flat;
     return rt * (fixed + base) + grow * rt * (rt + 1);
   }
 };
 
+template <bool MASK>
 __device__ __forceinline__ Cost cost_of(const FwdArgs& a, const Req& r, int part_cost) {
-  if (r.kv == 0) return Cost{(int64_t)kZeroCost * a.d.G, 0, 0};
-  return Cost{(int64_t)part_cost * a.d.G, (int64_t)max(r.kv - r.qn, 0) * a.d.G, 64};
+  if (r.kv == 0) return Cost{(int64_t)kZeroCost * a.d.G, 0, 0, 0, INT_MAX};
+  Cost c{(int64_t)part_cost * a.d.G, (int64_t)max(r.kv - r.qn, 0) * a.d.G, 64, 0, INT_MAX};
+  if constexpr (MASK) {
+    // A row tile goes over the context at most (a tree's does), and over the first tokens and a window
+    // of each of its tokens: the steps that these can touch.
+    int64_t most = a.masks ? r.kv : INT64_MAX;
+    if (a.window) {
+      const int64_t span = (int64_t)a.window + (a.masks ? r.qn : (kRows - 1) / a.d.G + 1);
+      most = min(most, kStep * ((span + kStep - 1) / kStep + 1 + first_tiles<kStep>(a)));
+    }
+    c.bend = 0;
+    if (!a.masks)
+      c.bend = (int)min(max(divide(max(most * a.d.G - c.base, (int64_t)0), kRows), (int64_t)0),
+                        (int64_t)INT_MAX);
+    c.flat = c.fixed + most * a.d.G;
+  }
+  return c;
 }
 
 __device__ __forceinline__ int row_tiles(const FwdArgs& a, const Req& r) {
@@ -230,7 +251,13 @@ __device__ __forceinline__ int seen_by(const Req& r, int tok) {
   return min(max(r.kv - r.qn + tok + 1, 0), r.kv);
 }
 
+// A bound of the window starts of a row tile whose first token is `tok`.
+__device__ __forceinline__ int tile_start(const FwdArgs& a, const Req& r, int tok) {
+  return a.masks ? first_start(a, r) : window_start(a, r.kv - r.qn + tok);
+}
+
 // The part that holds work w of the block's [w, w1).
+template <bool MASK>
 __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, int part_cost,
                                        int64_t w, int64_t w1) {
   Part p;
@@ -238,28 +265,35 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
   while (w < w1) {
     p.b = find_request(first, a.B, w);
     p.r = load_req(a, p.b);
-    const Cost c = cost_of(a, p.r, part_cost);
+    const Cost c = cost_of<MASK>(a, p.r, part_cost);
     const int rts = row_tiles(a, p.r);
-    const int64_t head = c.before(rts);
+    const int64_t head = c.template before<MASK>(rts);
     p.h = (int)divide(w - first[p.b], head);
     const int64_t at = first[p.b] + p.h * head;
     int rt;
-    if (c.grow) {
+    if (MASK && c.bend < rts && w - at >= c.template before<false>(c.bend)) {
+      rt = c.bend + (int)divide(w - at - c.template before<false>(c.bend), c.flat);
+    } else if (c.grow) {
       // 64 rt^2 + (fixed + base + 64) rt = w - at, then the exact tile beside the rounded root
       const float q = (float)(c.fixed + c.base + 64), x = (float)(w - at);
       rt = (int)(2.f * x / (q + sqrtf(fmaf(q, q, 256.f * x))));
       rt = min(max(rt, 0), rts - 1);
-      while (rt > 0 && c.before(rt) > w - at) --rt;
-      while (rt + 1 < rts && c.before(rt + 1) <= w - at) ++rt;
+      while (rt > 0 && c.template before<MASK>(rt) > w - at) --rt;
+      while (rt + 1 < rts && c.template before<MASK>(rt + 1) <= w - at) ++rt;
     } else {
       rt = (int)divide(w - at, c.fixed);
     }
     p.rt = rt;
     const int last = min((rt + 1) * kRows, p.r.qn * a.d.G) - 1;
-    p.tiles = (seen_by(p.r, last / a.d.G) + kStep - 1) / kStep;
-    const int64_t end = at + c.before(rt + 1);
+    const int seen = MASK && a.masks ? p.r.kv : seen_by(p.r, last / a.d.G);
+    p.tiles = (seen + kStep - 1) / kStep;
+    if (MASK) {
+      p.skip = skipped<kStep>(a, tile_start(a, p.r, rt * kRows / a.d.G));
+      p.tiles -= p.skip;
+    }
+    const int64_t end = at + c.template before<MASK>(rt + 1);
     p.unit = kStep * a.d.G;
-    p.start = at + c.before(rt) + c.fixed;
+    p.start = at + c.template before<MASK>(rt) + c.fixed;
     const int64_t stop = min(end, w1);
     // the steps that start in [w, stop)
     p.t0 = w <= p.start ? 0 : (int)min((int64_t)p.tiles, divide(w - p.start + p.unit - 1, p.unit));
@@ -267,7 +301,7 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
                ? 0
                : (int)min((int64_t)p.tiles, divide(stop - p.start + p.unit - 1, p.unit));
     // a row tile that sees nothing is one part without steps, where its work begins
-    p.some = p.t1 > p.t0 || (p.tiles == 0 && w <= at + c.before(rt));
+    p.some = p.t1 > p.t0 || (p.tiles == 0 && w <= at + c.template before<MASK>(rt));
     w = p.next = stop;
     if (p.some) break;
   }
@@ -309,6 +343,25 @@ __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Tokens of a context that its queries do not read: those behind it, and, with masks, those between the
+// first tokens and every window, whose pages may have been given back.
+template <bool MASK>
+struct Unread {
+  int kv;
+  int first, start;
+  __device__ __forceinline__ Unread(const FwdArgs& a, const Req& r) : kv(r.kv) {
+    if constexpr (MASK) first = a.sinks, start = first_start(a, r);
+  }
+  __device__ __forceinline__ bool token(int t) const {
+    return t >= kv || (MASK && t >= first && t < start);
+  }
+  // whether no token of a record is read
+  __device__ __forceinline__ bool record(int rec) const {
+    const int64_t t = 16 * (int64_t)rec;
+    return t >= kv || (MASK && t >= first && t + 16 <= start);
+  }
+};
+
 // Exponents of a record: keys were divided by 2^(ek + 6), values by 2^(ev + 6).
 struct __align__(16) Exps {
   float up_k;    // 2^ek
@@ -348,28 +401,31 @@ struct Dequant {
 
   // Parameters of token lane & 7, group (lane >> 3) % NG at offset `off` of the record (0 behind the
   // context), and the exponent of the record's 16 tokens.
-  static __device__ __forceinline__ uint32_t params(uint32_t rec, int off, int oct, int tok, int kv,
-                                                    int* e) {
+  template <bool MASK>
+  static __device__ __forceinline__ uint32_t params(uint32_t rec, int off, int oct, int tok,
+                                                    const Unread<MASK>& un, int* e) {
     const int lane = threadIdx.x & 31, t = lane & 7, g = (lane >> 3) % NG;
     const uint32_t par = rec + off + (8 * (oct & 1) + t) * R::kPar + 4 * g;
     const int other = (oct & 1) ? -8 : 8;  // the record's other half
     uint32_t w = lds32(par), w2 = lds32(par + other * R::kPar);
-    if (tok + t >= kv) w = 0;
-    if (tok + t + other >= kv) w2 = 0;
+    if (un.token(tok + t)) w = 0;
+    if (un.token(tok + t + other)) w2 = 0;
     *e = exponent_of(max_u16x2(magnitudes(w), magnitudes(w2)));
     return w;
   }
 
   // tok: the first token's index in the context.  Also leaves the record's exponents in *ex (those
   // of the values too: the softmax needs them with the scores).
-  __device__ __forceinline__ void keys(uint32_t raw, int oct, int tok, int kv, Exps* ex) {
+  template <bool MASK>
+  __device__ __forceinline__ void keys(uint32_t raw, int oct, int tok, const Unread<MASK>& un,
+                                       Exps* ex) {
     const int lane = threadIdx.x & 31;
     const int t = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
     const uint32_t rec = raw + (oct >> 1) * C::kSideK;
     const int row = 8 * (oct & 1) + t;
     int e, ev;
-    const uint32_t w = params(rec, R::kKp, oct, tok, kv, &e);
-    params(rec, R::kVp, oct, tok, kv, &ev);
+    const uint32_t w = params(rec, R::kKp, oct, tok, un, &e);
+    params(rec, R::kVp, oct, tok, un, &ev);
     if (lane == 0 && (oct & 1) == 0) *ex = Exps{pow2(e), (float)ev, pow2(-ev), 0.f};
     const float down = pow2(-(e + 6));
     const float s = bf16_lo(w) * down, b = bf16_hi(w) * down;
@@ -402,12 +458,14 @@ struct Dequant {
   // Row i * 32 + lane of the value operand is channel 64 g + 8 j + kWords sub + i (lane = (sub, g, j)),
   // so that the rows of a store differ in their last three bits, which the swizzle spreads over
   // the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.
-  __device__ __forceinline__ void values(uint32_t raw, uint4* table, int oct, int tok, int kv) {
+  template <bool MASK>
+  __device__ __forceinline__ void values(uint32_t raw, uint4* table, int oct, int tok,
+                                         const Unread<MASK>& un) {
     const int lane = threadIdx.x & 31;
     const uint32_t rec = raw + (oct >> 1) * C::kSideV;
     {
       int e;
-      const uint32_t w = params(rec, R::kVp, oct, tok, kv, &e);
+      const uint32_t w = params(rec, R::kVp, oct, tok, un, &e);
       const int t = lane & 7, g = (lane >> 3) % NG;
       const float down = pow2(-(e + 6));
       const uint32_t mate = __shfl_down_sync(~0u, w, 1);
@@ -542,7 +600,52 @@ __device__ __forceinline__ void copy_queries(uint32_t src, uint32_t tmem, int g0
   tc_fence_before();
 }
 
-template <int D>
+// Tokens t0 .. t0 + 63 of its context that a row sees, a bit each.
+struct RowView {
+  int lim;               // tokens below it: seen ones (causal), or cached before the new ones (a tree)
+  int start;             // first token of its window
+  const uint32_t* mask;  // of its drafted tokens, n of them; or none
+  int n;
+
+  static __device__ __forceinline__ uint64_t below(int k) {
+    return k <= 0 ? 0 : k >= 64 ? ~0ull : (1ull << k) - 1;
+  }
+
+  __device__ __forceinline__ RowView(const FwdArgs& a, const Part& p, int tok, bool on)
+      : lim(p.r.kv), start(INT_MIN), mask(nullptr), n(0) {
+    if (!on) return;  // sees everything: nothing of it is written
+    const int c = p.r.kv - p.r.qn;
+    if (a.masks) {
+      lim = c;
+      n = p.r.qn;
+      mask = a.masks + (int64_t)(p.r.q0 + tok) * a.mask_words;
+      int seen = 0;
+      if (a.window)
+        for (int k = 0; 32 * k < n; ++k) seen += __popc(mask[k] & (uint32_t)below(n - 32 * k));
+      start = window_start(a, c + max(seen - 1, 0));
+    } else {
+      lim = seen_by(p.r, tok);
+      start = window_start(a, c + tok);
+    }
+  }
+
+  __device__ __forceinline__ uint64_t seen(const FwdArgs& a, int t0) const {
+    uint64_t v = below(lim - t0);
+    if (mask) {
+      const int k = t0 - lim, w0 = k >> 5;  // first drafted token of the step, its word
+      uint32_t w[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        w[i] = w0 + i >= 0 && 32 * (w0 + i) < n ? mask[w0 + i] : 0;
+      const uint64_t bits = (uint64_t)__funnelshift_r(w[1], w[2], k & 31) << 32 |
+                            __funnelshift_r(w[0], w[1], k & 31);
+      v |= bits & below(n - k);
+    }
+    return start > t0 ? v & (below(a.sinks - t0) | ~below(start - t0)) : v;
+  }
+};
+
+template <int D, bool MASK>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   using C = Cfg<D>;
   constexpr int NG = C::NG;
@@ -602,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   {
     const Cut cut =
         cut_work<kThreads>(a, first, sums, (int64_t)kLeastSteps * kStep * a.d.G, [&](const Req& r) {
-          return a.d.Hkv * cost_of(a, r, part_cost).before(row_tiles(a, r));
+          return a.d.Hkv * cost_of<MASK>(a, r, part_cost).template before<MASK>(row_tiles(a, r));
         });
     if (tid == 0) {
       cut_s = cut;
@@ -626,36 +729,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   if (warp >= kMmaWarp) {
     registers_down<kRegsRest>();
     // copies the key (0) or value (1) sides of a part's records, a warp each
-    auto copy_sides = [&](int which, int b, int h, int kv, int t0, int t1) {
-      const int recs = (kv + 15) / 16, ring = which ? C::kRawV : C::kRawK;
-      uint32_t record = 0;
-      for (int t = t0; t < t1; ++t, ++n) {
-        const int slot = (t - t0) & 7;
+    auto copy_sides = [&](int which, const Part& p) {
+      const Unread<MASK> un(a, p.r);
+      const int ring = which ? C::kRawV : C::kRawK;
+      uint32_t record = 0, have = 0;
+      for (int t = p.t0; t < p.t1; ++t, ++n) {
+        const int slot = (t - p.t0) & 7;
         if (slot == 0) {  // the records of eight steps, one a lane
-          const int rec = t * kRecs + lane;
-          if (rec < recs) record = cache_record(a, b, h, rec);
+          const int rec = tile_at<MASK, kStep>(a, t + lane / kRecs, p.skip) * kRecs + lane % kRecs;
+          const bool some = !un.record(rec);
+          if (some) record = cache_record(a, p.b, p.h, rec);
+          have = __ballot_sync(~0u, some);
         }
         const int st = n % ring;
         uint64_t* full = &bars.raw_full[which][st];
         ok = mbar_wait(&bars.raw_empty[which][st], ((n / ring) & 1) ^ 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) return;
-        const int have = min(max(recs - t * kRecs, 0), kRecs);
+        const uint32_t mine = have >> (slot * kRecs) & ((1u << kRecs) - 1);
         const uint32_t rec = __shfl_sync(~0u, record, slot * kRecs + (lane & 3));
         const int side = which ? C::kSideV : C::kSideK;
-        if (lane == 0) mbar_arrive_expect_tx(full, have * side);
+        if (lane == 0) mbar_arrive_expect_tx(full, __popc(mine) * side);
         __syncwarp();
-        if (lane < have)
+        if (lane < kRecs && (mine >> lane & 1))
           copy_record(smem + (which ? C::kOffRawV : C::kOffRaw) + (st * kRecs + lane) * side,
                       a.cache + (uint64_t)rec * C::R::kBytes + (which ? C::R::kVp : 0), side, full);
       }
     };
-    // copies the prepared key (0) or value (1) operands of steps t0 .. t1 - 1 of a context whose
-    // first is `at`, a warp each: eight arrivals a step, as from the dequantising warps
-    auto copy_prepared = [&](int which, int at, int t0, int t1) {
+    // copies the prepared key (0) or value (1) operands of a part's steps, a warp each: eight arrivals
+    // a step, as from the dequantising warps
+    auto copy_prepared = [&](int which, const Part& p) {
+      // first prepared step of the context; of the steps behind the first tokens
+      const int left_out = MASK ? skipped<kStep>(a, first_start(a, p.r)) : 0;
+      const int at = a.prep_at[1 + p.b] + p.h * ((p.r.kv + kStep - 1) / kStep - left_out);
       constexpr int kRing = C::kOpsK;
       static_assert(C::kOpsK == C::kOpsV && kDeqWarps == 8, "one rule for both");
-      for (int t = t0; t < t1; ++t, ++n) {
+      for (int t = p.t0; t < p.t1; ++t, ++n) {
+        // (where a row tile leaves steps out, its context does as many or fewer)
+        int step = at + t;
+        if (MASK && t >= first_tiles<kStep>(a)) step += p.skip - left_out;
         const int op = n % kRing;
         uint64_t* full = which ? &bars.v_full[op] : &bars.k_full[op];
         ok = mbar_wait(which ? &bars.v_empty[op] : &bars.k_empty[op], ((n / kRing) & 1) ^ 1, a.err);
@@ -664,20 +776,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         if (lane == 0) {
           mbar_arrive_expect_tx(full, C::kK);
           copy_record(smem + (which ? C::kOffV : C::kOffK) + op * C::kK,
-                      a.prep + ((int64_t)(at + t) * 2 + which) * C::kK, C::kK, full);
+                      a.prep + ((int64_t)step * 2 + which) * C::kK, C::kK, full);
         } else if (lane < kDeqWarps) {
           mbar_arrive(full);
         } else if (lane == kDeqWarps && which == 0) {
           mbar_arrive_expect_tx(&bars.x_full[n % kExps], sizeof(exps[0]));
-          copy_record(exps[n % kExps], a.prep_exps + (int64_t)(at + t) * kRecs, sizeof(exps[0]),
+          copy_record(exps[n % kExps], a.prep_exps + (int64_t)step * kRecs, sizeof(exps[0]),
                       &bars.x_full[n % kExps]);
         }
         __syncwarp();
       }
-    };
-    // first prepared step of a part's context
-    auto prepared_at = [&](const Part& p) {
-      return a.prep_at[1 + p.b] + p.h * ((p.r.kv + kStep - 1) / kStep);
     };
     // nothing may be in flight when the block ends
     auto drain = [&](int which) {
@@ -698,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if ((int)blockIdx.x < cut_s.blocks)
         w = cut_s.bound(blockIdx.x), w1 = cut_s.bound(blockIdx.x + 1);
       for (int k = 0; ok; ++k) {
-        const Part p = locate(a, first, part_cost, w, w1);
+        const Part p = locate<MASK>(a, first, part_cost, w, w1);
         ok = mbar_wait(&bars.part_empty[k % kParts], ((k / kParts) & 1) ^ 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
@@ -718,8 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         __syncwarp();
         if (lane == 0) part_read(k);
         if (!p.some) break;
-        if (prepared) copy_prepared(which, prepared_at(p), p.t0, p.t1);
-        else copy_sides(which, p.b, p.h, p.r.kv, p.t0, p.t1);
+        if (prepared) copy_prepared(which, p);
+        else copy_sides(which, p);
       }
       drain(which);
     } else if (warp == kMmaWarp) {
@@ -908,20 +1016,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       ++kq;
       due = k;
       if (prepared) continue;  // (steps are counted by those who use them)
-      const int t0 = p.t0, t1 = p.t1, kv = p.r.kv;
+      const int t0 = p.t0, t1 = p.t1;
+      const Unread<MASK> un(a, p.r);
       for (int t = t0; t < t1; ++t, ++n) {
         const int which = is_key ? 0 : 1, ring = is_key ? C::kRawK : C::kRawV;
         const int st = n % ring;
-        const int tok = t * kStep + 8 * oct;
+        const int tok = tile_at<MASK, kStep>(a, t, p.skip) * kStep + 8 * oct;
         ok = mbar_wait(&bars.raw_full[which][st], (n / ring) & 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         if (is_key)
-          d.keys(ops + C::kOffRaw + st * kRecs * C::kSideK, oct, tok, kv,
+          d.keys(ops + C::kOffRaw + st * kRecs * C::kSideK, oct, tok, un,
                  &exps[n % kExps][oct >> 1]);
         else  // (a value side begins with its parameters: R::kVp from where the record would)
           d.values(ops + C::kOffRawV + st * kRecs * C::kSideV - C::R::kVp, tables[oct], oct, tok,
-                   kv);
+                   un);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.raw_empty[which][st]);
         const int op = is_key ? n % C::kOpsK : n % C::kOpsV;
@@ -952,8 +1061,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const int rows_left = p.r.qn * a.d.G;
       const int row = row0 + lane, tok = row / a.d.G;
       const bool on = row < rows_left;
-      const int lim = on ? seen_by(p.r, tok) : p.r.kv;
-      const int least = seen_by(p.r, p.rt * kRows / a.d.G);
+      int lim = on ? seen_by(p.r, tok) : p.r.kv;
+      int least = seen_by(p.r, p.rt * kRows / a.d.G);
+      // with masks: tokens from `low` on lie in every window of the row tile
+      int low = INT_MIN;
+      RowView view(a, p, tok, MASK && on);
+      if constexpr (MASK) {
+        lim = 0;  // (tokens seen so far, of this part: whether there are any)
+        if (a.masks) least = p.r.kv - p.r.qn;
+        const int last = p.r.kv - p.r.qn + (p.rt + 1) * kRows / a.d.G;  // or behind the row tile's
+        low = window_start(a, a.masks ? p.r.kv - 1 : min(p.r.kv - 1, last));
+      }
       float m = -INFINITY, l = 0.f, unit = 0.f, most_ev = -INFINITY;
       for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
         ok = mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err) &&
@@ -981,7 +1099,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         const bool spread = least_ev < most_ev - kSpread;
         wait_ld32(s);
         wait_ld32(s + 32);
-        if ((t + 1) * kStep > least) {
+        if constexpr (MASK) {
+          const int t0 = tile_at<MASK, kStep>(a, t, p.skip) * kStep;
+          if (t0 + kStep > least || (t0 < low && t0 + kStep > a.sinks)) {
+            const uint64_t seen = view.seen(a, t0);
+            const uint32_t half[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+#pragma unroll
+            for (int i = 0; i < kStep; ++i)
+              if (!(half[i / 32] >> (i % 32) & 1)) s[i] = 0xff800000u;  // -inf
+            lim |= seen != 0;
+          } else {
+            lim = 1;
+          }
+        } else if ((t + 1) * kStep > least) {
 #pragma unroll
           for (int i = 0; i < kStep; ++i)
             if (t * kStep + i >= lim) s[i] = 0xff800000u;  // -inf
@@ -1119,7 +1249,7 @@ __device__ __forceinline__ void store_operands(void* dst, uint32_t src, uint32_t
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-template <int D>
+template <int D, bool MASK>
 __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a) {
   using C = Cfg<D>;
   using P = PrepCfg<D>;
@@ -1132,14 +1262,23 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
   int64_t* first = reinterpret_cast<int64_t*>(smem + P::kFirst);
   pdl_wait();
   pdl_trigger();
+  // (those that are gone over)
+  auto steps_of = [&](const Req& r) {
+    return (r.kv + kStep - 1) / kStep - (MASK ? skipped<kStep>(a, first_start(a, r)) : 0);
+  };
   // Steps of each context in the lower half, steps of its row tiles (a causal prompt's on average)
   // in the upper one; both capped far above what is ever taken.
   constexpr int64_t kCap = 1 << 20;
   cut_work<kPrepThreads>(a, first, sums, 1, [&](const Req& r) {
     if (r.qn == 0) return (int64_t)0;
-    const int64_t steps = a.d.Hkv * (int64_t)((r.kv + kStep - 1) / kStep);
-    const int64_t mean = a.d.Hkv * (int64_t)((max(r.kv - r.qn / 2, 0) + kStep - 1) / kStep);
-    return min(steps, kCap) | min(mean * row_tiles(a, r), kCap) << 32;
+    const int64_t steps = a.d.Hkv * (int64_t)steps_of(r);
+    int64_t all;
+    if constexpr (MASK) {
+      all = cost_of<MASK>(a, r, 0).template before<MASK>(row_tiles(a, r)) * a.d.Hkv / (kStep * a.d.G);
+    } else {
+      all = a.d.Hkv * (int64_t)((max(r.kv - r.qn / 2, 0) + kStep - 1) / kStep) * row_tiles(a, r);
+    }
+    return min(steps, kCap) | min(all, kCap) << 32;
   });
   const int64_t both = first[a.B];
   __syncthreads();  // every thread has it, and decides alike, before the sums lose their upper halves
@@ -1156,12 +1295,15 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
   const uint32_t ops = smem_u32(smem);
   for (int u = blockIdx.x; u < (int)steps; u += gridDim.x) {
     const int b = find_request(first, a.B, u);
-    const int kv = load_req(a, b).kv, of = (kv + kStep - 1) / kStep;
-    const int h = (u - (int)first[b]) / of, t = (u - (int)first[b]) % of;
-    const int have = min((kv + 15) / 16 - t * kRecs, kRecs);
+    const Req r = load_req(a, b);
+    const Unread<MASK> un(a, r);
+    const int of = steps_of(r), h = (u - (int)first[b]) / of;
+    const int t = tile_at<MASK, kStep>(a, (u - (int)first[b]) % of,
+                                       MASK ? skipped<kStep>(a, first_start(a, r)) : 0);
     constexpr int kPieces = R::kBytes / 16;
-    for (int i = tid; i < have * kPieces; i += kPrepThreads) {
+    for (int i = tid; i < kRecs * kPieces; i += kPrepThreads) {
       const int rec = i / kPieces, at = i % kPieces * 16;
+      if (un.record(t * kRecs + rec)) continue;
       const uint4 w = *reinterpret_cast<const uint4*>(
           a.cache + (uint64_t)cache_record(a, b, h, t * kRecs + rec) * R::kBytes + at);
       if (at < R::kV) *reinterpret_cast<uint4*>(smem + P::kRaw + rec * C::kSideK + at) = w;
@@ -1172,10 +1314,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
     Dequant<D> d;
     const int oct = warp & 7, tok = t * kStep + 8 * oct;
     if (warp < kDeqWarps) {
-      d.keys(ops + P::kRaw, oct, tok, kv, &exps[oct >> 1]);
+      d.keys(ops + P::kRaw, oct, tok, un, &exps[oct >> 1]);
       d.store_keys(ops, oct);
     } else {
-      d.values(ops + P::kRawV - R::kVp, tables[oct], oct, tok, kv);
+      d.values(ops + P::kRawV - R::kVp, tables[oct], oct, tok, un);
       d.store_values(ops + C::kK, oct);
     }
     fence_proxy_async_smem();
@@ -1191,11 +1333,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-template <int D>
+template <int D, bool MASK>
 cudaError_t launch(const FwdArgs& args, int sms, cudaStream_t s) {
   FwdArgs a = args;
   if ((int64_t)a.max_q * a.d.G > (kPrepTiles - 1) * kRows) {
-    const cudaError_t e = launch_pdl(attn_prepare_kernel<D>, dim3(2 * sms), dim3(kPrepThreads),
+    const cudaError_t e = launch_pdl(attn_prepare_kernel<D, MASK>, dim3(2 * sms), dim3(kPrepThreads),
                                      PrepCfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
     if (e != cudaSuccess) return e;
   } else {
@@ -1203,20 +1345,35 @@ cudaError_t launch(const FwdArgs& args, int sms, cudaStream_t s) {
   }
   const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
   const cudaError_t e =
-      launch_pdl(attn_prefill_kernel<D>, dim3(blocks), dim3(kThreads),
+      launch_pdl(attn_prefill_kernel<D, MASK>, dim3(blocks), dim3(kThreads),
                  Cfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_join_kernel<D, kRows>, dim3(8 * sms), dim3(kJoinThreads), 0, s, a, blocks);
 }
 
-template <int D>
+template <bool MASK>
+cudaError_t launch_any(const FwdArgs& a, int sms, cudaStream_t s) {
+  if (a.d.D == 256) return launch<256, MASK>(a, sms, s);
+  if (a.d.D == 128) return launch<128, MASK>(a, sms, s);
+  return launch<64, MASK>(a, sms, s);
+}
+
+template <int D, bool MASK>
 cudaError_t prepare() {
   const cudaError_t e = cudaFuncSetAttribute(
-      attn_prepare_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      attn_prepare_kernel<D, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
       PrepCfg<D>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(attn_prefill_kernel<D, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Cfg<D>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
+}
+
+template <bool MASK>
+cudaError_t prepare_all() {
+  cudaError_t e;
+  if ((e = prepare<64, MASK>()) != cudaSuccess) return e;
+  if ((e = prepare<128, MASK>()) != cudaSuccess) return e;
+  return prepare<256, MASK>();
 }
 
 }  // namespace
@@ -1234,16 +1391,12 @@ int attn_prep_steps(const AttnDims& d, int max_requests) {
 }
 
 cudaError_t prepare_attn_prefill_kernels() {
-  cudaError_t e;
-  if ((e = prepare<64>()) != cudaSuccess) return e;
-  if ((e = prepare<128>()) != cudaSuccess) return e;
-  return prepare<256>();
+  const cudaError_t e = prepare_all<false>();
+  return e != cudaSuccess ? e : prepare_all<true>();
 }
 
 cudaError_t launch_attn_prefill(const FwdArgs& a, int sms, cudaStream_t s) {
-  if (a.d.D == 256) return launch<256>(a, sms, s);
-  if (a.d.D == 128) return launch<128>(a, sms, s);
-  return launch<64>(a, sms, s);
+  return a.window || a.masks ? launch_any<true>(a, sms, s) : launch_any<false>(a, sms, s);
 }
 
 }  // namespace moe

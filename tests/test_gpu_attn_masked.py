@@ -42,7 +42,7 @@ class View(Setup):
             pos = c + torch.arange(n)
             sees = t <= pos[:, None]
         else:
-            pos = torch.tensor([c - 1 + len([j for j in m if j < n]) for m in self.seen[b]],
+            pos = torch.tensor([c + max(len([j for j in m if j < n]) - 1, 0) for m in self.seen[b]],
                                dtype=torch.long)
             sees = (t < c).repeat(n, 1)
             for i, mine in enumerate(self.seen[b]):
