@@ -191,11 +191,11 @@ int attn_tree_plan(attn_handle h, const int32_t* parents, const int32_t* q_offse
 /* attn_qk_norm_rope of T tokens' queries and keys and attn_kv4_append of the turned keys and the
  * values v [T][Hkv][D], in one launch: the keys are not written as bf16.  Arguments as there, but
  * q_weight and k_weight may both be NULL: no norm then, the rotation alone.  q_out may be q itself.
- * The turned key rows are rounded to bf16 and quantised.  Before, every operation is a single one
- * in fp32, so the codes are the same everywhere: the sum of a row's squares, rounded once, times 1 / D,
- * plus eps; 1 / sqrt of it, two operations; x times that, times the weight; a cos - b sin and b cos + a
- * sin, three operations each.  (attn_qk_norm_rope rounds in other places, so its rows may differ in
- * the last bit.)  Queries of tokens whose slot is negative are formed all the same. */
+ * The turned key rows are rounded to bf16 and quantised.  Every operation on them before is a single
+ * one in fp32, so the codes are the same everywhere: the sum of a row's squares, rounded once, times
+ * 1 / D, plus eps; 1 / sqrt of it, two operations; x times that, times the weight; a cos - b sin and
+ * b cos + a sin, three operations each.  (attn_qk_norm_rope rounds in other places, so its rows may
+ * differ in the last bit.)  Queries of tokens whose slot is negative are formed all the same. */
 int attn_qk_norm_rope_append(attn_handle h, const void* q, int64_t q_stride, const void* k,
                              int64_t k_stride, const void* v, int64_t v_stride,
                              const int32_t* positions, const int32_t* slots, const void* q_weight,

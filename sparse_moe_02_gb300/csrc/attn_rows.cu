@@ -10,6 +10,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostHeads = 8;  // of a group of lanes, in the norm and rotation
+constexpr int kMostQueries = 4;  // the same where rows are appended too: registers of five blocks an SM
 
 struct Row8 {
   float x[8];
@@ -178,52 +179,110 @@ struct Coded {
   bool finite;
 };
 
+// A lane's 8 channels as the pairs (i, i + 4): what packed fp32 instructions work on.
+struct Pairs8 {
+  float2 p[4];
+};
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Packed operations.  (ptxas fuses a packed product and sum, .rn or not: measured, sums that nearly cancel
+// came out fused.  Where that would change a value, the product is formed by mul_each.)
+#define MOE_PACKED2(name, op)                                                                  \
+  __device__ __forceinline__ float2 name(float2 a, float2 b) {                                 \
+    float2 r;                                                                                  \
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t" op         \
+        ".rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"                                      \
+        : "=f"(r.x), "=f"(r.y)                                                                 \
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                             \
+    return r;                                                                                  \
+  }
+MOE_PACKED2(add2, "add")
+MOE_PACKED2(mul2, "mul")
+#undef MOE_PACKED2
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t"
+      "mov.b64 s, {%6, %7};\n\tfma.rn.f32x2 p, p, q, s;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+__device__ __forceinline__ Pairs8 widen_pairs(uint4 w) {
+  return Pairs8{{make_float2(bf16_lo(w.x), bf16_lo(w.z)), make_float2(bf16_hi(w.x), bf16_hi(w.z)),
+                 make_float2(bf16_lo(w.y), bf16_lo(w.w)), make_float2(bf16_hi(w.y), bf16_hi(w.w))}};
+}
+
+__device__ __forceinline__ uint4 narrow(const Pairs8& r) {
+  return make_uint4(pack_bf16(r.p[0].x, r.p[1].x), pack_bf16(r.p[2].x, r.p[3].x),
+                    pack_bf16(r.p[0].y, r.p[1].y), pack_bf16(r.p[2].y, r.p[3].y));
+}
+
+// Largest magnitude of three.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// bf16(range / 15), the quotient rounded to fp32 before.  The product with 1 / 15 is within two units in
+// the last place of that quotient, so both round to the same bf16 unless the product lies that near the
+// middle between two: then, and for quotients that are no normal numbers, the division itself decides.
+__device__ __forceinline__ __nv_bfloat16 step_of(float range) {
+  float p = __fmul_rn(range, 1.f / 15.f);
+  const uint32_t past = (__float_as_uint(p) & 0xffffu) - 0x7ffcu;
+  if (past <= 8u || !(p > 1e-30f && p < 1e38f)) p = __fdiv_rn(range, 15.f);
+  return __float2bfloat16_rn(p);
+}
+
 // Codes of the lane's 8 channels; the 8 lanes of a group share lo and step.  Every code equals the
 // one that the definition's fp32 division and rounding give.
 __device__ __forceinline__ Coded code_row(uint4 w) {
-  uint32_t lo2 = min_nan2(min_nan2(w.x, w.y), min_nan2(w.z, w.w));
-  uint32_t hi2 = max_nan2(max_nan2(w.x, w.y), max_nan2(w.z, w.w));
+  const uint32_t lo2 = min_nan2(min_nan2(w.x, w.y), min_nan2(w.z, w.w));
+  const uint32_t hi2 = max_nan2(max_nan2(w.x, w.y), max_nan2(w.z, w.w)) ^ 0x80008000u;
+  // (smallest, largest negated): the smaller of each
+  uint32_t ends = min_nan2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo2 = min_nan2(lo2, __shfl_xor_sync(~0u, lo2, o));
-    hi2 = max_nan2(hi2, __shfl_xor_sync(~0u, hi2, o));
-  }
-  const float lo = bf16_lo(min_nan2(lo2, lo2 >> 16)), hi = bf16_lo(max_nan2(hi2, hi2 >> 16));
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+  for (int o = 1; o < 8; o <<= 1) ends = min_nan2(ends, __shfl_xor_sync(~0u, ends, o));
+  const float lo = bf16_lo(ends), hi = -bf16_hi(ends);
+  const __nv_bfloat16 sb = step_of(__fsub_rn(hi, lo));
   const float step = __bfloat162float(sb);
-  const Row8 r = widen(w);
+  const Pairs8 r = widen_pairs(w);
   Coded c;
   c.finite = fabsf(lo) < kLargest && fabsf(hi) < kLargest;  // false for NaN
-  float q[8];
+  float2 q[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = 0.f;
+  for (int e = 0; e < 4; ++e) q[e] = both(0.f);
   if (step > 0.f) {
-    // The product with the reciprocal is within 2^-20 of the rounded quotient, so it rounds to the
-    // same code (at most 15) unless it lies near a half: then, and for steps whose reciprocal is
-    // no normal number, the quotient itself decides.  2^23 is added and taken off to round.
-    const float inv = __frcp_rn(step);
-    bool close = step < 1e-35f;
+    // The product with the reciprocal (itself within a unit in the last place) is within 2^-18 of the
+    // rounded quotient, so it rounds to the same code (at most 15) unless it lies near a half: then, and
+    // for steps whose reciprocal is no normal number, the quotient itself decides.  2^23 is added and
+    // taken off to round.
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+    float2 d[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float y = __fmul_rn(__fsub_rn(r.x[e], lo), inv);
-      q[e] = __fsub_rn(__fadd_rn(y, 8388608.f), 8388608.f);
-      close |= fabsf(__fsub_rn(y, q[e])) > 0.49998f;
+    for (int e = 0; e < 4; ++e) {
+      const float2 y = mul2(add2(r.p[e], both(-lo)), both(inv));
+      q[e] = add2(add2(y, both(8388608.f)), both(-8388608.f));
+      d[e] = fma2(q[e], both(-1.f), y);
     }
-    if (close) {
+    const float far = fmaxf(max_abs3(max_abs3(d[0].x, d[0].y, d[1].x), d[1].y, d[2].x),
+                            max_abs3(d[2].y, d[3].x, d[3].y));
+    if (far > 0.49998f || step < 1e-35f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        q[e] = fminf(rintf(__fdiv_rn(__fsub_rn(r.x[e], lo), step)), 15.f);
+      for (int e = 0; e < 4; ++e) {
+        q[e].x = fminf(rintf(__fdiv_rn(__fsub_rn(r.p[e].x, lo), step)), 15.f);
+        q[e].y = fminf(rintf(__fdiv_rn(__fsub_rn(r.p[e].y, lo), step)), 15.f);
+      }
     }
   }
   // four codes as the low 16 bits of 2^23 + c0 + 16 c1 + 256 c2 + 4096 c3
-  uint32_t half[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float a = fmaf(q[4 * i + 1], 16.f, q[4 * i]);
-    const float b = fmaf(q[4 * i + 3], 16.f, q[4 * i + 2]);
-    half[i] = __float_as_uint(__fadd_rn(fmaf(b, 256.f, a), 8388608.f));
-  }
-  c.word = __byte_perm(half[0], half[1], 0x5410);
+  const float2 a = fma2(q[1], both(16.f), q[0]), b = fma2(q[3], both(16.f), q[2]);
+  const float2 half = add2(fma2(b, both(256.f), a), both(8388608.f));
+  c.word = __byte_perm(__float_as_uint(half.x), __float_as_uint(half.y), 0x5410);
   const __nv_bfloat16 lb = __float2bfloat16_rn(lo);
   c.params = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(lb) << 16);
   return c;
@@ -284,144 +343,279 @@ __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
 
 // ------------------------------------------------------------------- norm, rotation and append
 
-// Sum over L neighbouring lanes of the lanes' squares, as if rounded once: two floats carry it, the
-// second what the first's additions round off (exactly, Knuth's two-sum; the squares of bf16 values are
-// fp32 numbers).
+// a times b, rounded by itself.
+__device__ __forceinline__ float2 mul_each(float2 a, float2 b) {
+  return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
+}
+
+// a b + c d, the products rounded before they are added.
+__device__ __forceinline__ float2 sum_of_products(float2 a, float2 b, float2 c, float2 d) {
+  return add2(mul_each(a, b), mul_each(c, d));
+}
+
+// s + p, with what the sum rounds off (exactly, Knuth's two-sum) added to e.
+__device__ __forceinline__ float add_exact(float s, float p, float& e) {
+  const float t = __fadd_rn(s, p), u = __fsub_rn(t, s);
+  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(p, u)));
+  return t;
+}
+
+__device__ __forceinline__ float2 add_exact(float2 s, float2 p, float2& e) {
+  const float2 less = both(-1.f);
+  const float2 t = add2(s, p), u = fma2(s, less, t);
+  const float2 ds = fma2(fma2(u, less, t), less, s), dp = fma2(u, less, p);
+  e = add2(e, add2(ds, dp));
+  return t;
+}
+
+// Sum over L neighbouring lanes of the lanes' squares (fp32 numbers, those of bf16 values), rounded once:
+// a second float carries what the first one's additions round off.
 template <int L>
-__device__ __forceinline__ float sum_squares(const Row8& r) {
-  float s = __fmul_rn(r.x[0], r.x[0]), e = 0.f;
-  auto add = [&](float p) {
-    const float t = __fadd_rn(s, p), u = __fsub_rn(t, s);
-    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(p, u)));
-    s = t;
-  };
+__device__ __forceinline__ float sum_squares_exact(const Pairs8& r) {
+  float2 e2 = both(0.f), s2 = mul2(r.p[0], r.p[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) add(__fmul_rn(r.x[i], r.x[i]));
+  for (int i = 1; i < 4; ++i) s2 = add_exact(s2, mul2(r.p[i], r.p[i]), e2);
+  float e = __fadd_rn(e2.x, e2.y), s = add_exact(s2.x, s2.y, e);
 #pragma unroll
   for (int o = L / 2; o; o >>= 1) {
     const float p = __shfl_xor_sync(~0u, s, o);
     e = __fadd_rn(e, __shfl_xor_sync(~0u, e, o));
-    add(p);
+    s = add_exact(s, p, e);
   }
   return s < INFINITY ? __fadd_rn(s, e) : s;
 }
 
-// The cosines and sines of the lane's channels ch .. ch + 7 at a token's position, a position out of
-// range at 0.  INTER: of pairs ch / 2 .. ch / 2 + 3 (the first four of each); else of the channels, the
-// sines of the lower half negated.
-template <bool INTER>
-__device__ __forceinline__ void load_turn(const RopeArgs& a, int t, int li, int ch, float (&cs)[8],
-                                          float (&sn)[8]) {
+// Cosines and sines of a lane's channels ch .. ch + 7 at a token's position (a position out of range at
+// 0), in pairs as the channels': of the channels' angles, the sines of the lower half negated; INTER: of
+// the angles of channels (2i, 2i + 1), the first two pairs.
+struct Turn {
+  float2 c[4], s[4];
+};
+
+// A token's row of the table; `first` lane records a position out of range.
+__device__ __forceinline__ const float* turn_row_at(const RopeArgs& a, int t, bool first) {
   int pos = a.positions[t];
   if (pos < 0 || pos >= a.n_positions) {
-    if (li == 0) record_error(a.err, kDevErrState);
+    if (first) record_error(a.err, kDevErrState);
     pos = 0;
   }
+  return a.cos_sin + (int64_t)pos * a.rot;
+}
+
+template <bool INTER>
+__device__ __forceinline__ void load_turn(const RopeArgs& a, int t, int li, int ch, Turn& x) {
   const int half = a.rot / 2;
-  const float* row = a.cos_sin + (int64_t)pos * a.rot;
+  const float* row = turn_row_at(a, t, li == 0);
   const int i = INTER ? ch / 2 : ch < half ? ch : ch - half;
-  const float sg = !INTER && ch < half ? -1.f : 1.f;
-#pragma unroll
-  for (int e = 0; e < (INTER ? 1 : 2); ++e) {
-    const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * e);
-    const float4 s = *reinterpret_cast<const float4*>(row + half + i + 4 * e);
-    cs[4 * e] = c.x; cs[4 * e + 1] = c.y; cs[4 * e + 2] = c.z; cs[4 * e + 3] = c.w;
-    sn[4 * e] = sg * s.x; sn[4 * e + 1] = sg * s.y; sn[4 * e + 2] = sg * s.z; sn[4 * e + 3] = sg * s.w;
+  const float4 c0 = *reinterpret_cast<const float4*>(row + i);
+  const float4 s0 = *reinterpret_cast<const float4*>(row + half + i);
+  if (INTER) {
+    x.c[0] = make_float2(c0.x, c0.z), x.c[1] = make_float2(c0.y, c0.w);
+    x.s[0] = make_float2(s0.x, s0.z), x.s[1] = make_float2(s0.y, s0.w);
+  } else {
+    const float4 c1 = *reinterpret_cast<const float4*>(row + i + 4);
+    const float4 s1 = *reinterpret_cast<const float4*>(row + half + i + 4);
+    const float2 sg = both(ch < half ? -1.f : 1.f);
+    x.c[0] = make_float2(c0.x, c1.x), x.c[1] = make_float2(c0.y, c1.y);
+    x.c[2] = make_float2(c0.z, c1.z), x.c[3] = make_float2(c0.w, c1.w);
+    x.s[0] = mul2(sg, make_float2(s0.x, s1.x)), x.s[1] = mul2(sg, make_float2(s0.y, s1.y));
+    x.s[2] = mul2(sg, make_float2(s0.z, s1.z)), x.s[3] = mul2(sg, make_float2(s0.w, s1.w));
   }
 }
 
-// Norm (NORM) and rotation of a row, in the single operations that include/attn.h states.
+// Norm (NORM) and rotation of a key row, in the single operations that include/attn.h states.
 template <int D, bool INTER, bool NORM>
-__device__ __forceinline__ uint4 turn_row(const RopeArgs& a, uint4 raw, const Row8& w, int li, int ch,
-                                          const float (&cs)[8], const float (&sn)[8]) {
+__device__ __forceinline__ uint4 turn_key(const RopeArgs& a, uint4 raw, const Pairs8& w, int li, int ch,
+                                          const Turn& x) {
   constexpr int L = D / 8;
-  Row8 r = widen(raw);
+  Pairs8 r = widen_pairs(raw);
   if (NORM) {
-    const float mean = __fadd_rn(__fmul_rn(sum_squares<L>(r), 1.f / D), a.eps);
-    const float inv = __frcp_rn(__fsqrt_rn(mean));
+    const float mean = __fmul_rn(sum_squares_exact<L>(r), 1.f / D);
+    const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, a.eps)));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r.x[e] = __fmul_rn(__fmul_rn(r.x[e], inv), w.x[e]);
+    for (int e = 0; e < 4; ++e) r.p[e] = mul2(mul2(r.p[e], both(inv)), w.p[e]);
   }
   if (a.rot) {
     const bool turn = ch < a.rot;
     if (INTER) {
       if (turn) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = r.x[2 * e], y = r.x[2 * e + 1];
-          r.x[2 * e] = __fsub_rn(__fmul_rn(x, cs[e]), __fmul_rn(y, sn[e]));
-          r.x[2 * e + 1] = __fadd_rn(__fmul_rn(y, cs[e]), __fmul_rn(x, sn[e]));
+        for (int e = 0; e < 2; ++e) {
+          const float2 u = r.p[2 * e], v = r.p[2 * e + 1];
+          const float2 minus = make_float2(-x.s[e].x, -x.s[e].y);
+          r.p[2 * e] = sum_of_products(u, x.c[e], v, minus);
+          r.p[2 * e + 1] = sum_of_products(v, x.c[e], u, x.s[e]);
         }
       }
     } else {
       // the pair's other half sits half / 8 lanes away
       const int half = a.rot / 2, lane = threadIdx.x & 31;
       const int mate = turn ? lane - li + (ch < half ? li + half / 8 : li - half / 8) : lane;
-      Row8 m;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m.x[e] = __shfl_sync(~0u, r.x[e], mate);
-      if (turn) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          r.x[e] = __fadd_rn(__fmul_rn(r.x[e], cs[e]), __fmul_rn(m.x[e], sn[e]));
+      for (int e = 0; e < 4; ++e) {
+        const float2 m = make_float2(__shfl_sync(~0u, r.p[e].x, mate), __shfl_sync(~0u, r.p[e].y, mate));
+        if (turn) r.p[e] = sum_of_products(r.p[e], x.c[e], m, x.s[e]);
       }
     }
   }
   return narrow(r);
 }
 
-// attn_qk_norm_rope_append: a group of L = D / 8 lanes per row.  The first blocks take a key and a value
-// row each group, the others heads_per neighbouring query heads of a token, as in the norm and rotation
-// alone.
+// A lane's 8 channels of a query row, laid out so that a rotation's pairs (u, v) lie in one lane: neighbouring
+// channels (INTER), or four channels and their mates half the rotated ones away; behind the rotated channels
+// eight neighbouring ones.
+template <bool INTER>
+struct QueryPiece {
+  int first, second;  // channels of the four lower and the four upper ones
+
+  __device__ __forceinline__ QueryPiece(int rot, int li) {
+    const bool split = !INTER && li < rot / 8;
+    first = split ? 4 * li : 8 * li;
+    second = split ? rot / 2 + 4 * li : 8 * li + 4;
+  }
+  __device__ __forceinline__ uint4 load(const __nv_bfloat16* row) const {
+    if (INTER) return *reinterpret_cast<const uint4*>(row + first);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + first);
+    const uint2 y = *reinterpret_cast<const uint2*>(row + second);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* row, uint4 w) const {
+    if (INTER) {
+      *reinterpret_cast<uint4*>(row + first) = w;
+    } else {
+      *reinterpret_cast<uint2*>(row + first) = make_uint2(w.x, w.y);
+      *reinterpret_cast<uint2*>(row + second) = make_uint2(w.z, w.w);
+    }
+  }
+  // u0, u1, v0, v1
+  static __device__ __forceinline__ Pairs8 pairs(uint4 w) {
+    if (INTER)
+      return Pairs8{{make_float2(bf16_lo(w.x), bf16_lo(w.y)), make_float2(bf16_lo(w.z), bf16_lo(w.w)),
+                     make_float2(bf16_hi(w.x), bf16_hi(w.y)), make_float2(bf16_hi(w.z), bf16_hi(w.w))}};
+    return Pairs8{{make_float2(bf16_lo(w.x), bf16_hi(w.x)), make_float2(bf16_lo(w.y), bf16_hi(w.y)),
+                   make_float2(bf16_lo(w.z), bf16_hi(w.z)), make_float2(bf16_lo(w.w), bf16_hi(w.w))}};
+  }
+  static __device__ __forceinline__ uint4 words(const Pairs8& r) {
+    if (INTER)
+      return make_uint4(pack_bf16(r.p[0].x, r.p[2].x), pack_bf16(r.p[0].y, r.p[2].y),
+                        pack_bf16(r.p[1].x, r.p[3].x), pack_bf16(r.p[1].y, r.p[3].y));
+    return make_uint4(pack_bf16(r.p[0].x, r.p[0].y), pack_bf16(r.p[1].x, r.p[1].y),
+                      pack_bf16(r.p[2].x, r.p[2].y), pack_bf16(r.p[3].x, r.p[3].y));
+  }
+};
+
+// Norm (NORM) and rotation (by angles with cosines c and sines s) of a query row.
 template <int D, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kThreads) attn_rope_append_kernel(RopeArgs r, RowsArgs a,
-                                                                    int heads_per, int kv_blocks) {
+__device__ __forceinline__ uint4 turn_query(const RopeArgs& a, uint4 raw, const Pairs8& w, bool turn,
+                                            const float2 (&c)[2], const float2 (&s)[2]) {
+  Pairs8 r = QueryPiece<INTER>::pairs(raw);
+  if (NORM) {
+    float2 s2 = mul2(r.p[0], r.p[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s2 = fma2(r.p[i], r.p[i], s2);
+    float sum = s2.x + s2.y;
+#pragma unroll
+    for (int o = D / 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    const float inv = rsqrtf(sum * (1.f / D) + a.eps);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r.p[e] = mul2(mul2(r.p[e], both(inv)), w.p[e]);
+  }
+  if (turn) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 u = r.p[e], v = r.p[2 + e];
+      r.p[e] = fma2(u, c[e], mul2(v, make_float2(-s[e].x, -s[e].y)));
+      r.p[2 + e] = fma2(v, c[e], mul2(u, s[e]));
+    }
+  }
+  return QueryPiece<INTER>::words(r);
+}
+
+// Division of numbers below 2^31 by d, 1 <= d <= 2^20: a product and a shift (a division takes some twenty
+// instructions, a row of 128 channels some hundred).  With 2^(l-1) < d <= 2^l and m = 2^(31+l) / d rounded up
+// (above it by less than 1), n m / 2^(31+l) lies above n / d by less than n / 2^(31+l) < 1 / d.
+struct Divide {
+  uint32_t m, shift;
+  explicit Divide(uint32_t d) {
+    uint32_t l = 0;
+    while ((1u << l) < d) ++l;
+    shift = 31 + l;
+    m = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (uint32_t)((uint64_t)n * m >> shift);
+  }
+};
+
+// How the blocks of attn_rope_append_kernel share the work.
+struct Shares {
+  int heads_per;     // neighbouring query heads of a token that a group of lanes takes
+  uint32_t splits;   // groups for a token's
+  uint32_t kv_rate;  // key and value blocks among all, over 2^32: block b is the (b kv_rate >> 32)-th
+  Divide by_heads, by_splits;
+};
+
+// attn_qk_norm_rope_append: a group of L = D / 8 lanes per row.  kv_blocks of the blocks take a key and a
+// value row each group, the others heads_per neighbouring query heads of a token, as in the norm and
+// rotation alone; both kinds evenly mixed, since the first is bound by instruction issue and the second by
+// memory.
+template <int D, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kThreads, 5) attn_rope_append_kernel(RopeArgs r, RowsArgs a,
+                                                                    Shares n) {
   constexpr int L = D / 8;
   constexpr int kPerBlock = kThreads / L;
   const int li = threadIdx.x % L;
   const int ch = 8 * li;
   const unsigned group_mask = L == 32 ? ~0u : ((1u << L) - 1) << ((threadIdx.x & 31) - li);
   const bool turn = ch < r.rot;
-  float cs[8], sn[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
   pdl_wait();
   pdl_trigger();
-  if ((int)blockIdx.x < kv_blocks) {
-    const uint32_t row = blockIdx.x * kPerBlock + threadIdx.x / L;
+  // block b's place among the blocks of its kind
+  const uint32_t kv_before = __umulhi(blockIdx.x, n.kv_rate);
+  if (__umulhi(blockIdx.x + 1, n.kv_rate) > kv_before) {
+    const uint32_t row = kv_before * kPerBlock + threadIdx.x / L;
     const bool live = row < (uint32_t)a.T * a.Hkv;  // below 2^27
-    const int t = live ? (int)(row / (uint32_t)a.Hkv) : 0, h = live ? (int)(row % (uint32_t)a.Hkv) : 0;
+    const int t = live ? (int)n.by_heads(row) : 0, h = live ? (int)row - t * a.Hkv : 0;
     const uint4 kw = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + ch);
     const uint4 vw = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + ch);
     const int slot = live ? a.slots[t] : -1;
-    if (turn && live) load_turn<INTER>(r, t, li, ch, cs, sn);
-    Row8 w;
-    if (NORM) w = widen(*reinterpret_cast<const uint4*>(r.kw + ch));
-    const uint4 turned = turn_row<D, INTER, NORM>(r, kw, w, li, ch, cs, sn);
+    Turn x;
+    if (turn && live) load_turn<INTER>(r, t, li, ch, x);
+    Pairs8 w;
+    if (NORM) w = widen_pairs(*reinterpret_cast<const uint4*>(r.kw + ch));
+    const uint4 turned = turn_key<D, INTER, NORM>(r, kw, w, li, ch, x);
     write_rows<D>(a, slot, h, li, group_mask, code_row(turned), code_row(vw));
     return;
   }
-  const uint32_t splits = (r.Hq + heads_per - 1) / heads_per;
-  const uint32_t item = (blockIdx.x - kv_blocks) * kPerBlock + threadIdx.x / L;
-  const bool live = item < (uint32_t)r.T * splits;
-  const int t = live ? (int)(item / splits) : 0;
-  const int h0 = live ? (int)(item % splits) * heads_per : r.Hq;
-  uint4 raw[kMostHeads];
+  const uint32_t item = (blockIdx.x - kv_before) * kPerBlock + threadIdx.x / L;
+  const bool live = item < (uint32_t)r.T * n.splits;
+  const int t = live ? (int)n.by_splits(item) : 0;
+  const int h0 = live ? (int)(item - t * n.splits) * n.heads_per : r.Hq;
+  const int heads = min(n.heads_per, r.Hq - h0);
+  const QueryPiece<INTER> piece(r.rot, li);
+  const __nv_bfloat16* src = r.q + t * r.q_stride + h0 * D;
+  __nv_bfloat16* dst = r.q_out + t * r.q_out_stride + h0 * D;
+  uint4 raw[kMostQueries];
 #pragma unroll
-  for (int i = 0; i < kMostHeads; ++i) {
+  for (int i = 0; i < kMostQueries; ++i) {
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (i < heads_per && h0 + i < r.Hq)
-      raw[i] = *reinterpret_cast<const uint4*>(r.q + t * r.q_stride + (int64_t)(h0 + i) * D + ch);
+    if (i < heads) raw[i] = piece.load(src + i * D);
   }
-  if (turn && live) load_turn<INTER>(r, t, li, ch, cs, sn);
-  Row8 w;
-  if (NORM) w = widen(*reinterpret_cast<const uint4*>(r.qw + ch));
+  float2 c[2], s[2];
+  if (turn && live) {
+    const float* row = turn_row_at(r, t, li == 0) + 4 * li;
+    const float4 x = *reinterpret_cast<const float4*>(row);
+    const float4 y = *reinterpret_cast<const float4*>(row + r.rot / 2);
+    c[0] = make_float2(x.x, x.y), c[1] = make_float2(x.z, x.w);
+    s[0] = make_float2(y.x, y.y), s[1] = make_float2(y.z, y.w);
+  }
+  Pairs8 w;
+  if (NORM) w = piece.pairs(piece.load(r.qw));
 #pragma unroll
-  for (int i = 0; i < kMostHeads; ++i) {
-    if (i >= heads_per) break;
-    const uint4 y = turn_row<D, INTER, NORM>(r, raw[i], w, li, ch, cs, sn);
-    if (h0 + i < r.Hq)
-      *reinterpret_cast<uint4*>(r.q_out + t * r.q_out_stride + (int64_t)(h0 + i) * D + ch) = y;
+  for (int i = 0; i < kMostQueries; ++i) {
+    if (i >= n.heads_per) break;
+    const uint4 y = turn_query<D, INTER, NORM>(r, raw[i], w, turn, c, s);
+    if (i < heads) piece.store(dst + i * D, y);
   }
 }
 
@@ -544,11 +738,11 @@ int row_grid(const RowsArgs& a, int D) {
 }
 
 // Items of neighbouring heads of a token: as few heads in each as still leave one item for every group of
-// lanes that fits the GPU, up to eight.
-int heads_per_item(int T, int heads, int D, int sms) {
+// lanes that fits the GPU, up to `most`.
+int heads_per_item(int T, int heads, int most, int D, int sms) {
   const int64_t groups = (int64_t)sms * (2048 / kThreads) * (kThreads / (D / 8));
   int64_t per = (T * (int64_t)heads + groups - 1) / groups;
-  if (per > kMostHeads) per = kMostHeads;
+  if (per > most) per = most;
   const int splits = (heads + (int)per - 1) / (int)per;
   return (heads + splits - 1) / splits;  // evenly
 }
@@ -556,14 +750,17 @@ int heads_per_item(int T, int heads, int D, int sms) {
 template <int D, bool INTER>
 cudaError_t launch_rope_append(const RopeArgs& r, const RowsArgs& a, int sms, cudaStream_t s) {
   const int per_block = kThreads / (D / 8);
-  const int heads_per = heads_per_item(r.T, r.Hq, D, sms);
-  const int splits = (r.Hq + heads_per - 1) / heads_per;
-  const int kv_blocks = row_grid(a, D);
-  const dim3 grid((unsigned)(kv_blocks + ((int64_t)r.T * splits + per_block - 1) / per_block));
-  return r.qw ? launch_pdl(attn_rope_append_kernel<D, INTER, true>, grid, dim3(kThreads), 0, s, r, a,
-                           heads_per, kv_blocks)
+  const int heads_per = heads_per_item(r.T, r.Hq, kMostQueries, D, sms);
+  const uint32_t splits = (r.Hq + heads_per - 1) / heads_per;
+  const int64_t kv_blocks = row_grid(a, D);
+  const int64_t blocks = kv_blocks + ((int64_t)r.T * splits + per_block - 1) / per_block;
+  // rounded up by less than 1, so over all blocks (below 2^32) the count comes to kv_blocks exactly
+  const uint32_t rate = (uint32_t)(((kv_blocks << 32) + blocks - 1) / blocks);
+  const Shares n{heads_per, splits, rate, Divide(a.Hkv), Divide(splits)};
+  const dim3 grid((unsigned)blocks);
+  return r.qw ? launch_pdl(attn_rope_append_kernel<D, INTER, true>, grid, dim3(kThreads), 0, s, r, a, n)
               : launch_pdl(attn_rope_append_kernel<D, INTER, false>, grid, dim3(kThreads), 0, s, r, a,
-                           heads_per, kv_blocks);
+                           n);
 }
 
 }  // namespace
@@ -572,7 +769,7 @@ cudaError_t launch_attn_qk_norm_rope(const RopeArgs& a, int D, bool inter, int s
                                      cudaStream_t s) {
   const int per_block = kThreads / (D / 8);
   const int heads = a.Hq + a.Hkv;
-  const int heads_per = heads_per_item(a.T, heads, D, sms);
+  const int heads_per = heads_per_item(a.T, heads, kMostHeads, D, sms);
   const int splits = (heads + heads_per - 1) / heads_per;
   const dim3 grid((unsigned)(((int64_t)a.T * splits + per_block - 1) / per_block)), block(kThreads);
   if (D == 64)
