@@ -74,8 +74,9 @@ __device__ __forceinline__ Cut cut_work(const FwdArgs& a, int64_t* first, int64_
     if (lane == 31) sums[warp] = end;
     __syncthreads();
     int64_t before = total;
+    const int busy = min((a.B - b0 + 31) / 32, kThreads / 32);  // warps with requests
 #pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < busy; ++w) {
       const int64_t x = sums[w];
       if (w < warp) before += x;
       total += x;
@@ -168,8 +169,8 @@ __device__ __forceinline__ float row_sum(float m, float l) {
   return m != -INFINITY && fabsf(m) >= 268435456.f ? NAN : l;  // 2^28
 }
 
-// Outputs are joined in the order in which the lanes hold them: float4 i of a column is channels
-// out_channel(i) .. + 3.
+// The few-row kernel's outputs are joined in the order in which its lanes hold them: float4 i of a column
+// is channels out_channel(i) .. + 3.
 __device__ __forceinline__ int out_channel(int i) {
   return (i >> 4) * 64 + (i & 7) * 8 + ((i >> 3) & 1) * 4;
 }
@@ -345,7 +346,23 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2)
 #pragma unroll
     for (int i = kAtOnce / 2; i; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
     l = row_sum(m, __shfl_sync(~0u, l, 0));
-    if constexpr (kCh == 2) {
+    if constexpr (kCols > 16) {  // channels in their own order
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
+                           (int64_t)(p.h * a.d.G + row % a.d.G) * D + lane * kCh;
+      uint32_t x[kCh / 2];
+#pragma unroll
+      for (int e = 0; e < kCh / 2; ++e) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+        x[e] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      if constexpr (kCh == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+      else if constexpr (kCh == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(x[0], x[1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst) = x[0];
+    } else if constexpr (kCh == 2) {
       // two lanes hold the four channels that are stored at once
       const float x = __shfl_down_sync(~0u, o[0], 1), y = __shfl_down_sync(~0u, o[1], 1);
       if ((lane & 1) == 0)

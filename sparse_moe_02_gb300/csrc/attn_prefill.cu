@@ -235,8 +235,7 @@ __device__ __forceinline__ Cost cost_of(const FwdArgs& a, const Req& r, int part
     }
     c.bend = 0;
     if (!a.masks)
-      c.bend = (int)min(max(divide(max(most * a.d.G - c.base, (int64_t)0), kRows), (int64_t)0),
-                        (int64_t)INT_MAX);
+      c.bend = (int)min(max(most * a.d.G - c.base, (int64_t)0) / kRows, (int64_t)INT_MAX);
     c.flat = c.fixed + most * a.d.G;
   }
   return c;
@@ -921,6 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const bool whole = p.t1 - p.t0 == p.tiles;
       const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows;
       const int c = lane & 3;
+      // (rows of outputs are only known to start on 16 bytes)
+      const bool sectors = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(2 * a.out_stride)) & 31) == 0;
 #pragma unroll 1
       for (int u = (warp - kKeyWarp) >> 2; u < 2 * NG; u += 4) {
         const int hf = u & 1, g = u >> 1;
@@ -942,25 +943,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           else if (row < p.r.qn * a.d.G)
             d = reinterpret_cast<uint8_t*>(a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
                                            (int64_t)(p.h * a.d.G + row % a.d.G) * D);
+          if (whole) {
+            uint32_t x[8];  // words 2c and 2c + 1, eight channels each
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[i][q + w]) * f;
-            if (whole) {
-              uint32_t x[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                x[i] = *reinterpret_cast<const uint32_t*>(&y);
+            for (int i = 0; i < 8; ++i) {
+              const int w = i / 4, m = 2 * (i % 4);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[m][q + w]) * f,
+                                                             __uint_as_float(o[m + 1][q + w]) * f);
+              x[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            if (d) {
+              d += 128 * g + 32 * c;
+              if (sectors) {
+                st_global_v8(d, x);
+              } else {
+                reinterpret_cast<uint4*>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<uint4*>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
               }
-              if (d)
-                *reinterpret_cast<uint4*>(d + 128 * g + 16 * (2 * c + w)) =
-                    make_uint4(x[0], x[1], x[2], x[3]);
-            } else {
-              float4* part = reinterpret_cast<float4*>(d) + 16 * g + 2 * c + w;
-              part[0] = make_float4(v[0], v[1], v[2], v[3]);
-              part[8] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+          } else {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              uint32_t v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(o[i][q + w]) * f);
+              st_global_v8(d + 256 * g + 64 * c + 32 * w, v);
             }
           }
         }
@@ -974,54 +981,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     for (int k = 0; ok; ++k) {
       ok = __all_sync(~0u, part_ready(k));
       if (!ok) break;
-      const Part p = parts[k % kParts];
-      if (!p.some) break;
-      if (p.t0 == p.t1) {
-        // (a part's place is held until its outputs are written: not across parts without steps)
-        if (due >= 0 && !(ok = outputs(due, kq - 1))) break;
-        due = -1;
-        __syncwarp();
-        if (lane == 0) part_read(k);
-        continue;
-      }
-      // queries: every warp scales eight rows, four warps (one for each 32 lanes) move them on once
-      // the part before has used its own
-      QueryRows<D> q;
-      q.load(a, p, 8 * (warp - kKeyWarp), row_exp[kq % kExps]);
+      const Part& p = parts[k % kParts];  // (there until part_read)
+      const bool some = p.some && p.t1 > p.t0;
+      if (some) {
+        // queries: every warp scales eight rows, four warps (one for each 32 lanes) move them on once
+        // the part before has used its own
+        QueryRows<D> q;
+        q.load(a, p, 8 * (warp - kKeyWarp), row_exp[kq % kExps]);
 #pragma unroll
-      for (int pass = 0; pass < C::kQPasses && ok; ++pass) {
-        const int turn = kq * C::kQPasses + pass;
-        if (turn > 0)
-          ok = __all_sync(~0u, mbar_wait(&bars.q_copied, (turn - 1) & 1, a.err));
-        if (!ok) break;
-        q.store(ops, 8 * (warp - kKeyWarp), pass * C::kQGroups);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.q_staged);
-        if (warp < kKeyWarp + 4) {
-          ok = mbar_wait(&bars.q_staged, turn & 1, a.err) &&
-               (pass > 0 || kq == 0 || mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
-          ok = __all_sync(~0u, ok);
+        for (int pass = 0; pass < C::kQPasses && ok; ++pass) {
+          const int turn = kq * C::kQPasses + pass;
+          if (turn > 0)
+            ok = __all_sync(~0u, mbar_wait(&bars.q_copied, (turn - 1) & 1, a.err));
           if (!ok) break;
-          tc_fence_after();
-          copy_queries<D>(ops, tmem, pass * C::kQGroups);
+          q.store(ops, 8 * (warp - kKeyWarp), pass * C::kQGroups);
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars.q_copied);
-            if (pass == C::kQPasses - 1) mbar_arrive(&bars.q_full);
+          if (lane == 0) mbar_arrive(&bars.q_staged);
+          if (warp < kKeyWarp + 4) {
+            ok = mbar_wait(&bars.q_staged, turn & 1, a.err) &&
+                 (pass > 0 || kq == 0 || mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc_fence_after();
+            copy_queries<D>(ops, tmem, pass * C::kQGroups);
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bars.q_copied);
+              if (pass == C::kQPasses - 1) mbar_arrive(&bars.q_full);
+            }
           }
         }
+        if (!ok) break;
       }
-      if (!ok) break;
-      if (due >= 0 && !(ok = outputs(due, kq - 1))) break;
-      ++kq;
-      due = k;
-      if (prepared) continue;  // (steps are counted by those who use them)
-      const int t0 = p.t0, t1 = p.t1;
+      const int steps = some && !prepared ? p.t1 - p.t0 : 0;
       const Unread<MASK> un(a, p.r);
-      for (int t = t0; t < t1; ++t, ++n) {
+      for (int t = 0;; ++t) {
+        // The outputs of the part before, behind the steps whose operands fit beside its last ones: the
+        // next product of values needs room that the first one frees, and that waits for them.
+        if (due >= 0 && (t == C::kOpsV || t == steps)) {
+          if (!(ok = outputs(due, kq - 1))) break;
+          due = -1;
+        }
+        if (t == steps) break;
         const int which = is_key ? 0 : 1, ring = is_key ? C::kRawK : C::kRawV;
         const int st = n % ring;
-        const int tok = tile_at<MASK, kStep>(a, t, p.skip) * kStep + 8 * oct;
+        const int tok = tile_at<MASK, kStep>(a, p.t0 + t, p.skip) * kStep + 8 * oct;
         ok = mbar_wait(&bars.raw_full[which][st], (n / ring) & 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
@@ -1043,9 +1047,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(is_key ? &bars.k_full[op] : &bars.v_full[op]);
+        ++n;  // (steps of prepared parts are counted by those who use them)
+      }
+      if (!ok || !p.some) break;
+      if (some) {
+        due = k;
+        ++kq;
+      } else {
+        __syncwarp();
+        if (lane == 0) part_read(k);
       }
     }
-    if (ok && due >= 0) outputs(due, kq - 1);
   } else {
     registers_up<kRegsSoft>();
     // softmax: row `tid` of the row tile, tensor memory lane tid
