@@ -93,6 +93,8 @@ struct Cfg {
   static constexpr int kOffRaw = kOffV + kOpsV * kK;
   static constexpr int kOffRawV = kOffRaw + kRawK * kRecs * kSideK;
   static constexpr int kFirst = kOffRawV + kRawV * kRecs * kSideV;
+  static_assert(kQPasses <= 2 && (kQPasses == 1 || kFirst - kOffRaw >= kQGroups * kRows * 128),
+                "room for the second half of the queries");
   static constexpr int kSmem = kFirst + 1024;  // the operands start on a 1024-byte boundary
   // tensor memory columns: O, Q, the score buffers
   static constexpr int kColQ = D;
@@ -214,6 +216,12 @@ constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 constexpr int kPartCost = 320;   // tokens: a row tile's fixed cost
 constexpr int kZeroCost = 96;
 constexpr int kLeastSteps = 4;   // of a block
+// Row tiles behind a window cost alike, so where a share is several of them blocks may take whole ones: no
+// partial results and nothing to join, for up to this many steps more in the block that has most.  Cut
+// against whole, 256 channels, a window of 1024: 7350 tokens (7.8 steps more) 155 and 149 us, 8192 (17.0)
+// 172.8 and 170.5, 2048 (18.5) 58.2 and 60.2, 7700 (28.5) 163.8 and 166.8; 128 channels: 4096 tokens (0.8)
+// 131 and 126, 7500 (9.7) 223 and 220; 64 channels: 8192 (7.9) 223 and 212.
+constexpr int kWholeMore = 18;
 
 struct Cost {
   int64_t fixed, base;  // per row tile, in units
@@ -228,18 +236,22 @@ struct Cost {
   }
 };
 
+// Steps that a row tile behind a window goes over at most: the first tokens, and a window of each of its
+// tokens.
+__device__ __forceinline__ int64_t window_steps(const FwdArgs& a, int tokens) {
+  return ((int64_t)a.window + tokens + kStep - 1) / kStep + 1 + first_tiles<kStep>(a);
+}
+
+__device__ __forceinline__ int tile_tokens(const FwdArgs& a) { return (kRows - 1) / a.d.G + 1; }
+
 template <bool MASK>
 __device__ __forceinline__ Cost cost_of(const FwdArgs& a, const Req& r, int part_cost) {
   if (r.kv == 0) return Cost{(int64_t)kZeroCost * a.d.G, 0, 0, 0, INT_MAX};
   Cost c{(int64_t)part_cost * a.d.G, (int64_t)max(r.kv - r.qn, 0) * a.d.G, 64, 0, INT_MAX};
   if constexpr (MASK) {
-    // A row tile goes over the context at most (a tree's does), and over the first tokens and a window
-    // of each of its tokens: the steps that these can touch.
+    // the context at most (a tree's does), and what a window leaves of it
     int64_t most = a.masks ? r.kv : INT64_MAX;
-    if (a.window) {
-      const int64_t span = (int64_t)a.window + (a.masks ? r.qn : (kRows - 1) / a.d.G + 1);
-      most = min(most, kStep * ((span + kStep - 1) / kStep + 1 + first_tiles<kStep>(a)));
-    }
+    if (a.window) most = min(most, kStep * window_steps(a, a.masks ? r.qn : tile_tokens(a)));
     c.bend = 0;
     if (!a.masks)
       c.bend = (int)min(max(most * a.d.G - c.base, (int64_t)0) / kRows, (int64_t)INT_MAX);
@@ -574,7 +586,7 @@ struct QueryRows {
     }
   }
 
-  // Groups g0 .. g0 + kQGroups - 1 into shared memory: [group][row] of 128 bytes, pieces swizzled.
+  // kQGroups groups from g0 on into shared memory: [group][row] of 128 bytes, pieces swizzled.
   __device__ __forceinline__ void store(uint32_t dst, int row0, int g0) {
     const int lane = threadIdx.x & 31, g = ((lane % kL) >> 3) - g0, j = lane & 7;
     if (g < 0 || g >= Cfg<D>::kQGroups) return;
@@ -587,23 +599,25 @@ struct QueryRows {
   }
 };
 
-// The warp's 32 rows (tensor memory lanes 32 (warp % 4) ..) of those groups into tensor memory.
+// A quarter of those groups' columns of the 32 rows (tensor memory lanes) that the warp may write into tensor
+// memory.
 template <int D>
-__device__ __forceinline__ void copy_queries(uint32_t src, uint32_t tmem, int g0) {
+__device__ __forceinline__ void copy_queries(uint32_t src, uint32_t tmem, int g0, int part) {
   using C = Cfg<D>;
+  constexpr int kPieces = 2 * C::kQGroups;  // 16 bytes each: 4 columns
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = 32 * quarter + lane;
-#pragma unroll 1
-  for (int g = 0; g < C::kQGroups; ++g) {
-    uint32_t q[32];
+  uint32_t q[4 * kPieces];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(q[4 * j]), "=r"(q[4 * j + 1]), "=r"(q[4 * j + 2]), "=r"(q[4 * j + 3])
-                   : "r"(src + g * (kRows * 128) + row * 128 + ((j ^ (row & 7)) << 4)));
-    tmem_st32(tmem + ((uint32_t)(32 * quarter) << 16) + C::kColQ + 32 * (g0 + g), q);
+  for (int i = 0; i < kPieces; ++i) {
+    const int at = part * kPieces + i, g = at >> 3, j = at & 7;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q[4 * i]), "=r"(q[4 * i + 1]), "=r"(q[4 * i + 2]), "=r"(q[4 * i + 3])
+                 : "r"(src + g * (kRows * 128) + row * 128 + ((j ^ (row & 7)) << 4)));
   }
-  tmem_wait_st();
-  tc_fence_before();
+  const uint32_t dst =
+      tmem + ((uint32_t)(32 * quarter) << 16) + C::kColQ + 32 * g0 + 4 * kPieces * part;
+  if constexpr (kPieces == 4) tmem_st16(dst, q);
+  else tmem_st8(dst, q);
 }
 
 // Tokens t0 .. t0 + 63 of its context that a row sees, a bit each.
@@ -693,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     }
     for (int i = 0; i < kExps; ++i) mbar_init(&bars.x_full[i], 1);
     mbar_init(&bars.q_staged, 2 * kDeqWarps);
-    mbar_init(&bars.q_copied, 4);
-    mbar_init(&bars.q_full, 4);
+    mbar_init(&bars.q_copied, 2 * kDeqWarps);
+    mbar_init(&bars.q_full, 2 * kDeqWarps);
     mbar_init(&bars.q_free, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bars.o_scaled[i], kSoftWarps);
     mbar_init(&bars.o_done, 1);
@@ -811,8 +825,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       int64_t w = 0, w1 = 0;
       if ((int)blockIdx.x < cut_s.blocks)
         w = cut_s.bound(blockIdx.x), w1 = cut_s.bound(blockIdx.x + 1);
+      bool whole = false;  // the row tiles that begin in the share, and nothing of others
+      if constexpr (MASK) {
+        if (a.window && !a.masks) {
+          const int64_t unit = kStep * a.d.G;
+          const int64_t tile = (int64_t)part_cost * a.d.G + window_steps(a, tile_tokens(a)) * unit;
+          const int64_t more = divide(cut_s.share + tile - 1, tile) * tile - cut_s.share;
+          whole = cut_s.share > tile && more <= kWholeMore * unit;
+        }
+        if (whole && w < w1) {
+          const Part p = locate<MASK>(a, first, part_cost, w, INT64_MAX);
+          // (a request without cached tokens has row tiles of one cost, without steps)
+          const int64_t begin = p.start - (int64_t)(p.r.kv ? part_cost : kZeroCost) * a.d.G;
+          if (begin < w) w = p.next;
+        }
+      }
       for (int k = 0; ok; ++k) {
-        const Part p = locate<MASK>(a, first, part_cost, w, w1);
+        // (behind the share's end nothing begins in it)
+        const Part p = locate<MASK>(a, first, part_cost, w, MASK && whole && w < w1 ? INT64_MAX : w1);
         ok = mbar_wait(&bars.part_empty[k % kParts], ((k / kParts) & 1) ^ 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
@@ -1019,31 +1049,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const Part& p = parts[k % kParts];  // (there until part_read)
       const bool some = p.some && p.t1 > p.t0;
       if (some) {
-        // queries: every warp scales eight rows, four warps (one for each 32 lanes) move them on once
-        // the part before has used its own
+        // queries: every warp scales eight rows and moves a quarter of 32 on once the part before has
+        // used its own
         QueryRows<D> q;
         q.load(a, p, 8 * (warp - kKeyWarp), row_exp[kq % kExps]);
-#pragma unroll
-        for (int pass = 0; pass < C::kQPasses && ok; ++pass) {
-          const int turn = kq * C::kQPasses + pass;
+        // prepared steps leave the room of the records free: all groups at once, the others there
+        const int passes = prepared ? 1 : C::kQPasses;
+#pragma unroll 1
+        for (int pass = 0; pass < passes && ok; ++pass) {
+          const int turn = kq * passes + pass;
           if (turn > 0)
             ok = __all_sync(~0u, mbar_wait(&bars.q_copied, (turn - 1) & 1, a.err));
           if (!ok) break;
+          const bool all = C::kQPasses > 1 && prepared;
           q.store(ops, 8 * (warp - kKeyWarp), pass * C::kQGroups);
+          if (all) q.store(ops + C::kOffRaw, 8 * (warp - kKeyWarp), C::kQGroups);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.q_staged);
-          if (warp < kKeyWarp + 4) {
-            ok = mbar_wait(&bars.q_staged, turn & 1, a.err) &&
-                 (pass > 0 || kq == 0 || mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
-            ok = __all_sync(~0u, ok);
-            if (!ok) break;
-            tc_fence_after();
-            copy_queries<D>(ops, tmem, pass * C::kQGroups);
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&bars.q_copied);
-              if (pass == C::kQPasses - 1) mbar_arrive(&bars.q_full);
-            }
+          ok = mbar_wait(&bars.q_staged, turn & 1, a.err) &&
+               (pass > 0 || kq == 0 || mbar_wait(&bars.q_free, (kq - 1) & 1, a.err));
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          tc_fence_after();
+          copy_queries<D>(ops, tmem, pass * C::kQGroups, (warp - kKeyWarp) >> 2);
+          if (all) copy_queries<D>(ops + C::kOffRaw, tmem, C::kQGroups, (warp - kKeyWarp) >> 2);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars.q_copied);
+            if (pass == passes - 1) mbar_arrive(&bars.q_full);
           }
         }
         if (!ok) break;
