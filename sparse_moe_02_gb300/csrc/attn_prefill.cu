@@ -1309,10 +1309,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
 // Forms the MMA operands of every step of every context once, for calls whose contexts many row
 // tiles read.
 constexpr int kPrepThreads = 512;
-// From this many row tiles per context, on average, it pays (256 channels, 16 contexts of 2000 to
-// 4000 tokens, prepared against not: 4 row tiles 97 and 87 us, 6 114 and 113, 8 133 and 138, 16 (8
-// contexts) 131 and 156; 128 channels: 4 206 and 181, 8 326 and 340).
-constexpr int kPrepTiles = 8;
+// From this many row tiles per context, on average, it pays (256 channels, 16 contexts of 2000 to 4000
+// tokens, prepared against not: 4 row tiles 105 and 90 us, 6 122 and 124, 8 145 and 158; 128 channels,
+// 8 contexts of 8000: 4 308 and 292).
+constexpr int kPrepTiles = 7;
 constexpr int64_t kMostPrep = 512ll << 20;  // bytes of operands held
 
 template <int D>
