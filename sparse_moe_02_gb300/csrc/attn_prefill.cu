@@ -82,9 +82,8 @@ struct Cfg {
   // steps of key operands, value operands, and the records' key and value sides held
   static constexpr int kOpsK = 2, kOpsV = 2, kRawK = D == 256 ? 3 : 4, kRawV = D == 256 ? 2 : 4;
   static constexpr int kS = D == 256 ? 2 : 4;  // score buffers: what tensor memory holds
-  // A record's key side (with the parameters of its values: the softmax needs their exponents with
-  // the scores) and its value side.
-  static constexpr int kSideK = R::kV, kSideV = R::kBytes - R::kVp;
+  // A record's key side and its value side.
+  static constexpr int kSideK = R::kVp, kSideV = R::kBytes - R::kVp;
   static constexpr int kK = kStep * D * 2;  // bytes of a key (or value) operand
   // queries pass through shared memory two groups at a time
   static constexpr int kQGroups = NG < 2 ? NG : 2, kQPasses = NG / kQGroups;
@@ -335,7 +334,7 @@ struct Bars {
   uint64_t raw_full[2][4], raw_empty[2][4];  // [keys, values]
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[C::kS], p_full[C::kS], pv_done[C::kS];
-  uint64_t x_full[kExps];  // exponents of prepared steps
+  uint64_t x_full[kExps], ev_full[kExps];  // exponents of prepared steps; of the values of others
   uint64_t q_staged, q_copied, q_full, q_free, o_done, o_free, ended;
   // Two in turn: the softmax of a part needs its queries, not the outputs of the part before, so it can
   // end while a warp has yet to look at the part before's; queries of the part after that are staged
@@ -432,8 +431,7 @@ struct Dequant {
     return w;
   }
 
-  // tok: the first token's index in the context.  Also leaves the record's exponents in *ex (those
-  // of the values too: the softmax needs them with the scores).
+  // tok: the first token's index in the context.  Also leaves the exponent of the record's keys in *ex.
   template <bool MASK>
   __device__ __forceinline__ void keys(uint32_t raw, int oct, int tok, const Unread<MASK>& un,
                                        Exps* ex) {
@@ -441,20 +439,20 @@ struct Dequant {
     const int t = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
     const uint32_t rec = raw + (oct >> 1) * C::kSideK;
     const int row = 8 * (oct & 1) + t;
-    int e, ev;
+    int e;
     const uint32_t w = params(rec, R::kKp, oct, tok, un, &e);
-    params(rec, R::kVp, oct, tok, un, &ev);
-    if (lane == 0 && (oct & 1) == 0) *ex = Exps{pow2(e), (float)ev, pow2(-ev), 0.f};
+    if (lane == 0 && (oct & 1) == 0) ex->up_k = pow2(e);
     const float down = pow2(-(e + 6));
     const float s = bf16_lo(w) * down, b = bf16_hi(w) * down;
     const uint32_t s24 = pack_f16(s * 16777216.f, s * 16777216.f);
     const uint32_t s20 = pack_f16(s * 1048576.f, s * 1048576.f);
     const uint32_t bb = pack_f16(b, b);
-    const uint32_t src = rec + row * R::kRow + 4 * g;
+    // (rows start on multiples of their length: words are taken by an exclusive or with the address)
+    const uint32_t src =
+        rec + row * R::kRow + 4 * g + ((sub * kWords) ^ (t >> 2) ^ row_swz(t)) * (4 * NG);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int j = (sub * kWords + i) ^ (t >> 2);
-      const uint32_t c = lds32(src + ((j ^ row_swz(t)) * NG) * 4), c8 = c >> 8;
+      const uint32_t c = lds32(src ^ (i * 4 * NG)), c8 = c >> 8;
       out[i][0] = fma_f16x2(c & kNib0, s24, bb);
       out[i][1] = fma_f16x2(c & kNib1, s20, bb);
       out[i][2] = fma_f16x2(c8 & kNib0, s24, bb);
@@ -465,25 +463,31 @@ struct Dequant {
   __device__ __forceinline__ void store_keys(uint32_t dst, int oct) {
     const int lane = threadIdx.x & 31;
     const int t = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
-    const uint32_t at = dst + g * (kStep * 128) + (8 * oct + t) * 128;
+    const uint32_t at = dst + g * (kStep * 128) + (8 * oct + t) * 128 +
+                        (((sub * kWords) ^ (t >> 2) ^ t) << 4);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const int j = (sub * kWords + i) ^ (t >> 2);
-      sts128(at + ((j ^ t) << 4), out[i][0], out[i][1], out[i][2], out[i][3]);
-    }
+    for (int i = 0; i < kWords; ++i)
+      sts128(at ^ (i << 4), out[i][0], out[i][1], out[i][2], out[i][3]);
   }
 
   // Row i * 32 + lane of the value operand is channel 64 g + 8 j + kWords sub + i (lane = (sub, g, j)),
   // so that the rows of a store differ in their last three bits, which the swizzle spreads over
-  // the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.
+  // the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.  Leaves the exponent of
+  // the record's values in *ex, and counts that on `left` if there is one (the softmax needs it with the
+  // scores).
   template <bool MASK>
   __device__ __forceinline__ void values(uint32_t raw, uint4* table, int oct, int tok,
-                                         const Unread<MASK>& un) {
+                                         const Unread<MASK>& un, Exps* ex, uint64_t* left) {
     const int lane = threadIdx.x & 31;
     const uint32_t rec = raw + (oct >> 1) * C::kSideV;
     {
       int e;
       const uint32_t w = params(rec, R::kVp, oct, tok, un, &e);
+      if (lane == 0 && (oct & 1) == 0) {
+        ex->ev = (float)e;
+        ex->down_v = pow2(-e);
+        if (left) mbar_arrive(left);
+      }
       const int t = lane & 7, g = (lane >> 3) % NG;
       const float down = pow2(-(e + 6));
       const uint32_t mate = __shfl_down_sync(~0u, w, 1);
@@ -497,12 +501,12 @@ struct Dequant {
       __syncwarp();
     }
     const int j = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
+    const uint32_t at = rec + R::kV + 8 * (oct & 1) * R::kRow + (j * NG + g) * 4;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t = 2 * m;
-      const uint32_t at = rec + R::kV + (8 * (oct & 1) + t) * R::kRow;
-      const uint32_t w0 = lds32(at + ((j ^ row_swz(t)) * NG + g) * 4);
-      const uint32_t w1 = lds32(at + R::kRow + ((j ^ row_swz(t + 1)) * NG + g) * 4);
+      const uint32_t w0 = lds32((at ^ (row_swz(t) * (4 * NG))) + t * R::kRow);
+      const uint32_t w1 = lds32((at ^ (row_swz(t + 1) * (4 * NG))) + (t + 1) * R::kRow);
       const uint4 p = table[m * NG + g];
       if constexpr (NG == 4) {
 #pragma unroll
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       mbar_init(&bars.p_full[i], 32 * kSoftWarps);
       mbar_init(&bars.pv_done[i], 1);
     }
-    for (int i = 0; i < kExps; ++i) mbar_init(&bars.x_full[i], 1);
+    for (int i = 0; i < kExps; ++i) mbar_init(&bars.x_full[i], 1), mbar_init(&bars.ev_full[i], kRecs);
     mbar_init(&bars.q_staged, 2 * kDeqWarps);
     mbar_init(&bars.q_copied, 2 * kDeqWarps);
     mbar_init(&bars.q_full, 2 * kDeqWarps);
@@ -1104,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
                  &exps[n % kExps][oct >> 1]);
         else  // (a value side begins with its parameters: R::kVp from where the record would)
           d.values(ops + C::kOffRawV + st * kRecs * C::kSideV - C::R::kVp, tables[oct], oct, tok,
-                   un);
+                   un, &exps[n % kExps][oct >> 1], &bars.ev_full[n % kExps]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.raw_empty[which][st]);
         const int op = is_key ? n % C::kOpsK : n % C::kOpsV;
@@ -1157,7 +1161,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       float m = -INFINITY, l = 0.f, unit = 0.f, most_ev = -INFINITY;
       for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
         ok = mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err) &&
-             (!prepared || mbar_wait(&bars.x_full[n % kExps], (n / kExps) & 1, a.err));
+             mbar_wait(prepared ? &bars.x_full[n % kExps] : &bars.ev_full[n % kExps], (n / kExps) & 1,
+                       a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         tc_fence_after();
@@ -1388,7 +1393,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
       if (un.record(t * kRecs + rec)) continue;
       const uint4 w = *reinterpret_cast<const uint4*>(
           a.cache + (uint64_t)cache_record(a, b, h, t * kRecs + rec) * R::kBytes + at);
-      if (at < R::kV) *reinterpret_cast<uint4*>(smem + P::kRaw + rec * C::kSideK + at) = w;
+      if (at < R::kVp)
+        *reinterpret_cast<uint4*>(smem + P::kRaw + rec * C::kSideK + at) = w;
       if (at >= R::kVp)
         *reinterpret_cast<uint4*>(smem + P::kRawV + rec * C::kSideV + at - R::kVp) = w;
     }
@@ -1399,7 +1405,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
       d.keys(ops + P::kRaw, oct, tok, un, &exps[oct >> 1]);
       d.store_keys(ops, oct);
     } else {
-      d.values(ops + P::kRawV - R::kVp, tables[oct], oct, tok, un);
+      d.values(ops + P::kRawV - R::kVp, tables[oct], oct, tok, un, &exps[oct >> 1], nullptr);
       d.store_values(ops + C::kK, oct);
     }
     fence_proxy_async_smem();
