@@ -26,11 +26,29 @@ constexpr float kLeastUnit = 1.17549435e-38f;  // 2^-126
 constexpr int kDevErrNoMemory = 7;
 constexpr int kDevErrArg = 1;
 
+// Division of numbers below 2^31 by d, 1 <= d <= 2^20: a product and a shift (a division takes some twenty
+// instructions).  With 2^(l-1) < d <= 2^l and m = 2^(31+l) / d rounded up
+// (above it by less than 1), n m / 2^(31+l) lies above n / d by less than n / 2^(31+l) < 1 / d.
+struct Divide {
+  uint32_t m = 1u << 31, shift = 31;  // d = 1
+  Divide() = default;
+  explicit Divide(uint32_t d) {
+    uint32_t l = 0;
+    while ((1u << l) < d) ++l;
+    shift = 31 + l;
+    m = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (uint32_t)((uint64_t)n * m >> shift);
+  }
+};
+
 struct AttnDims {
   int Hq, Hkv, G, D;
   int page_shift;  // log2 of the page size
   int n_pages;
   float scale_log2;  // softmax scale * log2(e)
+  Divide by_G;       // new token of a row
 };
 
 // A cache record: 16 tokens of one head.

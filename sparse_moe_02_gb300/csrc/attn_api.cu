@@ -194,6 +194,7 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
   h->d.Hkv = cfg->n_kv_heads;
   h->d.G = cfg->n_q_heads / cfg->n_kv_heads;
   h->d.D = cfg->head_dim;
+  h->d.by_G = moe::Divide(h->d.G);
   h->d.page_shift = 0;
   while ((1 << h->d.page_shift) < cfg->page_size) ++h->d.page_shift;
   h->d.n_pages = cfg->n_pages;

@@ -233,7 +233,7 @@ __device__ __forceinline__ void fetch_query(const FwdArgs& a, const Part& p, uin
   if (MASK && a.masks) {
     const int col = threadIdx.x - 8 * NT * kPieces, row = p.rt * 8 * NT + col;
     if (col >= 0 && col < 8 * NT && row < p.r.qn * a.d.G) {
-      const uint32_t* src = a.masks + (int64_t)(p.r.q0 + row / a.d.G) * a.mask_words;
+      const uint32_t* src = a.masks + (int64_t)(p.r.q0 + a.d.by_G(row)) * a.mask_words;
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                        smem_u32(raw + col * Cfg<D, NT>::kQPitch + 2 * D)),
                    "l"(src)
@@ -245,8 +245,9 @@ __device__ __forceinline__ void fetch_query(const FwdArgs& a, const Part& p, uin
     const int row = p.rt * 8 * NT + col;
     uint8_t* dst = raw + col * Cfg<D, NT>::kQPitch + 16 * piece;
     if (row < p.r.qn * a.d.G) {
-      const __nv_bfloat16* src = a.q + (int64_t)(p.r.q0 + row / a.d.G) * a.q_stride +
-                                 (int64_t)(p.h * a.d.G + row % a.d.G) * D + 8 * piece;
+      const int tok = a.d.by_G(row);
+      const __nv_bfloat16* src = a.q + (int64_t)(p.r.q0 + tok) * a.q_stride +
+                                 (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D + 8 * piece;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
                    : "memory");
     } else {
@@ -311,7 +312,7 @@ __device__ __forceinline__ void prepare_query(const FwdArgs& a, const Part& p, c
       // (at most the largest fp32: 2^126 2^11 would be inf, and negative scores would read as masked)
       S.scale[col] = fminf(fmaxf(up * (16777216.f / 8192.f) * a.d.scale_log2, kLeastUnit), FLT_MAX);
       // columns beyond the rows see everything: nothing of them is written
-      const int ctx = p.r.kv - p.r.qn, tok = row / a.d.G;
+      const int ctx = p.r.kv - p.r.qn, tok = a.d.by_G(row);
       const bool on = row < p.r.qn * a.d.G;
       if constexpr (MASK) {
         uint32_t bits = 0xffffffffu >> (32 - p.r.qn);

@@ -179,8 +179,9 @@ __device__ __forceinline__ void store_out4(const FwdArgs& a, const Part& p, int 
                                            float4 o, float l) {
   if (row >= p.r.qn * a.d.G) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
-                       (int64_t)(p.h * a.d.G + row % a.d.G) * D + out_channel(i);
+  const int tok = a.d.by_G(row);
+  __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
+                       (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D + out_channel(i);
   const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
   const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
@@ -348,8 +349,9 @@ __global__ void __launch_bounds__(kJoinThreads, kCols > 16 ? 4 : 2)
     l = row_sum(m, __shfl_sync(~0u, l, 0));
     if constexpr (kCols > 16) {  // channels in their own order
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
-                           (int64_t)(p.h * a.d.G + row % a.d.G) * D + lane * kCh;
+      const int tok = a.d.by_G(row);
+      __nv_bfloat16* dst = a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
+                           (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D + lane * kCh;
       uint32_t x[kCh / 2];
 #pragma unroll
       for (int e = 0; e < kCh / 2; ++e) {

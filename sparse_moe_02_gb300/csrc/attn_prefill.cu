@@ -302,10 +302,10 @@ __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, i
     }
     p.rt = rt;
     const int last = min((rt + 1) * kRows, p.r.qn * a.d.G) - 1;
-    const int seen = MASK && a.masks ? p.r.kv : seen_by(p.r, last / a.d.G);
+    const int seen = MASK && a.masks ? p.r.kv : seen_by(p.r, a.d.by_G(last));
     p.tiles = (seen + kStep - 1) / kStep;
     if (MASK) {
-      p.skip = skipped<kStep>(a, tile_start(a, p.r, rt * kRows / a.d.G));
+      p.skip = skipped<kStep>(a, tile_start(a, p.r, a.d.by_G(rt * kRows)));
       p.tiles -= p.skip;
     }
     const int64_t end = at + c.template before<MASK>(rt + 1);
@@ -560,11 +560,11 @@ struct QueryRows {
   __device__ __forceinline__ void load(const FwdArgs& a, const Part& p, int row0, int8_t* exps) {
     const int lane = threadIdx.x & 31;
     // addresses of the eight rows, a lane each
-    const int row = p.rt * kRows + row0 + (lane & 7);
+    const int row = p.rt * kRows + row0 + (lane & 7), tok = a.d.by_G(row);
     const uint64_t own =
         row < p.r.qn * a.d.G
-            ? (uint64_t)(a.q + (int64_t)(p.r.q0 + row / a.d.G) * a.q_stride +
-                         (int64_t)(p.h * a.d.G + row % a.d.G) * D)
+            ? (uint64_t)(a.q + (int64_t)(p.r.q0 + tok) * a.q_stride +
+                         (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D)
             : 0;
 #pragma unroll
     for (int i = 0; i < 8 / kPer; ++i) {
@@ -1006,8 +1006,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           for (int q = 0; q < 2; ++q) {
             const int row = p.rt * kRows + row_of(u, q);
             if (row >= p.r.qn * a.d.G) continue;
-            __nv_bfloat16* d = a.out + (int64_t)(p.r.q0 + row / a.d.G) * a.out_stride +
-                               (int64_t)(p.h * a.d.G + row % a.d.G) * D + 64 * (u >> 1) + 16 * c;
+            const int tok = a.d.by_G(row);
+            __nv_bfloat16* d = a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
+                               (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D + 64 * (u >> 1) + 16 * c;
             const uint32_t(&y)[8] = x[j][q];
             if (sectors) {
               st_global_v8(d, y);
@@ -1145,17 +1146,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (!p.some) break;
       const int row0 = p.rt * kRows + warp * 32;  // the warp's first row
       const int rows_left = p.r.qn * a.d.G;
-      const int row = row0 + lane, tok = row / a.d.G;
+      const int row = row0 + lane, tok = a.d.by_G(row);
       const bool on = row < rows_left;
       int lim = on ? seen_by(p.r, tok) : p.r.kv;
-      int least = seen_by(p.r, p.rt * kRows / a.d.G);
+      int least = seen_by(p.r, a.d.by_G(p.rt * kRows));
       // with masks: tokens from `low` on lie in every window of the row tile
       int low = INT_MIN;
       RowView view(a, p, tok, MASK && on);
       if constexpr (MASK) {
         lim = 0;  // (tokens seen so far, of this part: whether there are any)
         if (a.masks) least = p.r.kv - p.r.qn;
-        const int last = p.r.kv - p.r.qn + (p.rt + 1) * kRows / a.d.G;  // or behind the row tile's
+        // (or behind the row tile's last token)
+        const int last = p.r.kv - p.r.qn + a.d.by_G((p.rt + 1) * kRows);
         low = window_start(a, a.masks ? p.r.kv - 1 : min(p.r.kv - 1, last));
       }
       float m = -INFINITY, l = 0.f, unit = 0.f, most_ev = -INFINITY;
@@ -1272,7 +1274,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (p.tiles == 0) {  // rows that see nothing
         const uint64_t own =
             on ? reinterpret_cast<uint64_t>(a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
-                                            (int64_t)(p.h * a.d.G + row % a.d.G) * D)
+                                            (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D)
                : 0;
         for (int i = lane; i < 32 * (D / 8); i += 32) {
           const uint64_t dst = __shfl_sync(~0u, own, i / (D / 8));

@@ -531,22 +531,6 @@ __device__ __forceinline__ uint4 turn_query(const RopeArgs& a, uint4 raw, const 
   return QueryPiece<INTER>::words(r);
 }
 
-// Division of numbers below 2^31 by d, 1 <= d <= 2^20: a product and a shift (a division takes some twenty
-// instructions, a row of 128 channels some hundred).  With 2^(l-1) < d <= 2^l and m = 2^(31+l) / d rounded up
-// (above it by less than 1), n m / 2^(31+l) lies above n / d by less than n / 2^(31+l) < 1 / d.
-struct Divide {
-  uint32_t m, shift;
-  explicit Divide(uint32_t d) {
-    uint32_t l = 0;
-    while ((1u << l) < d) ++l;
-    shift = 31 + l;
-    m = (uint32_t)(((1ull << shift) + d - 1) / d);
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-    return (uint32_t)((uint64_t)n * m >> shift);
-  }
-};
-
 // How the blocks of attn_rope_append_kernel share the work.
 struct Shares {
   int heads_per;     // neighbouring query heads of a token that a group of lanes takes
