@@ -213,9 +213,9 @@ int attn_qk_norm_rope_append(attn_handle h, const void* q, int64_t q_stride, con
  *               kv_b - n_b plus the number of drafted tokens that it sees besides one (itself).
  *               max_q_len is at most 256 and 32 mask_words, and at most W if there is a window (so a
  *               window never hides drafted tokens).
- * A query that sees no token gives 0.  Pages that hold no token which any query of the request sees are
- * not read: their entries of block_table may be anything, such as those of pages given back
- * behind a window. */
+ * A query that sees no token gives 0.  Pages that lie between the first tokens and every window of their
+ * request are not read: their entries of block_table may be anything, such as those of pages given
+ * back. */
 int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, const void* cache,
                             const int32_t* block_table, int table_width, const int32_t* q_offsets,
                             const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
@@ -228,8 +228,9 @@ int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, cons
  *   paths [B][path_width] int32   accepted tokens by their index in their request, ascending; the
  *                            entries behind path_lens[b] are not read
  *   path_lens [B] int32      0 .. path_width
- * Rows behind the accepted ones keep what they hold.  Requests share none of the pages that they move
- * rows in.  A length out of range moves nothing, an entry that is negative or not above the one
+ * Rows behind the accepted ones keep what they hold.  attn_plan counts a request's pages from its ctx_lens:
+ * pages taken for rejected tokens alone are the caller's to put back on its free list, or they are
+ * replaced in the table by new ones.  Requests share none of the pages that they move rows in.  A length out of range moves nothing, an entry that is negative or not above the one
  * before it, or a row outside the table or the cache, is left out (MOE_ERR_DEVICE; the request's moved
  * rows are then undefined). */
 int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int table_width,

@@ -397,3 +397,52 @@ def test_long_contexts_through_a_window(L, window, sinks):
         s.check(got, ref)
         rel = ((got.double() - ref).square().sum() / ref.square().sum()).sqrt().item()
         assert rel < 2.0 ** -8, rel
+
+
+@pytest.mark.parametrize("kw", [dict(window=40, sinks=3), dict(tree=True), dict(window=128, tree=True)])
+@pytest.mark.parametrize("new,kv", [([1, 1, 2, 4], [0, 90, 0, 60]), ([30, 1, 100, 60], [0, 90, 0, 500])])
+def test_refused_requests_read_as_zeros(kw, new, kv):
+    kw = dict(kw)
+    rng = random.Random(9)
+    seen = [drafted(n, rng) for n in new] if kw.pop("tree", False) else None
+    s = View(16, 2, 256, 16, new, kv, seed=18, seen=seen, **kw)
+    s.table[0] = s.table[2] = -1
+    got = s.forward()
+    s.check(got)
+    for b in (0, 2):
+        first = sum(new[:b])
+        assert not got[first:first + new[b]].any()
+
+
+@pytest.mark.parametrize("window,sinks", [(300, 5), (0, 0)])
+def test_two_objects_at_once_on_two_streams(window, sinks):
+    import torch
+    rng = random.Random(2)
+    new, kv = [40, 3, 200], [700, 900, 1200]
+    seen = None if window else [drafted(n, rng) for n in new]
+    sides = [View(Hq, Hkv, D, 16, new, kv, seed=i, window=window, sinks=sinks, seen=seen)
+             for i, (Hq, Hkv, D) in enumerate(((16, 2, 256), (32, 8, 128)))]
+    want = [s.forward() for s in sides]
+    streams = [torch.cuda.Stream() for _ in sides]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for s, stream in zip(sides, streams):
+            got.append(s.forward(stream=stream))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 2])
+    for s in sides:
+        assert s.attn.device_error() == moe.MOE_OK
+
+
+def test_capacities_in_place_of_lengths():
+    # bounds that are far above the lengths, as a captured step gives them
+    rng = random.Random(3)
+    new, kv = [3, 1, 2], [90, 200, 17]
+    for kw in (dict(window=60, sinks=2), dict(seen=[drafted(n, rng) for n in new], words=8),
+               dict(window=300, sinks=2, seen=[drafted(n, rng) for n in new], words=8)):
+        s = View(16, 2, 256, 16, new, kv, seed=19, **kw)
+        for q, k in ((3, 200), (4, 1 << 30), (256, 1 << 30)):
+            if s.masks is not None or q < 256:
+                s.check(s.forward(max_q_len=q, max_kv_len=k))

@@ -438,3 +438,95 @@ def test_arguments_are_refused_on_the_host():
     assert rope(rot=40) == UNS and rope(rot=272) == UNS and rope(T=(1 << 20) + 1) == UNS
     assert rope(ks=504) == INV and rope(vs=516) == ALI and rope(qos=4104, q=A + 8) == ALI
     attn.close()
+
+
+def test_a_step_with_drafts_as_one_graph():
+    """Plan of the trees, one-pass append, attention and acceptance, captured once and replayed on other
+    inputs in the same tensors."""
+    import torch
+    Hq, Hkv, D, P, B, n = 16, 2, 256, 16, 3, 6
+    ctx = [40, 5, 90]
+    width = 8
+    attn = moe.PagedAttention(Hq, Hkv, D, P, B * width, B)
+    cache = attn.new_cache()
+    table = torch.randperm(B * width, generator=gen(1), device=DEV).int().view(B, width)
+    slots = torch.cat([(table[b].long()[torch.arange(c, c + n, device=DEV) // P] * P
+                        + torch.arange(c, c + n, device=DEV) % P).int() for b, c in enumerate(ctx)])
+    every = torch.arange(B * width * P, device=DEV).int()
+    g = gen(2)
+    k0, v0 = (randn(g, len(every), Hkv, D).bfloat16() for _ in range(2))
+    offs, kv = ints([0, n, 2 * n, 3 * n]), ints([c + n for c in ctx])
+    w = (1 + 0.1 * randn(g, D)).bfloat16()
+    turns = cos_sin_table(200, 64)
+    x = torch.empty(B * n, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    parents, paths, lens = ints([0] * (B * n)), ints([[0] * n] * B), ints([0] * B)
+
+    def step():
+        pos, masks = attn.tree_plan(parents, offs, kv, n)
+        q = attn.qk_norm_rope_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pos, slots, w, w,
+                                     turns, cache)
+        out = attn.forward(q, cache, table, offs, kv, n, 1000, window=64, sinks=2, masks=masks)
+        attn.accept(cache, table, ints_ctx, paths, lens)
+        return out
+
+    ints_ctx = ints(ctx)
+
+    def fill(seed):
+        rng = random.Random(seed)
+        trees = [tree(n, rng) for _ in range(B)]
+        attn.append(k0, v0, every, cache)
+        x.copy_(randn(gen(seed), *x.shape))
+        parents.copy_(ints(sum(trees, [])))
+        chosen = []
+        for t in trees:
+            node, path = rng.randrange(n), []
+            while node >= 0:
+                path.insert(0, node)
+                node = t[node]
+            chosen.append(path)
+        paths.copy_(ints([p + [0] * (n - len(p)) for p in chosen]))
+        lens.copy_(ints([len(p) for p in chosen]))
+
+    fill(3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (4, 5, 6):
+        fill(seed)
+        want = step().clone()
+        rows = cache.data.clone()
+        fill(seed)
+        graph.replay()
+        assert torch.equal(out, want) and bool(want.any())
+        assert torch.equal(cache.data, rows)
+    assert attn.device_error() == moe.MOE_OK
+    attn.close()
+
+
+def test_an_entry_twice_and_a_path_that_falls_are_recorded():
+    import torch
+    attn = moe.PagedAttention(8, 4, 128, 16, 4, 1)
+    cache = attn.new_cache()
+    table = ints([[0, 1, 2, 3]])
+    for path in ([1, 1, 2], [2, 1], [0, 3, 3]):
+        attn.accept(cache, table, ints([5]), ints([path]), ints([len(path)]))
+        assert attn.device_error() == moe.MOE_ERR_DEVICE
+    attn.accept(cache, table, ints([5]), ints([[0, 1, 2]]), ints([0]))
+    assert attn.device_error() == moe.MOE_OK
+    # nothing to do: no requests, no tokens
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    attn.accept(cache, none.view(0, 4), none, none.view(0, 3), none)
+    rows = torch.empty(0, 8, 128, dtype=torch.bfloat16, device=DEV)
+    keys = rows[:, :4]
+    got = attn.qk_norm_rope_append(rows, keys, keys, none, none, None, None, cos_sin_table(4, 16),
+                                   cache)
+    assert got.shape == (0, 8, 128)
+    pos, masks = attn.tree_plan(none, ints([0, 0]), ints([3]), 1)
+    assert pos.numel() == 0 and masks.shape == (0, 1)
+    assert attn.device_error() == moe.MOE_OK
+    attn.close()
