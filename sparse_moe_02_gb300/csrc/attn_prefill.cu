@@ -576,9 +576,12 @@ struct QueryRows {
     for (int i = 0; i < 8 / kPer; ++i) {
       uint32_t top = max_u16x2(max_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
                                max_u16x2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+      if constexpr (kL < 32) {
 #pragma unroll
-      for (int o = kL / 2; o; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(~0u, top, o));
+        for (int o = kL / 2; o; o >>= 1) top = max_u16x2(top, __shfl_xor_sync(~0u, top, o));
+      }
       top = max(top & 0xffffu, top >> 16);
+      if constexpr (kL == 32) top = __reduce_max_sync(~0u, top);
       const int e = min(max((int)(top >> 7) - 127, -100), 126);
       const float down = pow2(-e) * 8192.f;
       if (lane % kL == 0)
