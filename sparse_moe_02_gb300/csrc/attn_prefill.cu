@@ -147,13 +147,6 @@ __device__ __forceinline__ void wait_ld32(uint32_t* r) {
                  "+r"(r[30]), "+r"(r[31]));
 }
 
-__device__ __forceinline__ void wait_ld16(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-
 // 16 lanes x 8 columns: thread (n, c) = (i / 4, i % 4) of the warp gets columns 2c, 2c + 1 of lane n
 // (r[0], r[1]) and of lane n + 8 (r[2], r[3]).
 __device__ __forceinline__ void tmem_ld_16x8(uint32_t taddr, uint32_t* r) {
@@ -951,103 +944,76 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     const bool is_key = warp < kValueWarp;
     const int oct = warp - (is_key ? kKeyWarp : kValueWarp);
     Dequant<D> d;
-    // Outputs of part k, the kq-th with steps, from tensor memory: 16 rows of a group at a time (a unit), four
+    // Outputs of part k, the kq-th with steps, from tensor memory: 16 rows of a group at a time, four
     // warps to the 32 lanes that each of them may read.
     auto outputs = [&](int k, int kq) {
-      constexpr int kUnits = (NG + 1) / 2;  // of a warp
-      const int quarter = warp & 3, c = lane & 3, u0 = (warp - kKeyWarp) >> 2;
+      const int quarter = warp & 3;
       bool go = mbar_wait(&bars.o_done, kq & 1, a.err) &&
                 mbar_wait(&bars.o_scaled[kq & 1], (kq >> 1) & 1, a.err);
       go = __all_sync(~0u, go);
       if (!go) return false;
       tc_fence_after();
       const Part& p = parts[k % kParts];
-      // nibbles i0 .. i0 + 3 of unit u: [nibble][row n words 2c, 2c + 1; row n + 8 words 2c, 2c + 1], n the
-      // lane's row of its 16
-      auto load4 = [&](int u, int i0, uint32_t (&o)[4][4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          tmem_ld_16x8(tmem + ((uint32_t)(32 * quarter + 16 * (u & 1)) << 16) +
-                           out_column<NG>(u >> 1, i0 + i),
-                       o[i]);
-        wait_ld16(&o[0][0]);
-      };
-      auto row_of = [&](int u, int q) { return 32 * quarter + 16 * (u & 1) + (lane >> 2) + 8 * q; };
-      if (p.t1 - p.t0 == p.tiles) {
-        // rounded first, so that the next part's products need not wait for the stores
-        uint32_t x[kUnits][2][8];  // words 2c and 2c + 1 of both rows, eight channels each
-#pragma unroll
-        for (int j = 0; j < kUnits; ++j) {
-          const int u = u0 + 4 * j;
-          if (u >= 2 * NG) break;
-          const float f[2] = {out_scale[kq & 1][row_of(u, 0)], out_scale[kq & 1][row_of(u, 1)]};
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t o[4][4];
-            load4(u, 4 * hf, o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {  // (row, word, pair of nibbles)
-              const int q = i >> 2, w = (i >> 1) & 1, m = i & 1;
-              const __nv_bfloat162 y =
-                  __floats2bfloat162_rn(__uint_as_float(o[2 * m][2 * q + w]) * f[q],
-                                        __uint_as_float(o[2 * m + 1][2 * q + w]) * f[q]);
-              x[j][q][4 * w + 2 * hf + m] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.o_free);
-        // (rows of outputs are only known to start on 16 bytes)
-        const bool sectors =
-            ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(2 * a.out_stride)) & 31) == 0;
-#pragma unroll
-        for (int j = 0; j < kUnits; ++j) {
-          const int u = u0 + 4 * j;
-          if (u >= 2 * NG) break;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int row = p.rt * kRows + row_of(u, q);
-            if (row >= p.r.qn * a.d.G) continue;
-            const int tok = a.d.by_G(row);
-            __nv_bfloat16* d = a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
-                               (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D + 64 * (u >> 1) + 16 * c;
-            const uint32_t(&y)[8] = x[j][q];
-            if (sectors) {
-              st_global_v8(d, y);
-            } else {
-              reinterpret_cast<uint4*>(d)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-              reinterpret_cast<uint4*>(d)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) part_read(k);
-      } else {
-        float* part = a.part_o + (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows * D;
+      const bool whole = p.t1 - p.t0 == p.tiles;
+      const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows;
+      const int c = lane & 3;
+      // (rows of outputs are only known to start on 16 bytes)
+      const bool sectors = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(2 * a.out_stride)) & 31) == 0;
 #pragma unroll 1
-        for (int u = u0; u < 2 * NG; u += 4) {
-          uint32_t o[8][4];
-          load4(u, 0, *reinterpret_cast<uint32_t(*)[4][4]>(&o[0]));
-          load4(u, 4, *reinterpret_cast<uint32_t(*)[4][4]>(&o[4]));
+      for (int u = (warp - kKeyWarp) >> 2; u < 2 * NG; u += 4) {
+        const int hf = u & 1, g = u >> 1;
+        const int ra = 32 * quarter + 16 * hf + (lane >> 2);
+        // [nibble][row ra words 2c, 2c + 1; row ra + 8 words 2c, 2c + 1]
+        uint32_t o[8][4];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int r = row_of(u, q);
-            const float f = out_scale[kq & 1][r];
+        for (int i = 0; i < 8; ++i)
+          tmem_ld_16x8(tmem + ((uint32_t)(32 * quarter + 16 * hf) << 16) + out_column<NG>(g, i),
+                       o[i]);
+        wait_ld32(&o[0][0]);
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          const int r = ra + 4 * q, row = p.rt * kRows + r;
+          const float f = out_scale[kq & 1][r];
+          uint8_t* d = nullptr;
+          if (!whole) {
+            d = reinterpret_cast<uint8_t*>(a.part_o + (at + r) * D);
+          } else if (row < p.r.qn * a.d.G) {
+            const int tok = a.d.by_G(row);
+            d = reinterpret_cast<uint8_t*>(a.out + (int64_t)(p.r.q0 + tok) * a.out_stride +
+                                           (int64_t)(p.h * a.d.G + row - tok * a.d.G) * D);
+          }
+          if (whole) {
+            uint32_t x[8];  // words 2c and 2c + 1, eight channels each
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int w = i / 4, m = 2 * (i % 4);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[m][q + w]) * f,
+                                                             __uint_as_float(o[m + 1][q + w]) * f);
+              x[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            if (d) {
+              d += 128 * g + 32 * c;
+              if (sectors) {
+                st_global_v8(d, x);
+              } else {
+                reinterpret_cast<uint4*>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<uint4*>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+              }
+            }
+          } else {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               uint32_t v[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                v[i] = __float_as_uint(__uint_as_float(o[i][2 * q + w]) * f);
-              st_global_v8(part + r * D + 64 * (u >> 1) + 16 * c + 8 * w, v);
+              for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(o[i][q + w]) * f);
+              st_global_v8(d + 256 * g + 64 * c + 32 * w, v);
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.o_free), part_read(k);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.o_free), part_read(k);
       return true;
     };
     int due = -1, kq = 0;  // the part whose outputs are to be written; parts with steps so far
@@ -1091,19 +1057,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
         if (!ok) break;
       }
-      const int steps = some && !prepared ? p.t1 - p.t0 : 0;
+      if (due >= 0 && !(ok = outputs(due, kq - 1))) break;
+      due = -1;
+      if (!p.some) break;
+      if (!some) {
+        __syncwarp();
+        if (lane == 0) part_read(k);
+        continue;
+      }
+      due = k;
+      ++kq;
+      if (prepared) continue;  // (steps are counted by those who use them)
+      const int t0 = p.t0, t1 = p.t1, skip = MASK ? p.skip : 0;
       const Unread<MASK> un(a, p.r);
-      for (int t = 0;; ++t) {
-        // The outputs of the part before, behind the steps whose operands fit beside its last ones: the
-        // next product of values needs room that the first one frees, and that waits for them.
-        if (due >= 0 && (t == C::kOpsV || t == steps)) {
-          if (!(ok = outputs(due, kq - 1))) break;
-          due = -1;
-        }
-        if (t == steps) break;
+      for (int t = t0; t < t1; ++t, ++n) {
         const int which = is_key ? 0 : 1, ring = is_key ? C::kRawK : C::kRawV;
         const int st = n % ring;
-        const int tok = tile_at<MASK, kStep>(a, p.t0 + t, p.skip) * kStep + 8 * oct;
+        const int tok = tile_at<MASK, kStep>(a, t, skip) * kStep + 8 * oct;
         ok = mbar_wait(&bars.raw_full[which][st], (n / ring) & 1, a.err);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
@@ -1125,15 +1095,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(is_key ? &bars.k_full[op] : &bars.v_full[op]);
-        ++n;  // (steps of prepared parts are counted by those who use them)
-      }
-      if (!ok || !p.some) break;
-      if (some) {
-        due = k;
-        ++kq;
-      } else {
-        __syncwarp();
-        if (lane == 0) part_read(k);
       }
     }
   } else {
