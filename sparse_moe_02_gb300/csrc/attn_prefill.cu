@@ -46,6 +46,7 @@
 // in the few-row kernel; shared row tiles are joined by its second launch.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "attn_join.cuh"
@@ -1070,32 +1071,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (prepared) continue;  // (steps are counted by those who use them)
       const int t0 = p.t0, t1 = p.t1, skip = MASK ? p.skip : 0;
       const Unread<MASK> un(a, p.r);
-      for (int t = t0; t < t1; ++t, ++n) {
-        const int which = is_key ? 0 : 1, ring = is_key ? C::kRawK : C::kRawV;
-        const int st = n % ring;
-        const int tok = tile_at<MASK, kStep>(a, t, skip) * kStep + 8 * oct;
-        ok = mbar_wait(&bars.raw_full[which][st], (n / ring) & 1, a.err);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        if (is_key)
-          d.keys(ops + C::kOffRaw + st * kRecs * C::kSideK, oct, tok, un,
-                 &exps[n % kExps][oct >> 1]);
-        else  // (a value side begins with its parameters: R::kVp from where the record would)
-          d.values(ops + C::kOffRawV + st * kRecs * C::kSideV - C::R::kVp, tables[oct], oct, tok,
-                   un, &exps[n % kExps][oct >> 1], &bars.ev_full[n % kExps]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.raw_empty[which][st]);
-        const int op = is_key ? n % C::kOpsK : n % C::kOpsV;
-        const int turn = is_key ? n / C::kOpsK : n / C::kOpsV;
-        ok = mbar_wait(is_key ? &bars.k_empty[op] : &bars.v_empty[op], (turn & 1) ^ 1, a.err);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        if (is_key) d.store_keys(ops + C::kOffK + op * C::kK, oct);
-        else d.store_values(ops + C::kOffV + op * C::kK, oct);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(is_key ? &bars.k_full[op] : &bars.v_full[op]);
-      }
+      auto steps = [&](auto keys) {  // a loop for the keys' warps, one for the values'
+        constexpr bool kKeys = decltype(keys)::value;
+        constexpr int kRing = kKeys ? C::kRawK : C::kRawV, kOps = kKeys ? C::kOpsK : C::kOpsV;
+        for (int t = t0; t < t1; ++t, ++n) {
+          const int st = n % kRing, op = n % kOps;
+          const int tok = tile_at<MASK, kStep>(a, t, skip) * kStep + 8 * oct;
+          ok = mbar_wait(&bars.raw_full[!kKeys][st], (n / kRing) & 1, a.err);
+          ok = __all_sync(~0u, ok);
+          if (!ok) return;
+          Exps* ex = &exps[n % kExps][oct >> 1];
+          if constexpr (kKeys)
+            d.keys(ops + C::kOffRaw + st * kRecs * C::kSideK, oct, tok, un, ex);
+          else  // (a value side begins with its parameters: R::kVp from where the record would)
+            d.values(ops + C::kOffRawV + st * kRecs * C::kSideV - C::R::kVp, tables[oct], oct, tok, un,
+                     ex, &bars.ev_full[n % kExps]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.raw_empty[!kKeys][st]);
+          ok = mbar_wait(kKeys ? &bars.k_empty[op] : &bars.v_empty[op], ((n / kOps) & 1) ^ 1, a.err);
+          ok = __all_sync(~0u, ok);
+          if (!ok) return;
+          if constexpr (kKeys) d.store_keys(ops + C::kOffK + op * C::kK, oct);
+          else d.store_values(ops + C::kOffV + op * C::kK, oct);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kKeys ? &bars.k_full[op] : &bars.v_full[op]);
+        }
+      };
+      if (is_key) steps(std::true_type());
+      else steps(std::false_type());
     }
   } else {
     registers_up<kRegsSoft>();
