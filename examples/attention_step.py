@@ -3,7 +3,7 @@
 A batch of requests with ragged prompts runs through the layer: one step for the prompts, then a
 step per generated token, the latter as one CUDA graph that is replayed.  Each step is
 
-    plan -> projections -> norm and rotation -> append to the 4-bit cache -> attention
+    plan -> projections -> norm, rotation and append to the 4-bit cache -> attention
          -> output projection -> MoE FFN
 
 The layer's shapes are those of the model (16 query heads over 2 key/value heads of 256 channels,
@@ -78,9 +78,9 @@ class Layer:
         offsets, kv_lens, positions, slots, _ = self.attention.plan(
             self.table, ctx_lens, new_lens, self.free, self.cursor, T=qkv.shape[0],
             cursor_out=self.cursor)
-        q, k = self.attention.qk_norm_rope(qkv[:, :HQ], qkv[:, HQ:HQ + HKV], positions,
-                                           self.q_weight, self.k_weight, self.cos_sin)
-        self.attention.append(k, qkv[:, HQ + HKV:], slots, self.cache)
+        q = self.attention.qk_norm_rope_append(qkv[:, :HQ], qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:],
+                                               positions, slots, self.q_weight, self.k_weight,
+                                               self.cos_sin, self.cache)
         return self.attention.forward(q, self.cache, self.table, offsets, kv_lens, max_new,
                                       self.max_kv)
 

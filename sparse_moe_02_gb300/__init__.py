@@ -453,7 +453,8 @@ class PagedAttention:
 
     One object serves every layer of the same shape; each layer has a cache of its own
     (new_cache).  Queries, keys, values and outputs are bf16 [T][heads][head_dim], rows may be
-    strided (views of a fused projection's output).  Calls are enqueued on the current stream, or
+    strided (views of a fused projection's output).  tree_plan, qk_norm_rope_append, forward with a
+    window or masks, and accept serve drafted trees and window layers.  Calls are enqueued on the current stream, or
     on `stream`.  Outputs not given are allocated as memory of that stream: another one that uses
     them waits for it first, and has them recorded (Tensor.record_stream) if they may be freed
     before it is done.  The object belongs to the device that was current when it was made: tensors

@@ -111,9 +111,9 @@ struct Part {
   bool some;
 };
 
-// Narrower views (attn_kv4_forward_masked).  A kernel goes over the tiles (of kTile tokens) that hold the
-// first tokens and those from the first token of a window on: tile i of them is tile i of the context,
-// or, behind the first tokens, i + skip.
+// Narrower views (attn_kv4_forward_masked).  A kernel goes over the tiles (of kTile tokens) that hold
+// the first tokens and those from the first token of a window on: tile i of them is tile i of the
+// context, or, behind the first tokens, i + skip.
 
 // First token of the window of a query at position pos.
 __device__ __forceinline__ int window_start(const FwdArgs& a, int pos) {
@@ -169,8 +169,8 @@ __device__ __forceinline__ float row_sum(float m, float l) {
   return m != -INFINITY && fabsf(m) >= 268435456.f ? NAN : l;  // 2^28
 }
 
-// The few-row kernel's outputs are joined in the order in which its lanes hold them: float4 i of a column
-// is channels out_channel(i) .. + 3.
+// The few-row kernel's outputs are joined in the order in which its lanes hold them: float4 i of a
+// column is channels out_channel(i) .. + 3.
 __device__ __forceinline__ int out_channel(int i) {
   return (i >> 4) * 64 + (i & 7) * 8 + ((i >> 3) & 1) * 4;
 }

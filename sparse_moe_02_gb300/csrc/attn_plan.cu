@@ -149,11 +149,11 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(PlanArgs a) {
   }
 }
 
-// attn_tree_plan: a block per request, a thread per drafted token, which holds its mask (itself at first)
-// and a forebear (its parent at first).  A round adds the forebear's mask to its own and takes the
-// forebear's forebear: the path that a mask covers doubles, so a tree of depth d takes log2 d rounds (walks
-// of d steps took 7.2 us for 256 trees of up to 64 tokens, this takes 2.2, a launch, as one tree does).  Depths are the masks' counts.  Bound by
-// latency: offsets, then parents, then the rounds.
+// attn_tree_plan: a block per request, a thread per drafted token, which holds its mask (itself at
+// first) and a forebear (its parent at first).  A round adds the forebear's mask to its own and takes the
+// forebear's forebear: the path that a mask covers doubles, so a tree of depth d takes log2 d rounds
+// (walks of d steps took 7.2 us for 256 trees of up to 64 tokens; this takes 2.1, a launch, as one tree
+// does).  Depths are the masks' counts.  Bound by latency: offsets, then parents, then the rounds.
 template <int W>
 __global__ void __launch_bounds__(kMaxDrafts) attn_tree_plan_kernel(TreeArgs a) {
   __shared__ int forebear[2][kMaxDrafts];

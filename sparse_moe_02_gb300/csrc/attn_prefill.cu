@@ -1,5 +1,5 @@
 // Attention of many query rows over the paged 4-bit cache (include/attn.h): prompts, chunks of
-// prompts, and batches that hold any of them, on the tcgen05 tensor cores.
+// prompts, wide trees of drafted tokens, and batches that hold any of them, on the tcgen05 tensor cores.
 //
 // A block works on 128 query rows of one key/value head (row = new token * G + query head) in steps
 // of 64 cached tokens.  Four warps hold the softmax (a thread per row); eight turn cached keys and
@@ -14,8 +14,8 @@
 // descriptors that are formed once and stepped by constants in uniform registers: issued from one
 // thread's branch, the second case below took 957 us instead of 767.
 //
-// Every 128 rows of a head read the same context, and turning it into operands takes 2800 clocks a
-// step (16 warps, two thirds of the block's issue slots), twice the MMAs.  So where contexts are read
+// Every 128 rows of a head read the same context, and turning it into operands takes 2300 clocks a
+// step (16 warps, two thirds of the block's issue slots), nearly twice the MMAs.  So where contexts are read
 // by many row tiles (kPrepTiles) a first launch, attn_prepare_kernel, forms the operands of every
 // step once, in the handle's workspace, and this kernel copies them (64 KB a step from L2, 580 to 890
 // clocks with all SMs at it) while its dequantising warps only stage queries and write outputs.  A
@@ -23,11 +23,21 @@
 // lie where the next scores go (a third score buffer, with half of Q in shared memory, was no
 // faster).
 //
-// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 149 us (920 TFLOP/s,
+// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 138 us (990 TFLOP/s,
 // prepared; 209 us if not), 2048 over a context of 30000 755 us (1.37 PFLOP/s, 71% of a bf16 product's
-// rate; 1100 us); 4096 tokens of 32 heads over 8 of 128 channels 186 us (281), over 4 of 64 channels
-// 168 us (237); 7 ragged chunks and prompts of 28 heads over 4 of 128 85 us (106).  Of the 149 us the
-// prepare launch takes 8, start and tail of the blocks and the joins 20.
+// rate; 990 us); 4096 tokens of 32 heads over 8 of 128 channels 177 us, over 4 of 64 channels 162 us; 7
+// ragged chunks and prompts of 28 heads over 4 of 128 77 us.  Of the 138 us the prepare launch takes 8,
+// start and tail of the blocks and the joins 20.
+//
+// The form with masks (MASK) has the same steps over fewer of the context's tokens: the steps of the first
+// tokens and those from a row tile's first window on.  A row's visible tokens of a step are 64 bits, formed
+// only where a step holds a window's start, the first tokens' end or drafted tokens; of a wide tree all
+// steps before the drafted ones need none.  Measured, 256 channels: a prompt of 8192 through a window of
+// 1024 167 us (787 TFLOP/s of the visible pairs: a row tile's 18 steps touch 1152 tokens for the 1040 that a
+// row sees, and each of its 7 to a block costs some 5000 clocks besides, the change of queries and
+// outputs), 16 trees of 20 to 60 tokens over contexts to 16384 59 us, 32 of 8 to 31 through a window of 1024
+// 34 us: 5 steps a block, and around them the launch, the cut and the first row tile found (9000
+// clocks), its queries (8000), the first operands and scores (5000), outputs (5000) and the join.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -43,7 +53,8 @@
 // values of a group or a token do beside others that are 2^20 times as large and count.
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
-// in the few-row kernel; shared row tiles are joined by its second launch.
+// in the few-row kernel; shared row tiles are joined by its second launch.  Behind a window row tiles cost
+// alike and blocks may take whole ones (kWholeMore).
 #include <algorithm>
 #include <climits>
 #include <type_traits>

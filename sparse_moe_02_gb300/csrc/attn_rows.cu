@@ -1,6 +1,6 @@
 // The row kernels of the attention step (include/attn.h): norm and rotation of query and key
-// heads, quantisation of keys and values into the paged 4-bit cache, and the way back.  Each is
-// one pass over its rows, bound by launch latency for single tokens and for prompts as stated at each
+// heads, quantisation of keys and values into the paged 4-bit cache, both in one, accepted rows moved, and
+// the way back.  Each is one pass over its rows, bound by launch latency for single tokens and for prompts as stated at each
 // (by loads that wait for one another, append by instruction issue): a lane holds 8 channels (one
 // 16-byte load), the D / 8 lanes of a row reduce by shuffles.
 #include "attn.cuh"
@@ -317,10 +317,10 @@ __device__ __forceinline__ void write_rows(const RowsArgs& a, int slot, int h, i
 // A group of L = D / 8 lanes per (token, head): key row and value row together, since a
 // non-finite channel of either marks both.
 //
-// Bound by instruction issue for prompts (444 warp instructions a row and head, 80% of the slots): the
+// Bound by instruction issue for prompts (370 warp instructions a row and head, 72% of the slots): the
 // fp32 quotient of the definition would be 16 divisions a lane, so the reciprocal decides where it
-// provably rounds to the same code.  Measured: 32768 tokens, 2 heads of 256 channels, 34 us (2.5 TB/s)
-// with cold caches, their reading 20 us (4.2 TB/s), both in turn 47 us; 48 tokens 3.9 us for both.
+// provably rounds to the same code.  Measured: 32768 tokens, 2 heads of 256 channels, 27 us (3.1 TB/s),
+// their reading 16 us (5.3 TB/s), both in turn 46 us; 48 tokens 4.0 us for both.
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_append_kernel(RowsArgs a) {
   constexpr int L = D / 8;
@@ -543,6 +543,14 @@ struct Shares {
 // value row each group, the others heads_per neighbouring query heads of a token, as in the norm and
 // rotation alone; both kinds evenly mixed, since the first is bound by instruction issue and the second by
 // memory.
+//
+// Bound by instruction issue for prompts (68% of the slots, DRAM at 4.4 TB/s): a warp takes 87 instructions
+// a query row of two (128 channels), 500 for two key and value rows, of which the exact sum and root are 110
+// and the codes 300.  Measured: 16381 tokens, 32 query and 8 key/value heads of 128 channels 75 us with
+// neighbouring pairs, 80 with halves (the norm and rotation, then the append: 108 and 128), 16 and 2 of 256
+// 64 and 68 us; 48 tokens 2.9 us.  Steps of the way there: key and value blocks first 115 us, four query
+// heads a group and four blocks an SM instead of eight and three 96, products in place of divisions 86, five
+// blocks an SM 77, a rotation's pairs of a query in one lane 75 (halves: 101 to 80).
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads, 5) attn_rope_append_kernel(RopeArgs r, RowsArgs a,
                                                                     Shares n) {
@@ -617,7 +625,8 @@ __device__ __forceinline__ int64_t slot_of(const AcceptArgs& p, const RowsArgs& 
 
 // A block per request and head, L = D / 8 lanes per accepted row, kThreads / L rows at a time: all are
 // read before any is written.  Entry i of an ascending path is i at least, so no row is written before
-// a later round reads it.  Bound by latency: lengths, path and table, rows, one after another.
+// a later round reads it.  Bound by latency: lengths, path and table, rows, one after another (with its
+// reading back, 64 requests of up to 12 accepted tokens, 2 heads of 256 channels: 4.4 us, two launches).
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_accept_kernel(AcceptArgs p, RowsArgs a) {
   using R = Record<D>;
