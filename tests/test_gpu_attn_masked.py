@@ -446,3 +446,22 @@ def test_capacities_in_place_of_lengths():
         for q, k in ((3, 200), (4, 1 << 30), (256, 1 << 30)):
             if s.masks is not None or q < 256:
                 s.check(s.forward(max_q_len=q, max_kv_len=k))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 256), (28, 4, 128), (32, 4, 64)])
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("new,kv", [([1, 2], [300, 90]), ([70, 200], [700, 200]), ([1500], [1600])])
+def test_output_rows_on_sixteen_bytes(Hq, Hkv, D, window, new, kv):
+    # rows that start on 16 bytes but not on 32, as an odd number of eights in the stride gives them
+    import torch
+    s = View(Hq, Hkv, D, 16, new, kv, seed=20, window=window, sinks=3)
+    want = s.forward()
+    s.check(want)
+    width = Hq * D
+    for shift, more in ((8, 0), (0, 8), (8, 24)):
+        wide = torch.full((s.T, width + 8 + shift + more), 3.0, dtype=torch.bfloat16, device=DEV)
+        out = wide[:, shift:shift + width].unflatten(1, (Hq, D))
+        s.forward(out=out)
+        assert torch.equal(out, want)
+        wide[:, shift:shift + width] = 3.0
+        assert bool((wide == 3.0).all())
