@@ -687,7 +687,8 @@ class PagedAttention:
         T, B = parents.numel(), kv_lens.numel()
         positions = self._new(T, self._i32, stream) if positions is None else positions
         if masks is None:
-            masks = self._new((T, max(1, (max_q_len + 31) // 32)), self._i32, stream)
+            words = max(1, min((max_q_len + 31) // 32, 8))  # more are refused
+            masks = self._new((T, words), self._i32, stream)
         ints = self._ints
         mp, words = self._masks(masks, T)
         st = self._lib.attn_tree_plan(

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kMaxDrafts) attn_tree_plan_kernel(TreeArgs a) 
         if (k < a.mask_words) row[k] = w[k];
       }
       for (int k = W; k < a.mask_words; ++k) row[k] = 0;
-      a.positions[q0 + tid] = max(kv - n, 0) + seen - 1;
+      a.positions[q0 + tid] = max(max(kv, 0) - n, 0) + seen - 1;
     }
   }
   if (b == (int)gridDim.x - 1) {  // behind the last request

@@ -530,3 +530,22 @@ def test_an_entry_twice_and_a_path_that_falls_are_recorded():
     assert pos.numel() == 0 and masks.shape == (0, 1)
     assert attn.device_error() == moe.MOE_OK
     attn.close()
+
+
+def test_tree_plan_of_lengths_and_capacities_at_the_ends_of_their_type():
+    import torch
+    attn = moe.PagedAttention(16, 2, 256, 64, 1, 2)
+    pos, masks = run_tree_plan(attn, [-1, 0, -1], [0, 2, 3], [-(1 << 31), -1], 2)
+    assert pos == [0, 1, 0] and masks == [[1], [3], [1]]
+    assert attn.device_error() == moe.MOE_ERR_DEVICE
+    pos, masks = run_tree_plan(attn, [-1, 0, -1], [0, 2, 3], [(1 << 31) - 1, 1], 2)
+    assert pos == [(1 << 31) - 3, (1 << 31) - 2, 0] and masks == [[1], [3], [1]]
+    assert attn.device_error() == moe.MOE_OK
+    # refused before masks of that width are made
+    a = ints([-1]), ints([0, 1]), ints([1])
+    held = torch.cuda.memory_reserved()
+    for most in (257, (1 << 31) - 1):
+        with pytest.raises(moe.MoeError):
+            attn.tree_plan(*a, most)
+    assert torch.cuda.memory_reserved() == held
+    attn.close()
