@@ -178,8 +178,8 @@ int attn_kv4_forward(attn_handle h, const void* q, int64_t q_stride, const void*
  *                         follows the context.  Others are recorded (MOE_ERR_INVALID_ARG) and count
  *                         as -1.
  *   q_offsets, kv_lens    as for attn_kv4_forward
- *   max_q_len             1..256 and at most 32 mask_words: bounds n_b; a request beyond it is cut to it
- *                         (MOE_ERR_DEVICE)
+ *   max_q_len             1..256 and at most 32 mask_words: bounds n_b; a request beyond it is
+ *                         cut to it (MOE_ERR_DEVICE)
  *   positions [T] int32, out: kv_b - n_b (0 where that is negative) plus the token's depth
  *   masks [T][mask_words] uint32, out: bit j % 32 of word j / 32 for each token j of its request that
  *                         it sees: its ancestors and itself
@@ -213,9 +213,9 @@ int attn_qk_norm_rope_append(attn_handle h, const void* q, int64_t q_stride, con
  *               kv_b - n_b plus the number of drafted tokens that it sees besides one (itself).
  *               max_q_len is at most 256 and 32 mask_words, and at most W if there is a window (so a
  *               window never hides drafted tokens).
- * A query that sees no token gives 0.  Pages that lie between the first tokens and every window of their
- * request are not read: their entries of block_table may be anything, such as those of pages given
- * back. */
+ * A query that sees no token gives 0.  Pages that lie between the first tokens and every window of
+ * their request are not read: their entries of block_table may be anything, such as those of pages
+ * given back. */
 int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, const void* cache,
                             const int32_t* block_table, int table_width, const int32_t* q_offsets,
                             const int32_t* kv_lens, int B, int T, int max_q_len, int max_kv_len,
@@ -228,11 +228,12 @@ int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, cons
  *   paths [B][path_width] int32   accepted tokens by their index in their request, ascending; the
  *                            entries behind path_lens[b] are not read
  *   path_lens [B] int32      0 .. path_width
- * Rows behind the accepted ones keep what they hold.  attn_plan counts a request's pages from its ctx_lens:
- * pages taken for rejected tokens alone are the caller's to put back on its free list, or they are
- * replaced in the table by new ones.  Requests share none of the pages that they move rows in.  A length out of range moves nothing, an entry that is negative or not above the one
- * before it, or a row outside the table or the cache, is left out (MOE_ERR_DEVICE; the request's moved
- * rows are then undefined). */
+ * Rows behind the accepted ones keep what they hold.  attn_plan counts a request's pages from its
+ * ctx_lens: pages taken for rejected tokens alone are the caller's to put back on its free list, or
+ * they are replaced in the table by new ones.  Requests share none of the pages that they move rows
+ * in.  A length out of range moves nothing; an entry that is negative or not above the one before it,
+ * or a row outside the table or the cache, is left out (MOE_ERR_DEVICE; the request's moved rows are
+ * then undefined). */
 int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int table_width,
                     const int32_t* ctx_lens, const int32_t* paths, int path_width,
                     const int32_t* path_lens, int B, void* stream);

@@ -454,10 +454,10 @@ class PagedAttention:
     One object serves every layer of the same shape; each layer has a cache of its own
     (new_cache).  Queries, keys, values and outputs are bf16 [T][heads][head_dim], rows may be
     strided (views of a fused projection's output).  tree_plan, qk_norm_rope_append, forward with a
-    window or masks, and accept serve drafted trees and window layers.  Calls are enqueued on the current stream, or
-    on `stream`.  Outputs not given are allocated as memory of that stream: another one that uses
-    them waits for it first, and has them recorded (Tensor.record_stream) if they may be freed
-    before it is done.  The object belongs to the device that was current when it was made: tensors
+    window or masks, and accept serve drafted trees and window layers.  Calls are enqueued on the
+    current stream, or on `stream`.  Outputs not given are allocated as memory of that stream:
+    another one that uses them waits for it first, and has them recorded (Tensor.record_stream) if
+    they may be freed before it is done.  The object belongs to the device that was current when it was made: tensors
     are on that device, and calls are made while it is current.
     """
 
@@ -700,8 +700,8 @@ class PagedAttention:
         return positions, masks
 
     def accept(self, cache, block_table, ctx_lens, paths, path_lens, stream=None):
-        """Moves cached rows ctx_lens[b] + paths[b][i] to ctx_lens[b] + i, i < path_lens[b]: the accepted
-        tokens of paths [B][width], ascending indices in their request."""
+        """Moves cached rows ctx_lens[b] + paths[b][i] to ctx_lens[b] + i, i < path_lens[b]: the
+        accepted tokens of paths [B][width], ascending indices in their request."""
         if block_table is None or paths is None:
             _missing("block_table" if block_table is None else "paths")
         if block_table.dim() != 2 or paths.dim() != 2:

@@ -26,9 +26,9 @@ constexpr float kLeastUnit = 1.17549435e-38f;  // 2^-126
 constexpr int kDevErrNoMemory = 7;
 constexpr int kDevErrArg = 1;
 
-// Division of numbers below 2^31 by d, 1 <= d <= 2^20: a product and a shift (a division takes some twenty
-// instructions).  With 2^(l-1) < d <= 2^l and m = 2^(31+l) / d rounded up
-// (above it by less than 1), n m / 2^(31+l) lies above n / d by less than n / 2^(31+l) < 1 / d.
+// Division of numbers below 2^31 by d, 1 <= d <= 2^20: a product and a shift (a division takes some
+// twenty instructions).  With 2^(l-1) < d <= 2^l and m = 2^(31+l) / d rounded up (above it by less
+// than 1), n m / 2^(31+l) lies above n / d by less than n / 2^(31+l) < 1 / d.
 struct Divide {
   uint32_t m = 1u << 31, shift = 31;  // d = 1
   Divide() = default;
@@ -199,10 +199,11 @@ struct AcceptArgs {
 cudaError_t launch_attn_accept(const AcceptArgs& p, const RowsArgs& a, int D, cudaStream_t s);
 cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s);
 
-// Attention of few query rows per key/value head and request (n_b G <= 32): attn_decode.cu.  Its time
-// grows with every 8 (128 and 64 channels: 16) rows, the other kernel's with every 128: 8 requests of 2 to
-// 5 tokens, G = 4, contexts to 8000 took 26 us here and 41 there, of 8 tokens over 8000 61 and 73; with 256
-// channels 8 requests of 4 tokens, G = 8, over 4000 28 and 35, but 32 of them 73 and 67.
+// Attention of few query rows per key/value head and request (n_b G <= 32): attn_decode.cu.  Its
+// time grows with every 8 (128 and 64 channels: 16) rows, the other kernel's with every 128: 8
+// requests of 2 to 5 tokens, G = 4, contexts to 8000 took 26 us here and 41 there, of 8 tokens over
+// 8000 61 and 73; with 256 channels 8 requests of 4 tokens, G = 8, over 4000 28 and 35, but 32 of
+// them 73 and 67.
 constexpr int kDecodeRows = 32;
 cudaError_t prepare_attn_decode_kernels();
 int attn_part_slots(int sms);  // partial results of a launch, of either kernel

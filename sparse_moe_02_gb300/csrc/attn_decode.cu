@@ -29,11 +29,12 @@
 // 131072 24.6 us (3.1 TB/s with everything); 48 requests of up to 16248 24.8 us, 64 of 4096 38.8 us
 // (3.9 TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 27.1 us.
 //
-// The form with masks (MASK) goes over the tiles of the first tokens and of the window only, and hides
-// tokens by a word of drafted tokens and a window's start for each column.  Measured: 48 requests of one
-// token through a window of 2048, contexts to 32768 18.8 us (3882 tiles in all: a tenth of it; the rest
-// as above, most of it for 96 contexts' fixed costs), 8 trees of 2 to 8 tokens (32 heads over 8 of 128
-// channels), contexts to 8000 34 us (164 tiles an SM of 16 columns at 220 clocks each, 19 us).
+// The form with masks (MASK) goes over the tiles of the first tokens and of the window only, and
+// hides tokens by a word of drafted tokens and a window's start for each column.  Measured: 48
+// requests of one token through a window of 2048, contexts to 32768 18.8 us (3882 tiles in all: a
+// tenth of it; the rest as above, most of it for 96 contexts' fixed costs), 8 trees of 2 to 8
+// tokens (32 heads over 8 of 128 channels), contexts to 8000 34 us (164 tiles an SM of 16 columns
+// at 220 clocks each, 19 us).
 //
 // Layout of the work.  The rows of a key/value head (G query heads x new tokens) are the MMA's N
 // side in tiles of 8, its 16 tokens the M side of the scores.  A cached row is read once for 8 of
@@ -195,9 +196,9 @@ constexpr int kPartCost = 40;
 constexpr int kEachMore = 64;
 constexpr int kLeastWork = 12;  // of a block: a tile a warp (4096 tokens 10.5 us; with 32 12.5 us)
 
-// What a column sees.  Without masks: tokens below lim.  With: tokens below c, the cached ones before
-// the new ones, and those whose bit t - c is set (a request has at most kDecodeRows new tokens here); of
-// all these the first ones and those from lo on.
+// What a column sees.  Without masks: tokens below lim.  With: tokens below c, the cached ones
+// before the new ones, and those whose bit t - c is set (a request has at most kDecodeRows new
+// tokens here); of all these the first ones and those from lo on.
 template <bool MASK, int N, int M>
 struct Seen {
   int lim[N][M];

@@ -9,8 +9,9 @@
 // table entry that another block writes.  The last block to finish (a ticket) writes the cursor,
 // which the others read: cursor_out may therefore be the cursor.
 //
-// Measured (inside a CUDA graph): 64 requests of one token 4.3 us, 301 requests of up to 400 tokens with
-// pages of 16 5.4 us.  A block takes 1024 tokens, so one block serves token steps without the ticket.
+// Measured (inside a CUDA graph): 64 requests of one token 4.3 us, 301 requests of up to 400 tokens
+// with pages of 16 5.4 us.  A block takes 1024 tokens, so one block serves token steps without the
+// ticket.
 #include "attn.cuh"
 
 namespace moe {
@@ -150,10 +151,11 @@ __global__ void __launch_bounds__(kThreads) attn_plan_kernel(PlanArgs a) {
 }
 
 // attn_tree_plan: a block per request, a thread per drafted token, which holds its mask (itself at
-// first) and a forebear (its parent at first).  A round adds the forebear's mask to its own and takes the
-// forebear's forebear: the path that a mask covers doubles, so a tree of depth d takes log2 d rounds
-// (walks of d steps took 7.2 us for 256 trees of up to 64 tokens; this takes 2.1, a launch, as one tree
-// does).  Depths are the masks' counts.  Bound by latency: offsets, then parents, then the rounds.
+// first) and a forebear (its parent at first).  A round adds the forebear's mask to its own and
+// takes the forebear's forebear: the path that a mask covers doubles, so a tree of depth d takes
+// log2 d rounds (walks of d steps took 7.2 us for 256 trees of up to 64 tokens; this takes 2.1, a
+// launch, as one tree does).  Depths are the masks' counts.  Bound by latency: offsets, then
+// parents, then the rounds.
 template <int W>
 __global__ void __launch_bounds__(kMaxDrafts) attn_tree_plan_kernel(TreeArgs a) {
   __shared__ int forebear[2][kMaxDrafts];

@@ -1,5 +1,6 @@
 // Attention of many query rows over the paged 4-bit cache (include/attn.h): prompts, chunks of
-// prompts, wide trees of drafted tokens, and batches that hold any of them, on the tcgen05 tensor cores.
+// prompts, wide trees of drafted tokens, and batches that hold any of them, on the tcgen05 tensor
+// cores.
 //
 // A block works on 128 query rows of one key/value head (row = new token * G + query head) in steps
 // of 64 cached tokens.  Four warps hold the softmax (a thread per row); eight turn cached keys and
@@ -15,13 +16,13 @@
 // thread's branch, the second case below took 957 us instead of 767.
 //
 // Every 128 rows of a head read the same context, and turning it into operands takes 2300 clocks a
-// step (16 warps, two thirds of the block's issue slots), nearly twice the MMAs.  So where contexts are read
-// by many row tiles (kPrepTiles) a first launch, attn_prepare_kernel, forms the operands of every
-// step once, in the handle's workspace, and this kernel copies them (64 KB a step from L2, 580 to 890
-// clocks with all SMs at it) while its dequantising warps only stage queries and write outputs.  A
-// step then takes 1600 clocks; what is left over the MMAs is the wait for the product whose weights
-// lie where the next scores go (a third score buffer, with half of Q in shared memory, was no
-// faster).
+// step (16 warps, two thirds of the block's issue slots), nearly twice the MMAs.  So where contexts
+// are read by many row tiles (kPrepTiles) a first launch, attn_prepare_kernel, forms the operands
+// of every step once, in the handle's workspace, and this kernel copies them (64 KB a step from L2,
+// 580 to 890 clocks with all SMs at it) while its dequantising warps only stage queries and write
+// outputs.  A step then takes 1600 clocks; what is left over the MMAs is the wait for the product
+// whose weights lie where the next scores go (a third score buffer, with half of Q in shared
+// memory, was no faster).
 //
 // Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 138 us (990 TFLOP/s,
 // prepared; 209 us if not), 2048 over a context of 30000 755 us (1.37 PFLOP/s, 71% of a bf16 product's
@@ -29,15 +30,16 @@
 // ragged chunks and prompts of 28 heads over 4 of 128 77 us.  Of the 138 us the prepare launch takes 8,
 // start and tail of the blocks and the joins 20.
 //
-// The form with masks (MASK) has the same steps over fewer of the context's tokens: the steps of the first
-// tokens and those from a row tile's first window on.  A row's visible tokens of a step are 64 bits, formed
-// only where a step holds a window's start, the first tokens' end or drafted tokens; of a wide tree all
-// steps before the drafted ones need none.  Measured, 256 channels: a prompt of 8192 through a window of
-// 1024 167 us (787 TFLOP/s of the visible pairs: a row tile's 18 steps touch 1152 tokens for the 1040 that a
-// row sees, and each of its 7 to a block costs some 5000 clocks besides, the change of queries and
-// outputs), 16 trees of 20 to 60 tokens over contexts to 16384 59 us, 32 of 8 to 31 through a window of 1024
-// 34 us: 5 steps a block, and around them the launch, the cut and the first row tile found (9000
-// clocks), its queries (8000), the first operands and scores (5000), outputs (5000) and the join.
+// The form with masks (MASK) has the same steps over fewer of the context's tokens: the steps of
+// the first tokens and those from a row tile's first window on.  A row's visible tokens of a step
+// are 64 bits, formed only where a step holds a window's start, the first tokens' end or drafted
+// tokens; of a wide tree all steps before the drafted ones need none.  Measured, 256 channels: a
+// prompt of 8192 through a window of 1024 167 us (787 TFLOP/s of the visible pairs: a row tile's 18
+// steps touch 1152 tokens for the 1040 that a row sees, and each of its 7 to a block costs some
+// 5000 clocks besides, the change of queries and outputs), 16 trees of 20 to 60 tokens over
+// contexts to 16384 59 us, 32 of 8 to 31 through a window of 1024 34 us: 5 steps a block, and
+// around them the launch, the cut and the first row tile found (9000 clocks), its queries (8000),
+// the first operands and scores (5000), outputs (5000) and the join.
 //
 // Arithmetic.  Per record of 16 tokens, keys and values enter as f16(x 2^-(e + 6)), 2^e a bound of
 // the record's magnitudes: one fused multiply-add per pair of codes, since a nibble masked in place
@@ -53,8 +55,8 @@
 // values of a group or a token do beside others that are 2^20 times as large and count.
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
-// in the few-row kernel; shared row tiles are joined by its second launch.  Behind a window row tiles cost
-// alike and blocks may take whole ones (kWholeMore).
+// in the few-row kernel; shared row tiles are joined by its second launch.  Behind a window row
+// tiles cost alike and blocks may take whole ones (kWholeMore).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -220,11 +222,12 @@ constexpr uint32_t kNib0 = 0x000f000fu, kNib1 = 0x00f000f0u;
 constexpr int kPartCost = 320;   // tokens: a row tile's fixed cost
 constexpr int kZeroCost = 96;
 constexpr int kLeastSteps = 4;   // of a block
-// Row tiles behind a window cost alike, so where a share is several of them blocks may take whole ones: no
-// partial results and nothing to join, for up to this many steps more in the block that has most.  Cut
-// against whole, 256 channels, a window of 1024: 7350 tokens (7.8 steps more) 155 and 149 us, 8192 (17.0)
-// 172.8 and 170.5, 2048 (18.5) 58.2 and 60.2, 7700 (28.5) 163.8 and 166.8; 128 channels: 4096 tokens (0.8)
-// 131 and 126, 7500 (9.7) 223 and 220; 64 channels: 8192 (7.9) 223 and 212.
+// Row tiles behind a window cost alike, so where a share is several of them blocks may take whole
+// ones: no partial results and nothing to join, for up to this many steps more in the block that
+// has most.  Cut against whole, 256 channels, a window of 1024: 7350 tokens (7.8 steps more) 155
+// and 149 us, 8192 (17.0) 172.8 and 170.5, 2048 (18.5) 58.2 and 60.2, 7700 (28.5) 163.8 and 166.8;
+// 128 channels: 4096 tokens (0.8) 131 and 126, 7500 (9.7) 223 and 220; 64 channels: 8192 (7.9) 223
+// and 212.
 constexpr int kWholeMore = 18;
 
 struct Cost {
@@ -240,8 +243,8 @@ struct Cost {
   }
 };
 
-// Steps that a row tile behind a window goes over at most: the first tokens, and a window of each of its
-// tokens.
+// Steps that a row tile behind a window goes over at most: the first tokens, and a window of each
+// of its tokens.
 __device__ __forceinline__ int64_t window_steps(const FwdArgs& a, int tokens) {
   return ((int64_t)a.window + tokens + kStep - 1) / kStep + 1 + first_tiles<kStep>(a);
 }
@@ -475,11 +478,11 @@ struct Dequant {
       sts128(at ^ (i << 4), out[i][0], out[i][1], out[i][2], out[i][3]);
   }
 
-  // Row i * 32 + lane of the value operand is channel 64 g + 8 j + kWords sub + i (lane = (sub, g, j)),
-  // so that the rows of a store differ in their last three bits, which the swizzle spreads over
-  // the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.  Leaves the exponent of
-  // the record's values in *ex, and counts that on `left` if there is one (the softmax needs it with the
-  // scores).
+  // Row i * 32 + lane of the value operand is channel 64 g + 8 j + kWords sub + i (lane = (sub, g,
+  // j)), so that the rows of a store differ in their last three bits, which the swizzle spreads
+  // over the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.  Leaves the
+  // exponent of the record's values in *ex, and counts that on `left` if there is one (the softmax
+  // needs it with the scores).
   template <bool MASK>
   __device__ __forceinline__ void values(uint32_t raw, uint4* table, int oct, int tok,
                                          const Unread<MASK>& un, Exps* ex, uint64_t* left) {
@@ -611,8 +614,8 @@ struct QueryRows {
   }
 };
 
-// A quarter of those groups' columns of the 32 rows (tensor memory lanes) that the warp may write into tensor
-// memory.
+// A quarter of those groups' columns of the 32 rows (tensor memory lanes) that the warp may write
+// into tensor memory.
 template <int D>
 __device__ __forceinline__ void copy_queries(uint32_t src, uint32_t tmem, int g0, int part) {
   using C = Cfg<D>;
@@ -970,7 +973,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const int64_t at = (int64_t)(2 * blockIdx.x + (p.t0 == 0)) * kRows;
       const int c = lane & 3;
       // (rows of outputs are only known to start on 16 bytes)
-      const bool sectors = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(2 * a.out_stride)) & 31) == 0;
+      const bool sectors =
+          ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(2 * a.out_stride)) & 31) == 0;
 #pragma unroll 1
       for (int u = (warp - kKeyWarp) >> 2; u < 2 * NG; u += 4) {
         const int hf = u & 1, g = u >> 1;

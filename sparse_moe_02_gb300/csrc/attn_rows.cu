@@ -1,8 +1,9 @@
 // The row kernels of the attention step (include/attn.h): norm and rotation of query and key
-// heads, quantisation of keys and values into the paged 4-bit cache, both in one, accepted rows moved, and
-// the way back.  Each is one pass over its rows, bound by launch latency for single tokens and for prompts as stated at each
-// (by loads that wait for one another, append by instruction issue): a lane holds 8 channels (one
-// 16-byte load), the D / 8 lanes of a row reduce by shuffles.
+// heads, quantisation of keys and values into the paged 4-bit cache, both in one, accepted rows
+// moved, and the way back.  Each is one pass over its rows, bound by launch latency for single
+// tokens and for prompts as stated at each (by loads that wait for one another, append by
+// instruction issue): a lane holds 8 channels (one 16-byte load), the D / 8 lanes of a row reduce
+// by shuffles.
 #include "attn.cuh"
 
 namespace moe {
@@ -186,8 +187,8 @@ struct Pairs8 {
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Packed operations.  (ptxas fuses a packed product and sum, .rn or not: measured, sums that nearly cancel
-// came out fused.  Where that would change a value, the product is formed by mul_each.)
+// Packed operations.  (ptxas fuses a packed product and sum, .rn or not: measured, sums that nearly
+// cancel came out fused.  Where that would change a value, the product is formed by mul_each.)
 #define MOE_PACKED2(name, op)                                                                  \
   __device__ __forceinline__ float2 name(float2 a, float2 b) {                                 \
     float2 r;                                                                                  \
@@ -227,9 +228,10 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   return r;
 }
 
-// bf16(range / 15), the quotient rounded to fp32 before.  The product with 1 / 15 is within two units in
-// the last place of that quotient, so both round to the same bf16 unless the product lies that near the
-// middle between two: then, and for quotients that are no normal numbers, the division itself decides.
+// bf16(range / 15), the quotient rounded to fp32 before.  The product with 1 / 15 is within two
+// units in the last place of that quotient, so both round to the same bf16 unless the product lies
+// that near the middle between two: then, and for quotients that are no normal numbers, the
+// division itself decides.
 __device__ __forceinline__ __nv_bfloat16 step_of(float range) {
   float p = __fmul_rn(range, 1.f / 15.f);
   const uint32_t past = (__float_as_uint(p) & 0xffffu) - 0x7ffcu;
@@ -256,10 +258,10 @@ __device__ __forceinline__ Coded code_row(uint4 w) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) q[e] = both(0.f);
   if (step > 0.f) {
-    // The product with the reciprocal (itself within a unit in the last place) is within 2^-18 of the
-    // rounded quotient, so it rounds to the same code (at most 15) unless it lies near a half: then, and
-    // for steps whose reciprocal is no normal number, the quotient itself decides.  2^23 is added and
-    // taken off to round.
+    // The product with the reciprocal (itself within a unit in the last place) is within 2^-18 of
+    // the rounded quotient, so it rounds to the same code (at most 15) unless it lies near a half:
+    // then, and for steps whose reciprocal is no normal number, the quotient itself decides.  2^23
+    // is added and taken off to round.
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
     float2 d[4];
@@ -368,8 +370,8 @@ __device__ __forceinline__ float2 add_exact(float2 s, float2 p, float2& e) {
   return t;
 }
 
-// Sum over L neighbouring lanes of the lanes' squares (fp32 numbers, those of bf16 values), rounded once:
-// a second float carries what the first one's additions round off.
+// Sum over L neighbouring lanes of the lanes' squares (fp32 numbers, those of bf16 values), rounded
+// once: a second float carries what the first one's additions round off.
 template <int L>
 __device__ __forceinline__ float sum_squares_exact(const Pairs8& r) {
   float2 e2 = both(0.f), s2 = mul2(r.p[0], r.p[0]);
@@ -385,9 +387,9 @@ __device__ __forceinline__ float sum_squares_exact(const Pairs8& r) {
   return s < INFINITY ? __fadd_rn(s, e) : s;
 }
 
-// Cosines and sines of a lane's channels ch .. ch + 7 at a token's position (a position out of range at
-// 0), in pairs as the channels': of the channels' angles, the sines of the lower half negated; INTER: of
-// the angles of channels (2i, 2i + 1), the first two pairs.
+// Cosines and sines of a lane's channels ch .. ch + 7 at a token's position (a position out of
+// range at 0), in pairs as the channels': of the channels' angles, the sines of the lower half
+// negated; INTER: of the angles of channels (2i, 2i + 1), the first two pairs.
 struct Turn {
   float2 c[4], s[4];
 };
@@ -453,7 +455,8 @@ __device__ __forceinline__ uint4 turn_key(const RopeArgs& a, uint4 raw, const Pa
       const int mate = turn ? lane - li + (ch < half ? li + half / 8 : li - half / 8) : lane;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 m = make_float2(__shfl_sync(~0u, r.p[e].x, mate), __shfl_sync(~0u, r.p[e].y, mate));
+        const float2 m = make_float2(__shfl_sync(~0u, r.p[e].x, mate),
+                                     __shfl_sync(~0u, r.p[e].y, mate));
         if (turn) r.p[e] = sum_of_products(r.p[e], x.c[e], m, x.s[e]);
       }
     }
@@ -461,9 +464,9 @@ __device__ __forceinline__ uint4 turn_key(const RopeArgs& a, uint4 raw, const Pa
   return narrow(r);
 }
 
-// A lane's 8 channels of a query row, laid out so that a rotation's pairs (u, v) lie in one lane: neighbouring
-// channels (INTER), or four channels and their mates half the rotated ones away; behind the rotated channels
-// eight neighbouring ones.
+// A lane's 8 channels of a query row, laid out so that a rotation's pairs (u, v) lie in one lane:
+// neighbouring channels (INTER), or four channels and their mates half the rotated ones away;
+// behind the rotated channels eight neighbouring ones.
 template <bool INTER>
 struct QueryPiece {
   int first, second;  // channels of the four lower and the four upper ones
@@ -539,18 +542,19 @@ struct Shares {
   Divide by_heads, by_splits;
 };
 
-// attn_qk_norm_rope_append: a group of L = D / 8 lanes per row.  kv_blocks of the blocks take a key and a
-// value row each group, the others heads_per neighbouring query heads of a token, as in the norm and
-// rotation alone; both kinds evenly mixed, since the first is bound by instruction issue and the second by
-// memory.
+// attn_qk_norm_rope_append: a group of L = D / 8 lanes per row.  kv_blocks of the blocks take a key
+// and a value row each group, the others heads_per neighbouring query heads of a token, as in the
+// norm and rotation alone; both kinds evenly mixed, since the first is bound by instruction issue
+// and the second by memory.
 //
-// Bound by instruction issue for prompts (68% of the slots, DRAM at 4.4 TB/s): a warp takes 87 instructions
-// a query row of two (128 channels), 500 for two key and value rows, of which the exact sum and root are 110
-// and the codes 300.  Measured: 16381 tokens, 32 query and 8 key/value heads of 128 channels 75 us with
-// neighbouring pairs, 80 with halves (the norm and rotation, then the append: 108 and 128), 16 and 2 of 256
-// 64 and 68 us; 48 tokens 2.9 us.  Steps of the way there: key and value blocks first 115 us, four query
-// heads a group and four blocks an SM instead of eight and three 96, products in place of divisions 86, five
-// blocks an SM 77, a rotation's pairs of a query in one lane 75 (halves: 101 to 80).
+// Bound by instruction issue for prompts (68% of the slots, DRAM at 4.4 TB/s): a warp takes 87
+// instructions a query row of two (128 channels), 500 for two key and value rows, of which the
+// exact sum and root are 110 and the codes 300.  Measured: 16381 tokens, 32 query and 8 key/value
+// heads of 128 channels 75 us with neighbouring pairs, 80 with halves (the norm and rotation, then
+// the append: 108 and 128), 16 and 2 of 256 64 and 68 us; 48 tokens 2.9 us.  Steps of the way
+// there: key and value blocks first 115 us, four query heads a group and four blocks an SM instead
+// of eight and three 96, products in place of divisions 86, five blocks an SM 77, a rotation's
+// pairs of a query in one lane 75 (halves: 101 to 80).
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads, 5) attn_rope_append_kernel(RopeArgs r, RowsArgs a,
                                                                     Shares n) {
@@ -623,10 +627,11 @@ __device__ __forceinline__ int64_t slot_of(const AcceptArgs& p, const RowsArgs& 
   return slot < a.n_slots ? slot : -1;
 }
 
-// A block per request and head, L = D / 8 lanes per accepted row, kThreads / L rows at a time: all are
-// read before any is written.  Entry i of an ascending path is i at least, so no row is written before
-// a later round reads it.  Bound by latency: lengths, path and table, rows, one after another (with its
-// reading back, 64 requests of up to 12 accepted tokens, 2 heads of 256 channels: 4.4 us, two launches).
+// A block per request and head, L = D / 8 lanes per accepted row, kThreads / L rows at a time: all
+// are read before any is written.  Entry i of an ascending path is i at least, so no row is written
+// before a later round reads it.  Bound by latency: lengths, path and table, rows, one after
+// another (with its reading back, 64 requests of up to 12 accepted tokens, 2 heads of 256 channels:
+// 4.4 us, two launches).
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_accept_kernel(AcceptArgs p, RowsArgs a) {
   using R = Record<D>;
@@ -730,8 +735,8 @@ int row_grid(const RowsArgs& a, int D) {
   return (int)(((int64_t)a.T * a.Hkv + per_block - 1) / per_block);
 }
 
-// Items of neighbouring heads of a token: as few heads in each as still leave one item for every group of
-// lanes that fits the GPU, up to `most`.
+// Items of neighbouring heads of a token: as few heads in each as still leave one item for every
+// group of lanes that fits the GPU, up to `most`.
 int heads_per_item(int T, int heads, int most, int D, int sms) {
   const int64_t groups = (int64_t)sms * (2048 / kThreads) * (kThreads / (D / 8));
   int64_t per = (T * (int64_t)heads + groups - 1) / groups;
