@@ -15,7 +15,7 @@
 // So that w fits f16 for any bf16 scale, the running softmax reference of a row is the maximum
 // of score + exponent(largest |s_tg|), which bounds w, instead of the score alone (where all scales
 // are 0 or nearly so, the biases' exponent less kBiasMore); it only moves (and the accumulators are
-// only rescaled) when a tile exceeds it by 2^6.
+// only rescaled) when a token exceeds it by 2^6.
 //
 // What bounds it.  A tile of 16 tokens (4608 bytes with 256 channels) costs about 540 warp
 // instructions for 8 rows; twelve warps an SM, each with 14 KB of copies in flight, read the cache at
@@ -473,26 +473,33 @@ __device__ __forceinline__ void tile_step(uint32_t st, uint32_t frags, int tok0,
       }
     }
   }
-  // 2^ev bounds the tile's scales (nonnegative bf16, the lower halves), 2^(ev + kBiasMore) its biases
-  uint32_t big = 0;
+  // 2^ev bounds a token's scales (nonnegative bf16, the lower halves), 2^(ev + kBiasMore) its biases.  The
+  // reference takes each token's bound with its own score: tokens that the row does not see (-inf) or
+  // hardly weighs leave it alone, whatever they hold.
+  float ev[2];
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int r = 0; r < 2; ++r) {
+    uint32_t big = 0;
 #pragma unroll
     for (int g = 0; g < NG; ++g) big = max_u16x2(big, vp[r].w[g] & 0x7fff7fffu);
-  const int most =
-      __reduce_max_sync(~0u, max((int)(big & 0xffffu), (int)(big >> 16) - (kBiasMore << 7)));
-  const float ev = (float)max((most >> 7) - 126, -90);
+    const int most =
+        max(max((int)(big & 0xffffu), (int)(big >> 16) - (kBiasMore << 7)), (126 - 90) << 7);
+    // (most >> 7) - 126 as a float: 2^23 + most / 128, less 2^23 + 126
+    ev[r] = __uint_as_float(0x4b000000u | (uint32_t)most >> 7) - 8388734.f;
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float top[2];
 #pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      top[cc] = fmaxf(x[nt][cc], x[nt][2 + cc]);
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top[cc] = fmaxf(top[cc], __shfl_xor_sync(~0u, top[cc], o));
-      top[cc] = fmaf(top[cc], Q.scale[nt][cc], ev);
-    }
+    for (int cc = 0; cc < 2; ++cc)  // of the lane's tokens
+      top[cc] = fmaxf(fmaf(x[nt][cc], Q.scale[nt][cc], ev[0]),
+                      fmaf(x[nt][2 + cc], Q.scale[nt][cc], ev[1]));
     if (__any_sync(~0u, top[0] > s.m[nt][0] + kSlack || top[1] > s.m[nt][1] + kSlack)) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc)
+          top[cc] = fmaxf(top[cc], __shfl_xor_sync(~0u, top[cc], o));
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const float m = fmaxf(s.m[nt][cc], top[cc]);
