@@ -44,6 +44,10 @@
  *     gives 0.  Scores, softmax sums and outputs are held in fp32 and rounded once to bf16.
  *     Scores are in range below 2^23 (in units of log 2): a row with larger ones may read NaN, and
  *     from 2^28 on it does.
+ *     A value loses bits beside another one, 2^20 times as large, of a weight that counts (with more
+ *     than 32 query rows a key/value head, where tokens have the largest weight of the 16 that share a
+ *     record, and channels 2^18 below its largest lose bits too).  Tokens that a query does not see cost
+ *     it nothing, whatever they hold.
  *   window and first tokens: a query at position p sees the cached tokens t <= p with t < S or t > p -
  *     W (a window of W tokens, the query's own among them, and S first tokens).
  *   tree: the n_b new tokens of request b are drafted, token i behind token parent_i < i, or

@@ -23,6 +23,7 @@ constexpr float kLargest = 8.307675e34f;  // 2^116
 // Least unit of a score (the smallest normal fp32): masked scores are -inf times it, which a unit that
 // vanished, of a zero query row over empty or zero keys, would make NaN.
 constexpr float kLeastUnit = 1.17549435e-38f;  // 2^-126
+constexpr int kPrepExps = 12;  // 16-byte words of exponents of a step (64 tokens) held as operands
 constexpr int kDevErrNoMemory = 7;
 constexpr int kDevErrArg = 1;
 
@@ -100,7 +101,7 @@ struct FwdArgs {
   int* prep_at;
   int prep_cap;
   uint8_t* prep;      // [steps]: a step's key operand, then its value operand
-  uint4* prep_exps;   // [steps][4]: exponents of the records
+  uint4* prep_exps;   // [steps][kPrepExps]: exponents of the records and their tokens
   int* err;
   // Narrower views (attn_kv4_forward_masked): a window of 0 is none, no masks is causal.
   int window, sinks;

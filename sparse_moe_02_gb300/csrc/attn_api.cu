@@ -208,7 +208,7 @@ int attn_create(const attn_config* cfg, attn_handle* out) {
   const size_t desc_bytes = round256(slots * sizeof(int4));
   h->prep_cap = moe::attn_prep_steps(h->d, cfg->max_requests);
   const size_t prep_bytes = round256(h->prep_cap * moe::attn_prep_step_bytes(cfg->head_dim));
-  const size_t exps_bytes = round256(h->prep_cap * 4 * sizeof(uint4));
+  const size_t exps_bytes = round256((size_t)h->prep_cap * moe::kPrepExps * sizeof(uint4));
   const size_t at_bytes = round256((1 + (size_t)cfg->max_requests) * sizeof(int));
   const size_t zeroed = 2 * sizeof(int);  // the plan's ticket, the error word
   const size_t bytes =

@@ -52,7 +52,16 @@
 // outputs are fp32; 2^x is ex2.approx, within 2^-22.  The outputs are rescaled (in tensor memory)
 // only when the reference grows by more than 2^6.  Entries 2^18 and more below the largest of their
 // record lose bits, and weights 2^24 and more below the row's largest share of any value vanish: the
-// values of a group or a token do beside others that are 2^20 times as large and count.
+// values of a group or a token do beside others that are 2^20 times as large and count, where a token
+// counts as the one of its record with the largest weight.
+//
+// Uneven records.  What a row does not see must not cost it bits, so a record of which some rows see
+// only a part is formed with an exponent for each token where the tokens' bounds differ by more than
+// 2^kEven; the softmax then brings each score and weight to its token's.  Such records are looked for
+// first: by the find warp, in a part's steps with edges, or by the prepare launch.  Parts without any run
+// through loops that know nothing of them: checked for in every step (by the softmax, by the warps that
+// form operands) they cost 3 to 20%, most of it instruction fetches.  As it is, prompts take 1 to 2%
+// more than without, trees 6% (16 of 20 to 60 tokens over 16384: 59 to 63 us).
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
 // in the few-row kernel; shared row tiles are joined by its second launch.  Behind a window row
@@ -84,6 +93,13 @@ constexpr float kSlack = 6.f, kLift = 9.f;  // as in the few-row kernel
 // far above the record's weights that they leave fp32's range.
 constexpr float kSpread = 64.f;
 constexpr int kExps = 8;             // steps of record exponents kept
+// Exponents by which the tokens of an even record differ at most.  An operand's rounding is half of
+// f16's least spacing, 2^-25, so at most 2^(kEven + 6 - 25) of the bound of its own token, which is below
+// 8 times the token's largest entry (|bias| and 15 |step|, rounded up to powers of two): 2^-11 of it.
+constexpr int kEven = 5;
+// Least unit of a score among uneven records: scores times it are nothing beside any that count, and
+// what a token's exponent takes off, 209 at most, may be divided by it.
+constexpr float kLeastUp = 7.8886091e-31f;  // 2^-100
 constexpr int kNotFinite = 127;      // in place of the exponent of a query row that is not finite
 
 template <int D>
@@ -281,6 +297,29 @@ __device__ __forceinline__ int tile_start(const FwdArgs& a, const Req& r, int to
   return a.masks ? first_start(a, r) : window_start(a, r.kv - r.qn + tok);
 }
 
+// Where the queries of a row tile do not all see the same: tokens from `least` on, and, with masks, those
+// between the first tokens and `low`, from which on tokens lie in every window.
+template <bool MASK>
+struct Edges {
+  int least, low, first;
+  __device__ __forceinline__ Edges(const FwdArgs& a, const Part& p) {
+    least = seen_by(p.r, a.d.by_G(p.rt * kRows));
+    low = INT_MIN;
+    first = 0;
+    if constexpr (MASK) {
+      if (a.masks) least = p.r.kv - p.r.qn;
+      // (or behind the row tile's last token)
+      const int last = p.r.kv - p.r.qn + a.d.by_G((p.rt + 1) * kRows);
+      low = window_start(a, a.masks ? p.r.kv - 1 : min(p.r.kv - 1, last));
+      first = a.sinks;
+    }
+  }
+  // whether the step from token t0 on holds such tokens
+  __device__ __forceinline__ bool in(int t0) const {
+    return t0 + kStep > least || (MASK && t0 < low && t0 + kStep > first);
+  }
+};
+
 // The part that holds work w of the block's [w, w1).
 template <bool MASK>
 __device__ __forceinline__ Part locate(const FwdArgs& a, const int64_t* first, int part_cost,
@@ -339,6 +378,7 @@ template <int D>
 struct Bars {
   using C = Cfg<D>;
   uint64_t part_full[kParts], part_empty[kParts];
+  uint64_t looked[kParts];  // whether a part has uneven records is known
   uint64_t raw_full[2][4], raw_empty[2][4];  // [keys, values]
   uint64_t k_full[C::kOpsK], k_empty[C::kOpsK], v_full[C::kOpsV], v_empty[C::kOpsV];
   uint64_t s_full[C::kS], p_full[C::kS], pv_done[C::kS];
@@ -387,13 +427,21 @@ struct Unread {
   }
 };
 
-// Exponents of a record: keys were divided by 2^(ek + 6), values by 2^(ev + 6).
+// Exponents of a record: keys were divided by 2^(ek + 6), values by 2^(ev + 6).  Of uneven ones (marked
+// by the last bit of up_k or down_v) by those of their tokens.
 struct __align__(16) Exps {
   float up_k;    // 2^ek
   float ev;      // ev
   float down_v;  // 2^-ev
-  float pad;
+  uint32_t some;  // of a prepared step's first record: whether any is uneven
 };
+struct StepExps {
+  Exps rec[kRecs];
+  int8_t tok[2][kStep];  // [keys, values], of uneven records
+};
+static_assert(sizeof(StepExps) == kPrepExps * sizeof(uint4), "as many words a prepared step");
+
+__device__ __forceinline__ bool marked(float x) { return __float_as_uint(x) & 1; }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -411,6 +459,38 @@ __device__ __forceinline__ int exponent_of(uint32_t packed) {
   return max(max(s + 4, b) - 125, -90);  // 15 step < 2^(4 + its exponent + 1)
 }
 
+// e + 125 of a word's magnitudes alone, 0 where both are.
+__device__ __forceinline__ uint32_t bound_of(uint32_t packed) {
+  return packed ? max(((packed & 0xffffu) >> 7) + 4, packed >> 23) : 0u;
+}
+
+__device__ __forceinline__ int exponent_of_bound(uint32_t bound) { return max((int)bound - 125, -90); }
+
+// Exponents of a record, `all` that of the largest, from the bounds of a lane's tokens (own half, other
+// half) in one of kGroups groups, 8 lanes apart: returns what to form the own token with.  Of uneven ones
+// the warp of the first half leaves the tokens' in `left` and marks *scale.
+template <int kGroups>
+__device__ __forceinline__ int token_exponent(uint32_t own, uint32_t other, int all, int oct,
+                                              int8_t* left, float* scale) {
+  const int lane = threadIdx.x & 31;
+  uint32_t both = own << 16 | other;
+#pragma unroll
+  for (int o = 8; o < 8 * kGroups; o <<= 1) both = max_u16x2(both, __shfl_xor_sync(~0u, both, o));
+  // (tokens of zeros fit any exponent)
+  const int e = both >> 16 ? exponent_of_bound(both >> 16) : all;
+  const int e2 = both & 0xffffu ? exponent_of_bound(both & 0xffffu) : all;
+  if (!__any_sync(~0u, min(e, e2) < all - kEven)) return all;
+  if ((oct & 1) == 0) {
+    if (lane < 8) {
+      left[8 * oct + lane] = (int8_t)e;
+      left[8 * oct + 8 + lane] = (int8_t)e2;
+    }
+    if (lane == 0) *scale = __uint_as_float(__float_as_uint(*scale) | 1u);
+    __syncwarp();
+  }
+  return e;
+}
+
 // One warp turns 8 cached tokens (half a record) of a step into operands: rows of the key operand
 // [64 tokens][D] or columns of the value operand [D][64 tokens], both in the 128-byte swizzle.  The
 // values are formed in registers first and stored once the operand's last readers are done, so
@@ -424,11 +504,13 @@ struct Dequant {
   static constexpr int NG = C::NG;
   static constexpr int kWords = 2 * NG;  // a lane's words of a key row; nibbles of its value words
 
-  // Parameters of token lane & 7, group (lane >> 3) % NG at offset `off` of the record (0 behind the
-  // context), and the exponent of the record's 16 tokens.
-  template <bool MASK>
-  static __device__ __forceinline__ uint32_t params(uint32_t rec, int off, int oct, int tok,
-                                                    const Unread<MASK>& un, int* e) {
+  // Parameters of token lane & 7, group (lane >> 3) % NG of the record (0 behind the context) and *e, the
+  // exponent of the record's 16 tokens, which the warp of its first half leaves in *ex; with LOOK, of
+  // uneven records the token's own.
+  template <bool kKeys, bool LOOK, bool MASK>
+  static __device__ __forceinline__ uint32_t params(uint32_t rec, int oct, int tok,
+                                                    const Unread<MASK>& un, StepExps* ex, int* e) {
+    constexpr int off = kKeys ? R::kKp : R::kVp;
     const int lane = threadIdx.x & 31, t = lane & 7, g = (lane >> 3) % NG;
     const uint32_t par = rec + off + (8 * (oct & 1) + t) * R::kPar + 4 * g;
     const int other = (oct & 1) ? -8 : 8;  // the record's other half
@@ -436,20 +518,35 @@ struct Dequant {
     if (un.token(tok + t)) w = 0;
     if (un.token(tok + t + other)) w2 = 0;
     *e = exponent_of(max_u16x2(magnitudes(w), magnitudes(w2)));
+    Exps* own = &ex->rec[oct >> 1];
+    if (lane == 0 && (oct & 1) == 0) {
+      if (kKeys) {
+        own->up_k = pow2(*e);
+      } else {
+        own->ev = (float)*e;
+        own->down_v = pow2(-*e);
+      }
+    }
+    if constexpr (LOOK) {
+      // (groups of a token may be as small; seldom are all)
+      const uint32_t b = bound_of(magnitudes(w)), b2 = bound_of(magnitudes(w2));
+      if (__any_sync(~0u, (b && exponent_of_bound(b) < *e - kEven) ||
+                              (b2 && exponent_of_bound(b2) < *e - kEven)))
+        *e = token_exponent<NG>(b, b2, *e, oct, ex->tok[!kKeys], kKeys ? &own->up_k : &own->down_v);
+    }
     return w;
   }
 
-  // tok: the first token's index in the context.  Also leaves the exponent of the record's keys in *ex.
-  template <bool MASK>
+  // tok: the first token's index in the context.  Also leaves the exponents of the record's keys in *ex.
+  template <bool LOOK, bool MASK>
   __device__ __forceinline__ void keys(uint32_t raw, int oct, int tok, const Unread<MASK>& un,
-                                       Exps* ex) {
+                                       StepExps* ex) {
     const int lane = threadIdx.x & 31;
     const int t = lane & 7, g = (lane >> 3) % NG, sub = lane / (8 * NG);
     const uint32_t rec = raw + (oct >> 1) * C::kSideK;
     const int row = 8 * (oct & 1) + t;
     int e;
-    const uint32_t w = params(rec, R::kKp, oct, tok, un, &e);
-    if (lane == 0 && (oct & 1) == 0) ex->up_k = pow2(e);
+    const uint32_t w = params<true, LOOK>(rec, oct, tok, un, ex, &e);
     const float down = pow2(-(e + 6));
     const float s = bf16_lo(w) * down, b = bf16_hi(w) * down;
     const uint32_t s24 = pack_f16(s * 16777216.f, s * 16777216.f);
@@ -481,30 +578,27 @@ struct Dequant {
   // Row i * 32 + lane of the value operand is channel 64 g + 8 j + kWords sub + i (lane = (sub, g,
   // j)), so that the rows of a store differ in their last three bits, which the swizzle spreads
   // over the banks.  `table`: 16 bytes for each pair of tokens and group, of this warp.  Leaves the
-  // exponent of the record's values in *ex, and counts that on `left` if there is one (the softmax
-  // needs it with the scores).
-  template <bool MASK>
+  // exponents of the record's values in *ex, and counts that on `left` if there is one (the softmax
+  // needs them with the scores).
+  template <bool LOOK, bool MASK>
   __device__ __forceinline__ void values(uint32_t raw, uint4* table, int oct, int tok,
-                                         const Unread<MASK>& un, Exps* ex, uint64_t* left) {
+                                         const Unread<MASK>& un, StepExps* ex, uint64_t* left) {
     const int lane = threadIdx.x & 31;
     const uint32_t rec = raw + (oct >> 1) * C::kSideV;
     {
       int e;
-      const uint32_t w = params(rec, R::kVp, oct, tok, un, &e);
-      if (lane == 0 && (oct & 1) == 0) {
-        ex->ev = (float)e;
-        ex->down_v = pow2(-e);
-        if (left) mbar_arrive(left);
-      }
+      const uint32_t w = params<false, LOOK>(rec, oct, tok, un, ex, &e);
+      if (lane == 0 && (oct & 1) == 0 && left) mbar_arrive(left);
       const int t = lane & 7, g = (lane >> 3) % NG;
       const float down = pow2(-(e + 6));
       const uint32_t mate = __shfl_down_sync(~0u, w, 1);
+      const float down1 = LOOK ? __shfl_down_sync(~0u, down, 1) : down;  // the next token's
       if ((t & 1) == 0 && lane < 8 * NG) {
-        const float s0 = bf16_lo(w) * down, s1 = bf16_lo(mate) * down;
+        const float s0 = bf16_lo(w) * down, s1 = bf16_lo(mate) * down1;
         table[(t >> 1) * NG + g] =
             make_uint4(pack_f16(s0 * 16777216.f, s1 * 16777216.f),
                        pack_f16(s0 * 1048576.f, s1 * 1048576.f),
-                       pack_f16(bf16_hi(w) * down, bf16_hi(mate) * down), 0u);
+                       pack_f16(bf16_hi(w) * down, bf16_hi(mate) * down1), 0u);
       }
       __syncwarp();
     }
@@ -548,6 +642,53 @@ struct Dequant {
              out[i][3]);
   }
 };
+
+// The exponents of 16 tokens.
+struct TokenBytes {
+  uint4 w;
+  __device__ __forceinline__ int operator[](int i) const {
+    const uint32_t x = i < 4 ? w.x : i < 8 ? w.y : i < 12 ? w.z : w.w;
+    return (int8_t)(x >> (8 * (i & 3)));
+  }
+};
+
+__device__ __forceinline__ TokenBytes token_bytes(const int8_t* p) {
+  return TokenBytes{*reinterpret_cast<const uint4*>(p)};
+}
+
+// Turns a row's scores of a step, 64 columns of tensor memory from `at` on, of uneven records into those
+// of even ones: each as if its key had the record's exponent, and with what its value's exponent lies
+// below the record's taken off.  Whether there are any.
+__device__ __forceinline__ bool scores_of_tokens(uint32_t at, const StepExps& ex, float unit) {
+  uint32_t marks = 0;
+#pragma unroll
+  for (int r = 0; r < kRecs; ++r)
+    marks |= __float_as_uint(ex.rec[r].up_k) | __float_as_uint(ex.rec[r].down_v);
+  if (!(marks & 1)) return false;
+#pragma unroll 1
+  for (int r = 0; r < kRecs; r += 2) {
+    uint32_t s[32];
+    tmem_ld32(at + 16 * r, s);
+    wait_ld32(s);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Exps rec = ex.rec[r + k];
+      const TokenBytes ek = token_bytes(ex.tok[0] + 16 * (r + k));
+      const TokenBytes ev = token_bytes(ex.tok[1] + 16 * (r + k));
+      const float up = fmaxf(unit * rec.up_k, kLeastUp), down = 1.f / up;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float x = __uint_as_float(s[16 * k + i]);
+        if (marked(rec.up_k)) x *= fmaxf(unit * pow2(ek[i]), kLeastUp) * down;
+        if (marked(rec.down_v)) x = fmaf((float)ev[i] - rec.ev, down, x);
+        s[16 * k + i] = __float_as_uint(x);
+      }
+    }
+    tmem_st32(at + 16 * r, s);
+  }
+  tmem_wait_st();
+  return true;
+}
 
 // Column of O that holds nibble k of word j of group g (see Dequant::values).
 template <int NG>
@@ -680,15 +821,110 @@ struct RowView {
   }
 };
 
+// First prepared step of a part's context and head.
+template <bool MASK>
+__device__ __forceinline__ int first_prepared(const FwdArgs& a, const Part& p) {
+  const int left_out = MASK ? skipped<kStep>(a, first_start(a, p.r)) : 0;
+  return a.prep_at[1 + p.b] + p.h * ((p.r.kv + kStep - 1) / kStep - left_out);
+}
+
+// The one of the part's step t.  (Where a row tile leaves steps out, its context does as many or fewer.)
+template <bool MASK>
+__device__ __forceinline__ int prepared_step(const FwdArgs& a, const Part& p, int first, int t) {
+  if (MASK && t >= first_tiles<kStep>(a))
+    return first + t + p.skip - skipped<kStep>(a, first_start(a, p.r));
+  return first + t;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
+  if constexpr (N == 4) {
+    const uint4 x = __ldg(static_cast<const uint4*>(p));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = __ldg(static_cast<const uint2*>(p));
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = __ldg(static_cast<const uint32_t*>(p));
+  }
+}
+
+// Whether a part has uneven records in steps with edges (of prepared contexts: any that were formed as
+// such).  One warp: page ids of eight steps, a lane a record, then the parameters of four records at a
+// time, those of a token's keys or values to a lane.
 template <int D, bool MASK>
+__device__ __forceinline__ bool look_for_uneven(const FwdArgs& a, const Part& p, bool prepared) {
+  using R = Record<D>;
+  constexpr int NG = D / kGroup, kAtOnce = 4;
+  static_assert(R::kVp == R::kKp + 16 * R::kPar, "keys' and values' parameters lie together");
+  const int lane = threadIdx.x & 31;
+  bool some = false;
+  if (p.t0 >= p.t1) return false;
+  if (prepared) {
+    const int at = first_prepared<MASK>(a, p);
+    for (int t = p.t0 + lane; t < p.t1; t += 32)
+      some |= a.prep_exps[(int64_t)prepared_step<MASK>(a, p, at, t) * kPrepExps].w != 0;
+    return __any_sync(~0u, some);
+  }
+  const Edges<MASK> edges(a, p);
+  const Unread<MASK> un(a, p.r);
+#pragma unroll 1
+  for (int t0 = p.t0; t0 < p.t1; t0 += 32) {
+    const int mine = t0 + lane;
+    unsigned with = __ballot_sync(
+        ~0u, mine < p.t1 && edges.in(tile_at<MASK, kStep>(a, mine, p.skip) * kStep));
+#pragma unroll 1
+    while (with) {
+      int tile = 0, taken = 0;
+#pragma unroll 1
+      for (; with && taken < 8; ++taken, with &= with - 1) {
+        const int t = tile_at<MASK, kStep>(a, t0 + __ffs(with) - 1, p.skip);
+        if (lane / kRecs == taken) tile = t;
+      }
+      const int rec = tile * kRecs + lane % kRecs;
+      const bool held = lane < taken * kRecs && !un.record(rec);
+      uint32_t record = 0;
+      if (held) record = cache_record(a, p.b, p.h, rec);
+      const unsigned have = __ballot_sync(~0u, held);
+#pragma unroll 1
+      for (int k0 = 0; k0 < taken * kRecs; k0 += kAtOnce) {
+        uint32_t w[kAtOnce][NG];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const uint8_t* at = a.cache + (uint64_t)__shfl_sync(~0u, record, k0 + i) * R::kBytes +
+                              R::kKp + lane * R::kPar;
+          const int tok = 16 * __shfl_sync(~0u, rec, k0 + i) + (lane & 15);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) w[i][g] = 0;
+          if ((have >> (k0 + i) & 1) && !un.token(tok)) load_words<NG>(w[i], at);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) m = max_u16x2(m, magnitudes(w[i][g]));
+          const uint32_t b = bound_of(m);
+          const uint32_t of_keys = __reduce_max_sync(~0u, lane < 16 ? b : 0u);
+          const uint32_t of_values = __reduce_max_sync(~0u, lane < 16 ? 0u : b);
+          const int all = exponent_of_bound(lane < 16 ? of_keys : of_values);
+          some |= b && exponent_of_bound(b) < all - kEven;
+        }
+      }
+    }
+  }
+  return __any_sync(~0u, some);
+}
+
+template <int D, bool MASK, bool PREP>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   using C = Cfg<D>;
   constexpr int NG = C::NG;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars<D> bars;
-  __shared__ Exps exps[kExps][kRecs];
+  __shared__ __align__(16) StepExps exps[kExps];
   __shared__ uint4 tables[kDeqWarps][4 * NG];
   __shared__ Part parts[kParts];
+  __shared__ bool uneven[kParts];  // whether they have uneven records
   __shared__ int8_t row_exp[kExps][kRows];  // of the queries of the last parts
   __shared__ float out_scale[2][kRows];  // of the outputs of the last parts
   __shared__ uint32_t tmem_base;
@@ -700,6 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   if (tid == 0) {
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&bars.part_full[i], 1);
+      mbar_init(&bars.looked[i], 1);
       mbar_init(&bars.part_empty[i], kSoftWarps + 2 * kDeqWarps + 3);
     }
     for (int side = 0; side < 2; ++side)
@@ -735,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   pdl_wait();
   pdl_trigger();
   int64_t* first = reinterpret_cast<int64_t*>(smem + C::kFirst);
-  const bool prepared = a.prep_cap > 0 && a.prep_at[0];
+  const bool prepared = PREP && a.prep_cap > 0 && a.prep_at[0];
   const int part_cost = prepared ? C::kPartCostPrep : kPartCost;
   {
     const Cut cut =
@@ -758,6 +995,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
   // The block's parts in order, as the load warp announces them: part k in parts[k % kParts].
   auto part_ready = [&](int k) {
     return mbar_wait(&bars.part_full[k % kParts], (k / kParts) & 1, a.err);
+  };
+  auto part_looked = [&](int k) {
+    return mbar_wait(&bars.looked[k % kParts], (k / kParts) & 1, a.err);
   };
   auto part_read = [&](int k) { mbar_arrive(&bars.part_empty[k % kParts]); };
 
@@ -794,15 +1034,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
     // copies the prepared key (0) or value (1) operands of a part's steps, a warp each: eight arrivals
     // a step, as from the dequantising warps
     auto copy_prepared = [&](int which, const Part& p) {
-      // first prepared step of the context; of the steps behind the first tokens
-      const int left_out = MASK ? skipped<kStep>(a, first_start(a, p.r)) : 0;
-      const int at = a.prep_at[1 + p.b] + p.h * ((p.r.kv + kStep - 1) / kStep - left_out);
+      const int at = first_prepared<MASK>(a, p);
       constexpr int kRing = C::kOpsK;
       static_assert(C::kOpsK == C::kOpsV && kDeqWarps == 8, "one rule for both");
       for (int t = p.t0; t < p.t1; ++t, ++n) {
-        // (where a row tile leaves steps out, its context does as many or fewer)
-        int step = at + t;
-        if (MASK && t >= first_tiles<kStep>(a)) step += p.skip - left_out;
+        const int step = prepared_step<MASK>(a, p, at, t);
         const int op = n % kRing;
         uint64_t* full = which ? &bars.v_full[op] : &bars.k_full[op];
         ok = mbar_wait(which ? &bars.v_empty[op] : &bars.k_empty[op], ((n / kRing) & 1) ^ 1, a.err);
@@ -816,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           mbar_arrive(full);
         } else if (lane == kDeqWarps && which == 0) {
           mbar_arrive_expect_tx(&bars.x_full[n % kExps], sizeof(exps[0]));
-          copy_record(exps[n % kExps], a.prep_exps + (int64_t)step * kRecs, sizeof(exps[0]),
+          copy_record(&exps[n % kExps], a.prep_exps + (int64_t)step * kPrepExps, sizeof(exps[0]),
                       &bars.x_full[n % kExps]);
         }
         __syncwarp();
@@ -866,6 +1102,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           mbar_arrive(&bars.part_full[k % kParts]);
         }
         if (!p.some) break;
+        const bool look = look_for_uneven<D, MASK>(a, p, prepared);
+        if (lane == 0) {
+          uneven[k % kParts] = look;
+          mbar_arrive(&bars.looked[k % kParts]);
+        }
         w = p.next;
       }
     } else if (warp == kLoadWarp || warp == kValueLoadWarp) {
@@ -1086,8 +1327,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       if (prepared) continue;  // (steps are counted by those who use them)
       const int t0 = p.t0, t1 = p.t1, skip = MASK ? p.skip : 0;
       const Unread<MASK> un(a, p.r);
-      auto steps = [&](auto keys) {  // a loop for the keys' warps, one for the values'
-        constexpr bool kKeys = decltype(keys)::value;
+      // loops for the keys' warps and for the values', of parts without uneven records and with them
+      auto steps = [&](auto keys, auto look) {
+        constexpr bool kKeys = decltype(keys)::value, kLook = decltype(look)::value;
         constexpr int kRing = kKeys ? C::kRawK : C::kRawV, kOps = kKeys ? C::kOpsK : C::kOpsV;
         for (int t = t0; t < t1; ++t, ++n) {
           const int st = n % kRing, op = n % kOps;
@@ -1095,12 +1337,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           ok = mbar_wait(&bars.raw_full[!kKeys][st], (n / kRing) & 1, a.err);
           ok = __all_sync(~0u, ok);
           if (!ok) return;
-          Exps* ex = &exps[n % kExps][oct >> 1];
+          StepExps* ex = &exps[n % kExps];
           if constexpr (kKeys)
-            d.keys(ops + C::kOffRaw + st * kRecs * C::kSideK, oct, tok, un, ex);
+            d.template keys<kLook>(ops + C::kOffRaw + st * kRecs * C::kSideK, oct, tok, un, ex);
           else  // (a value side begins with its parameters: R::kVp from where the record would)
-            d.values(ops + C::kOffRawV + st * kRecs * C::kSideV - C::R::kVp, tables[oct], oct, tok, un,
-                     ex, &bars.ev_full[n % kExps]);
+            d.template values<kLook>(ops + C::kOffRawV + st * kRecs * C::kSideV - C::R::kVp, tables[oct],
+                                     oct, tok, un, ex, &bars.ev_full[n % kExps]);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.raw_empty[!kKeys][st]);
           ok = mbar_wait(kKeys ? &bars.k_empty[op] : &bars.v_empty[op], ((n / kOps) & 1) ^ 1, a.err);
@@ -1113,8 +1355,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           if (lane == 0) mbar_arrive(kKeys ? &bars.k_full[op] : &bars.v_full[op]);
         }
       };
-      if (is_key) steps(std::true_type());
-      else steps(std::false_type());
+      ok = __all_sync(~0u, part_looked(k));
+      if (!ok) break;
+      const bool look = uneven[k % kParts];
+      if (is_key && !look) steps(std::true_type(), std::false_type());
+      else if (!look) steps(std::false_type(), std::false_type());
+      else if (is_key) steps(std::true_type(), std::true_type());
+      else steps(std::false_type(), std::true_type());
     }
   } else {
     registers_up<kRegsSoft>();
@@ -1132,126 +1379,140 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       const int row = row0 + lane, tok = a.d.by_G(row);
       const bool on = row < rows_left;
       int lim = on ? seen_by(p.r, tok) : p.r.kv;
-      int least = seen_by(p.r, a.d.by_G(p.rt * kRows));
-      // with masks: tokens from `low` on lie in every window of the row tile
-      int low = INT_MIN;
+      const Edges<MASK> edges(a, p);
       RowView view(a, p, tok, MASK && on);
       if constexpr (MASK) {
         lim = 0;  // (tokens seen so far, of this part: whether there are any)
-        if (a.masks) least = p.r.kv - p.r.qn;
-        // (or behind the row tile's last token)
-        const int last = p.r.kv - p.r.qn + a.d.by_G((p.rt + 1) * kRows);
-        low = window_start(a, a.masks ? p.r.kv - 1 : min(p.r.kv - 1, last));
       }
       float m = -INFINITY, l = 0.f, unit = 0.f, most_ev = -INFINITY;
-      for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-        ok = mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err) &&
-             mbar_wait(prepared ? &bars.x_full[n % kExps] : &bars.ev_full[n % kExps], (n / kExps) & 1,
-                       a.err);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (t == p.t0)  // back from the scaled queries' units to log2 units
-          unit = pow2(row_exp[kq % kExps][tid]) * (64.f / 8192.f) * a.d.scale_log2;
-        const uint32_t sb = lane_base + C::kColS + (n % C::kS) * kStep;
-        uint32_t s[kStep];
-        tmem_ld32(sb, s);
-        tmem_ld32(sb + 32, s + 32);
-        Exps ex[kRecs];
+      // the steps of a part without uneven records, or with them
+      auto steps = [&](auto has_uneven) {
+        constexpr bool kLook = decltype(has_uneven)::value;
+        for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
+          ok = mbar_wait(&bars.s_full[n % C::kS], (n / C::kS) & 1, a.err) &&
+               mbar_wait(prepared ? &bars.x_full[n % kExps] : &bars.ev_full[n % kExps], (n / kExps) & 1,
+                         a.err);
+          ok = __all_sync(~0u, ok);
+          if (!ok) return;
+          tc_fence_after();
+          if (t == p.t0)  // back from the scaled queries' units to log2 units
+            unit = pow2(row_exp[kq % kExps][tid]) * (64.f / 8192.f) * a.d.scale_log2;
+          const uint32_t sb = lane_base + C::kColS + (n % C::kS) * kStep;
+          bool apart = false;  // some weights enter the sum without their values' exponents
+          if constexpr (kLook) apart = scores_of_tokens(sb, exps[n % kExps], unit);
+          uint32_t s[kStep];
+          tmem_ld32(sb, s);
+          tmem_ld32(sb + 32, s + 32);
+          Exps ex[kRecs];
 #pragma unroll
-        for (int r = 0; r < kRecs; ++r) {
-          const float4 v = *reinterpret_cast<const float4*>(&exps[n % kExps][r]);
-          ex[r] = Exps{fmaxf(unit * v.x, kLeastUnit), v.y, v.z, 0.f};
-        }
-        float least_ev = ex[0].ev;
-        most_ev = fmaxf(most_ev, ex[0].ev);
+          for (int r = 0; r < kRecs; ++r) {
+            const float4 v = *reinterpret_cast<const float4*>(&exps[n % kExps].rec[r]);
+            ex[r] = Exps{fmaxf(unit * v.x, kLook ? kLeastUp : kLeastUnit), v.y, v.z, 0u};
+          }
+          float least_ev = ex[0].ev;
+          most_ev = fmaxf(most_ev, ex[0].ev);
 #pragma unroll
-        for (int r = 1; r < kRecs; ++r)
-          least_ev = fminf(least_ev, ex[r].ev), most_ev = fmaxf(most_ev, ex[r].ev);
-        const bool spread = least_ev < most_ev - kSpread;
-        wait_ld32(s);
-        wait_ld32(s + 32);
-        if constexpr (MASK) {
-          const int t0 = tile_at<MASK, kStep>(a, t, p.skip) * kStep;
-          if (t0 + kStep > least || (t0 < low && t0 + kStep > a.sinks)) {
-            const uint64_t seen = view.seen(a, t0);
-            const uint32_t half[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+          for (int r = 1; r < kRecs; ++r)
+            least_ev = fminf(least_ev, ex[r].ev), most_ev = fmaxf(most_ev, ex[r].ev);
+          const bool spread = least_ev < most_ev - kSpread;
+          wait_ld32(s);
+          wait_ld32(s + 32);
+          if constexpr (MASK) {
+            const int t0 = tile_at<MASK, kStep>(a, t, p.skip) * kStep;
+            if (edges.in(t0)) {
+              const uint64_t seen = view.seen(a, t0);
+              const uint32_t half[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+#pragma unroll
+              for (int i = 0; i < kStep; ++i)
+                if (!(half[i / 32] >> (i % 32) & 1)) s[i] = 0xff800000u;  // -inf
+              lim |= seen != 0;
+            } else {
+              lim = 1;
+            }
+          } else if (edges.in(t * kStep)) {
 #pragma unroll
             for (int i = 0; i < kStep; ++i)
-              if (!(half[i / 32] >> (i % 32) & 1)) s[i] = 0xff800000u;  // -inf
-            lim |= seen != 0;
-          } else {
-            lim = 1;
+              if (t * kStep + i >= lim) s[i] = 0xff800000u;  // -inf
           }
-        } else if ((t + 1) * kStep > least) {
+          float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < kStep; ++i)
-            if (t * kStep + i >= lim) s[i] = 0xff800000u;  // -inf
-        }
-        float top = -INFINITY;
+          for (int r = 0; r < kRecs; ++r) {
+            float x = __uint_as_float(s[16 * r]);
 #pragma unroll
-        for (int r = 0; r < kRecs; ++r) {
-          float x = __uint_as_float(s[16 * r]);
-#pragma unroll
-          for (int i = 1; i < 16; ++i) x = fmaxf(x, __uint_as_float(s[16 * r + i]));
-          top = fmaxf(top, fmaf(x, ex[r].up_k, ex[r].ev));
-        }
-        if (__any_sync(~0u, top > m + kSlack)) {
-          const float m_new = fmaxf(m, top);
-          const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
-          const float root = m_new == -INFINITY ? 1.f : exp2_fast(0.5f * (m - m_new));
-          m = m_new;
-          l = l * root * root;  // (see part_root)
-          if (t > p.t0) {
-            // the outputs so far, once the last product has landed
-            ok = mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err);
-            ok = __all_sync(~0u, ok);
-            if (!ok) break;
-            tc_fence_after();
+            for (int i = 1; i < 16; ++i) x = fmaxf(x, __uint_as_float(s[16 * r + i]));
+            top = fmaxf(top, fmaf(x, ex[r].up_k, ex[r].ev));
+          }
+          if (__any_sync(~0u, top > m + kSlack)) {
+            const float m_new = fmaxf(m, top);
+            const float f = m_new == -INFINITY ? 1.f : exp2_fast(m - m_new);
+            const float root = m_new == -INFINITY ? 1.f : exp2_fast(0.5f * (m - m_new));
+            m = m_new;
+            l = l * root * root;  // (see part_root)
+            if (t > p.t0) {
+              // the outputs so far, once the last product has landed
+              ok = mbar_wait(&bars.pv_done[(n - 1) % C::kS], ((n - 1) / C::kS) & 1, a.err);
+              ok = __all_sync(~0u, ok);
+              if (!ok) return;
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(lane_base + c, o);
-              wait_ld32(o);
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(lane_base + c, o);
+                wait_ld32(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(lane_base + c, o);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(lane_base + c, o);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
           }
-        }
-        const float ref = m == -INFINITY ? 0.f : kLift - m;
-        if (__any_sync(~0u, spread)) {
-          // with 2^ev weights may vanish that count in the sum: there they enter it without
+          const float ref = m == -INFINITY ? 0.f : kLift - m;
+          if (__any_sync(~0u, spread || (kLook && apart))) {
+            // with 2^ev weights may vanish that count in the sum: there they enter it without
 #pragma unroll
-          for (int r = 0; r < kRecs; ++r)
-            if (ex[r].ev < most_ev - kSpread) {
+            for (int r = 0; r < kRecs; ++r)
+              if (kLook && marked(ex[r].down_v)) {
+                const TokenBytes ev = token_bytes(exps[n % kExps].tok[1] + 16 * r);
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                l += exp2_fast(fmaf(__uint_as_float(s[16 * r + i]), ex[r].up_k, ref));
-              ex[r].down_v = 0.f;
+                for (int i = 0; i < 16; ++i)
+                  l += exp2_fast(fmaf(__uint_as_float(s[16 * r + i]), ex[r].up_k,
+                                      ref + (ex[r].ev - (float)ev[i])));
+                ex[r].down_v = 0.f;
+              } else if (ex[r].ev < most_ev - kSpread) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  l += exp2_fast(fmaf(__uint_as_float(s[16 * r + i]), ex[r].up_k, ref));
+                ex[r].down_v = 0.f;
+              }
+          }
+          uint32_t w[kStep / 2];
+#pragma unroll
+          for (int r = 0; r < kRecs; ++r) {
+            const uint64_t add = pair(ref + ex[r].ev), mul = pair(ex[r].up_k);
+            uint64_t sum = 0;  // two fp32 zeros
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float x0, x1;
+              fma_pair(x0, x1, s[16 * r + i], s[16 * r + i + 1], mul, add);
+              const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
+              add_pair(sum, p0, p1);
+              w[8 * r + i / 2] = pack_f16(p0, p1);
             }
-        }
-        uint32_t w[kStep / 2];
-#pragma unroll
-        for (int r = 0; r < kRecs; ++r) {
-          const uint64_t add = pair(ref + ex[r].ev), mul = pair(ex[r].up_k);
-          uint64_t sum = 0;  // two fp32 zeros
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x0, x1;
-            fma_pair(x0, x1, s[16 * r + i], s[16 * r + i + 1], mul, add);
-            const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
-            add_pair(sum, p0, p1);
-            w[8 * r + i / 2] = pack_f16(p0, p1);
+            l = fmaf(__uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32)),
+                     ex[r].down_v, l);
           }
-          l = fmaf(__uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32)),
-                   ex[r].down_v, l);
+          tmem_st32(sb, w);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars.p_full[n % C::kS]);
         }
-        tmem_st32(sb, w);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars.p_full[n % C::kS]);
+      };
+      if (p.t1 > p.t0) {
+        ok = __all_sync(~0u, part_looked(k));
+        if (!ok) break;
+        // (written again for part k + kParts, once the outputs of this one are on their way)
+        if (uneven[k % kParts]) steps(std::true_type());
+        else steps(std::false_type());
       }
       if (!ok) break;
       if (p.tiles == 0) {  // rows that see nothing
@@ -1328,7 +1589,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
   using R = Record<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint4 tables[kDeqWarps][4 * C::NG];
-  __shared__ Exps exps[kRecs];
+  __shared__ __align__(16) StepExps exps;
   __shared__ int64_t sums[kPrepThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5;
   int64_t* first = reinterpret_cast<int64_t*>(smem + P::kFirst);
@@ -1387,10 +1648,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
     Dequant<D> d;
     const int oct = warp & 7, tok = t * kStep + 8 * oct;
     if (warp < kDeqWarps) {
-      d.keys(ops + P::kRaw, oct, tok, un, &exps[oct >> 1]);
+      d.template keys<true>(ops + P::kRaw, oct, tok, un, &exps);
       d.store_keys(ops, oct);
     } else {
-      d.values(ops + P::kRawV - R::kVp, tables[oct], oct, tok, un, &exps[oct >> 1], nullptr);
+      d.template values<true>(ops + P::kRawV - R::kVp, tables[oct], oct, tok, un, &exps, nullptr);
       d.store_values(ops + C::kK, oct);
     }
     fence_proxy_async_smem();
@@ -1398,8 +1659,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
     if (tid == 0) {
       store_operands(a.prep + (int64_t)u * 2 * C::kK, ops, 2 * C::kK);
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    } else if (tid >= 32 && tid < 32 + kRecs) {
-      a.prep_exps[(int64_t)u * kRecs + tid - 32] = *reinterpret_cast<const uint4*>(&exps[tid - 32]);
+    } else if (tid >= 32 && tid < 32 + kPrepExps) {
+      uint4 w = reinterpret_cast<const uint4*>(&exps)[tid - 32];
+      if (tid == 32) {
+        w.w = 0;
+        for (int r = 0; r < kRecs; ++r) w.w |= marked(exps.rec[r].up_k) || marked(exps.rec[r].down_v);
+      }
+      a.prep_exps[(int64_t)u * kPrepExps + tid - 32] = w;
     }
     __syncthreads();
   }
@@ -1407,19 +1673,20 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
 }
 
 template <int D, bool MASK>
-cudaError_t launch(const FwdArgs& args, int sms, cudaStream_t s) {
-  FwdArgs a = args;
-  if ((int64_t)a.max_q * a.d.G > (kPrepTiles - 1) * kRows) {
-    const cudaError_t e = launch_pdl(attn_prepare_kernel<D, MASK>, dim3(2 * sms), dim3(kPrepThreads),
-                                     PrepCfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
-    if (e != cudaSuccess) return e;
-  } else {
-    a.prep_cap = 0;
-  }
+cudaError_t launch(const FwdArgs& a, int sms, cudaStream_t s) {
+  // Calls that never form contexts first have a kernel without that: what it leaves out saves instruction
+  // fetches (the trees above 66 and 63 us, 8 requests of 64 tokens over 8000, 64 channels, 109 and 104).
   const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
-  const cudaError_t e =
-      launch_pdl(attn_prefill_kernel<D, MASK>, dim3(blocks), dim3(kThreads),
-                 Cfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
+  const size_t smem = Cfg<D>::kSmem + (a.B + 1) * sizeof(int64_t);
+  cudaError_t e;
+  if ((int64_t)a.max_q * a.d.G > (kPrepTiles - 1) * kRows) {
+    e = launch_pdl(attn_prepare_kernel<D, MASK>, dim3(2 * sms), dim3(kPrepThreads),
+                   PrepCfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attn_prefill_kernel<D, MASK, true>, dim3(blocks), dim3(kThreads), smem, s, a);
+  } else {
+    e = launch_pdl(attn_prefill_kernel<D, MASK, false>, dim3(blocks), dim3(kThreads), smem, s, a);
+  }
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_join_kernel<D, kRows>, dim3(8 * sms), dim3(kJoinThreads), 0, s, a, blocks);
 }
@@ -1433,12 +1700,14 @@ cudaError_t launch_any(const FwdArgs& a, int sms, cudaStream_t s) {
 
 template <int D, bool MASK>
 cudaError_t prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(
-      attn_prepare_kernel<D, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      PrepCfg<D>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_prefill_kernel<D, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<D>::kSmem + (kMaxRequests + 1) * (int)sizeof(int64_t));
+  constexpr cudaFuncAttribute kMost = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  constexpr int kFirsts = (kMaxRequests + 1) * (int)sizeof(int64_t), kSmem = Cfg<D>::kSmem + kFirsts;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(attn_prepare_kernel<D, MASK>, kMost, PrepCfg<D>::kSmem + kFirsts)) !=
+          cudaSuccess ||
+      (e = cudaFuncSetAttribute(attn_prefill_kernel<D, MASK, true>, kMost, kSmem)) != cudaSuccess)
+    return e;
+  return cudaFuncSetAttribute(attn_prefill_kernel<D, MASK, false>, kMost, kSmem);
 }
 
 template <bool MASK>
