@@ -1560,10 +1560,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
 // Forms the MMA operands of every step of every context once, for calls whose contexts many row
 // tiles read.
 constexpr int kPrepThreads = 512;
-// From this many row tiles per context, on average, it pays (256 channels, 16 contexts of 2000 to 4000
-// tokens, prepared against not: 4 row tiles 105 and 90 us, 6 122 and 124, 8 145 and 158; 128 channels,
-// 8 contexts of 8000: 4 308 and 292).
-constexpr int kPrepTiles = 7;
+// From this many row tiles per context, on average, it pays.  Row tiles of chunks, 8 contexts of 8000
+// tokens, then 16 of 3000, prepared against not: 256 channels 8 row tiles 183 and 159, 141 and 134 us, 9 177
+// and 176, 141 and 148, 10 187 and 192, 150 and 161; 128 channels 9 463 and 444, 380 and 368, 10 521 and 490,
+// 408 and 410, 12 514 and 579, 449 and 478; 64 channels 4 115 and 110, 93 and 95, 5 131 and 133, 106 and
+// 113, 6 147 and 156, 118 and 133.
+template <int D>
+constexpr int kPrepTiles = D == 64 ? 5 : D == 128 ? 11 : 9;
+// The same behind a window, by a bound of the steps that its row tiles go over (for narrow windows twice
+// what they do).  Prompts of 1200 over 3000, 4 of them, 256, 128 and 64 channels: a window of 16 51 and 58,
+// 76 and 80, 68 and 79 us, of 600 78 and 104, 118 and 146, 97 and 131.
+constexpr int kPrepTilesWindow = 7;
 constexpr int64_t kMostPrep = 512ll << 20;  // bytes of operands held
 
 template <int D>
@@ -1616,7 +1623,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
   const int64_t both = first[a.B];
   __syncthreads();  // every thread has it, and decides alike, before the sums lose their upper halves
   const int64_t steps = both & 0xffffffff;
-  const bool prepared = steps <= a.prep_cap && (both >> 32) >= kPrepTiles * steps;
+  const int tiles = MASK && a.window ? kPrepTilesWindow : kPrepTiles<D>;
+  const bool prepared = steps <= a.prep_cap && (both >> 32) >= tiles * steps;
   for (int b = tid; b <= a.B; b += kPrepThreads) {
     first[b] &= 0xffffffff;
     if (blockIdx.x == 0 && b < a.B) a.prep_at[1 + b] = (int)min(first[b], (int64_t)INT_MAX);
@@ -1679,7 +1687,8 @@ cudaError_t launch(const FwdArgs& a, int sms, cudaStream_t s) {
   const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
   const size_t smem = Cfg<D>::kSmem + (a.B + 1) * sizeof(int64_t);
   cudaError_t e;
-  if ((int64_t)a.max_q * a.d.G > (kPrepTiles - 1) * kRows) {
+  const int tiles = MASK && a.window ? kPrepTilesWindow : kPrepTiles<D>;
+  if ((int64_t)a.max_q * a.d.G > (tiles - 1) * kRows) {
     e = launch_pdl(attn_prepare_kernel<D, MASK>, dim3(2 * sms), dim3(kPrepThreads),
                    PrepCfg<D>::kSmem + (a.B + 1) * sizeof(int64_t), s, a);
     if (e != cudaSuccess) return e;

@@ -20,7 +20,7 @@ WAYS = [(2.0 ** e, False) for e in (5, 8, 9, 12, 24, 100)] + [(2.0 ** e, True) f
 
 
 def n_prepared(G):
-    return -(-9 * 128 // G)
+    return -(-12 * 128 // G)
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)
