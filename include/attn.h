@@ -15,6 +15,7 @@
  *   attn_qk_norm_rope_append   norm, rotation and quantisation of a step's rows, one pass
  *   attn_kv4_forward_masked    attention through a window with first tokens, or of a tree
  *   attn_kv4_accept            the accepted tokens' cached rows moved to where they belong
+ *   attn_kv4_accept_pages      the same, and the rejected ones' pages put back on the free list
  *
  * Source: "Optimizing on-device inference for Apple Silicon", § "Read attention cache
  * efficiently" (16 query heads over 2 key/value heads of 256 channels; the query heads of a
@@ -233,14 +234,29 @@ int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, cons
  *                            entries behind path_lens[b] are not read
  *   path_lens [B] int32      0 .. path_width
  * Rows behind the accepted ones keep what they hold.  attn_plan counts a request's pages from its
- * ctx_lens: pages taken for rejected tokens alone are the caller's to put back on its free list, or
- * they are replaced in the table by new ones.  Requests share none of the pages that they move rows
+ * ctx_lens: pages taken for rejected tokens alone are put back by attn_kv4_accept_pages, or else by the
+ * caller; the next plan replaces them in the table, and what is not put back is lost.  Requests share none of the pages that they move rows
  * in.  A length out of range moves nothing; an entry that is negative or not above the one before it,
  * or a row outside the table or the cache, is left out (MOE_ERR_DEVICE; the request's moved rows are
  * then undefined). */
 int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int table_width,
                     const int32_t* ctx_lens, const int32_t* paths, int path_width,
                     const int32_t* path_lens, int B, void* stream);
+
+/* The same, and the pages that the step's plan took for rejected tokens alone go back on the free list:
+ * of request b the table's entries from page (ctx_lens[b] + path_lens[b] + P - 1) / P up to the last one of
+ * kv_lens[b] tokens, to free_pages [n_free] in front of *cursor, requests in order; the cursor moves
+ * back by as many.  One launch as well.
+ *   kv_lens [B] int32   lengths with the drafted tokens, as attn_plan wrote them (a refused request's 0
+ *                       puts nothing back, nor does one below ctx_lens[b])
+ *   free_pages, n_free, cursor   of the plan; read and written
+ * The table keeps its entries; the next plan replaces them.  A request whose path_lens or ctx_lens is out of
+ * range puts nothing back; a page id that the cache does not have is left out, and a cursor that is not
+ * in 0 .. n_free, or with fewer entries before it, leaves list and cursor alone (MOE_ERR_DEVICE). */
+int attn_kv4_accept_pages(attn_handle h, void* cache, const int32_t* block_table, int table_width,
+                          const int32_t* ctx_lens, const int32_t* paths, int path_width,
+                          const int32_t* path_lens, int B, const int32_t* kv_lens,
+                          int32_t* free_pages, int n_free, int32_t* cursor, void* stream);
 
 #ifdef __cplusplus
 }

@@ -41,7 +41,7 @@ EXPORTS = ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_ge
 ATTN_EXPORTS = ("attn_create", "attn_destroy", "attn_get_device_error", "attn_plan",
                 "attn_qk_norm_rope", "attn_kv4_append", "attn_kv4_read", "attn_kv4_forward",
                 "attn_tree_plan", "attn_qk_norm_rope_append", "attn_kv4_forward_masked",
-                "attn_kv4_accept")
+                "attn_kv4_accept", "attn_kv4_accept_pages")
 
 # kernel order reported by moe_profile_end
 KERNELS_GEMM = ("router_topk", "route_plan_scatter", "experts", "combine")
@@ -146,6 +146,9 @@ def lib():
                                               i64, _c_void_p]
         L.attn_kv4_accept.argtypes = [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p,
                                       _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p]
+        L.attn_kv4_accept_pages.argtypes = [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p,
+                                            _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
+                                            _c_void_p, _c_int, _c_void_p, _c_void_p]
         for fn in ATTN_EXPORTS:
             getattr(L, fn).restype = _c_int
         for fn in ("moe_create", "moe_create_q4", "moe_read_probe", "moe_route", "moe_forward", "moe_forward_host",
@@ -290,6 +293,13 @@ def attn_kv4_accept(h, cache, block_table, table_width, ctx_lens, paths, path_wi
                     stream):
     return lib().attn_kv4_accept(h, cache, block_table, table_width, ctx_lens, paths, path_width,
                                  path_lens, B, stream)
+
+
+def attn_kv4_accept_pages(h, cache, block_table, table_width, ctx_lens, paths, path_width, path_lens,
+                          B, kv_lens, free_pages, n_free, cursor, stream):
+    return lib().attn_kv4_accept_pages(h, cache, block_table, table_width, ctx_lens, paths,
+                                       path_width, path_lens, B, kv_lens, free_pages, n_free, cursor,
+                                       stream)
 
 
 def moe_test_expire_waits(h, n_calls):
@@ -699,9 +709,13 @@ class PagedAttention:
             _check(st, "attn_tree_plan")
         return positions, masks
 
-    def accept(self, cache, block_table, ctx_lens, paths, path_lens, stream=None):
+    def accept(self, cache, block_table, ctx_lens, paths, path_lens, stream=None, kv_lens=None,
+               free_pages=None, cursor=None):
         """Moves cached rows ctx_lens[b] + paths[b][i] to ctx_lens[b] + i, i < path_lens[b]: the
-        accepted tokens of paths [B][width], ascending indices in their request."""
+        accepted tokens of paths [B][width], ascending indices in their request.  With the plan's
+        kv_lens, free_pages and cursor (which is moved back in place), pages that it took for
+        rejected tokens alone go back on the free list; without, they are the caller's to put back,
+        or the next plan's table loses them."""
         if block_table is None or paths is None:
             _missing("block_table" if block_table is None else "paths")
         if block_table.dim() != 2 or paths.dim() != 2:
@@ -709,10 +723,21 @@ class PagedAttention:
         B, width = block_table.shape
         path_width = paths.shape[1]
         ints = self._ints
-        st = self._lib.attn_kv4_accept(
-            self.handle, self._cache(cache), ints(block_table, "block_table", B * width), width,
-            ints(ctx_lens, "ctx_lens", B), ints(paths, "paths", B * path_width), path_width,
-            ints(path_lens, "path_lens", B), B, self._stream(stream))
+        back = [x is not None for x in (kv_lens, free_pages, cursor)]
+        if any(back) and not all(back):
+            _missing("kv_lens, free_pages or cursor (all or none)")
+        a = (self.handle, self._cache(cache), ints(block_table, "block_table", B * width), width,
+             ints(ctx_lens, "ctx_lens", B), ints(paths, "paths", B * path_width), path_width,
+             ints(path_lens, "path_lens", B), B)
+        if any(back):
+            n_free = free_pages.numel()
+            st = self._lib.attn_kv4_accept_pages(
+                *a, ints(kv_lens, "kv_lens", B), ints(free_pages, "free_pages", n_free), n_free,
+                ints(cursor, "cursor", 1), self._stream(stream))
+            if st:
+                _check(st, "attn_kv4_accept_pages")
+            return
+        st = self._lib.attn_kv4_accept(*a, self._stream(stream))
         if st:
             _check(st, "attn_kv4_accept")
 

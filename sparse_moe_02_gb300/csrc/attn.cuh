@@ -195,6 +195,11 @@ struct AcceptArgs {
   int table_width;
   const int32_t *ctx, *paths, *path_lens;
   int path_width, B;
+  // Pages of rejected tokens put back: lengths with the drafted tokens (NULL: none are), the free list.
+  const int32_t* kv_lens;
+  int32_t* free_pages;
+  int n_free;
+  int32_t* cursor;
 };
 
 cudaError_t launch_attn_accept(const AcceptArgs& p, const RowsArgs& a, int D, cudaStream_t s);

@@ -446,6 +446,29 @@ int attn_tree_plan(attn_handle h, const int32_t* parents, const int32_t* q_offse
   return record_cuda_status(moe::launch_attn_tree_plan(a, static_cast<cudaStream_t>(stream)));
 }
 
+int attn_kv4_accept_pages(attn_handle h, void* cache, const int32_t* block_table, int table_width,
+                          const int32_t* ctx_lens, const int32_t* paths, int path_width,
+                          const int32_t* path_lens, int B, const int32_t* kv_lens,
+                          int32_t* free_pages, int n_free, int32_t* cursor, void* stream) {
+  if (!h || B < 0 || table_width < 0 || path_width < 0 || n_free < 0) return MOE_ERR_INVALID_ARG;
+  if (B > h->cfg.max_requests || path_width > kMaxTokens) return MOE_ERR_UNSUPPORTED;
+  if (B == 0) return MOE_OK;
+  const int st = check_cache(cache);
+  if (st) return st;
+  if (!ctx_lens || !path_lens || !kv_lens || !cursor || (path_width > 0 && !paths) ||
+      (table_width > 0 && !block_table) || (n_free > 0 && !free_pages))
+    return MOE_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)block_table, (const void*)ctx_lens, (const void*)paths,
+                        (const void*)path_lens, (const void*)kv_lens, (const void*)free_pages,
+                        (const void*)cursor})
+    if (off4(p)) return MOE_ERR_ALIGNMENT;
+  const moe::RowsArgs a = rows_args(h, cache, nullptr, 0);
+  const moe::AcceptArgs p{block_table, table_width, ctx_lens, paths,      path_lens, path_width,
+                          B,           kv_lens,     free_pages, n_free, cursor};
+  return record_cuda_status(
+      moe::launch_attn_accept(p, a, h->d.D, static_cast<cudaStream_t>(stream)));
+}
+
 int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int table_width,
                     const int32_t* ctx_lens, const int32_t* paths, int path_width,
                     const int32_t* path_lens, int B, void* stream) {
@@ -459,7 +482,8 @@ int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int 
   if (off4(block_table) || off4(ctx_lens) || off4(paths) || off4(path_lens))
     return MOE_ERR_ALIGNMENT;
   const moe::RowsArgs a = rows_args(h, cache, nullptr, 0);
-  const moe::AcceptArgs p{block_table, table_width, ctx_lens, paths, path_lens, path_width, B};
+  const moe::AcceptArgs p{block_table, table_width, ctx_lens, paths, path_lens, path_width, B,
+                          nullptr,     nullptr,     0,        nullptr};
   return record_cuda_status(
       moe::launch_attn_accept(p, a, h->d.D, static_cast<cudaStream_t>(stream)));
 }

@@ -627,6 +627,73 @@ __device__ __forceinline__ int64_t slot_of(const AcceptArgs& p, const RowsArgs& 
   return slot < a.n_slots ? slot : -1;
 }
 
+// A request's table entries whose pages hold no accepted token: none where its lengths make no sense.
+__device__ __forceinline__ int2 rejected_pages(const AcceptArgs& p, const RowsArgs& a, int b) {
+  const int len = p.path_lens[b], ctx = p.ctx[b], kv = p.kv_lens[b];
+  if (len < 0 || len > p.path_width || ctx < 0 || kv < ctx) return make_int2(0, 0);
+  auto pages = [&](int64_t tokens) { return (tokens + (1 << a.page_shift) - 1) >> a.page_shift; };
+  const int64_t to = min(pages(kv), (int64_t)p.table_width);
+  return make_int2((int)min(pages((int64_t)ctx + len), to), (int)to);
+}
+
+// Puts them back in front of the free list's cursor, requests in order, and moves the cursor; one block, a
+// thread per request.  Page ids that the cache does not have are left out (and recorded).
+__device__ __forceinline__ void put_back(const AcceptArgs& p, const RowsArgs& a) {
+  __shared__ int sums[kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t n_pages = a.n_slots >> a.page_shift;
+  auto there = [&](int b, int i) {
+    const int page = p.table[(int64_t)b * p.table_width + i];
+    return page >= 0 && page < n_pages;
+  };
+  int all = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    int n = 0;
+    if (b0 + tid < p.B) {
+      const int2 r = rejected_pages(p, a, b0 + tid);
+      for (int i = r.x; i < r.y; ++i) n += there(b0 + tid, i);
+      if (n < r.y - r.x) record_error(a.err, kDevErrState);
+    }
+    n = __reduce_add_sync(~0u, n);
+    if (lane == 0) sums[warp] = n;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) all += sums[w];
+    __syncthreads();
+  }
+  const int cursor = *p.cursor;
+  if (cursor < all || cursor > p.n_free) {  // not a cursor of this list
+    if (tid == 0) record_error(a.err, kDevErrState);
+    return;
+  }
+  int32_t* dst = p.free_pages + (cursor - all);
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    int2 r = make_int2(0, 0);
+    int n = 0;
+    if (b0 + tid < p.B) {
+      r = rejected_pages(p, a, b0 + tid);
+      for (int i = r.x; i < r.y; ++i) n += there(b0 + tid, i);
+    }
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(~0u, end, o);
+      if (lane >= o) end += x;
+    }
+    if (lane == 31) sums[warp] = end;
+    __syncthreads();
+    int at = end - n, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += sums[w];
+      total += sums[w];
+    }
+    for (int i = r.x; i < r.y; ++i)
+      if (there(b0 + tid, i)) dst[at++] = p.table[(int64_t)(b0 + tid) * p.table_width + i];
+    dst += total;
+    __syncthreads();  // (the sums are free)
+  }
+  if (tid == 0) *p.cursor = cursor - all;
+}
+
 // A block per request and head, L = D / 8 lanes per accepted row, kThreads / L rows at a time: all
 // are read before any is written.  Entry i of an ascending path is i at least, so no row is written
 // before a later round reads it.  Bound by latency: lengths, path and table, rows, one after
@@ -641,6 +708,10 @@ __global__ void __launch_bounds__(kThreads) attn_accept_kernel(AcceptArgs p, Row
   const int b = blockIdx.x, h = blockIdx.y;
   pdl_wait();
   pdl_trigger();
+  if (b == p.B) {  // (there where pages are put back)
+    if (h == 0) put_back(p, a);
+    return;
+  }
   int len = p.path_lens[b];
   const int ctx = p.ctx[b];
   if (len < 0 || len > p.path_width || ctx < 0) {
@@ -793,7 +864,7 @@ cudaError_t launch_attn_rope_append(const RopeArgs& r, const RowsArgs& a, int D,
 }
 
 cudaError_t launch_attn_accept(const AcceptArgs& p, const RowsArgs& a, int D, cudaStream_t s) {
-  const dim3 grid(p.B, a.Hkv), block(kThreads);
+  const dim3 grid(p.B + (p.kv_lens != nullptr), a.Hkv), block(kThreads);
   if (D == 64) return launch_pdl(attn_accept_kernel<64>, grid, block, 0, s, p, a);
   if (D == 128) return launch_pdl(attn_accept_kernel<128>, grid, block, 0, s, p, a);
   return launch_pdl(attn_accept_kernel<256>, grid, block, 0, s, p, a);
