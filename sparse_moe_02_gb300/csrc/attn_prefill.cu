@@ -1358,10 +1358,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
       ok = __all_sync(~0u, part_looked(k));
       if (!ok) break;
       const bool look = uneven[k % kParts];
-      if (is_key && !look) steps(std::true_type(), std::false_type());
-      else if (!look) steps(std::false_type(), std::false_type());
-      else if (is_key) steps(std::true_type(), std::true_type());
-      else steps(std::false_type(), std::true_type());
+      if (__builtin_expect(look, 0)) {
+        if (is_key) steps(std::true_type(), std::true_type());
+        else steps(std::false_type(), std::true_type());
+      } else if (is_key) {
+        steps(std::true_type(), std::false_type());
+      } else {
+        steps(std::false_type(), std::false_type());
+      }
     }
   } else {
     registers_up<kRegsSoft>();
@@ -1511,7 +1515,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         ok = __all_sync(~0u, part_looked(k));
         if (!ok) break;
         // (written again for part k + kParts, once the outputs of this one are on their way)
-        if (uneven[k % kParts]) steps(std::true_type());
+        if (__builtin_expect(uneven[k % kParts], 0)) steps(std::true_type());
         else steps(std::false_type());
       }
       if (!ok) break;
