@@ -72,6 +72,17 @@ def test_prompts_over_prepared_contexts(Hq, Hkv, D, gain, keys, window):
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+@pytest.mark.parametrize("gain,keys", WAYS)
+def test_prompts_whose_contexts_are_formed_by_each_block(Hq, Hkv, D, gain, keys):
+    # long enough to ask whether contexts are formed first, too short for it
+    n = {256: 129, 128: 321, 64: 65}[D]
+    L = n + 350
+    tokens = [L - n // 2, L - 9]
+    s = View(Hq, Hkv, D, 32, [n], [L], seed=7, alive=plant(tokens, gain, keys))
+    check(s, s.forward(), without=tokens if keys else [])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
 @pytest.mark.parametrize("n", [40, None])
 def test_every_token_of_another_size(Hq, Hkv, D, n):
     # keys and values whose sizes jump from token to token, some of them zero: scores stay ordinary, as the
