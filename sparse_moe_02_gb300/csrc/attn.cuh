@@ -206,10 +206,11 @@ cudaError_t launch_attn_accept(const AcceptArgs& p, const RowsArgs& a, int D, cu
 cudaError_t launch_attn_read(const RowsArgs& a, int D, cudaStream_t s);
 
 // Attention of few query rows per key/value head and request (n_b G <= 32): attn_decode.cu.  Its
-// time grows with every 8 (128 and 64 channels: 16) rows, the other kernel's with every 128: 8
-// requests of 2 to 5 tokens, G = 4, contexts to 8000 took 26 us here and 41 there, of 8 tokens over
-// 8000 61 and 73; with 256 channels 8 requests of 4 tokens, G = 8, over 4000 28 and 35, but 32 of
-// them 73 and 67.
+// time grows with every 8 (128 and 64 channels: 16) rows, the other kernel's with every 128.  Here
+// and there, requests over 4000 tokens: 8 of 4 tokens, 256 channels, G = 8, 27 and 32 us, 16 38 and 39;
+// 32 of 8, 128 channels, G = 4, 115 and 120; 32 of 4, 64 channels, G = 8, 48 and 60.  From 25 rows on many
+// long contexts of 256 channels would be faster there (32 of 4 tokens 69 and 56, but over 1000 25
+// and 33): the rule takes no lengths.
 constexpr int kDecodeRows = 32;
 cudaError_t prepare_attn_decode_kernels();
 int attn_part_slots(int sms);  // partial results of a launch, of either kernel

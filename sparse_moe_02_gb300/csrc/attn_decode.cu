@@ -26,8 +26,8 @@
 // tokens, three blocks of four warps an SM); one block of twelve warps, the even cut and copies
 // ahead into the next context made it 42, a block per context where lengths are alike 39.
 // Measured, 16 query heads over 2 of 256 channels, one token: 256 cached tokens 7.4 us, 4096 10.7 us,
-// 131072 24.6 us (3.1 TB/s with everything); 48 requests of up to 16248 24.8 us, 64 of 4096 38.8 us
-// (3.9 TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 27.1 us.
+// 131072 23.8 us (3.2 TB/s with everything); 48 requests of up to 16248 23.9 us, 64 of 4096 38.2 us
+// (3.9 TB/s); 8 requests of 2 to 5 tokens, 32 heads over 8 of 128 channels, contexts to 8000, 25.7 us.
 //
 // The form with masks (MASK) goes over the tiles of the first tokens and of the window only, and
 // hides tokens by a word of drafted tokens and a window's start for each column.  Measured: 48

@@ -24,20 +24,20 @@
 // whose weights lie where the next scores go (a third score buffer, with half of Q in shared
 // memory, was no faster).
 //
-// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 138 us (990 TFLOP/s,
-// prepared; 209 us if not), 2048 over a context of 30000 755 us (1.37 PFLOP/s, 71% of a bf16 product's
-// rate; 990 us); 4096 tokens of 32 heads over 8 of 128 channels 177 us, over 4 of 64 channels 162 us; 7
-// ragged chunks and prompts of 28 heads over 4 of 128 77 us.  Of the 138 us the prepare launch takes 8,
+// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 140 us (980 TFLOP/s,
+// prepared; 209 us if not), 2048 over a context of 30000 757 us (1.36 PFLOP/s, 71% of a bf16 product's
+// rate; 990 us); 4096 tokens of 32 heads over 8 of 128 channels 179 us, over 4 of 64 channels 165 us; 7
+// ragged chunks and prompts of 28 heads over 4 of 128 80 us.  Of the 140 us the prepare launch takes 9,
 // start and tail of the blocks and the joins 20.
 //
 // The form with masks (MASK) has the same steps over fewer of the context's tokens: the steps of
 // the first tokens and those from a row tile's first window on.  A row's visible tokens of a step
 // are 64 bits, formed only where a step holds a window's start, the first tokens' end or drafted
 // tokens; of a wide tree all steps before the drafted ones need none.  Measured, 256 channels: a
-// prompt of 8192 through a window of 1024 167 us (787 TFLOP/s of the visible pairs: a row tile's 18
+// prompt of 8192 through a window of 1024 169 us (773 TFLOP/s of the visible pairs: a row tile's 18
 // steps touch 1152 tokens for the 1040 that a row sees, and each of its 7 to a block costs some
 // 5000 clocks besides, the change of queries and outputs), 16 trees of 20 to 60 tokens over
-// contexts to 16384 59 us, 32 of 8 to 31 through a window of 1024 34 us: 5 steps a block, and
+// contexts to 16384 60 us, 32 of 8 to 31 through a window of 1024 35 us: 5 steps a block, and
 // around them the launch, the cut and the first row tile found (9000 clocks), its queries (8000),
 // the first operands and scores (5000), outputs (5000) and the join.
 //
@@ -61,7 +61,7 @@
 // first: by the find warp, in a part's steps with edges, or by the prepare launch.  Parts without any run
 // through loops that know nothing of them: checked for in every step (by the softmax, by the warps that
 // form operands) they cost 3 to 20%, most of it instruction fetches.  As it is, prompts take 1 to 2%
-// more than without, trees 6% (16 of 20 to 60 tokens over 16384: 59 to 63 us).
+// more than without, chunks 5%, trees 3 to 5%.
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
 // in the few-row kernel; shared row tiles are joined by its second launch.  Behind a window row
@@ -240,10 +240,12 @@ constexpr int kZeroCost = 96;
 constexpr int kLeastSteps = 4;   // of a block
 // Row tiles behind a window cost alike, so where a share is several of them blocks may take whole
 // ones: no partial results and nothing to join, for up to this many steps more in the block that
-// has most.  Cut against whole, 256 channels, a window of 1024: 7350 tokens (7.8 steps more) 155
-// and 149 us, 8192 (17.0) 172.8 and 170.5, 2048 (18.5) 58.2 and 60.2, 7700 (28.5) 163.8 and 166.8;
-// 128 channels: 4096 tokens (0.8) 131 and 126, 7500 (9.7) 223 and 220; 64 channels: 8192 (7.9) 223
-// and 212.
+// has most.  Cut against whole, 256 channels, a window of 1024: 7350 tokens (7.8 steps more) 151 and 145
+// us, 6000 (11.3) 131 and 125, 8192 (17.0) 167 and 164.5, 2048 (18.5) 58.5 and 59.2, 4096 (27.7) 95
+// and 100, 7700 (28.5) 158 and 160; a window of 300: 4096 (12.0) 68 and 63; of 3000: 8192 (21.2) 298 and
+// 314; 128 channels: 4096 (0.8) 133 and 124, 2048 (9.7) 73 and 66, 6000 (21.0) 187 and 182; 64
+// channels: 8192 (7.9) 235 and 218, 11000 (16.3) 305 and 287.  As a part of the share the border is no
+// sharper: 0.24 gains 8% (2048 through 300), 0.06 loses 5% (8192 through 3000).
 constexpr int kWholeMore = 18;
 
 struct Cost {
@@ -1687,7 +1689,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prepare_kernel(FwdArgs a
 template <int D, bool MASK>
 cudaError_t launch(const FwdArgs& a, int sms, cudaStream_t s) {
   // Calls that never form contexts first have a kernel without that: what it leaves out saves instruction
-  // fetches (the trees above 66 and 63 us, 8 requests of 64 tokens over 8000, 64 channels, 109 and 104).
+  // fetches (16 trees of 20 to 60 tokens 65 and 63 us, 8 requests of 64 tokens over 8000, 64 channels, 109
+  // and 104).
   const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
   const size_t smem = Cfg<D>::kSmem + (a.B + 1) * sizeof(int64_t);
   cudaError_t e;

@@ -34,6 +34,10 @@ def check(s, got, without=()):
     _, v = s.cached()
     row = key = 0
     for b, (n, L) in enumerate(zip(s.new, s.kv)):
+        if L == 0:
+            assert not got[row:row + n].any()
+            row += n
+            continue
         sees = s.visible(b)
         top = v[key:key + L].abs().amax(-1)  # [tokens][heads]
         most = torch.where(sees[:, :, None], top[None], 0.0).amax(1)
