@@ -34,7 +34,7 @@
 // the first tokens and those from a row tile's first window on.  A row's visible tokens of a step
 // are 64 bits, formed only where a step holds a window's start, the first tokens' end or drafted
 // tokens; of a wide tree all steps before the drafted ones need none.  Measured, 256 channels: a
-// prompt of 8192 through a window of 1024 169 us (773 TFLOP/s of the visible pairs: a row tile's 18
+// prompt of 8192 through a window of 1024 167 us (787 TFLOP/s of the visible pairs: a row tile's 18
 // steps touch 1152 tokens for the 1040 that a row sees, and each of its 7 to a block costs some
 // 5000 clocks besides, the change of queries and outputs), 16 trees of 20 to 60 tokens over
 // contexts to 16384 60 us, 32 of 8 to 31 through a window of 1024 35 us: 5 steps a block, and
@@ -58,10 +58,11 @@
 // Uneven records.  What a row does not see must not cost it bits, so a record of which some rows see
 // only a part is formed with an exponent for each token where the tokens' bounds differ by more than
 // 2^kEven; the softmax then brings each score and weight to its token's.  Such records are looked for
-// first: by the find warp, in a part's steps with edges, or by the prepare launch.  Parts without any run
-// through loops that know nothing of them: checked for in every step (by the softmax, by the warps that
-// form operands) they cost 3 to 20%, most of it instruction fetches.  As it is, prompts take 1 to 2%
-// more than without, chunks 5%, trees 3 to 5%.
+// first: by the find warp, in a part's steps with edges, or by the prepare launch, whose findings the
+// softmax warps read (where the find warp did, chunks through a window took 88 us instead of 85).  Parts
+// without any run through loops that know nothing of them: checked for in every step (by the softmax,
+// by the warps that form operands) they cost 3 to 20%, most of it instruction fetches.  As it is, prompts
+// take 1% more than without, chunks 2 to 4%, trees 3 to 5%.
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
 // in the few-row kernel; shared row tiles are joined by its second launch.  Behind a window row
@@ -838,6 +839,17 @@ __device__ __forceinline__ int prepared_step(const FwdArgs& a, const Part& p, in
   return first + t;
 }
 
+// Whether any of a part's prepared steps has uneven records.  One warp.
+template <bool MASK>
+__device__ __forceinline__ bool prepared_uneven(const FwdArgs& a, const Part& p) {
+  const int at = first_prepared<MASK>(a, p);
+  bool some = false;
+#pragma unroll 1
+  for (int t = p.t0 + (threadIdx.x & 31); t < p.t1; t += 32)
+    some |= a.prep_exps[(int64_t)prepared_step<MASK>(a, p, at, t) * kPrepExps].w != 0;
+  return __any_sync(~0u, some);
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
   if constexpr (N == 4) {
@@ -851,23 +863,16 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
   }
 }
 
-// Whether a part has uneven records in steps with edges (of prepared contexts: any that were formed as
-// such).  One warp: page ids of eight steps, a lane a record, then the parameters of four records at a
-// time, those of a token's keys or values to a lane.
+// Whether a part has uneven records in steps with edges.  One warp: page ids of eight steps, a lane a
+// record, then the parameters of four records at a time, those of a token's keys or values to a lane.
 template <int D, bool MASK>
-__device__ __forceinline__ bool look_for_uneven(const FwdArgs& a, const Part& p, bool prepared) {
+__device__ __forceinline__ bool look_for_uneven(const FwdArgs& a, const Part& p) {
   using R = Record<D>;
   constexpr int NG = D / kGroup, kAtOnce = 4;
   static_assert(R::kVp == R::kKp + 16 * R::kPar, "keys' and values' parameters lie together");
   const int lane = threadIdx.x & 31;
   bool some = false;
   if (p.t0 >= p.t1) return false;
-  if (prepared) {
-    const int at = first_prepared<MASK>(a, p);
-    for (int t = p.t0 + lane; t < p.t1; t += 32)
-      some |= a.prep_exps[(int64_t)prepared_step<MASK>(a, p, at, t) * kPrepExps].w != 0;
-    return __any_sync(~0u, some);
-  }
   const Edges<MASK> edges(a, p);
   const Unread<MASK> un(a, p.r);
 #pragma unroll 1
@@ -1104,10 +1109,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           mbar_arrive(&bars.part_full[k % kParts]);
         }
         if (!p.some) break;
-        const bool look = look_for_uneven<D, MASK>(a, p, prepared);
-        if (lane == 0) {
-          uneven[k % kParts] = look;
-          mbar_arrive(&bars.looked[k % kParts]);
+        if (!prepared) {
+          const bool look = look_for_uneven<D, MASK>(a, p);
+          if (lane == 0) {
+            uneven[k % kParts] = look;
+            mbar_arrive(&bars.looked[k % kParts]);
+          }
         }
         w = p.next;
       }
@@ -1514,10 +1521,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
         }
       };
       if (p.t1 > p.t0) {
-        ok = __all_sync(~0u, part_looked(k));
-        if (!ok) break;
-        // (written again for part k + kParts, once the outputs of this one are on their way)
-        if (__builtin_expect(uneven[k % kParts], 0)) steps(std::true_type());
+        bool look;
+        if (prepared) {
+          look = prepared_uneven<MASK>(a, p);
+        } else {
+          ok = __all_sync(~0u, part_looked(k));
+          if (!ok) break;
+          // (written again for part k + kParts, once the outputs of this one are on their way)
+          look = uneven[k % kParts];
+        }
+        if (__builtin_expect(look, 0)) steps(std::true_type());
         else steps(std::false_type());
       }
       if (!ok) break;
