@@ -235,10 +235,10 @@ int attn_kv4_forward_masked(attn_handle h, const void* q, int64_t q_stride, cons
  *   path_lens [B] int32      0 .. path_width
  * Rows behind the accepted ones keep what they hold.  attn_plan counts a request's pages from its
  * ctx_lens: pages taken for rejected tokens alone are put back by attn_kv4_accept_pages, or else by the
- * caller; the next plan replaces them in the table, and what is not put back is lost.  Requests share none of the pages that they move rows
- * in.  A length out of range moves nothing; an entry that is negative or not above the one before it,
- * or a row outside the table or the cache, is left out (MOE_ERR_DEVICE; the request's moved rows are
- * then undefined). */
+ * caller; the next plan replaces them in the table, and what is not put back is lost.  Requests share
+ * none of the pages that they move rows in.  A length out of range moves nothing; an entry that is negative
+ * or not above the one before it, or a row outside the table or the cache, is left out
+ * (MOE_ERR_DEVICE; the request's moved rows are then undefined). */
 int attn_kv4_accept(attn_handle h, void* cache, const int32_t* block_table, int table_width,
                     const int32_t* ctx_lens, const int32_t* paths, int path_width,
                     const int32_t* path_lens, int B, void* stream);

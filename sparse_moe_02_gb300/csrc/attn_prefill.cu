@@ -62,7 +62,7 @@
 // softmax warps read (where the find warp did, chunks through a window took 88 us instead of 85).  Parts
 // without any run through loops that know nothing of them: checked for in every step (by the softmax,
 // by the warps that form operands) they cost 3 to 20%, most of it instruction fetches.  As it is, prompts
-// take 1% more than without, chunks 2 to 4%, trees 3 to 5%.
+// take 1 to 2% more than without, chunks 3%, trees 1 to 3%.
 //
 // Work.  Row tiles of all requests and heads, causally shortened, are cut evenly over the blocks as
 // in the few-row kernel; shared row tiles are joined by its second launch.  Behind a window row
@@ -98,9 +98,10 @@ constexpr int kExps = 8;             // steps of record exponents kept
 // f16's least spacing, 2^-25, so at most 2^(kEven + 6 - 25) of the bound of its own token, which is below
 // 8 times the token's largest entry (|bias| and 15 |step|, rounded up to powers of two): 2^-11 of it.
 constexpr int kEven = 5;
-// Least unit of a score among uneven records: scores times it are nothing beside any that count, and
-// what a token's exponent takes off, 209 at most, may be divided by it.
-constexpr float kLeastUp = 7.8886091e-31f;  // 2^-100
+// Bounds of a score's unit where there are uneven records.  Scores times the least are nothing beside any
+// that count, and what a token's exponent takes off, 209 at most, may be divided by it; the largest is far
+// beyond the range of scores, but a number where the unit of keys that a row does not see is none.
+constexpr float kLeastUp = 7.8886091e-31f, kMostUp = 1.2676506e30f;  // 2^-100, 2^100
 constexpr int kNotFinite = 127;      // in place of the exponent of a query row that is not finite
 
 template <int D>
@@ -467,21 +468,25 @@ __device__ __forceinline__ uint32_t bound_of(uint32_t packed) {
   return packed ? max(((packed & 0xffffu) >> 7) + 4, packed >> 23) : 0u;
 }
 
-__device__ __forceinline__ int exponent_of_bound(uint32_t bound) { return max((int)bound - 125, -90); }
+// A token's exponent from its bound, in a record whose largest is `all`.  Tokens that are not read fit
+// any; those of zeros are formed with 1 at most, lest a row's unit times a larger one is no number.
+__device__ __forceinline__ int exponent_of_bound(uint32_t bound, bool read, int all) {
+  return bound ? max((int)bound - 125, -90) : read ? min(all, 0) : all;
+}
 
 // Exponents of a record, `all` that of the largest, from the bounds of a lane's tokens (own half, other
-// half) in one of kGroups groups, 8 lanes apart: returns what to form the own token with.  Of uneven ones
-// the warp of the first half leaves the tokens' in `left` and marks *scale.
+// half; whether they are read) in one of kGroups groups, 8 lanes apart: returns what to form the own
+// token with.  Of uneven ones the warp of the first half leaves the tokens' in `left` and marks *scale.
 template <int kGroups>
-__device__ __forceinline__ int token_exponent(uint32_t own, uint32_t other, int all, int oct,
-                                              int8_t* left, float* scale) {
+__device__ __forceinline__ int token_exponent(uint32_t own, bool read, uint32_t other,
+                                              bool read_other, int all, int oct, int8_t* left,
+                                              float* scale) {
   const int lane = threadIdx.x & 31;
   uint32_t both = own << 16 | other;
 #pragma unroll
   for (int o = 8; o < 8 * kGroups; o <<= 1) both = max_u16x2(both, __shfl_xor_sync(~0u, both, o));
-  // (tokens of zeros fit any exponent)
-  const int e = both >> 16 ? exponent_of_bound(both >> 16) : all;
-  const int e2 = both & 0xffffu ? exponent_of_bound(both & 0xffffu) : all;
+  const int e = exponent_of_bound(both >> 16, read, all);
+  const int e2 = exponent_of_bound(both & 0xffffu, read_other, all);
   if (!__any_sync(~0u, min(e, e2) < all - kEven)) return all;
   if ((oct & 1) == 0) {
     if (lane < 8) {
@@ -533,9 +538,11 @@ struct Dequant {
     if constexpr (LOOK) {
       // (groups of a token may be as small; seldom are all)
       const uint32_t b = bound_of(magnitudes(w)), b2 = bound_of(magnitudes(w2));
-      if (__any_sync(~0u, (b && exponent_of_bound(b) < *e - kEven) ||
-                              (b2 && exponent_of_bound(b2) < *e - kEven)))
-        *e = token_exponent<NG>(b, b2, *e, oct, ex->tok[!kKeys], kKeys ? &own->up_k : &own->down_v);
+      const bool read = !un.token(tok + t), read2 = !un.token(tok + t + other);
+      if (__any_sync(~0u, min(exponent_of_bound(b, read, *e), exponent_of_bound(b2, read2, *e)) <
+                              *e - kEven))
+        *e = token_exponent<NG>(b, read, b2, read2, *e, oct, ex->tok[!kKeys],
+                                kKeys ? &own->up_k : &own->down_v);
     }
     return w;
   }
@@ -678,7 +685,7 @@ __device__ __forceinline__ bool scores_of_tokens(uint32_t at, const StepExps& ex
       const Exps rec = ex.rec[r + k];
       const TokenBytes ek = token_bytes(ex.tok[0] + 16 * (r + k));
       const TokenBytes ev = token_bytes(ex.tok[1] + 16 * (r + k));
-      const float up = fmaxf(unit * rec.up_k, kLeastUp), down = 1.f / up;
+      const float up = fminf(fmaxf(unit * rec.up_k, kLeastUp), kMostUp), down = 1.f / up;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float x = __uint_as_float(s[16 * k + i]);
@@ -895,7 +902,7 @@ __device__ __forceinline__ bool look_for_uneven(const FwdArgs& a, const Part& p)
       const unsigned have = __ballot_sync(~0u, held);
 #pragma unroll 1
       for (int k0 = 0; k0 < taken * kRecs; k0 += kAtOnce) {
-        uint32_t w[kAtOnce][NG];
+        uint32_t w[kAtOnce][NG], read = 0;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
           const uint8_t* at = a.cache + (uint64_t)__shfl_sync(~0u, record, k0 + i) * R::kBytes +
@@ -903,7 +910,10 @@ __device__ __forceinline__ bool look_for_uneven(const FwdArgs& a, const Part& p)
           const int tok = 16 * __shfl_sync(~0u, rec, k0 + i) + (lane & 15);
 #pragma unroll
           for (int g = 0; g < NG; ++g) w[i][g] = 0;
-          if ((have >> (k0 + i) & 1) && !un.token(tok)) load_words<NG>(w[i], at);
+          if ((have >> (k0 + i) & 1) && !un.token(tok)) {
+            load_words<NG>(w[i], at);
+            read |= 1u << i;
+          }
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
@@ -913,8 +923,8 @@ __device__ __forceinline__ bool look_for_uneven(const FwdArgs& a, const Part& p)
           const uint32_t b = bound_of(m);
           const uint32_t of_keys = __reduce_max_sync(~0u, lane < 16 ? b : 0u);
           const uint32_t of_values = __reduce_max_sync(~0u, lane < 16 ? 0u : b);
-          const int all = exponent_of_bound(lane < 16 ? of_keys : of_values);
-          some |= b && exponent_of_bound(b) < all - kEven;
+          const int all = max((int)(lane < 16 ? of_keys : of_values) - 125, -90);
+          some |= exponent_of_bound(b, read >> i & 1, all) < all - kEven;
         }
       }
     }
@@ -1421,6 +1431,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(FwdArgs a) {
           for (int r = 0; r < kRecs; ++r) {
             const float4 v = *reinterpret_cast<const float4*>(&exps[n % kExps].rec[r]);
             ex[r] = Exps{fmaxf(unit * v.x, kLook ? kLeastUp : kLeastUnit), v.y, v.z, 0u};
+            if (kLook) ex[r].up_k = fminf(ex[r].up_k, kMostUp);
           }
           float least_ev = ex[0].ev;
           most_ev = fmaxf(most_ev, ex[0].ev);

@@ -111,3 +111,23 @@ def test_a_large_value_of_next_to_no_weight(Hq, Hkv, D):
     v = s.cached()[1]
     v[at] = 0.0
     assert bool(((got - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * v.abs().max()).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+@pytest.mark.parametrize("form", ["drafts", "chunk", "prompt"])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_unseen_large_keys_beside_large_queries(Hq, Hkv, D, form, zeros):
+    # ordinary scores of queries 2^40 times as large and keys as much smaller (or none at all beside it); the
+    # last token's keys are so large that a query's unit times theirs leaves fp32
+    import torch
+    n = {"drafts": 4, "chunk": 40, "prompt": -(-12 * 128 * Hkv // Hq)}[form]
+    L = n + 300
+    q = (randn(gen(3), n, Hq, D) * 1.5 * 2.0 ** 40).bfloat16()
+
+    def alive(s):
+        s.k *= 2.0 ** -40
+        if zeros:
+            s.k[L - 50:L - 1] = 0.0
+        plant([L - 1], 2.0 ** 110, True)(s)
+    s = View(Hq, Hkv, D, 32, [n], [L], seed=8, alive=alive, q=q)
+    check(s, s.forward(), without=[L - 1])
