@@ -24,10 +24,10 @@
 // whose weights lie where the next scores go (a third score buffer, with half of Q in shared
 // memory, was no faster).
 //
-// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 140 us (980 TFLOP/s,
+// Measured, 16 query heads over 2 of 256 channels: 4096 tokens from nothing 141 us (970 TFLOP/s,
 // prepared; 209 us if not), 2048 over a context of 30000 757 us (1.36 PFLOP/s, 71% of a bf16 product's
 // rate; 990 us); 4096 tokens of 32 heads over 8 of 128 channels 179 us, over 4 of 64 channels 165 us; 7
-// ragged chunks and prompts of 28 heads over 4 of 128 80 us.  Of the 140 us the prepare launch takes 9,
+// ragged chunks and prompts of 28 heads over 4 of 128 80 us.  Of the 141 us the prepare launch takes 9,
 // start and tail of the blocks and the joins 20.
 //
 // The form with masks (MASK) has the same steps over fewer of the context's tokens: the steps of
@@ -37,7 +37,7 @@
 // prompt of 8192 through a window of 1024 167 us (787 TFLOP/s of the visible pairs: a row tile's 18
 // steps touch 1152 tokens for the 1040 that a row sees, and each of its 7 to a block costs some
 // 5000 clocks besides, the change of queries and outputs), 16 trees of 20 to 60 tokens over
-// contexts to 16384 60 us, 32 of 8 to 31 through a window of 1024 35 us: 5 steps a block, and
+// contexts to 16384 59 us, 32 of 8 to 31 through a window of 1024 35 us: 5 steps a block, and
 // around them the launch, the cut and the first row tile found (9000 clocks), its queries (8000),
 // the first operands and scores (5000), outputs (5000) and the join.
 //
